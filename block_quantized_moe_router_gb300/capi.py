@@ -22,11 +22,14 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_HASH, MOE_SCORE_SQRTSOFTPLUS = 0
 MOE_SCORE_SOFTMAX_BIAS, MOE_SCORE_HASH_SQRTSOFTPLUS = 4, 5
 MOE_FMT_NVFP4, MOE_FMT_MXFP4 = 0, 1
 MOE_ACT_BF16, MOE_ACT_NVFP4 = 0, 1
+MOE_DT_BF16, MOE_DT_F16 = 0, 1
+MOE_FUNC_NONE, MOE_FUNC_SILU, MOE_FUNC_GELU, MOE_FUNC_GELU_TANH, MOE_FUNC_RELU = range(5)
 
 # Every symbol include/moe.h declares.
 EXPORTED = ["moe_route", "moe_workspace_size", "moe_prepare_weights", "moe_release_weights",
             "moe_ffn_forward", "moe_forward", "moe_workspace_size_host", "moe_forward_host",
-            "moe_ffn_forward_noalloc", "moe_quantize_act_nvfp4",
+            "moe_ffn_forward_noalloc", "moe_quantize_act_nvfp4", "moe_route_grouped", "moe_linear",
+            "moe_add_rms_norm",
             "moe_set_wait_limit", "moe_skew_barrier", "moe_profile_enable", "moe_profile_read",
             "moe_status_string"]
 
@@ -59,6 +62,18 @@ class moe_route_desc(ctypes.Structure):
                 ("token_ids", ctypes.c_void_p), ("zero_experts", ctypes.c_int32)]
 
 
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("func", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -75,6 +90,13 @@ def load_library(path: str = LIB_PATH):
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_route.argtypes = [ctypes.POINTER(moe_route_desc), vp, vp, vp, vp, vp, vp, vp]
     lib.moe_route.restype = ctypes.c_int
+    lib.moe_route_grouped.argtypes = [ctypes.POINTER(moe_route_desc), i32, i32, i32, vp, vp, vp, vp,
+                                      vp, vp, vp]
+    lib.moe_route_grouped.restype = ctypes.c_int
+    lib.moe_linear.argtypes = [ctypes.POINTER(moe_linear_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_linear.restype = ctypes.c_int
+    lib.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_desc), vp, vp, vp, vp, vp, vp]
+    lib.moe_add_rms_norm.restype = ctypes.c_int
     lib.moe_workspace_size.argtypes = [ctypes.POINTER(moe_ffn_desc), i32, i32, ctypes.POINTER(sz)]
     lib.moe_workspace_size.restype = ctypes.c_int
     lib.moe_prepare_weights.argtypes = [ctypes.POINTER(moe_ffn_desc), ctypes.POINTER(vp), vp]
@@ -145,6 +167,39 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+
+
+def _stream_device(stream):
+    """The stream's handle and the current device, which every tensor of the call must be on."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    dev = s.device_index
+    if stream is not None and dev != torch.cuda.current_device():
+        raise ValueError("the stream must belong to the current CUDA device")
+    return s.cuda_stream, dev
+
+
+def _tptr(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of a stated type and shape on the current device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on the current CUDA "
+                         f"device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, rows, cols, dev, name):
+    """Pointer and row stride of a matrix of a stated type whose rows are contiguous."""
+    if t.dtype != dtype or t.shape != (rows, cols) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} matrix {(rows, cols)} on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (ld if rows > 1 else cols)
+
+
 def qtensor(p: Optional[dict]) -> moe_qtensor:
     """Weight dict {packed, scales, globals, fmt} of CUDA tensors -> moe_qtensor."""
     if p is None:
@@ -184,6 +239,78 @@ def moe_route(*, T, E, H, top_k, scoring, renormalize, routed_scaling, x=None, w
                        _dptr(topk_ids, torch.int32, "topk_ids"), _dptr(topk_w, torch.float32, "topk_w"),
                        _dptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "moe_route")
+
+
+def moe_route_grouped(*, T, E, H, top_k, scoring, renormalize, routed_scaling, n_group, topk_group,
+                      group_top=1, x=None, w_router=None, logits_in=None, logits_out=None,
+                      correction_bias=None, topk_ids, topk_w, dev_status=None, stream=None):
+    """moe_route with the top-K limited to the topk_group best of n_group expert groups."""
+    st, dev = _stream_device(stream)
+    E, H, top_k, T = int(E), int(H), int(top_k), int(T)
+    given = logits_in is not None
+    d = moe_route_desc(T, E, H, top_k, scoring, 1 if renormalize else 0, routed_scaling,
+                       None if given else _tptr(w_router, torch.bfloat16, (E, H), dev, "w_router"),
+                       _tptr(correction_bias, torch.float32, (E,), dev, "correction_bias"),
+                       None, 0, None, 0)
+    rc = load_library().moe_route_grouped(
+        ctypes.byref(d), n_group, topk_group, group_top,
+        None if given else _tptr(x, torch.bfloat16, (T, H), dev, "x"),
+        _tptr(logits_in, torch.float32, (T, E), dev, "logits_in"),
+        _tptr(logits_out, torch.float32, (T, E), dev, "logits_out"),
+        _tptr(topk_ids, torch.int32, (T, top_k), dev, "topk_ids"),
+        _tptr(topk_w, torch.float32, (T, top_k), dev, "topk_w"),
+        _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_route_grouped")
+
+
+def moe_linear(x, w, out, *, w_mul=None, bias=None, bias_mul=None, residual=None, func=MOE_FUNC_NONE,
+               dev_status=None, stream=None):
+    """out = f(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual]; x [T][K], w and w_mul [N][K],
+    residual and out [T][N] of one type (bf16 or f16), rows of any stride."""
+    st, dev = _stream_device(stream)
+    dt = x.dtype
+    T, K = x.shape
+    N = w.shape[0]
+    px, ldx = _rows(x, dt, T, K, dev, "x")
+    pw, ldw = _rows(w, dt, N, K, dev, "w")
+    po, ldo = _rows(out, dt, T, N, dev, "out")
+    pm = pr = None
+    ldr = N
+    if w_mul is not None:
+        pm, ldm = _rows(w_mul, dt, N, K, dev, "w_mul")
+        if ldm != ldw:
+            raise ValueError("w_mul must have the row stride of w")
+    if residual is not None:
+        pr, ldr = _rows(residual, dt, T, N, dev, "residual")
+    d = moe_linear_desc(T, N, K, _DTYPES.get(dt, -1), func, ldx, ldw, ldr, ldo)
+    rc = load_library().moe_linear(
+        ctypes.byref(d), px, pw, pm, _tptr(bias, torch.float32, (N,), dev, "bias"),
+        _tptr(bias_mul, torch.float32, (N,), dev, "bias_mul"), pr, po,
+        _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_linear")
+
+
+def moe_add_rms_norm(x, weight, out, *, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """s = x + residual; out = s * weight / sqrt(mean(s^2) + eps); sum_out = s.  x, residual, sum_out
+    and out [T][H], weight [H], of one type (bf16 or f16), rows of any stride."""
+    st, dev = _stream_device(stream)
+    dt = x.dtype
+    T, H = x.shape
+    px, ldx = _rows(x, dt, T, H, dev, "x")
+    po, ldo = _rows(out, dt, T, H, dev, "out")
+    pr = ps = None
+    ldr = lds = H
+    if residual is not None:
+        pr, ldr = _rows(residual, dt, T, H, dev, "residual")
+    if sum_out is not None:
+        ps, lds = _rows(sum_out, dt, T, H, dev, "sum_out")
+    d = moe_norm_desc(T, H, _DTYPES.get(dt, -1), eps, ldx, ldr, lds, ldo)
+    rc = load_library().moe_add_rms_norm(ctypes.byref(d), px, pr, _tptr(weight, dt, (H,), dev, "weight"),
+                                         ps, po, st)
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_add_rms_norm")
 
 
 def moe_workspace_size(desc: moe_ffn_desc, T: int, act: int) -> int:

@@ -125,6 +125,12 @@ moe_status_t validate_route(const moe_route_desc* d, const float* logits_in) {
     return MOE_OK;
 }
 
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned2(const void* p) { return reinterpret_cast<uintptr_t>(p) % 2 == 0; }
+
+constexpr int64_t kMaxLd = int64_t(1) << 38;  // 2-byte elements: row pitches below 2^39 bytes
+bool valid_ld(int64_t ld, int64_t n) { return ld >= n && ld < kMaxLd; }
+
 // The FFN launch description of one call; the workspace carve-up follows the path's plan.
 FfnLaunch make_launch(const Handle* h, int T, int act, float g1, float g2, int path,
                       const Workspace& ws, char* base, const void* x, const int32_t* ids,
@@ -237,6 +243,76 @@ moe_status_t moe_route(const moe_route_desc* d, const void* x_bf16, const float*
     const float* bias = d->scoring != MOE_SCORE_SOFTMAX ? d->correction_bias : nullptr;
     return launch_topk(logits, bias, d->T, Er, d->top_k, d->scoring, d->renormalize ? 1 : 0,
                        d->routed_scaling, topk_ids, topk_w, dev_status, st) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_route_grouped(const moe_route_desc* d, int32_t n_group, int32_t topk_group,
+                               int32_t group_top, const void* x_bf16, const float* logits_in,
+                               float* logits_out, int32_t* topk_ids, float* topk_w,
+                               int32_t* dev_status, void* stream) {
+    const moe_status_t v = validate_route(d, logits_in);
+    if (v != MOE_OK) return v;
+    if (is_hash(d->scoring) || d->zero_experts != 0) return MOE_ERR_UNSUPPORTED;
+    if (n_group < 1 || n_group > kMaxGroups || d->E % n_group || topk_group < 1 || topk_group > n_group)
+        return MOE_ERR_INVALID_ARG;
+    const int size = d->E / n_group;
+    if (group_top < 1 || group_top > 2 || group_top > size || d->top_k > topk_group * size)
+        return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (!topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const float* logits = logits_in;
+    if (!logits) {
+        if (!d->w_router || !x_bf16 || !logits_out || !aligned16(x_bf16) || !aligned16(d->w_router))
+            return MOE_ERR_INVALID_ARG;
+        cudaError_t err = launch_router_tc(x_bf16, d->w_router, logits_out, d->T, d->E, d->H,
+                                           dev_status, st);
+        if (err == cudaErrorNotSupported)
+            err = launch_router_logits(x_bf16, d->w_router, logits_out, d->T, d->E, d->H, st);
+        if (err != cudaSuccess) return MOE_ERR_CUDA;
+        logits = logits_out;
+    }
+    const float* bias = d->scoring != MOE_SCORE_SOFTMAX ? d->correction_bias : nullptr;
+    return launch_topk_grouped(logits, bias, d->T, d->E, d->top_k, d->scoring, d->renormalize ? 1 : 0,
+                               d->routed_scaling, n_group, topk_group, group_top, topk_ids, topk_w,
+                               dev_status, st) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_linear(const moe_linear_desc* d, const void* x, const void* w, const void* w_mul,
+                        const float* bias, const float* bias_mul, const void* residual, void* out,
+                        int32_t* dev_status, void* stream) {
+    if (!d || d->T < 0 || d->N < 1 || d->N > kMaxLinear || d->K < 8 || d->K > kMaxLinear || d->K % 8)
+        return MOE_ERR_INVALID_ARG;
+    if ((d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16) || d->func < MOE_FUNC_NONE ||
+        d->func > MOE_FUNC_RELU)
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_ld(d->ldx, d->K) || d->ldx % 8 || !valid_ld(d->ldw, d->K) || d->ldw % 8 ||
+        !valid_ld(d->ldo, d->N) || (residual && !valid_ld(d->ldr, d->N)) || (bias_mul && !w_mul))
+        return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(w_mul) || !aligned2(residual) ||
+        !aligned2(out))
+        return MOE_ERR_INVALID_ARG;
+    return launch_linear(*d, x, w, w_mul, bias, bias_mul, residual, out, dev_status,
+                         static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_add_rms_norm(const moe_norm_desc* d, const void* x, const void* residual,
+                              const void* weight, void* sum_out, void* out, void* stream) {
+    if (!d || d->T < 0 || d->H < 1 || d->H > kMaxNorm || !(d->eps >= 0.f) || !std::isfinite(d->eps) ||
+        (d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16))
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_ld(d->ldx, d->H) || !valid_ld(d->ldo, d->H) || (residual && !valid_ld(d->ldr, d->H)) ||
+        (sum_out && !valid_ld(d->lds, d->H)))
+        return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (!x || !weight || !out || sum_out == out || !aligned2(x) || !aligned2(residual) ||
+        !aligned2(weight) || !aligned2(sum_out) || !aligned2(out))
+        return MOE_ERR_INVALID_ARG;
+    return launch_add_rms_norm(*d, x, residual, weight, sum_out, out,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "moe.h"
+
 namespace moe {
 
 // ---- routing (route.cu) -------------------------------------------------------------------
@@ -24,6 +26,18 @@ cudaError_t launch_topk(const float* logits, const float* bias, int T, int E, in
 cudaError_t launch_hash_route(const int64_t* tid2eid, const int32_t* token_ids, int64_t vocab,
                               int T, int E, int k, float scaling, const float* logits, int renorm,
                               int32_t* ids, float* w, int32_t* status, cudaStream_t st);
+
+// Top-K limited to expert groups (route_grouped.cu).
+cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k, int scoring,
+                                int renorm, float scaling, int n_group, int topk_group, int group_top,
+                                int32_t* ids, float* w, int32_t* status, cudaStream_t st);
+
+// ---- dense layers around the experts (linear.cu, norm.cu) -----------------------------------
+cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
+                          const float* bias, const float* bias_mul, const void* residual, void* out,
+                          int32_t* status, cudaStream_t st);
+cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const void* r, const void* w,
+                                void* sum, void* out, cudaStream_t st);
 
 // ---- expert FFN (ffn.cu) --------------------------------------------------------------------
 // One projection as the kernels see it: packed codes, block scales, and a per-expert fp32

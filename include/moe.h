@@ -70,6 +70,17 @@ typedef enum { MOE_FMT_NVFP4 = 0, MOE_FMT_MXFP4 = 1 } moe_fmt_t;
  * (per 16 elements, E4M3 scale, static power-of-two f32 global) before the block-scaled FP4
  * MMA. */
 typedef enum { MOE_ACT_BF16 = 0, MOE_ACT_NVFP4 = 1 } moe_act_t;
+/* Element type of the matrices of moe_linear and the rows of moe_add_rms_norm. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1 } moe_dtype_t;
+/* Function of moe_linear's epilogue: z; z * sigmoid(z); z * Phi(z); the tanh form
+ * z / 2 * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))); max(z, 0). */
+typedef enum {
+    MOE_FUNC_NONE = 0,
+    MOE_FUNC_SILU = 1,
+    MOE_FUNC_GELU = 2,
+    MOE_FUNC_GELU_TANH = 3,
+    MOE_FUNC_RELU = 4
+} moe_func_t;
 
 /* One block-quantized projection, stacked over experts (layout in the header comment). */
 typedef struct {
@@ -111,6 +122,27 @@ typedef struct {
     int32_t zero_experts;      /* Z >= 0 zero-computation experts after the E real ones    */
 } moe_route_desc;
 
+/* A dense layer over T rows (moe_linear): x [T][K], w and w_mul [N][K], residual and out [T][N].
+ * The ld fields are the distances between rows in elements.  Constraints (checked): T >= 0;
+ * 1 <= N <= 1048576; K a multiple of 8, 8 <= K <= 1048576; ldx, ldw >= K and multiples of 8;
+ * ldr, ldo >= N; every ld below 2^38. */
+typedef struct {
+    int32_t T, N, K;
+    int32_t dtype;             /* moe_dtype_t of x, w, w_mul, residual and out             */
+    int32_t func;              /* moe_func_t                                               */
+    int64_t ldx, ldw, ldr, ldo;
+} moe_linear_desc;
+
+/* Rows of moe_add_rms_norm: x, residual, sum and out are [T][H] with rows ldx, ldr, lds, ldo
+ * elements apart.  Constraints (checked): T >= 0; 1 <= H <= 16384; every ld in use >= H and
+ * below 2^38; eps >= 0 and finite. */
+typedef struct {
+    int32_t T, H;
+    int32_t dtype;             /* moe_dtype_t of every tensor                              */
+    float eps;
+    int64_t ldx, ldr, lds, ldo;
+} moe_norm_desc;
+
 /* Router GEMM + top-K (every rule below runs over the E + zero_experts router outputs).
  *   Softmax: p = softmax(logits) over all E; the top_k largest are selected; weight =
  *     p / sum(selected p) when renormalize, else p; times routed_scaling.
@@ -145,6 +177,58 @@ typedef struct {
 moe_status_t moe_route(const moe_route_desc* desc, const void* x_bf16, const float* logits_in,
                        float* logits_out, int32_t* topk_ids, float* topk_w, int32_t* dev_status,
                        void* stream);
+
+/* moe_route with the top-K limited to expert groups.  The pages have no counterpart (their
+ * routers rank all experts); the scores, the correction bias and the weights are moe_route's.
+ * The E experts form n_group groups of E / n_group consecutive ids.  With s the score of the
+ * descriptor's scoring kind and v = s + correction_bias (v = s for plain softmax or a NULL bias):
+ *   a group's score is the sum of its group_top (1 or 2) largest v;
+ *   the topk_group groups with the largest scores are kept (ties: the lower group);
+ *   ids are the top_k largest v among the experts of the kept groups (ties: the lower expert), in
+ *   descending order; weight = s / sum(selected s) when renormalize, else s (for softmax kinds the
+ *   probability over all E); times routed_scaling.
+ * The order is that of the scores' exact values (fp32 scores too close to tell are compared again
+ * in fp64), so it does not depend on how fp32 rounds them.  A non-finite logit ranks below every
+ * finite one, counts as -infinity in its group's sum, weighs 0 and sets MOE_DEV_NONFINITE; a bias
+ * that is not finite ranks its expert with those, but the expert keeps its weight if it is
+ * selected for want of others.
+ * Arguments, outputs and T == 0 as for moe_route.  Further checks: scoring is not a hash kind
+ * (MOE_ERR_UNSUPPORTED); zero_experts == 0 (MOE_ERR_UNSUPPORTED); 1 <= n_group <= 64 divides E;
+ * 1 <= topk_group <= n_group; group_top is 1 or 2 and at most E / n_group; top_k <= topk_group *
+ * E / n_group; x_bf16 and w_router 16-byte aligned when the router GEMM runs. */
+moe_status_t moe_route_grouped(const moe_route_desc* desc, int32_t n_group, int32_t topk_group,
+                               int32_t group_top, const void* x_bf16, const float* logits_in,
+                               float* logits_out, int32_t* topk_ids, float* topk_w,
+                               int32_t* dev_status, void* stream);
+
+/* One dense layer: out = f(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual], for the bf16
+ * shared expert of the pages (moe/init.rs, the bf16 shared-expert handle lookups) and for plain
+ * layers next to the MoE ones.  Products accumulate in fp32; bias, function, the second factor
+ * and the residual are applied in fp32 and the result is rounded once (fp16 overflows to
+ * infinity).  The order of the sums depends on the sizes alone: equal calls give equal bits.
+ * x, w      [device] desc->dtype, 16-byte aligned.
+ * w_mul     [device] or NULL: the second matrix of the gated form, 16-byte aligned.
+ * bias, bias_mul [device] float [N] or NULL; bias_mul needs w_mul.
+ * residual  [device] or NULL; it may be out itself (same rows), not another overlapping buffer.
+ * out       [device]; must not overlap x, w or w_mul.
+ * dev_status [device] int32 [1] or NULL (MOE_DEV_TIMEOUT: a wait inside the kernel gave up and out
+ *           is invalid).
+ * Needs no workspace.  T == 0 is a valid no-op.  Errors: MOE_ERR_INVALID_ARG for the checks of
+ * moe_linear_desc, a NULL or misaligned pointer or bias_mul without w_mul; MOE_ERR_CUDA. */
+moe_status_t moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const void* w_mul,
+                        const float* bias, const float* bias_mul, const void* residual, void* out,
+                        int32_t* dev_status, void* stream);
+
+/* Residual add and RMS norm (qwen3_attention/init.rs and moe/init.rs, the `rms_norm` and
+ * `bf16_residual_add` handles, in one pass): s = x + residual, out = s * weight / sqrt(mean(s^2) +
+ * eps), over each of the T rows.  Computed in fp32 from the unrounded s; s and out are each
+ * rounded once.
+ * x, weight [H], out [device] desc->dtype; residual and sum_out [device] or NULL (s = x without
+ * a residual).  out and sum_out may each be x or residual itself (same rows), but not one another.
+ * T == 0 is a valid no-op.  Errors: MOE_ERR_INVALID_ARG for the checks of moe_norm_desc, a NULL
+ * x, weight or out, or sum_out == out; MOE_ERR_CUDA. */
+moe_status_t moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const void* residual,
+                              const void* weight, void* sum_out, void* out, void* stream);
 
 /* Bytes of device workspace moe_ffn_forward needs for T tokens in activation mode act.
  * Source: the spark_model MoE pages, moe/mod.rs, `zero_accum_dev` field doc (the layer's
