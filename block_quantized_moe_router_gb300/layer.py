@@ -4,6 +4,12 @@ Weights are dicts of CUDA tensors ({packed, scales, globals, fmt}) laid out as i
 describes.  The layer prepares them once (moe_prepare_weights), keeps a workspace sized for
 the largest token count seen, and runs route + FFN on the current CUDA stream with no host
 synchronisation.
+
+Optional parts around the expert FFN:
+  n_group / topk_group / group_top   routing limited to expert groups (moe_route_grouped)
+  shared   a bf16 shared expert {gate, up [I][H], down [H][I], and float biases gate_bias, up_bias
+           [I], down_bias [H] if it has them}, added through moe_linear; instead of an FP4 one
+  norm_weight / norm_eps   the RMS norm before the layer, with the residual add (block())
 """
 from __future__ import annotations
 
@@ -18,12 +24,21 @@ class MoeLayer:
     def __init__(self, *, E, H, I, top_k, scoring, gate, up, down, I_shared=0, sh_gate=None,
                  sh_up=None, sh_down=None, w_router=None, correction_bias=None, tid2eid=None,
                  renormalize=True, routed_scaling=1.0, act=capi.MOE_ACT_BF16, g_act1=1.0,
-                 g_act2=1.0, zero_experts=0):
+                 g_act2=1.0, zero_experts=0, n_group=0, topk_group=0, group_top=2, shared=None,
+                 norm_weight=None, norm_eps=1e-6):
         self.E, self.H, self.I, self.top_k, self.I_shared = E, H, I, top_k, I_shared
         self.zero_experts = zero_experts
         self.scoring, self.renormalize, self.routed_scaling = scoring, renormalize, routed_scaling
         self.act, self.g_act1, self.g_act2 = act, g_act1, g_act2
         self.w_router, self.correction_bias, self.tid2eid = w_router, correction_bias, tid2eid
+        if n_group and (zero_experts or scoring in (capi.MOE_SCORE_HASH,
+                                                    capi.MOE_SCORE_HASH_SQRTSOFTPLUS)):
+            raise ValueError("expert groups need a learned router without zero-computation experts")
+        if shared is not None and I_shared:
+            raise ValueError("a layer has one shared expert: FP4 (I_shared) or bf16 (shared)")
+        self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
+        self.shared, self.norm_weight, self.norm_eps = shared, norm_weight, norm_eps
+        self._shared_h = None
         self._weights = (gate, up, down, sh_gate, sh_up, sh_down)  # keep alive
         self.desc = capi.ffn_desc(E, H, I, top_k, I_shared, gate, up, down, sh_gate, sh_up, sh_down,
                                   zero_experts)
@@ -81,6 +96,15 @@ class MoeLayer:
         if (logits_out is None and logits_in is None and self.scoring != capi.MOE_SCORE_HASH):
             logits_out = torch.empty((T, self.E + self.zero_experts), dtype=torch.float32,
                                      device="cuda")
+        if self.n_group:
+            capi.moe_route_grouped(T=T, E=self.E, H=self.H, top_k=self.top_k, scoring=self.scoring,
+                                   renormalize=self.renormalize, routed_scaling=self.routed_scaling,
+                                   n_group=self.n_group, topk_group=self.topk_group,
+                                   group_top=self.group_top, x=x, w_router=self.w_router,
+                                   logits_in=logits_in, logits_out=logits_out,
+                                   correction_bias=self.correction_bias, topk_ids=topk_ids,
+                                   topk_w=topk_w, dev_status=self.status, stream=stream)
+            return topk_ids, topk_w, logits_out
         capi.moe_route(T=T, E=self.E, H=self.H, top_k=self.top_k, scoring=self.scoring,
                        renormalize=self.renormalize, routed_scaling=self.routed_scaling, x=x,
                        w_router=None if logits_in is not None else self.w_router,
@@ -97,15 +121,47 @@ class MoeLayer:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
         capi.moe_ffn_forward(self.handle, T, self.act, self.g_act1, self.g_act2, x, topk_ids,
                              topk_w, out, self.workspace(T), dev_status=self.status, stream=stream)
+        self._add_shared(x, out, stream)
         return out
+
+    def _add_shared(self, x, out, stream):
+        """out += down(SiLU(gate x) * up x) of the bf16 shared expert, if the layer has one."""
+        if self.shared is None:
+            return
+        s = self.shared
+        T, I = x.shape[0], s["gate"].shape[0]
+        if self._shared_h is None or self._shared_h.shape[0] < T:
+            self._shared_h = torch.empty((T, I), dtype=torch.bfloat16, device="cuda")
+        h = self._shared_h[:T]
+        capi.moe_linear(x, s["gate"], h, w_mul=s["up"], bias=s.get("gate_bias"),
+                        bias_mul=s.get("up_bias"), func=capi.MOE_FUNC_SILU, dev_status=self.status,
+                        stream=stream)
+        capi.moe_linear(h, s["down"], out, bias=s.get("down_bias"), residual=out,
+                        dev_status=self.status, stream=stream)
+
+    def block(self, delta, residual=None, *, logits_in=None, stream=None):
+        """The layer with the residual add and norm before it: r = delta + residual, n = RMS norm of
+        r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta."""
+        if self.norm_weight is None:
+            raise ValueError("the layer was built without norm_weight")
+        n = torch.empty_like(delta)
+        r = torch.empty_like(delta)
+        capi.moe_add_rms_norm(delta, self.norm_weight, n, residual=residual, sum_out=r,
+                              eps=self.norm_eps, stream=stream)
+        return self.forward(n, logits_in=logits_in, stream=stream)[0], r
 
     def forward(self, x=None, *, token_ids=None, logits_in=None, out=None, topk_ids=None,
                 topk_w=None, logits_out=None, stream=None):
-        """Route + FFN through moe_forward (one launch for a few tokens).
-        Returns (out, topk_ids, topk_w, logits_out)."""
+        """Route + FFN through moe_forward (one launch for a few tokens; with expert groups the
+        routing runs first on its own).  Returns (out, topk_ids, topk_w, logits_out)."""
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
+        if self.n_group:
+            topk_ids, topk_w, logits_out = self.route(
+                x, logits_in=logits_in, topk_ids=topk_ids, topk_w=topk_w, logits_out=logits_out,
+                stream=stream)
+            return self.ffn(x, topk_ids, topk_w, out=out, stream=stream), topk_ids, topk_w, logits_out
         if topk_ids is None:
             topk_ids = torch.empty((T, self.top_k), dtype=torch.int32, device="cuda")
         if topk_w is None:
@@ -122,6 +178,7 @@ class MoeLayer:
         capi.moe_forward(self.handle, d, self.act, self.g_act1, self.g_act2, x, topk_ids, topk_w,
                          out, self.workspace(T), logits_in=logits_in, logits_out=logits_out,
                          dev_status=self.status, stream=stream)
+        self._add_shared(x, out, stream)
         return out, topk_ids, topk_w, logits_out
 
     def forward_host(self, x_host, out_host, *, token_ids_host=None, topk_ids_host=None,
@@ -129,6 +186,8 @@ class MoeLayer:
         """Route + FFN on host buffers through moe_forward_host: x_host (and token_ids_host for
         hash routing) are copied in, out_host (and the ids / weights when given) copied back, all
         enqueued on the stream; the caller synchronises before reading the outputs."""
+        if self.n_group or self.shared is not None:
+            raise ValueError("the host-buffer entry has no expert groups and no bf16 shared expert")
         T = x_host.shape[0]
         cached = self._host_route.get(T)
         if cached is None:
