@@ -33,15 +33,15 @@ constexpr int kLinK = 64;                       // K elements per stage (128 byt
 constexpr int kLinA = 128 * 128;                // bytes of a 128-row operand stage
 
 struct LinMaps {
-    CUtensorMap x, w, v;
+    CUtensorMap x, w, v, res, out;
 };
 
 struct LinArgs {
     int T, N, nk;       // nk: stages of K in all
     int func, gated, f16;
-    int rows_t;         // rows of x per tile (few) / unused
-    int cols;           // weight rows per tile pair (many) / unused
-    int stages;
+    int rows_t, stages; // few rows: rows of x per tile, stages of the ring
+    int tma_rows;       // many rows: out and the residual go by TMA
+    int wave;           // many rows: CTA pairs the device holds
     int64_t ldr, ldo;
     const float *bias, *bias_mul;
     const void* res;
@@ -184,8 +184,31 @@ __device__ __forceinline__ void finish(const LinArgs& a, int64_t t, int n, float
     }
 }
 
+// 16 outputs of one row, biases in shared memory, the residual's 16 values packed in rw (zeros
+// without one), to packed results.
+__device__ __forceinline__ void combine16(const LinArgs& a, const float* bias, const float* bias_mul,
+                                          float (&z)[16], const float (&u)[16], const uint32_t (&rw)[8],
+                                          uint32_t (&ow)[8]) {
+    const bool f16 = a.f16;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float4 b = a.bias ? *reinterpret_cast<const float4*>(bias + i) : make_float4(0, 0, 0, 0);
+        const float4 c = a.bias_mul ? *reinterpret_cast<const float4*>(bias_mul + i) : make_float4(0, 0, 0, 0);
+        const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float y = apply_func(a.func, z[i + j] + bb[j]);
+            if (a.gated) y *= u[i + j] + cc[j];
+            if (a.res) y += unpack16(j & 1 ? rw[(i + j) / 2] >> 16 : rw[(i + j) / 2] & 0xFFFFu, f16);
+            z[i + j] = y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ow[i] = pack16x2(z[2 * i], z[2 * i + 1], f16);
+}
+
 // Whether rows of `p` (ld elements apart) all start at multiples of `bytes`.
-__device__ __forceinline__ bool rows_aligned(const void* p, int64_t ld, int bytes) {
+__host__ __device__ __forceinline__ bool rows_aligned(const void* p, int64_t ld, int bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(2 * ld)) & (uintptr_t)(bytes - 1)) == 0;
 }
 
@@ -321,39 +344,69 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 
 // ------------------------------------------------------------------------------------------
 // Many rows.  Clusters of two CTAs, one per SM; pair p takes tiles p, p + pairs, ...  A tile is 256 rows
-// of x by `cols` rows of W (gated: cols / 2 rows of W and as many of V); each CTA holds 128 rows of x
-// and all columns.  Warp 0 loads, warp 1 of the leading CTA issues the MMAs, warps 2-9 (two per
-// lane quarter, half the columns each) turn accumulators into rows.
+// of x by 256 rows of W (gated: 128 of W and 128 of V); each CTA holds 128 rows of x and all columns.
+// Tiles of a last wave that would leave half of the pairs idle are cut in two by columns.  Warp 0
+// loads, warp 1 of the leading CTA issues the MMAs, warps 2-9 (two per lane quarter, half the
+// columns each) turn accumulators into rows.  Rows go out, and the residual comes in, by TMA through
+// a 64 KB staging area (128-byte swizzled, so a thread per row meets no bank conflicts): the next
+// tile's residual loads while its MMAs run.  Rows that TMA cannot address (not 16-byte aligned) are
+// read and written by the threads.
 // ------------------------------------------------------------------------------------------
 constexpr int kManyThreads = 320;
-constexpr int kManyStages = 6;
+constexpr int kManyStages = 5;
 constexpr int kManyStageBytes = 2 * kLinA;  // 128 rows of x, at most 128 of W
-constexpr int kManySmem = kManyStages * kManyStageBytes + 1024;
+constexpr int kManyBox = 64 * 128;          // bytes of a 64-row box of weights
+constexpr int kManySmem = kManyStages * kManyStageBytes + 4 * kLinA + 1024;
 constexpr int kManyGroup = 8;  // row tiles that share a pass over the weights
 
-__device__ __forceinline__ void tile_of(int64_t i, int tiles_t, int tiles_n, int& tt, int& tn) {
-    const int64_t per = (int64_t)kManyGroup * tiles_n;
-    const int g = (int)(i / per);
-    const int rest = (int)(i % per);
-    const int rows = min(kManyGroup, tiles_t - g * kManyGroup);
-    tt = g * kManyGroup + rest % rows;
-    tn = rest / rows;
+struct ManyTile {
+    int t0, f0, boxes;  // first row, first feature, 64-row weight boxes per CTA (2, or 1: half a tile)
+};
+
+struct ManySched {
+    int tiles_t, tiles_n, gated;
+    int64_t whole, total;
+    __host__ __device__ ManySched(int T, int N, int gated_, int pairs) : gated(gated_) {
+        tiles_t = (int)(((int64_t)T + 255) / 256);
+        tiles_n = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+        const int64_t all = (int64_t)tiles_t * tiles_n, last = all % pairs;
+        const int64_t cut = 2 * last <= pairs ? last : 0;
+        whole = all - cut;
+        total = whole + 2 * cut;
+    }
+    __device__ __forceinline__ ManyTile tile(int64_t i) const {
+        const bool half = i >= whole;
+        const int64_t w = half ? whole + (i - whole) / 2 : i;
+        const int64_t per = (int64_t)kManyGroup * tiles_n;
+        const int g = (int)(w / per), rest = (int)(w % per);
+        const int rows = min(kManyGroup, tiles_t - g * kManyGroup);
+        ManyTile r;
+        r.t0 = (g * kManyGroup + rest % rows) * 256;
+        r.boxes = half ? 1 : 2;
+        r.f0 = (rest / rows) * (gated ? 128 : 256) + (half ? (int)((i - whole) & 1) * (gated ? 64 : 128) : 0);
+        return r;
+    }
+};
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kManyThreads, 1)
 linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
     extern __shared__ uint8_t lin_smem[];
-    __shared__ uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2];
+    __shared__ uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2], res_full;
+    __shared__ __align__(16) float bias_s[256];  // gated: 128 of bias, 128 of bias_mul
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag;
+    __shared__ volatile int abort_flag, stop;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
+    uint8_t* staging = smem + kManyStages * kManyStageBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int half = a.cols / 2;
-    const int per_tile = a.gated ? half : a.cols;  // features per tile
-    const int tiles_t = (a.T + 255) / 256, tiles_n = (a.N + per_tile - 1) / per_tile;
-    const int64_t tiles = (int64_t)tiles_t * tiles_n;
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const ManySched sched(a.T, a.N, a.gated, a.wave);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kManyStages; ++s) {
             mbar_init(&full[s], 1);
@@ -363,11 +416,14 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 16);  // the epilogue warps of both CTAs
         }
+        mbar_init(&res_full, 1);
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.x);
         prefetch_tmap(&maps.w);
         if (a.gated) prefetch_tmap(&maps.v);
+        if (a.tma_rows) prefetch_tmap(&maps.out);
+        if (a.tma_rows && a.res) prefetch_tmap(&maps.res);
     }
     if (warp == 1) tmem_alloc_pair(&tmem_slot, 512);
     tc_fence_before();
@@ -384,11 +440,10 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     if (warp == 0 && lane == 0) {  // TMA producer of this CTA's halves
         const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
         int it = 0;
-        for (int64_t i = pair; i < tiles && !abort_flag; i += pairs) {
-            int tt, tn;
-            tile_of(i, tiles_t, tiles_n, tt, tn);
-            const int t0 = tt * 256 + (int)rank * 128;
-            const int n0 = tn * per_tile + (a.gated ? 0 : (int)rank * half);
+        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs) {
+            const ManyTile tl = sched.tile(i);
+            const int t0 = tl.t0 + (int)rank * 128;
+            const int n0 = tl.f0 + (a.gated ? 0 : (int)rank * 64 * tl.boxes);
             for (int k = 0; k < a.nk; ++k, ++it) {
                 const int s = it % kManyStages;
                 if (!mbar_wait_bounded(&empty[s], ((it / kManyStages) & 1) ^ 1, kLinWaitLimit) || abort_flag) {
@@ -396,19 +451,20 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                     break;
                 }
                 const uint32_t base = smem_u32(smem + s * kManyStageBytes);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kLinA + half * 128));
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kLinA + tl.boxes * kManyBox));
                 const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
                 tma_load_pair(base, &maps.x, k * kLinK, t0, bar);
                 tma_load_pair(base + kLinA, wmap, k * kLinK, n0, bar);
+                if (tl.boxes == 2) tma_load_pair(base + kLinA + kManyBox, wmap, k * kLinK, n0 + 64, bar);
             }
         }
         if (abort_flag && rank == 0)  // wait (bounded) for the pair's copies still in flight
             for (int j = it - 1; j >= 0 && j >= it - kManyStages; --j)
                 mbar_wait_bounded(&full[j % kManyStages], (j / kManyStages) & 1, kLinWaitLimit);
     } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA issuer of the pair
-        const uint32_t idesc = idesc_f16kind(256, a.cols, a.f16);
         int it = 0, n = 0;
-        for (int64_t i = pair; i < tiles && !abort_flag; i += pairs, ++n) {
+        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
+            const uint32_t idesc = idesc_f16kind(256, 128 * sched.tile(i).boxes, a.f16);
             const int b = n & 1;
             if (!mbar_wait_bounded(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinWaitLimit)) {
                 give_up();
@@ -433,33 +489,78 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         }
     } else if (warp >= 2) {
         const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, half of the columns
+        const int etid = threadIdx.x - 64;
+        const int row = 32 * q + lane;
+        const bool leader = etid == 0;
+        const bool by_tma = a.tma_rows, res_tma = by_tma && a.res;
         const bool vec = rows_aligned(a.out, a.ldo, 16) && (!a.res || rows_aligned(a.res, a.ldr, 16));
+        auto load_residual = [&](int64_t i) {  // a tile's residual rows into the staging area
+            const ManyTile tl = sched.tile(i);
+            const int subs = (a.gated ? 1 : 2) * tl.boxes;
+            mbar_arrive_expect_tx(&res_full, subs * kLinA);
+            for (int s = 0; s < subs; ++s)
+                tma_load_2d(staging + s * kLinA, &maps.res, tl.f0 + 64 * s, tl.t0 + (int)rank * 128, &res_full);
+        };
+        if (leader && res_tma && pair < sched.total) load_residual(pair);
         int n = 0;
-        for (int64_t i = pair; i < tiles && !abort_flag; i += pairs, ++n) {
+        bool ok = true;
+        for (int64_t i = pair; i < sched.total; i += pairs, ++n) {
             const int b = n & 1;
-            int tt, tn;
-            tile_of(i, tiles_t, tiles_n, tt, tn);
-            if (!mbar_wait_bounded(&acc_full[b], (n >> 1) & 1, kLinWaitLimit)) {
-                give_up();
-                break;
+            const ManyTile tl = sched.tile(i);
+            const int subs = (a.gated ? 1 : 2) * tl.boxes;  // 64-feature pieces of the tile
+            if (a.bias || a.bias_mul) {
+                const bool second = a.gated && etid >= 128;
+                const float* src = second ? a.bias_mul : a.bias;
+                const int f = tl.f0 + (second ? etid - 128 : etid);
+                bias_s[etid] = src && f < a.N ? __ldg(src + f) : 0.f;
             }
+            ok = mbar_wait_bounded(&acc_full[b], (n >> 1) & 1, kLinWaitLimit) && ok;
+            if (res_tma) ok = mbar_wait_bounded(&res_full, n & 1, kLinWaitLimit) && ok;
+            if (!ok) give_up();
+            epilogue_barrier();  // bias_s is written; the staging area is free or holds the residual
             tc_fence_after();
-            const int64_t t = (int64_t)tt * 256 + rank * 128 + 32 * q + lane;
             const uint32_t trow = tmem + 256 * b + ((uint32_t)(32 * q) << 16);
-            const int chunks = per_tile / 16;
-            for (int c = side; c < chunks; c += 2) {
+            const int64_t t = (int64_t)tl.t0 + rank * 128 + row;
+            for (int c = side; c < subs * 4; c += 2) {  // 16 features each
                 float z[16], u[16];
                 tmem_ld_16(trow + 16 * c, reinterpret_cast<uint32_t(&)[16]>(z));
-                if (a.gated) tmem_ld_16(trow + half + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
+                if (a.gated) tmem_ld_16(trow + 64 * tl.boxes + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
                 tmem_ld_wait();
-                const int f = tn * per_tile + 16 * c;
-                if (t < a.T && f < a.N) finish<16>(a, t, f, z, u, vec);
+                if (by_tma) {
+                    uint8_t* line = staging + (c >> 2) * kLinA + row * 128;
+                    uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 3)) ^ (row & 7)) << 4));
+                    uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 3) + 1) ^ (row & 7)) << 4));
+                    uint32_t rw[8] = {};
+                    if (res_tma) {
+                        *reinterpret_cast<uint4*>(rw) = *p0;
+                        *reinterpret_cast<uint4*>(rw + 4) = *p1;
+                    }
+                    uint32_t ow[8];
+                    combine16(a, bias_s + 16 * c, bias_s + 128 + 16 * c, z, u, rw, ow);
+                    *p0 = *reinterpret_cast<uint4*>(ow);
+                    *p1 = *reinterpret_cast<uint4*>(ow + 4);
+                } else if (t < a.T && tl.f0 + 16 * c < a.N) {
+                    finish<16>(a, t, tl.f0 + 16 * c, z, u, vec);
+                }
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[b]), 0));
+            if (by_tma) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (leader) stop = abort_flag;  // one answer for all the epilogue's warps
+            epilogue_barrier();
+            if (leader && by_tma) {
+                for (int s = 0; s < subs; ++s)
+                    if (tl.f0 + 64 * s < a.N && tl.t0 + (int)rank * 128 < a.T)
+                        tma_store_2d(&maps.out, staging + s * kLinA, tl.f0 + 64 * s, tl.t0 + (int)rank * 128);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (res_tma && i + pairs < sched.total && !stop) load_residual(i + pairs);
+            }
+            if (stop) break;
         }
+        if (leader && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();
     cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done
@@ -547,13 +648,16 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
         return launch_clusters(linear_few_kernel, dim3(tiles_n * splits, tiles_t), splits, kFewThreads,
                                a.stages * stage + 1024, m, a, st);
     }
-    a.cols = 256;
-    const int half = a.cols / 2;
-    if (!encode16(&m.x, x, d.K, d.T, d.ldx, 128) || !encode16(&m.w, w, d.K, d.N, d.ldw, half) ||
-        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, half)))
+    // TMA addresses rows that start at multiples of 16 bytes
+    a.tma_rows = rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
+    if (!encode16(&m.x, x, d.K, d.T, d.ldx, 128) || !encode16(&m.w, w, d.K, d.N, d.ldw, 64) ||
+        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, 64)) ||
+        (a.tma_rows && !encode16(&m.out, out, d.N, d.T, d.ldo, 128)) ||
+        (a.tma_rows && residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128)))
         return cudaErrorInvalidValue;
-    const int64_t tiles = ((int64_t)d.T + 255) / 256 * ((d.N + (a.gated ? half : a.cols) - 1) / (a.gated ? half : a.cols));
-    const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+    a.wave = sms / 2;
+    const int64_t total = ManySched(d.T, d.N, a.gated, a.wave).total;
+    const int pairs = (int)(total < a.wave ? total : a.wave);
     return launch_clusters(linear_many_kernel, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
 }
 
