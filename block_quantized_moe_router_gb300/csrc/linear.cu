@@ -41,7 +41,7 @@ struct LinArgs {
     int func, gated, f16;
     int rows_t, stages; // few rows: rows of x per tile, stages of the ring
     int tma_rows;       // many rows: out and the residual go by TMA
-    int wave;           // many rows: CTA pairs the device holds
+    int width;          // many rows: rows of weights per tile
     int64_t ldr, ldo;
     const float *bias, *bias_mul;
     const void* res;
@@ -113,24 +113,59 @@ __device__ __forceinline__ uint32_t idesc_f16kind(uint32_t M, uint32_t N, bool f
 }
 
 // ---- epilogue arithmetic -------------------------------------------------------------------------
-__device__ __forceinline__ float apply_func(int func, float z) {
+// The function over C values: one branch for all of them (a branch per value, unrolled, costs more
+// in instruction fetch than the arithmetic).
+template <int C>
+__device__ __forceinline__ void apply_func(int func, float (&z)[C]) {
     switch (func) {
-        case MOE_FUNC_SILU: return __fdividef(z, 1.f + __expf(-z));
-        case MOE_FUNC_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-        // 0.5 (1 + tanh u) = sigmoid(2 u)
-        case MOE_FUNC_GELU_TANH: return z / (1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
-        case MOE_FUNC_RELU: return fmaxf(z, 0.f);
+        case MOE_FUNC_SILU:
+#pragma unroll
+            for (int i = 0; i < C; ++i) z[i] = z[i] / (1.f + __expf(-z[i]));
+            break;
+        case MOE_FUNC_GELU:
+#pragma unroll
+            for (int i = 0; i < C; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678f));
+            break;
+        case MOE_FUNC_GELU_TANH:  // 0.5 (1 + tanh u) = sigmoid(2 u)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                z[i] = z[i] / (1.f + __expf(-1.5957691f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+            break;
+        case MOE_FUNC_RELU:  // not fmaxf: a NaN stays
+#pragma unroll
+            for (int i = 0; i < C; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
+            break;
     }
-    return z;
 }
-__device__ __forceinline__ float unpack16(uint32_t h, bool f16) {
-    return f16 ? __half2float(__ushort_as_half((unsigned short)h)) : __uint_as_float(h << 16);
+// z += the C 16-bit values packed in w.
+template <int C>
+__device__ __forceinline__ void add_packed(float (&z)[C], const uint32_t (&w)[C / 2], bool f16) {
+    if (f16) {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            z[2 * i] += f.x;
+            z[2 * i + 1] += f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            z[2 * i] += __uint_as_float(w[i] << 16);
+            z[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
 }
-__device__ __forceinline__ uint32_t pack16x2(float lo, float hi, bool f16) {
-    uint32_t r;
-    if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+template <int C>
+__device__ __forceinline__ void pack_all(const float (&z)[C], uint32_t (&w)[C / 2], bool f16) {
+    if (f16) {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(z[2 * i + 1]), "f"(z[2 * i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(z[2 * i + 1]), "f"(z[2 * i]));
+    }
 }
 
 // C consecutive outputs of row t from feature n on: bias, function, factor, residual, one rounding.
@@ -142,7 +177,7 @@ __device__ __forceinline__ void finish(const LinArgs& a, int64_t t, int n, float
     uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ldo + n;
     const uint16_t* res = a.res ? static_cast<const uint16_t*>(a.res) + t * a.ldr + n : nullptr;
     const bool full = vec && n + C <= a.N;
-    uint32_t rw[C / 2];
+    uint32_t rw[C / 2] = {};
     if (res && full) {
 #pragma unroll
         for (int i = 0; i < C / 2; i += C >= 8 ? 4 : 2) {
@@ -154,21 +189,24 @@ __device__ __forceinline__ void finish(const LinArgs& a, int64_t t, int n, float
                 rw[i] = q.x; rw[i + 1] = q.y;
             }
         }
-    }
+    } else if (res) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const bool in = n + i < a.N;
-        if (a.bias && in) z[i] += __ldg(a.bias + n + i);
-        z[i] = apply_func(a.func, z[i]);
-        if (a.gated) z[i] *= u[i] + (a.bias_mul && in ? __ldg(a.bias_mul + n + i) : 0.f);
-        if (res) {
-            if (full) z[i] += unpack16(i & 1 ? rw[i / 2] >> 16 : rw[i / 2] & 0xFFFFu, f16);
-            else if (in) z[i] += unpack16(res[i], f16);
-        }
+        for (int i = 0; i < C; ++i)
+            if (n + i < a.N) rw[i / 2] |= (uint32_t)res[i] << (i & 1 ? 16 : 0);
     }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) z[i] += n + i < a.N ? __ldg(a.bias + n + i) : 0.f;
+    }
+    apply_func(a.func, z);
+    if (a.gated) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            z[i] *= u[i] + (a.bias_mul && n + i < a.N ? __ldg(a.bias_mul + n + i) : 0.f);
+    }
+    if (res) add_packed(z, rw, f16);
     uint32_t ow[C / 2];
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i) ow[i] = pack16x2(z[2 * i], z[2 * i + 1], f16);
+    pack_all(z, ow, f16);
     if (full) {
 #pragma unroll
         for (int i = 0; i < C / 2; i += C >= 8 ? 4 : 2) {
@@ -189,22 +227,26 @@ __device__ __forceinline__ void finish(const LinArgs& a, int64_t t, int n, float
 __device__ __forceinline__ void combine16(const LinArgs& a, const float* bias, const float* bias_mul,
                                           float (&z)[16], const float (&u)[16], const uint32_t (&rw)[8],
                                           uint32_t (&ow)[8]) {
-    const bool f16 = a.f16;
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        const float4 b = a.bias ? *reinterpret_cast<const float4*>(bias + i) : make_float4(0, 0, 0, 0);
-        const float4 c = a.bias_mul ? *reinterpret_cast<const float4*>(bias_mul + i) : make_float4(0, 0, 0, 0);
-        const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float y = apply_func(a.func, z[i + j] + bb[j]);
-            if (a.gated) y *= u[i + j] + cc[j];
-            if (a.res) y += unpack16(j & 1 ? rw[(i + j) / 2] >> 16 : rw[(i + j) / 2] & 0xFFFFu, f16);
-            z[i + j] = y;
+        for (int i = 0; i < 16; i += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(bias + i);
+            z[i] += b.x; z[i + 1] += b.y; z[i + 2] += b.z; z[i + 3] += b.w;
         }
     }
+    apply_func(a.func, z);
+    if (a.bias_mul) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ow[i] = pack16x2(z[2 * i], z[2 * i + 1], f16);
+        for (int i = 0; i < 16; i += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(bias_mul + i);
+            z[i] *= u[i] + b.x; z[i + 1] *= u[i + 1] + b.y; z[i + 2] *= u[i + 2] + b.z; z[i + 3] *= u[i + 3] + b.w;
+        }
+    } else if (a.gated) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] *= u[i];
+    }
+    if (a.res) add_packed(z, rw, a.f16);
+    pack_all(z, ow, a.f16);
 }
 
 // Whether rows of `p` (ld elements apart) all start at multiples of `bytes`.
@@ -343,48 +385,42 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------------------------------
-// Many rows.  Clusters of two CTAs, one per SM; pair p takes tiles p, p + pairs, ...  A tile is 256 rows
-// of x by 256 rows of W (gated: 128 of W and 128 of V); each CTA holds 128 rows of x and all columns.
-// Tiles of a last wave that would leave half of the pairs idle are cut in two by columns.  Warp 0
-// loads, warp 1 of the leading CTA issues the MMAs, warps 2-9 (two per lane quarter, half the
-// columns each) turn accumulators into rows.  Rows go out, and the residual comes in, by TMA through
-// a 64 KB staging area (128-byte swizzled, so a thread per row meets no bank conflicts): the next
-// tile's residual loads while its MMAs run.  Rows that TMA cannot address (not 16-byte aligned) are
-// read and written by the threads.
+// Many rows.  Clusters of two CTAs, one per SM; a pair's tile is 256 rows of x by `width` rows of W
+// (gated: width / 2 of W and of V), each CTA holding 128 rows of x and all columns.  Warp 0 loads,
+// warp 1 of the pair's first CTA issues the MMAs, warps 2-9 (two per lane quarter, alternate
+// columns) turn accumulators into rows and warp 10 moves rows: the residual comes in and results
+// go out by TMA through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per
+// row meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
+// meanwhile.  Rows that TMA cannot address (not 16-byte aligned) are read and written by the threads.
+//
+// A stage is 128 elements of K: with 64 the commit and barrier round trips of twice as many stages
+// held the MMAs back (8192^3 without its epilogue 620 us, against 563 with 128, of 574 at the
+// measured cuBLAS rate).  Two pairs sharing x by multicast were no faster: clusters of four occupy
+// 144 of the 152 SMs.
 // ------------------------------------------------------------------------------------------
-constexpr int kManyThreads = 320;
-constexpr int kManyStages = 5;
-constexpr int kManyStageBytes = 2 * kLinA;  // 128 rows of x, at most 128 of W
-constexpr int kManyBox = 64 * 128;          // bytes of a 64-row box of weights
-constexpr int kManySmem = kManyStages * kManyStageBytes + 4 * kLinA + 1024;
+constexpr int kManyThreads = 352;
+constexpr int kManyStages = 3;
+constexpr int kManyHalf = 2 * kLinA;             // 64 elements of K: 128 rows of x, at most 128 of W
+constexpr int kManyStageBytes = 2 * kManyHalf;
+constexpr int kManySub = 128 * 64;               // bytes of 32 features of 128 rows
+constexpr int kManySmem = kManyStages * kManyStageBytes + 4 * kManySub + 1024;
 constexpr int kManyGroup = 8;  // row tiles that share a pass over the weights
 
-struct ManyTile {
-    int t0, f0, boxes;  // first row, first feature, 64-row weight boxes per CTA (2, or 1: half a tile)
-};
-
 struct ManySched {
-    int tiles_t, tiles_n, gated;
-    int64_t whole, total;
-    __host__ __device__ ManySched(int T, int N, int gated_, int pairs) : gated(gated_) {
+    int tiles_t, tiles_n;
+    int64_t total;
+    __host__ __device__ ManySched(int T, int N, int features) {
         tiles_t = (int)(((int64_t)T + 255) / 256);
-        tiles_n = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-        const int64_t all = (int64_t)tiles_t * tiles_n, last = all % pairs;
-        const int64_t cut = 2 * last <= pairs ? last : 0;
-        whole = all - cut;
-        total = whole + 2 * cut;
+        tiles_n = (N + features - 1) / features;
+        total = (int64_t)tiles_t * tiles_n;
     }
-    __device__ __forceinline__ ManyTile tile(int64_t i) const {
-        const bool half = i >= whole;
-        const int64_t w = half ? whole + (i - whole) / 2 : i;
+    // tile i: its row tile and column tile; kManyGroup row tiles run through all columns together
+    __device__ __forceinline__ void tile(int64_t i, int& tt, int& tn) const {
         const int64_t per = (int64_t)kManyGroup * tiles_n;
-        const int g = (int)(w / per), rest = (int)(w % per);
+        const int g = (int)(i / per), rest = (int)(i % per);
         const int rows = min(kManyGroup, tiles_t - g * kManyGroup);
-        ManyTile r;
-        r.t0 = (g * kManyGroup + rest % rows) * 256;
-        r.boxes = half ? 1 : 2;
-        r.f0 = (rest / rows) * (gated ? 128 : 256) + (half ? (int)((i - whole) & 1) * (gated ? 64 : 128) : 0);
-        return r;
+        tt = g * kManyGroup + rest % rows;
+        tn = rest / rows;
     }
 };
 
@@ -392,21 +428,25 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kManyThreads, 1)
 linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
     extern __shared__ uint8_t lin_smem[];
-    __shared__ uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2], res_full;
-    __shared__ __align__(16) float bias_s[256];  // gated: 128 of bias, 128 of bias_mul
+    __shared__ uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2];
+    __shared__ uint64_t buf_ready[2], buf_done[2];  // row buffers: usable by the epilogue; written by it
+    __shared__ __align__(16) float bias_s[2][128];  // per buffer: 64 of bias, 64 of bias_mul
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag, stop;
+    __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
-    uint8_t* staging = smem + kManyStages * kManyStageBytes;
+    uint8_t* rows_s = smem + kManyStages * kManyStageBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const int rank = (int)cluster_rank();
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-    const ManySched sched(a.T, a.N, a.gated, a.wave);
+    const int half = a.width / 2;
+    const int per_tile = a.gated ? half : a.width;  // features per tile
+    const int subs = per_tile / 32, passes = (per_tile + 63) / 64;
+    const bool by_tma = a.tma_rows, res_tma = by_tma && a.res;
+    const ManySched sched(a.T, a.N, per_tile);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kManyStages; ++s) {
             mbar_init(&full[s], 1);
@@ -415,15 +455,16 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 16);  // the epilogue warps of both CTAs
+            mbar_init(&buf_ready[b], 1);
+            mbar_init(&buf_done[b], 8);
         }
-        mbar_init(&res_full, 1);
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.x);
         prefetch_tmap(&maps.w);
         if (a.gated) prefetch_tmap(&maps.v);
-        if (a.tma_rows) prefetch_tmap(&maps.out);
-        if (a.tma_rows && a.res) prefetch_tmap(&maps.res);
+        if (by_tma) prefetch_tmap(&maps.out);
+        if (res_tma) prefetch_tmap(&maps.res);
     }
     if (warp == 1) tmem_alloc_pair(&tmem_slot, 512);
     tc_fence_before();
@@ -437,130 +478,180 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         abort_flag = 1;
         status_or(a.status, MOE_DEV_TIMEOUT);
     };
+    auto first = [&](int64_t i, int& r0, int& f0) {  // this CTA's first row, the first feature of tile i
+        int tt, tn;
+        sched.tile(i, tt, tn);
+        r0 = tt * 256 + rank * 128;
+        f0 = tn * per_tile;
+    };
     if (warp == 0 && lane == 0) {  // TMA producer of this CTA's halves
         const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
         int it = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs) {
-            const ManyTile tl = sched.tile(i);
-            const int t0 = tl.t0 + (int)rank * 128;
-            const int n0 = tl.f0 + (a.gated ? 0 : (int)rank * 64 * tl.boxes);
-            for (int k = 0; k < a.nk; ++k, ++it) {
-                const int s = it % kManyStages;
+            int t0, n0;
+            first(i, t0, n0);
+            if (!a.gated) n0 += rank * half;
+            for (int k = 0; k < a.nk; k += 2, ++it) {
+                const int s = it % kManyStages, parts = min(2, a.nk - k);
                 if (!mbar_wait_bounded(&empty[s], ((it / kManyStages) & 1) ^ 1, kLinWaitLimit) || abort_flag) {
                     give_up();
                     break;
                 }
                 const uint32_t base = smem_u32(smem + s * kManyStageBytes);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kLinA + tl.boxes * kManyBox));
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * parts * (kLinA + half * 128));
                 const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-                tma_load_pair(base, &maps.x, k * kLinK, t0, bar);
-                tma_load_pair(base + kLinA, wmap, k * kLinK, n0, bar);
-                if (tl.boxes == 2) tma_load_pair(base + kLinA + kManyBox, wmap, k * kLinK, n0 + 64, bar);
+                for (int h = 0; h < parts; ++h) {
+                    tma_load_pair(base + h * kManyHalf, &maps.x, (k + h) * kLinK, t0, bar);
+                    tma_load_pair(base + h * kManyHalf + kLinA, wmap, (k + h) * kLinK, n0, bar);
+                }
             }
         }
         if (abort_flag && rank == 0)  // wait (bounded) for the pair's copies still in flight
             for (int j = it - 1; j >= 0 && j >= it - kManyStages; --j)
                 mbar_wait_bounded(&full[j % kManyStages], (j / kManyStages) & 1, kLinWaitLimit);
     } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA issuer of the pair
+        const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
         int it = 0, n = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
-            const uint32_t idesc = idesc_f16kind(256, 128 * sched.tile(i).boxes, a.f16);
             const int b = n & 1;
             if (!mbar_wait_bounded(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinWaitLimit)) {
                 give_up();
                 break;
             }
             tc_fence_after();
-            for (int k = 0; k < a.nk; ++k, ++it) {
-                const int s = it % kManyStages;
+            for (int k = 0; k < a.nk; k += 2, ++it) {
+                const int s = it % kManyStages, parts = min(2, a.nk - k);
                 if (!mbar_wait_bounded(&full[s], (it / kManyStages) & 1, kLinWaitLimit) || abort_flag) {
                     give_up();
                     break;
                 }
                 tc_fence_after();
                 const uint32_t sb = smem_u32(smem + s * kManyStageBytes);
+                for (int h = 0; h < parts; ++h)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_f16kind<1>(tmem + 256 * b, smem_desc(sb + 32 * j, 16, 1024, kLayoutSw128),
-                                   smem_desc(sb + kLinA + 32 * j, 16, 1024, kLayoutSw128), idesc, (k | j) != 0);
+                    for (int j = 0; j < 4; ++j) {  // K 16 per MMA: 32 bytes along the swizzled row
+                        const uint32_t at = sb + h * kManyHalf + 32 * j;
+                        mma_f16kind<1>(tmem + 256 * b, smem_desc(at, 16, 1024, kLayoutSw128),
+                                       smem_desc(at + kLinA, 16, 1024, kLayoutSw128), idesc, (k | h | j) != 0);
+                    }
                 tc_commit_pair(&empty[s]);
             }
             tc_commit_pair(&acc_full[b]);
         }
-    } else if (warp >= 2) {
-        const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, half of the columns
-        const int etid = threadIdx.x - 64;
-        const int row = 32 * q + lane;
-        const bool leader = etid == 0;
-        const bool by_tma = a.tma_rows, res_tma = by_tma && a.res;
+    } else if (warp >= 2 && warp < 10) {
+        const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, parity of the columns' 16s
+        const int row = 32 * q + lane, sw = (row >> 1) & 3;
         const bool vec = rows_aligned(a.out, a.ldo, 16) && (!a.res || rows_aligned(a.res, a.ldr, 16));
-        auto load_residual = [&](int64_t i) {  // a tile's residual rows into the staging area
-            const ManyTile tl = sched.tile(i);
-            const int subs = (a.gated ? 1 : 2) * tl.boxes;
-            mbar_arrive_expect_tx(&res_full, subs * kLinA);
-            for (int s = 0; s < subs; ++s)
-                tma_load_2d(staging + s * kLinA, &maps.res, tl.f0 + 64 * s, tl.t0 + (int)rank * 128, &res_full);
-        };
-        if (leader && res_tma && pair < sched.total) load_residual(pair);
         int n = 0;
-        bool ok = true;
-        for (int64_t i = pair; i < sched.total; i += pairs, ++n) {
+        uint32_t pass = 0;
+        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
             const int b = n & 1;
-            const ManyTile tl = sched.tile(i);
-            const int subs = (a.gated ? 1 : 2) * tl.boxes;  // 64-feature pieces of the tile
-            if (a.bias || a.bias_mul) {
-                const bool second = a.gated && etid >= 128;
-                const float* src = second ? a.bias_mul : a.bias;
-                const int f = tl.f0 + (second ? etid - 128 : etid);
-                bias_s[etid] = src && f < a.N ? __ldg(src + f) : 0.f;
+            int r0, f0;
+            first(i, r0, f0);
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], (n >> 1) & 1, kLinWaitLimit))) {
+                give_up();
+                break;
             }
-            ok = mbar_wait_bounded(&acc_full[b], (n >> 1) & 1, kLinWaitLimit) && ok;
-            if (res_tma) ok = mbar_wait_bounded(&res_full, n & 1, kLinWaitLimit) && ok;
-            if (!ok) give_up();
-            epilogue_barrier();  // bias_s is written; the staging area is free or holds the residual
             tc_fence_after();
             const uint32_t trow = tmem + 256 * b + ((uint32_t)(32 * q) << 16);
-            const int64_t t = (int64_t)tl.t0 + rank * 128 + row;
-            for (int c = side; c < subs * 4; c += 2) {  // 16 features each
-                float z[16], u[16];
-                tmem_ld_16(trow + 16 * c, reinterpret_cast<uint32_t(&)[16]>(z));
-                if (a.gated) tmem_ld_16(trow + 64 * tl.boxes + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
-                tmem_ld_wait();
-                if (by_tma) {
-                    uint8_t* line = staging + (c >> 2) * kLinA + row * 128;
-                    uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 3)) ^ (row & 7)) << 4));
-                    uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 3) + 1) ^ (row & 7)) << 4));
-                    uint32_t rw[8] = {};
-                    if (res_tma) {
-                        *reinterpret_cast<uint4*>(rw) = *p0;
-                        *reinterpret_cast<uint4*>(rw + 4) = *p1;
+            const int64_t t = (int64_t)r0 + row;
+            for (int p = 0; p < passes; ++p, ++pass) {
+                const int buf = pass & 1;
+                if (by_tma && !__all_sync(0xffffffffu, mbar_wait_bounded(&buf_ready[buf], (pass >> 1) & 1,
+                                                                          kLinWaitLimit)))
+                    give_up();  // carries on: the row mover stops, and with it this loop
+                for (int c = 4 * p + side; c < min(4 * p + 4, 2 * subs); c += 2) {  // 16 features each
+                    float z[16], u[16];
+                    tmem_ld_16(trow + 16 * c, reinterpret_cast<uint32_t(&)[16]>(z));
+                    if (a.gated) tmem_ld_16(trow + half + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
+                    tmem_ld_wait();
+                    if (by_tma) {
+                        uint8_t* line = rows_s + buf * 2 * kManySub + ((c >> 1) & 1) * kManySub + row * 64;
+                        uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 1)) ^ sw) << 4));
+                        uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 1) + 1) ^ sw) << 4));
+                        uint32_t rw[8] = {};
+                        if (res_tma) {
+                            *reinterpret_cast<uint4*>(rw) = *p0;
+                            *reinterpret_cast<uint4*>(rw + 4) = *p1;
+                        }
+                        uint32_t ow[8];
+                        const float* bias = bias_s[buf] + 16 * (c & 3);
+                        combine16(a, bias, bias + 64, z, u, rw, ow);
+                        *p0 = *reinterpret_cast<uint4*>(ow);
+                        *p1 = *reinterpret_cast<uint4*>(ow + 4);
+                    } else if (t < a.T && f0 + 16 * c < a.N) {
+                        finish<16>(a, t, f0 + 16 * c, z, u, vec);
                     }
-                    uint32_t ow[8];
-                    combine16(a, bias_s + 16 * c, bias_s + 128 + 16 * c, z, u, rw, ow);
-                    *p0 = *reinterpret_cast<uint4*>(ow);
-                    *p1 = *reinterpret_cast<uint4*>(ow + 4);
-                } else if (t < a.T && tl.f0 + 16 * c < a.N) {
-                    finish<16>(a, t, tl.f0 + 16 * c, z, u, vec);
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (by_tma) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&buf_done[buf]);
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[b]), 0));
-            if (by_tma) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (leader) stop = abort_flag;  // one answer for all the epilogue's warps
-            epilogue_barrier();
-            if (leader && by_tma) {
-                for (int s = 0; s < subs; ++s)
-                    if (tl.f0 + 64 * s < a.N && tl.t0 + (int)rank * 128 < a.T)
-                        tma_store_2d(&maps.out, staging + s * kLinA, tl.f0 + 64 * s, tl.t0 + (int)rank * 128);
+        }
+    } else if (warp == 10 && by_tma) {  // row mover
+        const int64_t tiles = pair < sched.total ? (sched.total - pair + pairs - 1) / pairs : 0;
+        const int64_t all = tiles * passes;
+        // makes buffer g & 1 ready for pass g: its biases, and the residual if there is one
+        auto prepare = [&](int64_t g) {
+            if (g >= all) return;
+            const int buf = (int)(g & 1);
+            int r0, f0;
+            first(pair + g / passes * pairs, r0, f0);
+            const int p = (int)(g % passes), fp = f0 + 64 * p;
+            if (a.bias || a.bias_mul) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float* src = j < 2 ? a.bias : a.bias_mul;
+                    const int f = fp + lane + 32 * (j & 1);
+                    bias_s[buf][lane + 32 * j] = src && f < a.N ? __ldg(src + f) : 0.f;
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {
+                if (!res_tma) {
+                    mbar_arrive(&buf_ready[buf]);
+                } else {
+                    const int pieces = min(2, subs - 2 * p);
+                    mbar_arrive_expect_tx(&buf_ready[buf], pieces * kManySub);
+                    for (int s = 0; s < pieces; ++s)
+                        tma_load_2d(rows_s + (2 * buf + s) * kManySub, &maps.res, fp + 32 * s, r0, &buf_ready[buf]);
+                }
+            }
+            __syncwarp();
+        };
+        prepare(0);
+        prepare(1);
+        int64_t g = 0;
+        for (; g < all; ++g) {
+            const int buf = (int)(g & 1);
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&buf_done[buf], (g >> 1) & 1, kLinWaitLimit)) ||
+                __any_sync(0xffffffffu, abort_flag)) {
+                give_up();
+                break;
+            }
+            if (lane == 0) {
+                int r0, f0;
+                first(pair + g / passes * pairs, r0, f0);
+                const int p = (int)(g % passes), fp = f0 + 64 * p;
+                for (int s = 0; s < min(2, subs - 2 * p); ++s)
+                    if (fp + 32 * s < a.N && r0 < a.T)
+                        tma_store_2d(&maps.out, rows_s + (2 * buf + s) * kManySub, fp + 32 * s, r0);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                if (res_tma && i + pairs < sched.total && !stop) load_residual(i + pairs);
             }
-            if (stop) break;
+            __syncwarp();
+            prepare(g + 2);
         }
-        if (leader && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (g < all)  // gave up: wait (bounded) for the residual copies in flight
+            for (int64_t j = g; j < g + 2 && j < all; ++j)
+                mbar_wait_bounded(&buf_ready[j & 1], (j >> 1) & 1, kLinWaitLimit);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();
     cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done
@@ -583,17 +674,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// [rows][cols] 16-bit elements, rows ld apart; boxes of 64 columns x box_rows, 128-byte swizzle.
-bool encode16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+// [rows][cols] 16-bit elements, rows ld apart; boxes of box_cols columns (64 bytes or 128, swizzled
+// over as many) x box_rows.
+bool encode16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
+              int box_cols = kLinK) {
     const auto fn = encoder();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {(cuuint32_t)kLinK, (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename K>
@@ -650,14 +744,15 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     }
     // TMA addresses rows that start at multiples of 16 bytes
     a.tma_rows = rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
-    if (!encode16(&m.x, x, d.K, d.T, d.ldx, 128) || !encode16(&m.w, w, d.K, d.N, d.ldw, 64) ||
-        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, 64)) ||
-        (a.tma_rows && !encode16(&m.out, out, d.N, d.T, d.ldo, 128)) ||
-        (a.tma_rows && residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128)))
+    a.width = 256;
+    const int half = a.width / 2;
+    if (!encode16(&m.x, x, d.K, d.T, d.ldx, 128) || !encode16(&m.w, w, d.K, d.N, d.ldw, half) ||
+        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, half)) ||
+        (a.tma_rows && !encode16(&m.out, out, d.N, d.T, d.ldo, 128, 32)) ||
+        (a.tma_rows && residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128, 32)))
         return cudaErrorInvalidValue;
-    a.wave = sms / 2;
-    const int64_t total = ManySched(d.T, d.N, a.gated, a.wave).total;
-    const int pairs = (int)(total < a.wave ? total : a.wave);
+    const int64_t total = ManySched(d.T, d.N, a.gated ? half : a.width).total;
+    const int pairs = (int)(total < sms / 2 ? total : sms / 2);
     return launch_clusters(linear_many_kernel, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
 }
 
