@@ -65,12 +65,11 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
     return a;
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_v4(uint32_t mapped, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mapped), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
@@ -168,6 +167,33 @@ __device__ __forceinline__ void pack_all(const float (&z)[C], uint32_t (&w)[C / 
     }
 }
 
+// Feature n of up to four consecutive rows from t on (the lanes of a warp hold consecutive features).
+__device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[4],
+                                               const float (&u)[4]) {
+    uint32_t rw[4] = {};
+    if (a.res) {
+        const uint16_t* res = static_cast<const uint16_t*>(a.res) + t * a.ldr + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < rows) rw[i] = res[i * a.ldr];
+    }
+    const float b = a.bias ? __ldg(a.bias + n) : 0.f, c = a.bias_mul ? __ldg(a.bias_mul + n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += b;
+    apply_func(a.func, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (a.gated) z[i] *= u[i] + c;
+        if (a.res) z[i] += a.f16 ? __half2float(__ushort_as_half((unsigned short)rw[i])) : __uint_as_float(rw[i] << 16);
+    }
+    uint32_t w[2];
+    pack_all(z, w, a.f16);
+    uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ldo + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < rows) out[i * a.ldo] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+}
+
 // C consecutive outputs of row t from feature n on: bias, function, factor, residual, one rounding.
 // u: the factor's sums (gated).  vec: every row starts at a multiple of 2 C bytes.
 template <int C>
@@ -256,11 +282,21 @@ __host__ __device__ __forceinline__ bool rows_aligned(const void* p, int64_t ld,
 
 // ------------------------------------------------------------------------------------------
 // Few rows.  grid (tiles of W rows * splits of K, tiles of x rows), clusters of `splits` CTAs.  A tile
-// is 128 rows of W, or 64 of W and 64 of V.  Warp 0 loads, warp 1 issues the MMAs, warps 2-5 move
-// the accumulator (lane = W row, column = row of x) to shared memory, then all six warps add
-// the cluster's partial sums: CTA r takes columns r, r + splits, ...
+// is 128 rows of W, or 64 of W and 64 of V.  Warp 0 loads, warp 1 issues the MMAs, warps 2-5 send the
+// accumulator (lane = W row, column = row of x) to its owners: each CTA of the cluster owns `own`
+// columns and has a landing area for every CTA's part of them.  After one cluster barrier each CTA
+// adds its columns' parts, in rank order, from its own shared memory.
 // ------------------------------------------------------------------------------------------
-constexpr int kFewThreads = 192;
+constexpr int kFewThreads = 256;
+constexpr int kFewSplits = 8;    // CTAs per cluster at most (the portable cluster size)
+constexpr int kFewRows = 128;    // rows of x per tile at most
+constexpr int kSmSmem = 228 * 1024, kFewSmemMax = 226 * 1024;  // shared memory of an SM, and of a CTA here
+__host__ __device__ constexpr int few_own(int rows, int splits) { return ((rows + splits - 1) / splits + 3) / 4 * 4; }
+__host__ __device__ constexpr int few_pitch(int own) { return own | 4; }  // own is a multiple of 4
+__host__ __device__ constexpr int few_smem(int rows, int splits, int stages) {
+    return stages * (kLinA + rows * 128) + splits * 128 * few_pitch(few_own(rows, splits)) * 4 + 1024;
+}
+
 
 __global__ void __launch_bounds__(kFewThreads)
 linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
@@ -279,6 +315,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     const int NT = a.rows_t;
     const int k_begin = (int)((int64_t)a.nk * rank / splits), k_end = (int)((int64_t)a.nk * (rank + 1) / splits);
     const int stage_bytes = kLinA + NT * 128;
+    const int ncols = min(NT, a.T - t0);
+    // [rank][W row][own columns, padded so that 16-byte accesses of 8 rows meet 32 banks]
+    float* landing = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
+    const int own = few_own(NT, (int)splits), pitch = few_pitch(own);
     uint32_t tm_cols = 32;
     while (tm_cols < (uint32_t)NT) tm_cols *= 2;
     if (threadIdx.x == 0) {
@@ -344,40 +384,59 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         tc_commit(&acc_full);  // arrives when every MMA has completed
         mbar_wait_bounded(&acc_full, 0, kLinWaitLimit);
     }
-    const int ncols = min(NT, a.T - t0);
-    float* part = reinterpret_cast<float*>(smem);  // [column][128]; the ring is idle by then
-    if (warp >= 2) {
+    const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
+    if (warp >= 6) {
+        // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
+        if (a.res)
+            for (int i = threadIdx.x - 192; i < my_cols * 2; i += 64) {
+                const int n = n0 + 64 * (i & 1);
+                if (n < a.N && (i & 1) * 64 < per_tile)
+                    prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
+            }
+    } else if (warp >= 2) {
         if (!mbar_wait_bounded(&acc_full, 0, kLinWaitLimit)) give_up();
         tc_fence_after();
         const int q = warp & 3;
+        const uint32_t mine = smem_u32(landing + ((int)rank * 128 + 32 * q + lane) * pitch);
+        int owner = 0, at = 0;  // of the next four columns
         for (int c = 0; c < ncols; c += 16) {
             uint32_t v[16];
             tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < NT) part[(c + i) * 128 + 32 * q + lane] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; i += 4)
+                if (c + i < ncols) {
+                    st_cluster_v4(map_rank(mine + at * 4, owner), v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    at += 4;
+                    if (at == own) {
+                        at = 0;
+                        ++owner;
+                    }
+                }
         }
         tc_fence_before();
     }
-    __syncthreads();
-    cluster_sync();  // every partial sum is in shared memory
-    {
-        const bool vec = rows_aligned(a.out, a.ldo, 8) && (!a.res || rows_aligned(a.res, a.ldr, 8));
-        const uint32_t pbase = smem_u32(part);
-        for (int c = (int)rank + (int)splits * warp; c < ncols; c += (int)splits * (kFewThreads / 32)) {
-            float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4];
-            for (uint32_t s = 0; s < splits; ++s) {
-                const float4 p = ld_cluster_f4(map_rank(pbase + (uint32_t)(c * 128 + 4 * lane) * 4, s));
-                z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
-            }
+    cluster_sync();  // every part has landed
+    // items of 32 features x 4 rows of x, lane = feature
+    const int blocks = per_tile / 32, items = blocks * ((my_cols + 3) / 4);
+    for (int item = warp; item < items; item += kFewThreads / 32) {
+        const int r = (item % blocks) * 32 + lane, c = item / blocks * 4;
+        const float* src = landing + r * pitch + c;
+        float z[4] = {}, u[4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = __shfl_down_sync(0xffffffffu, z[i], 16);
-            const int n = n0 + 4 * lane;
-            if (n < a.N && (!a.gated || lane < 16)) finish<4>(a, (int64_t)t0 + c, n, z, u, vec);
-        }
+        for (int s = 0; s < kFewSplits; ++s)
+            if (s < (int)splits) {
+                const float4 p = *reinterpret_cast<const float4*>(src + s * 128 * pitch);
+                z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
+                if (a.gated) {
+                    const float4 g = *reinterpret_cast<const float4*>(src + (s * 128 + 64) * pitch);
+                    u[0] += g.x; u[1] += g.y; u[2] += g.z; u[3] += g.w;
+                }
+            }
+        const int n = n0 + r;
+        if (n < a.N) finish_feature(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z, u);
     }
-    cluster_sync();  // no CTA leaves while others read its sums
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, tm_cols);
@@ -713,6 +772,66 @@ cudaError_t launch_clusters(K* kernel, dim3 grid, int cluster, int threads, int 
 
 }  // namespace
 
+namespace {
+
+// Which kernel, and its tiles, by estimated time in microseconds (fitted to measurements over 1 to
+// 16384 rows, N 2048 to 8192, K 2048 to 8192; the estimates are within about 15 % of them).
+//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.34 / 0.30 / 0.27 us
+//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 1 us a tile
+//     besides, and 6 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.6 at 256.
+//   few rows: 64 elements cost a CTA 0.37 us and more with the rows of x, or what its SM's share of
+//     the L2 rate (105 GB/s) allows; 4.5 us besides, and the exchange of the parts.
+//     64 rows of the gated 2 x 2048 x 7168: 17.2 us, against 37.7 for the other kernel; 256 rows of
+//     7168 x 2048: 27 against 15.0.
+struct LinPlan {
+    bool few;
+    int width;                   // many: columns per tile
+    int splits, stages, rows_t;  // few: CTAs per cluster, ring stages, rows of x per tile
+};
+
+LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
+    LinPlan best{};
+    float best_us = 1e30f;
+    const float per_k[3] = {0.34f, 0.30f, 0.27f};
+    for (int i = 0; i < 3; ++i) {
+        const int width = 256 - 64 * i;
+        const int64_t tiles = ManySched(T, N, gated ? width / 2 : width).total;
+        const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
+        const float us = (float)waves * ((float)nk * per_k[i] + 1.f) + 6.f;
+        if (us < best_us) {
+            best_us = us;
+            best = LinPlan{false, width, 0, 0, 0};
+        }
+    }
+    if (T > 4 * kFewRows) return best;
+    const int tiles_t = (T + kFewRows - 1) / kFewRows;
+    const int rows = ((T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
+    const int64_t tiles = (int64_t)tiles_t * ((N + (gated ? 63 : 127)) / (gated ? 64 : 128));
+    const float stage_kb = (float)(kLinA + rows * 128) / 1024.f;
+    for (int splits = 1; splits <= kFewSplits && splits <= nk; splits *= 2) {
+        const int kbs = (nk + splits - 1) / splits;
+        const int stages = kbs < 4 ? (kbs < 2 ? 2 : kbs) : 4;
+        const int smem = few_smem(rows, splits, stages);
+        if (smem > kFewSmemMax) continue;
+        // CTAs an SM holds, and what clusters of 4 and 8 leave usable of these places (a device of
+        // 152 SMs holds 120 CTAs in clusters of 8 at one per SM, 288 at two)
+        const int fit = kSmSmem / (smem + 1024 + 256);
+        const int64_t places = (int64_t)sms * fit * (splits < 4 ? 32 : splits == 4 ? 30 : fit == 1 ? 25 : 28) / 32;
+        const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
+        const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
+        const float per_k_lat = 0.37f + 0.0008f * (float)rows, per_k_bw = (float)on_sm * stage_kb / 105.f;
+        const float us = (float)waves * ((float)kbs * (per_k_lat > per_k_bw ? per_k_lat : per_k_bw) + 4.5f +
+                                         0.03f * (float)rows);
+        if (us < best_us) {
+            best_us = us;
+            best = LinPlan{true, 0, splits, stages, rows};
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
                           const float* bias, const float* bias_mul, const void* residual, void* out,
                           int32_t* status, cudaStream_t st) {
@@ -725,33 +844,27 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     a.func = d.func; a.gated = w_mul != nullptr; a.f16 = d.dtype == MOE_DT_F16;
     a.ldr = d.ldr; a.ldo = d.ldo;
     a.bias = bias; a.bias_mul = bias_mul; a.res = residual; a.out = out; a.status = status;
+    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms);
     LinMaps m{};
-    if (d.T <= 512) {
-        const int tiles_t = (d.T + 255) / 256;
-        a.rows_t = ((d.T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
-        const int per_tile = a.gated ? 64 : 128;
-        const int tiles_n = (d.N + per_tile - 1) / per_tile;
-        const int stage = kLinA + a.rows_t * 128;
-        a.stages = a.rows_t <= 32 ? 4 : a.rows_t <= 96 ? 4 : 4;
-        if (!encode16(&m.x, x, d.K, d.T, d.ldx, a.rows_t) ||
-            !encode16(&m.w, w, d.K, d.N, d.ldw, per_tile) ||
-            (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, per_tile)))
-            return cudaErrorInvalidValue;
-        int splits = 1;
-        while (splits < 8 && 2 * splits <= a.nk && (int64_t)tiles_n * tiles_t * splits * 2 <= 2 * sms) splits *= 2;
-        return launch_clusters(linear_few_kernel, dim3(tiles_n * splits, tiles_t), splits, kFewThreads,
-                               a.stages * stage + 1024, m, a, st);
+    // rows of W per box, and rows of x
+    const int box_w = plan.few ? (a.gated ? 64 : 128) : plan.width / 2, box_x = plan.few ? plan.rows_t : 128;
+    if (!encode16(&m.x, x, d.K, d.T, d.ldx, box_x) || !encode16(&m.w, w, d.K, d.N, d.ldw, box_w) ||
+        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, box_w)))
+        return cudaErrorInvalidValue;
+    if (plan.few) {
+        a.rows_t = plan.rows_t;
+        a.stages = plan.stages;
+        const int tiles_n = (d.N + box_w - 1) / box_w, tiles_t = (d.T + plan.rows_t - 1) / plan.rows_t;
+        return launch_clusters(linear_few_kernel, dim3(tiles_n * plan.splits, tiles_t), plan.splits, kFewThreads,
+                               few_smem(plan.rows_t, plan.splits, plan.stages), m, a, st);
     }
     // TMA addresses rows that start at multiples of 16 bytes
+    a.width = plan.width;
     a.tma_rows = rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
-    a.width = 256;
-    const int half = a.width / 2;
-    if (!encode16(&m.x, x, d.K, d.T, d.ldx, 128) || !encode16(&m.w, w, d.K, d.N, d.ldw, half) ||
-        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, half)) ||
-        (a.tma_rows && !encode16(&m.out, out, d.N, d.T, d.ldo, 128, 32)) ||
-        (a.tma_rows && residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128, 32)))
+    if (a.tma_rows && (!encode16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
+                       (residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
         return cudaErrorInvalidValue;
-    const int64_t total = ManySched(d.T, d.N, a.gated ? half : a.width).total;
+    const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);
     return launch_clusters(linear_many_kernel, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
 }
