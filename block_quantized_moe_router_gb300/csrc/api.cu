@@ -262,17 +262,20 @@ moe_status_t moe_route_grouped(const moe_route_desc* d, int32_t n_group, int32_t
     if (!topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const float* logits = logits_in;
+    const float* bias = d->scoring != MOE_SCORE_SOFTMAX ? d->correction_bias : nullptr;
     if (!logits) {
         if (!d->w_router || !x_bf16 || !logits_out || !aligned16(x_bf16) || !aligned16(d->w_router))
             return MOE_ERR_INVALID_ARG;
-        cudaError_t err = launch_router_tc(x_bf16, d->w_router, logits_out, d->T, d->E, d->H,
-                                           dev_status, st);
+        cudaError_t err = launch_route_fused(x_bf16, d->w_router, bias, d->T, d->E, d->H, d->top_k, d->scoring,
+                                             d->renormalize ? 1 : 0, d->routed_scaling, n_group, topk_group,
+                                             group_top, logits_out, topk_ids, topk_w, dev_status, st);
+        if (err != cudaErrorNotSupported) return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        err = launch_router_tc(x_bf16, d->w_router, logits_out, d->T, d->E, d->H, dev_status, st);
         if (err == cudaErrorNotSupported)
             err = launch_router_logits(x_bf16, d->w_router, logits_out, d->T, d->E, d->H, st);
         if (err != cudaSuccess) return MOE_ERR_CUDA;
         logits = logits_out;
     }
-    const float* bias = d->scoring != MOE_SCORE_SOFTMAX ? d->correction_bias : nullptr;
     return launch_topk_grouped(logits, bias, d->T, d->E, d->top_k, d->scoring, d->renormalize ? 1 : 0,
                                d->routed_scaling, n_group, topk_group, group_top, topk_ids, topk_w,
                                dev_status, st) == cudaSuccess

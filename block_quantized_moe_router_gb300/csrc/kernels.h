@@ -31,6 +31,12 @@ cudaError_t launch_hash_route(const int64_t* tid2eid, const int32_t* token_ids, 
 cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k, int scoring,
                                 int renorm, float scaling, int n_group, int topk_group, int group_top,
                                 int32_t* ids, float* w, int32_t* status, cudaStream_t st);
+// The router product and that selection in one launch: E <= 256, x and wr 16-byte aligned;
+// cudaErrorNotSupported (nothing launched) otherwise.
+cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias, int T, int E, int H, int k,
+                               int scoring, int renorm, float scaling, int n_group, int topk_group,
+                               int group_top, float* logits, int32_t* ids, float* w, int32_t* status,
+                               cudaStream_t st);
 
 // ---- dense layers around the experts (linear.cu, norm.cu) -----------------------------------
 cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,

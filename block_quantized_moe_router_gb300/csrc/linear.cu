@@ -16,8 +16,7 @@
 // The gated form takes its weight rows half from W and half from V, so z and its factor meet in one
 // accumulator and neither goes through memory.  Every wait is bounded: one that gives up sets
 // MOE_DEV_TIMEOUT and the CTA winds down.
-#include <cudaTypedefs.h>
-
+#include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -49,30 +48,8 @@ struct LinArgs {
     int32_t* status;
 };
 
-// ---- cluster and CTA-pair primitives -----------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of this CTA's shared-memory location `saddr` in the CTA of rank `rank`.
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ void st_cluster_v4(uint32_t mapped, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mapped), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
+// ---- CTA-pair primitives -------------------------------------------------------------------------
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-__device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
-}
 // TMA load of a CTA pair: the bytes land here, the count on the mapped barrier of either CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m, int x, int y,
                                               uint32_t mapped_bar) {
@@ -306,8 +283,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t splits;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+    const uint32_t splits = cluster_size();
     const uint32_t rank = cluster_rank();
     const int per_tile = a.gated ? 64 : 128;
     const int n0 = (int)(blockIdx.x / splits) * per_tile;
@@ -338,6 +314,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
     auto give_up = [&]() {
@@ -384,6 +361,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         tc_commit(&acc_full);  // arrives when every MMA has completed
         mbar_wait_bounded(&acc_full, 0, kLinWaitLimit);
     }
+    cluster_wait();
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     if (warp >= 6) {
         // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
@@ -721,34 +699,6 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
 }
 
 // ---- host ------------------------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess || q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
-// [rows][cols] 16-bit elements, rows ld apart; boxes of box_cols columns (64 bytes or 128, swizzled
-// over as many) x box_rows.
-bool encode16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
-              int box_cols = kLinK) {
-    const auto fn = encoder();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename K>
 cudaError_t launch_clusters(K* kernel, dim3 grid, int cluster, int threads, int smem, const LinMaps& m,
                             const LinArgs& a, cudaStream_t st) {
@@ -848,8 +798,8 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     LinMaps m{};
     // rows of W per box, and rows of x
     const int box_w = plan.few ? (a.gated ? 64 : 128) : plan.width / 2, box_x = plan.few ? plan.rows_t : 128;
-    if (!encode16(&m.x, x, d.K, d.T, d.ldx, box_x) || !encode16(&m.w, w, d.K, d.N, d.ldw, box_w) ||
-        (a.gated && !encode16(&m.v, w_mul, d.K, d.N, d.ldw, box_w)))
+    if (!encode_rows16(&m.x, x, d.K, d.T, d.ldx, box_x, kLinK) || !encode_rows16(&m.w, w, d.K, d.N, d.ldw, box_w, kLinK) ||
+        (a.gated && !encode_rows16(&m.v, w_mul, d.K, d.N, d.ldw, box_w, kLinK)))
         return cudaErrorInvalidValue;
     if (plan.few) {
         a.rows_t = plan.rows_t;
@@ -861,8 +811,8 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     // TMA addresses rows that start at multiples of 16 bytes
     a.width = plan.width;
     a.tma_rows = rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
-    if (a.tma_rows && (!encode16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
-                       (residual && !encode16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
+    if (a.tma_rows && (!encode_rows16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
+                       (residual && !encode_rows16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
         return cudaErrorInvalidValue;
     const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);

@@ -12,52 +12,69 @@
 // where a comparison that decides the result falls inside the bound, the token's selection runs
 // again in fp64.  Without a bias every score grows with its logit, and experts are ranked by
 // the logits themselves, which needs no bound.
+//
+// One warp routes one token (lane l holds experts l, l + 32, ...).  Only the kept groups' experts
+// go into the K rounds, dealt anew over the lanes, so a round looks at topk_group / n_group of the
+// values.
+#include <cudaTypedefs.h>
+
+#include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 #include "topk.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kRgWarps = 8;  // tokens per CTA
+struct GroupRule {
+    int E, k, scoring, renorm, n_group, topk_group, group_top, by_logit;
+    int size;       // experts per group
+    int size_inv;   // ceil(2^20 / size): (r * size_inv) >> 20 == r / size for r < 512
+    float scaling;
+};
+
+__device__ __forceinline__ bool is_softmax(int scoring) {
+    return scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SOFTMAX_BIAS;
+}
 
 template <typename R>
 __device__ __forceinline__ R score_of(int scoring, R l, R lmax, R zall) {
     if (l == -INFINITY) return R(0);
-    if (scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SOFTMAX_BIAS) return exp(l - lmax) / zall;
+    if (is_softmax(scoring)) return exp(l - lmax) / zall;
     if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrt(l > R(40) ? l : log1p(exp(l)));
     return R(1) / (R(1) + exp(-l));
 }
 
-struct GroupRule {
-    int E, k, scoring, renorm, n_group, topk_group, group_top, by_logit;
-    float scaling;
-};
-
 // Relative error bound of an fp32 selection score: expf, the additions and the division are
 // within 2^-22 of |s|; a softmax denominator summed over 512 logits adds up to 2^-19.7.
-__device__ __forceinline__ float score_eps(int scoring) {
-    return scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SOFTMAX_BIAS ? 0x1p-19f : 0x1p-21f;
+__device__ __forceinline__ float score_eps(int scoring) { return is_softmax(scoring) ? 0x1p-19f : 0x1p-21f; }
+
+__device__ __forceinline__ float from_orderable(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
-// One warp selects one token's experts, in R = float or double.  lg: the lane's logits (-inf for
-// a non-finite one or beyond E), bv: their biases; sm: E values of scratch.  On return lane j < k
-// holds pick j.  The result says (float only) whether a comparison fell inside the error bound.
-template <int EPL, typename R>
-__device__ __forceinline__ bool select_grouped(const GroupRule& P, const float (&lg)[EPL],
-                                               const float (&bv)[EPL], float lmax32, R* sm, int lane,
-                                               int& my_e) {
-    constexpr bool kFloat = sizeof(R) == 4;
-    const bool softmax = P.scoring == MOE_SCORE_SOFTMAX || P.scoring == MOE_SCORE_SOFTMAX_BIAS;
-    const bool need_score = !P.by_logit || P.group_top == 2;
-    const R lmax = lmax32;
-    R v[EPL];    // ranks the experts
-    R zall = 1;
-    if (need_score && softmax) {
+// Shared memory of one routing warp.
+template <int EPL>
+struct alignas(16) RouteScratch {
+    double v64[32 * EPL];  // the fp64 selection's values; the fp32 one's in the same place
+    float logit[32 * EPL];
+    float group[64];
+    int kept[64];
+};
+
+// The selection in fp64, from the logits in shared memory (-inf: not finite); rare, so kept short.
+// On return lane j < k holds pick j.
+template <int EPL>
+__device__ __noinline__ int select_fp64(const GroupRule& P, const float* bias, float lmax32,
+                                        RouteScratch<EPL>* sc, int lane) {
+    const double lmax = lmax32;
+    double v[EPL], zall = 1;
+    if (is_softmax(P.scoring)) {
         zall = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) zall += lg[j] == -INFINITY ? R(0) : exp(R(lg[j]) - lmax);
+        for (int e = lane; e < P.E; e += 32)
+            if (sc->logit[e] != -INFINITY) zall += exp((double)sc->logit[e] - lmax);
 #pragma unroll
         for (int o = 16; o; o >>= 1) zall += __shfl_xor_sync(0xffffffffu, zall, o);
     }
@@ -65,100 +82,52 @@ __device__ __forceinline__ bool select_grouped(const GroupRule& P, const float (
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        R s = -INFINITY;
-        v[j] = -INFINITY;
-        if (e < P.E && lg[j] != -INFINITY) {
-            if (need_score) s = score_of<R>(P.scoring, R(lg[j]), lmax, zall);
-            // a bias that is not finite ranks its expert last
-            v[j] = P.by_logit ? R(lg[j]) : (isfinite(bv[j]) ? s + R(bv[j]) : R(-INFINITY));
-        }
-        // what the groups add up: the ranking value, or with two per group the scores
-        if (e < P.E) sm[e] = P.by_logit && P.group_top == 2 ? s : v[j];
+        v[j] = NAN;  // never picked
+        if (e >= P.E) continue;
+        const float l = sc->logit[e], b = bias ? bias[e] : 0.f;
+        const double s = score_of<double>(P.scoring, l, lmax, zall);
+        v[j] = P.by_logit ? (double)l : l != -INFINITY && isfinite(b) ? s + (double)b : (double)-INFINITY;
+        sc->v64[e] = P.by_logit && P.group_top == 2 && l != -INFINITY ? s : v[j];
     }
     __syncwarp();
-    const R smax = kFloat && need_score ? score_of<R>(P.scoring, lmax, lmax, zall) : R(0);
-    const R eps = kFloat ? R(score_eps(P.scoring)) : R(0);
-    bool close = false;
-
-    // group scores: 32 / n_group lanes (a power of two) share a group; lanes of sub-index 0 keep
-    // the score of groups lane / per and, above 32 groups, + 32
-    const int size = P.E / P.n_group;
-    int per = 1;
-    while (per * 2 * P.n_group <= 32) per *= 2;
-    unsigned long long kept = ~0ull;
     if (P.topk_group < P.n_group) {
-        R gs[2], tol[2];
-#pragma unroll
+        double gs[2];
         for (int q = 0; q < 2; ++q) {
-            const int g = lane / per + 32 * q;
-            R m1 = -INFINITY, m2 = -INFINITY;
-            if (g < P.n_group) {
-                for (int i = lane % per; i < size; i += per) {
-                    const R x = sm[g * size + i];
+            const int g = lane + 32 * q;
+            double m1 = -INFINITY, m2 = -INFINITY;
+            if (g < P.n_group)
+                for (int i = 0; i < P.size; ++i) {
+                    const double x = sc->v64[g * P.size + i];
                     m2 = x > m1 ? m1 : (x > m2 ? x : m2);
                     m1 = x > m1 ? x : m1;
                 }
-            }
-            for (int o = per / 2; o; o >>= 1) {
-                const R b1 = __shfl_xor_sync(0xffffffffu, m1, o);
-                const R b2 = __shfl_xor_sync(0xffffffffu, m2, o);
-                const R lo = m1 < b1 ? m1 : b1;
-                const R hi2 = m1 > b1 ? m2 : b2;
-                m1 = m1 > b1 ? m1 : b1;
-                m2 = lo > hi2 ? lo : hi2;
-            }
             gs[q] = P.group_top == 2 ? m1 + m2 : m1;
-            tol[q] = !need_score ? R(0)
-                                 : eps * (fabs(m1) + (P.group_top == 2 ? fabs(m2) : R(0)) + 4 * smax);
         }
-        // rank of each group among all: the kept ones are those with rank < topk_group
-        kept = 0;
+        unsigned long long kept = 0;
         for (int g = 0; g < P.n_group; ++g) {
-            const R mine = __shfl_sync(0xffffffffu, g < 32 ? gs[0] : gs[1], (g & 31) * per);
-            // groups above 32 come only with per == 1, so lane l holds groups l and l + 32
-            bool ahead0 = false, ahead1 = false, amb = false;
-            const R mtol = kFloat ? __shfl_sync(0xffffffffu, g < 32 ? tol[0] : tol[1], (g & 31) * per) : R(0);
-            const bool judge = kFloat && need_score && mine > -INFINITY;
-            const int g0 = lane / per;
-            if (lane % per == 0 && g0 < P.n_group && g0 != g) {
-                ahead0 = gs[0] > mine || (gs[0] == mine && g0 < g);
-                amb = judge && gs[0] > -INFINITY && fabs(gs[0] - mine) <= tol[0] + mtol;
-            }
-            if (g0 + 32 < P.n_group && per == 1 && g0 + 32 != g) {
-                ahead1 = gs[1] > mine || (gs[1] == mine && g0 + 32 < g);
-                amb = amb || (judge && gs[1] > -INFINITY && fabs(gs[1] - mine) <= tol[1] + mtol);
-            }
-            const unsigned b0 = __ballot_sync(0xffffffffu, ahead0);
-            const unsigned b1 = __ballot_sync(0xffffffffu, ahead1);
-            const int rank = __popc(b0) + __popc(b1);
+            const double mine = __shfl_sync(0xffffffffu, g < 32 ? gs[0] : gs[1], g & 31);
+            const bool a0 = lane < P.n_group && (gs[0] > mine || (gs[0] == mine && lane < g));
+            const bool a1 = lane + 32 < P.n_group && (gs[1] > mine || (gs[1] == mine && lane + 32 < g));
+            const int rank = __popc(__ballot_sync(0xffffffffu, a0)) + __popc(__ballot_sync(0xffffffffu, a1));
             if (rank < P.topk_group) kept |= 1ull << g;
-            // only the border between kept and dropped matters
-            if (kFloat && (rank == P.topk_group - 1 || rank == P.topk_group))
-                close = close || __any_sync(0xffffffffu, amb);
         }
-    }
-
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 32 * j;
-        if (e >= P.E || !((kept >> (e / size)) & 1)) v[j] = NAN;  // never picked
+        for (int j = 0; j < EPL; ++j)
+            if (lane + 32 * j < P.E && !((kept >> ((lane + 32 * j) / P.size)) & 1)) v[j] = NAN;
     }
-    my_e = 0;
-    R prev = INFINITY;
+    int my_e = 0;
     for (int r = 0; r < P.k; ++r) {
-        R best = -INFINITY;
+        double best = -INFINITY;
         int be = 0x7fffffff;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const int e = lane + 32 * j;
-            if (v[j] > best || (v[j] == best && e < be)) {
+        for (int j = 0; j < EPL; ++j)
+            if (v[j] > best || (v[j] == best && lane + 32 * j < be)) {
                 best = v[j];
-                be = e;
+                be = lane + 32 * j;
             }
-        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            const R ob = __shfl_xor_sync(0xffffffffu, best, o);
+            const double ob = __shfl_xor_sync(0xffffffffu, best, o);
             const int oe = __shfl_xor_sync(0xffffffffu, be, o);
             if (ob > best || (ob == best && oe < be)) {
                 best = ob;
@@ -169,72 +138,183 @@ __device__ __forceinline__ bool select_grouped(const GroupRule& P, const float (
         for (int j = 0; j < EPL; ++j)
             if (lane + 32 * j == be) v[j] = NAN;
         if (lane == r) my_e = be;
-        if (kFloat && !P.by_logit && best > -INFINITY)
-            close = close || prev - best <= 2 * eps * (fabs(best) + 2 * smax);
-        prev = best;
     }
-    if (kFloat && !P.by_logit && prev > -INFINITY) {  // the best of those left behind
-        bool amb = false;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            amb = amb || (v[j] > -INFINITY && prev - v[j] <= 2 * eps * (fabs(prev) + 2 * smax));
-        close = close || __any_sync(0xffffffffu, amb);
-    }
-    return close;
+    return my_e;
 }
 
+// One warp routes one token: raw[j] is the logit of expert lane + 32 j (anything beyond E).
 template <int EPL>
-__global__ void __launch_bounds__(kRgWarps * 32)
-topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, GroupRule P,
-                    int32_t* __restrict__ ids, float* __restrict__ wout, int32_t* __restrict__ status) {
-    extern __shared__ double rg_smem[];
-    pdl_wait();  // logits come from the router kernel
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kRgWarps + warp;
-    if (t >= T) return;
-    double* sm = rg_smem + warp * P.E;
-    const float* row = logits + (size_t)t * P.E;
-    float lg[EPL], bv[EPL];
-    float lmax = -INFINITY;
+__device__ __forceinline__ void route_token(const GroupRule& P, const float (&raw)[EPL], const float* bias,
+                                            RouteScratch<EPL>* sc, int lane, int32_t* ids, float* wout,
+                                            int32_t* status) {
+    const bool softmax = is_softmax(P.scoring), grouped = P.topk_group < P.n_group;
+    float lg[EPL], v[EPL], lmax = -INFINITY;
     bool nonfinite = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        lg[j] = e < P.E ? row[e] : -INFINITY;
-        bv[j] = bias && e < P.E ? bias[e] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        if (lane + 32 * j < P.E && !isfinite(lg[j])) {
-            nonfinite = true;
-            lg[j] = -INFINITY;
+        lg[j] = -INFINITY;
+        if (e < P.E) {
+            if (isfinite(raw[j])) lg[j] = raw[j];
+            else nonfinite = true;
+            sc->logit[e] = lg[j];
         }
         lmax = fmaxf(lmax, lg[j]);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
     if (__any_sync(0xffffffffu, nonfinite) && lane == 0) status_or(status, MOE_DEV_NONFINITE);
+    lmax = from_orderable(__reduce_max_sync(0xffffffffu, orderable(lmax)));
 
-    int e;
-    if (select_grouped<EPL, float>(P, lg, bv, lmax, reinterpret_cast<float*>(sm), lane, e))
-        select_grouped<EPL, double>(P, lg, bv, lmax, sm, lane, e);
-
-    // weights of the picks
-    const bool softmax = P.scoring == MOE_SCORE_SOFTMAX || P.scoring == MOE_SCORE_SOFTMAX_BIAS;
-    float z = 1.f;
-    if (softmax && !P.renorm) {
-        z = 0.f;
+    const bool need_score = !P.by_logit || (grouped && P.group_top == 2);
+    float zall = 1.f;  // softmax denominator: for the scores, or for weights that are not renormalised
+    if (softmax && (need_score || !P.renorm)) {
+        zall = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) z += lg[j] == -INFINITY ? 0.f : expf(lg[j] - lmax);
+        for (int j = 0; j < EPL; ++j) zall += lg[j] == -INFINITY ? 0.f : expf(lg[j] - lmax);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        for (int o = 16; o; o >>= 1) zall += __shfl_xor_sync(0xffffffffu, zall, o);
     }
+    float* sv = reinterpret_cast<float*>(sc->v64);
+    const bool score_groups = P.by_logit && P.group_top == 2;  // groups add scores, experts rank by logit
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const int e = lane + 32 * j;
+        v[j] = -INFINITY;
+        if (e < P.E) {
+            float s = -INFINITY;
+            if (lg[j] != -INFINITY) {
+                if (need_score) s = score_of<float>(P.scoring, lg[j], lmax, zall);
+                if (P.by_logit) {
+                    v[j] = lg[j] + 0.f;  // -0 and +0 are equal
+                } else {
+                    const float b = bias ? __ldg(bias + e) : 0.f;
+                    v[j] = isfinite(b) ? s + b : -INFINITY;
+                }
+            }
+            sv[e] = score_groups ? s : v[j];
+        }
+    }
+    const float smax = need_score ? score_of<float>(P.scoring, lmax, lmax, zall) : 0.f;
+    const float eps = score_eps(P.scoring);
+    bool close = false;  // a deciding comparison fell inside the error bound
+
+    uint32_t key[EPL];
+    int ee[EPL];
+    if (grouped) {
+        __syncwarp();
+        // 32 / n_group lanes (a power of two) share a group; above 32 groups a lane has two
+        int per = 1;
+        while (per * 2 * P.n_group <= 32) per *= 2;
+        const int slots = P.n_group > 32 ? 2 : 1;
+        float gs[2] = {-INFINITY, -INFINITY}, tol[2] = {};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (q >= slots) break;
+            const int g = lane / per + 32 * q;
+            float m1 = -INFINITY, m2 = -INFINITY;
+            if (g < P.n_group)
+                for (int i = lane % per; i < P.size; i += per) {
+                    const float x = sv[g * P.size + i];
+                    m2 = fmaxf(m2, fminf(m1, x));
+                    m1 = fmaxf(m1, x);
+                }
+            for (int o = per / 2; o; o >>= 1) {
+                const float b1 = __shfl_xor_sync(0xffffffffu, m1, o);
+                const float b2 = __shfl_xor_sync(0xffffffffu, m2, o);
+                m2 = fmaxf(fminf(m1, b1), m1 > b1 ? m2 : b2);
+                m1 = fmaxf(m1, b1);
+            }
+            gs[q] = P.group_top == 2 ? m1 + m2 : m1;
+            if (need_score) tol[q] = eps * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f) + 4.f * smax);
+            if (lane % per == 0 && g < P.n_group) sc->group[g] = gs[q];
+        }
+        __syncwarp();
+        unsigned before = 0;  // kept groups in earlier slots
+        float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (q >= slots) break;
+            const int g = lane / per + 32 * q;
+            int rank = 0;
+            for (int i = 0; i < P.n_group; ++i) {
+                const float o = sc->group[i];
+                rank += o > gs[q] || (o == gs[q] && i < g) ? 1 : 0;
+            }
+            const bool mine = lane % per == 0 && g < P.n_group, keep = mine && rank < P.topk_group;
+            const unsigned b = __ballot_sync(0xffffffffu, keep);
+            if (keep) sc->kept[before + __popc(b & ((1u << lane) - 1u))] = g;
+            before += __popc(b);
+            if (keep) lo = fminf(lo, gs[q] - tol[q]);
+            if (mine && !keep) hi = fmaxf(hi, gs[q] + tol[q]);
+        }
+        if (need_score) {
+            lo = from_orderable(__reduce_min_sync(0xffffffffu, orderable(lo)));
+            hi = from_orderable(__reduce_max_sync(0xffffffffu, orderable(hi)));
+            close = hi > -INFINITY && lo > -INFINITY && hi >= lo;
+        }
+        __syncwarp();
+        if (score_groups) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (lane + 32 * j < P.E) sv[lane + 32 * j] = v[j];
+            __syncwarp();
+        }
+        const int count = P.topk_group * P.size;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int r = lane + 32 * j;
+            key[j] = 0;
+            ee[j] = 0x7fffffff;
+            if (r < count) {
+                const int q = (r * P.size_inv) >> 20;
+                ee[j] = sc->kept[q] * P.size + r - q * P.size;
+                key[j] = orderable(sv[ee[j]]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            ee[j] = lane + 32 * j;
+            key[j] = ee[j] < P.E ? orderable(v[j]) : 0u;
+        }
+    }
+    const int live = grouped ? (P.topk_group * P.size + 31) / 32 : EPL;  // values per lane
+    int my_e = 0;
+    float prev = INFINITY;
+    for (int r = 0; r < P.k; ++r) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (j < live) m = max(m, key[j]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+        uint32_t e = 0x7fffffffu;
+        if (m == top) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (j < live && key[j] == top) e = min(e, (uint32_t)ee[j]);
+        }
+        e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (j < live && ee[j] == (int)e) key[j] = 0;
+        if (lane == r) my_e = (int)e;
+        if (!P.by_logit) {
+            const float best = from_orderable(top);
+            if (best > -INFINITY) close = close || prev - best <= 2.f * eps * (fabsf(best) + 2.f * smax);
+            prev = best;
+        }
+    }
+    if (!P.by_logit && prev > -INFINITY) {  // the best of those left behind
+        const uint32_t bar = orderable(prev - 2.f * eps * (fabsf(prev) + 2.f * smax));
+        bool amb = false;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) amb = amb || (j < live && key[j] >= bar);
+        close = __any_sync(0xffffffffu, close || amb);
+    }
+    __syncwarp();
+    if (close) my_e = select_fp64<EPL>(P, bias, lmax, sc, lane);
+
     float s = 0.f;
-    if (lane < P.k) {
-        const float l = row[e];
-        s = isfinite(l) ? score_of<float>(P.scoring, l, lmax, z) : 0.f;
-    }
+    if (lane < P.k) s = score_of<float>(P.scoring, sc->logit[my_e], lmax, zall);
     if (P.renorm) {
         float den = s;
 #pragma unroll
@@ -242,25 +322,253 @@ topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ 
         s = den > 0.f ? s / den : 0.f;
     }
     if (lane < P.k) {
-        ids[(size_t)t * P.k + lane] = e;
-        wout[(size_t)t * P.k + lane] = s * P.scaling;
+        ids[lane] = my_e;
+        wout[lane] = s * P.scaling;
+    }
+    __syncwarp();  // the scratch is the next token's
+}
+
+// ------------------------------------------------------------------------------------------
+// From logits in memory: one warp per token.
+// ------------------------------------------------------------------------------------------
+template <int EPL>
+constexpr int given_warps() { return EPL == 16 ? 4 : 8; }
+
+template <int EPL>
+__global__ void __launch_bounds__(given_warps<EPL>() * 32)
+topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, GroupRule P,
+                    int32_t* __restrict__ ids, float* __restrict__ wout, int32_t* __restrict__ status) {
+    __shared__ RouteScratch<EPL> scratch[given_warps<EPL>()];
+    pdl_wait();  // logits come from the router kernel
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * given_warps<EPL>() + warp;
+    if (t >= T) return;
+    const float* row = logits + t * P.E;
+    float raw[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) raw[j] = lane + 32 * j < P.E ? __ldg(row + lane + 32 * j) : 0.f;
+    route_token<EPL>(P, raw, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
+}
+
+template <int EPL>
+cudaError_t launch_given(const float* logits, const float* bias, int T, const GroupRule& P, int32_t* ids,
+                         float* w, int32_t* status, cudaStream_t st) {
+    constexpr int W = given_warps<EPL>();
+    return launch_pdl(topk_grouped_kernel<EPL>, dim3((unsigned)(((int64_t)T + W - 1) / W)), dim3(32 * W), st,
+                      logits, bias, T, P, ids, w, status);
+}
+
+// ------------------------------------------------------------------------------------------
+// From tokens: the router product and the selection in one launch, for E <= 256.
+//
+// A cluster takes 128 tokens, its CTAs a part of K each: x (the MMA's 128 rows) and the router (all
+// experts as the N side) stream through a TMA ring into a TMEM accumulator.  Each CTA owns
+// 128 / splits of the tokens; the partial logits go from tensor memory to the owners' shared memory,
+// where a warp per token adds them in rank order, writes the logits and selects.  The logits never
+// come back from memory, and for few tokens a launch is saved.
+// ------------------------------------------------------------------------------------------
+constexpr int kFusedThreads = 512;
+constexpr int kFusedK = 64;
+constexpr int kFusedA = 128 * 128;
+constexpr uint64_t kFusedWaitLimit = 1ull << 26;  // polls before a wait is declared stuck
+constexpr int kFusedSmemMax = 226 * 1024;
+constexpr int kFusedStagesMax = 8;
+
+struct FusedMaps {
+    CUtensorMap x, w;
+};
+
+struct FusedArgs {
+    int T, nk, n;           // n: experts rounded up to 16, the MMA's columns
+    int own, stages;        // tokens per CTA of a tile; ring stages
+    int box_x;              // token rows a TMA box brings
+    int landing_at;         // byte offsets: of the landing area (0: over the ring)
+    int scratch_at;         // and of the warps' scratch
+    const float* bias;
+    float* logits;
+    int32_t* ids;
+    float* w;
+    int32_t* status;
+};
+
+template <int EPL>
+__global__ void __launch_bounds__(kFusedThreads, 1)
+route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant__ FusedArgs a, const GroupRule P) {
+    using namespace tc;
+    extern __shared__ uint8_t rf_smem[];
+    __shared__ uint64_t full[kFusedStagesMax], empty[kFusedStagesMax], acc_full;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rf_smem) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int splits = (int)cluster_size(), rank = (int)cluster_rank();
+    const int64_t t0 = (int64_t)(blockIdx.x / splits) * 128;
+    const int rows = (int)min((int64_t)128, a.T - t0);  // tokens of this tile
+    const int stage_bytes = kFusedA + a.n * 128;
+    const int k_begin = (int)((int64_t)a.nk * rank / splits), k_end = (int)((int64_t)a.nk * (rank + 1) / splits);
+    const int steps = k_end - k_begin;
+    const int pitch = a.n + 4;  // floats: 16-byte accesses of eight rows meet 32 banks
+    float* landing = reinterpret_cast<float*>(smem + a.landing_at);  // [rank][own token][pitch]
+    uint32_t tm_cols = 32;
+    while (tm_cols < (uint32_t)a.n) tm_cols *= 2;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&acc_full, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&maps.x);
+        prefetch_tmap(&maps.w);
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, tm_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+    pdl_wait();
+    pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
+    auto give_up = [&]() {
+        abort_flag = 1;
+        status_or(a.status, MOE_DEV_TIMEOUT);
+    };
+    if (warp == 0 && lane == 0) {  // TMA producer
+        const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
+        int issued = 0;
+        for (int i = 0; i < steps && !abort_flag; ++i) {
+            const int s = i % a.stages;
+            if (!mbar_wait_bounded(&empty[s], ((i / a.stages) & 1) ^ 1, kFusedWaitLimit)) {
+                give_up();
+                break;
+            }
+            uint8_t* base = smem + s * stage_bytes;
+            const int kx = (k_begin + i) * kFusedK;
+            mbar_arrive_expect_tx(&full[s], bytes);
+            tma_load_2d(base + kFusedA, &maps.w, kx, 0, &full[s]);
+            tma_load_2d(base, &maps.x, kx, (int)t0, &full[s]);  // rows beyond the box: never read back
+            ++issued;
+        }
+        if (abort_flag)  // wait (bounded) for the copies still in flight
+            for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
+                mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kFusedWaitLimit);
+    } else if (warp == 1 && lane == 0) {  // MMA issuer
+        const uint32_t idesc = idesc_bf16(128, a.n);
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % a.stages;
+            if (!mbar_wait_bounded(&full[s], (i / a.stages) & 1, kFusedWaitLimit) || abort_flag) {
+                give_up();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sb = smem_u32(smem + s * stage_bytes);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes along the swizzled row
+                tc_mma_bf16(tmem, smem_desc(sb + 32 * j, 16, 1024, kLayoutSw128),
+                            smem_desc(sb + kFusedA + 32 * j, 16, 1024, kLayoutSw128), idesc, (i | j) != 0);
+            tc_commit(&empty[s]);
+        }
+        tc_commit(&acc_full);  // arrives when every MMA has completed
+        mbar_wait_bounded(&acc_full, 0, kFusedWaitLimit);
+    }
+    cluster_wait();
+    if (a.landing_at == 0) {  // over the ring: no CTA's copies or MMAs may still use it
+        __syncthreads();
+        cluster_sync();
+    }
+    if (warp >= 2 && warp < 6) {  // warp's lane quarter: tokens 32 q + lane
+        if (!mbar_wait_bounded(&acc_full, 0, kFusedWaitLimit)) give_up();
+        tc_fence_after();
+        const int q = warp & 3, row = 32 * q + lane;
+        if (32 * q < rows) {
+            const int owner = min(row / a.own, splits - 1), at = row - owner * a.own;
+            const uint32_t dst = map_rank(smem_u32(landing + ((int64_t)rank * a.own + at) * pitch), owner);
+            for (int c = 0; c < a.n; c += 16) {
+                uint32_t v[16];
+                tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+                tmem_ld_wait();
+                if (row < rows)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        st_cluster_v4(dst + (c + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3]);
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();  // every part has landed
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tm_cols);
+    }
+    auto* scratch = reinterpret_cast<RouteScratch<EPL>*>(smem + a.scratch_at) + warp;
+    const int mine = min(a.own, rows - rank * a.own);  // tokens of this CTA (may be negative)
+    for (int i = warp; i < mine; i += kFusedThreads / 32) {
+        const int64_t t = t0 + (int64_t)rank * a.own + i;
+        float raw[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) raw[j] = 0.f;
+        for (int s = 0; s < splits; ++s) {
+            const float* src = landing + ((int64_t)s * a.own + i) * pitch + lane;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (lane + 32 * j < P.E) raw[j] += src[32 * j];
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (lane + 32 * j < P.E) a.logits[t * P.E + lane + 32 * j] = raw[j];
+        route_token<EPL>(P, raw, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
     }
 }
 
 template <int EPL>
-cudaError_t launch_epl(const float* logits, const float* bias, int T, const GroupRule& P, int32_t* ids,
-                       float* w, int32_t* status, cudaStream_t st) {
+cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, int splits, cudaStream_t st) {
+    // ring | landing | scratch, or the last two over the ring where they do not fit beside it
+    const int stage = kFusedA + a.n * 128;
+    const int landing = splits * a.own * (a.n + 4) * 4;
+    const int scratch = (int)sizeof(RouteScratch<EPL>) * (kFusedThreads / 32);
+    const int steps = (a.nk + splits - 1) / splits;
+    const int landing16 = (landing + 15) / 16 * 16;
+    a.stages = (kFusedSmemMax - 1024 - landing16 - scratch) / stage;
+    const bool beside = a.stages >= 3 || a.stages >= steps;
+    if (!beside) a.stages = (kFusedSmemMax - 1024) / stage;
+    a.stages = a.stages < steps ? a.stages : steps;
+    a.stages = a.stages < 1 ? 1 : a.stages < kFusedStagesMax ? a.stages : kFusedStagesMax;
+    a.landing_at = beside ? a.stages * stage : 0;
+    a.scratch_at = a.landing_at + landing16;
+    int smem = a.scratch_at + scratch;
+    if (a.stages * stage > smem) smem = a.stages * stage;
+    smem += 1024;
+    if (smem > kFusedSmemMax) return cudaErrorNotSupported;
+    const auto kernel = route_fused_kernel<EPL>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess && splits > 8)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((T + kRgWarps - 1) / kRgWarps);
-    cfg.blockDim = dim3(kRgWarps * 32);
-    cfg.dynamicSmemBytes = sizeof(double) * kRgWarps * P.E;
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * splits));
+    cfg.blockDim = dim3(kFusedThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, topk_grouped_kernel<EPL>, logits, bias, T, P, ids, w, status);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, m, a, P);
+}
+
+GroupRule make_rule(const float* bias, int E, int k, int scoring, int renorm, float scaling, int n_group,
+                    int topk_group, int group_top) {
+    const int size = E / n_group;
+    return GroupRule{E, k, scoring, renorm, n_group, topk_group, group_top, bias == nullptr, size,
+                     ((1 << 20) + size - 1) / size, scaling};
 }
 
 }  // namespace
@@ -268,12 +576,40 @@ cudaError_t launch_epl(const float* logits, const float* bias, int T, const Grou
 cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k, int scoring,
                                 int renorm, float scaling, int n_group, int topk_group, int group_top,
                                 int32_t* ids, float* w, int32_t* status, cudaStream_t st) {
-    const GroupRule P{E, k, scoring, renorm, n_group, topk_group, group_top, bias == nullptr, scaling};
-    if (E <= 32) return launch_epl<1>(logits, bias, T, P, ids, w, status, st);
-    if (E <= 64) return launch_epl<2>(logits, bias, T, P, ids, w, status, st);
-    if (E <= 128) return launch_epl<4>(logits, bias, T, P, ids, w, status, st);
-    if (E <= 256) return launch_epl<8>(logits, bias, T, P, ids, w, status, st);
-    return launch_epl<16>(logits, bias, T, P, ids, w, status, st);
+    const GroupRule P = make_rule(bias, E, k, scoring, renorm, scaling, n_group, topk_group, group_top);
+    if (E <= 32) return launch_given<1>(logits, bias, T, P, ids, w, status, st);
+    if (E <= 64) return launch_given<2>(logits, bias, T, P, ids, w, status, st);
+    if (E <= 128) return launch_given<4>(logits, bias, T, P, ids, w, status, st);
+    if (E <= 256) return launch_given<8>(logits, bias, T, P, ids, w, status, st);
+    return launch_given<16>(logits, bias, T, P, ids, w, status, st);
+}
+
+cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias, int T, int E, int H, int k,
+                               int scoring, int renorm, float scaling, int n_group, int topk_group,
+                               int group_top, float* logits, int32_t* ids, float* w, int32_t* status,
+                               cudaStream_t st) {
+    if (E > 256) return cudaErrorNotSupported;
+    const GroupRule P = make_rule(bias, E, k, scoring, renorm, scaling, n_group, topk_group, group_top);
+    FusedArgs a{};
+    a.T = T;
+    a.nk = (H + kFusedK - 1) / kFusedK;
+    a.n = (E + 15) / 16 * 16;
+    a.bias = bias; a.logits = logits; a.ids = ids; a.w = w; a.status = status;
+    // as many CTAs per tile as keep every cluster resident at one CTA per SM (152 SMs hold 7, 15,
+    // 36 and 76 clusters of 16, 8, 4 and 2)
+    const int64_t tiles = ((int64_t)T + 127) / 128;
+    int splits = tiles <= 7 ? 16 : tiles <= 15 ? 8 : tiles <= 36 ? 4 : tiles <= 76 ? 2 : 1;
+    while (splits > a.nk) splits /= 2;
+    const int rows = T < 128 ? T : 128;
+    a.own = (rows + splits - 1) / splits;
+    a.box_x = (rows + 7) / 8 * 8;
+    FusedMaps m{};
+    if (!encode_rows16(&m.x, x, H, T, H, a.box_x, 64) || !encode_rows16(&m.w, wr, H, E, H, a.n, 64))
+        return cudaErrorNotSupported;
+    if (E <= 32) return launch_fused<1>(m, a, P, splits, st);
+    if (E <= 64) return launch_fused<2>(m, a, P, splits, st);
+    if (E <= 128) return launch_fused<4>(m, a, P, splits, st);
+    return launch_fused<8>(m, a, P, splits, st);
 }
 
 }  // namespace moe
