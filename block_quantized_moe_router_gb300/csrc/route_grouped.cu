@@ -9,8 +9,8 @@
 //
 // The order is that of the exact values.  fp32 scores carry an error of some 2^-22 of their
 // size, so two scores closer than a bound on that error could be picked the wrong way round;
-// where a comparison that decides the result falls inside the bound, the token's selection runs
-// again in fp64.  Without a bias every score grows with its logit, and experts are ranked by
+// where a comparison that decides the result falls inside the bound, the values concerned are
+// computed again in fp64.  Without a bias every score grows with its logit, and experts are ranked by
 // the logits themselves, which needs no bound.
 //
 // One warp routes one token (lane l holds experts l, l + 32, ...).  Only the kept groups' experts
@@ -32,114 +32,261 @@ struct GroupRule {
     int E, k, scoring, renorm, n_group, topk_group, group_top, by_logit;
     int size;       // experts per group
     int size_inv;   // ceil(2^20 / size): (r * size_inv) >> 20 == r / size for r < 512
+    int group_lanes, group_shift;  // lanes that share a group, the largest power of two <= 32 / n_group
     float scaling;
+};
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
 };
 
 __device__ __forceinline__ bool is_softmax(int scoring) {
     return scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SOFTMAX_BIAS;
 }
 
-template <typename R>
-__device__ __forceinline__ R score_of(int scoring, R l, R lmax, R zall) {
-    if (l == -INFINITY) return R(0);
-    if (is_softmax(scoring)) return exp(l - lmax) / zall;
-    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrt(l > R(40) ? l : log1p(exp(l)));
-    return R(1) / (R(1) + exp(-l));
+// Score of a finite logit.  fp32: expf within 2 units in the last place, the reciprocal within 1.
+__device__ __forceinline__ float score32(int scoring, float l, float lmax, float inv_z) {
+    if (is_softmax(scoring)) return expf(l - lmax) * inv_z;
+    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(l > 30.f ? l : log1pf(expf(l)));
+    return __fdividef(1.f, 1.f + expf(-l));
 }
-
-// Relative error bound of an fp32 selection score: expf, the additions and the division are
-// within 2^-22 of |s|; a softmax denominator summed over 512 logits adds up to 2^-19.7.
-__device__ __forceinline__ float score_eps(int scoring) { return is_softmax(scoring) ? 0x1p-19f : 0x1p-21f; }
+__device__ __forceinline__ double score64(int scoring, double l, double lmax, double inv_z) {
+    if (is_softmax(scoring)) return exp(l - lmax) * inv_z;
+    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrt(l > 40. ? l : log1p(exp(l)));
+    return 1. / (1. + exp(-l));
+}
 
 __device__ __forceinline__ float from_orderable(uint32_t u) {
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+// fp64 -> uint64 with the same order as the values (0 is below every value)
+__device__ __forceinline__ unsigned long long orderable64(double v) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.);  // -0 and +0 are equal
+    return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+__device__ __forceinline__ double from_orderable64(unsigned long long u) {
+    return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 
 // Shared memory of one routing warp.
 template <int EPL>
 struct alignas(16) RouteScratch {
-    double v64[32 * EPL];  // the fp64 selection's values; the fp32 one's in the same place
-    float logit[32 * EPL];
+    unsigned long long key64[32 * EPL];  // fp64 selection; the fp32 ranking values in the same place
+    float val[32 * EPL];                 // scores (logits where no score was needed, or for fp64)
     float group[64];
     int kept[64];
 };
 
-// The selection in fp64, from the logits in shared memory (-inf: not finite); rare, so kept short.
-// On return lane j < k holds pick j.
+// 1 / softmax denominator over the finite logits in sc->val, in fp64.
 template <int EPL>
-__device__ __noinline__ int select_fp64(const GroupRule& P, const float* bias, float lmax32,
-                                        RouteScratch<EPL>* sc, int lane) {
-    const double lmax = lmax32;
-    double v[EPL], zall = 1;
-    if (is_softmax(P.scoring)) {
-        zall = 0;
-        for (int e = lane; e < P.E; e += 32)
-            if (sc->logit[e] != -INFINITY) zall += exp((double)sc->logit[e] - lmax);
+__device__ __forceinline__ double inv_z64(const GroupRule& P, float lmax, const RouteScratch<EPL>* sc, int lane) {
+    if (!is_softmax(P.scoring)) return 1.;
+    double z = 0.;
+    for (int e = lane; e < P.E; e += 32)
+        if (sc->val[e] != -INFINITY) z += exp((double)sc->val[e] - (double)lmax);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) zall += __shfl_xor_sync(0xffffffffu, zall, o);
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return 1. / z;
+}
+
+// The ranking value of expert e in fp64 as an ordered key, from the logits in sc->val.
+template <int EPL>
+__device__ __forceinline__ unsigned long long key_of(const GroupRule& P, const float* bias, int e, float lmax,
+                                                     double inv_z, const RouteScratch<EPL>* sc) {
+    const float l = sc->val[e], b = bias ? bias[e] : 0.f;
+    if (l == -INFINITY || !isfinite(b)) return orderable64(-INFINITY);
+    if (P.by_logit) return orderable64(l);
+    return orderable64(score64(P.scoring, l, lmax, inv_z) + (double)b);
+}
+
+// Which of the groups in `close` are kept, `room` of them, by their scores in fp64, from the logits in
+// sc->val.
+template <int EPL>
+__device__ __noinline__ unsigned long long kept_fp64(const GroupRule& P, const float* bias, float lmax,
+                                                     unsigned long long close, int room,
+                                                     const RouteScratch<EPL>* sc, int lane) {
+    const double inv_z = inv_z64<EPL>(P, lmax, sc, lane);
+    unsigned long long mine[2] = {0, 0}, kept = 0;
+    for (unsigned long long left = close; left; left &= left - 1) {
+        const int g = __ffsll((long long)left) - 1;
+        unsigned long long m1 = 0, m2 = 0;
+        for (int i = lane; i < P.size; i += 32) {
+            const int e = g * P.size + i;
+            const float l = sc->val[e];
+            const unsigned long long x =
+                P.by_logit && P.group_top == 2 && l != -INFINITY
+                    ? orderable64(score64(P.scoring, l, lmax, inv_z))
+                    : key_of<EPL>(P, bias, e, lmax, inv_z, sc);
+            m2 = max(m2, min(m1, x));
+            m1 = max(m1, x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const unsigned long long b1 = __shfl_xor_sync(0xffffffffu, m1, o);
+            const unsigned long long b2 = __shfl_xor_sync(0xffffffffu, m2, o);
+            m2 = max(min(m1, b1), m1 > b1 ? m2 : b2);
+            m1 = max(m1, b1);
+        }
+        const unsigned long long key =
+            P.group_top == 2 ? orderable64(from_orderable64(m1) + from_orderable64(m2)) : m1;
+        if (lane == (g & 31)) mine[g >> 5] = key;
     }
-    __syncwarp();
+    for (unsigned long long left = close; left; left &= left - 1) {
+        const int g = __ffsll((long long)left) - 1;
+        const unsigned long long x = __shfl_sync(0xffffffffu, g < 32 ? mine[0] : mine[1], g & 31);
+        const bool a0 = ((close >> lane) & 1) && (mine[0] > x || (mine[0] == x && lane < g));
+        const bool a1 = ((close >> (lane + 32)) & 1) && (mine[1] > x || (mine[1] == x && lane + 32 < g));
+        const int rank = __popc(__ballot_sync(0xffffffffu, a0)) + __popc(__ballot_sync(0xffffffffu, a1));
+        if (rank < room) kept |= 1ull << g;
+    }
+    return kept;
+}
+
+// The whole selection in fp64 (more candidates are too close together than a warp's lanes rank), from
+// the logits in sc->val.  On return lane j < k holds pick j.
+template <int EPL>
+__device__ __noinline__ int select_fp64(const GroupRule& P, const float* bias, float lmax, RouteScratch<EPL>* sc,
+                                        int lane) {
+    const double inv_z = inv_z64<EPL>(P, lmax, sc, lane);
+    const bool score_groups = P.by_logit && P.group_top == 2;
+    unsigned long long key[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        v[j] = NAN;  // never picked
+        key[j] = 0;
         if (e >= P.E) continue;
-        const float l = sc->logit[e], b = bias ? bias[e] : 0.f;
-        const double s = score_of<double>(P.scoring, l, lmax, zall);
-        v[j] = P.by_logit ? (double)l : l != -INFINITY && isfinite(b) ? s + (double)b : (double)-INFINITY;
-        sc->v64[e] = P.by_logit && P.group_top == 2 && l != -INFINITY ? s : v[j];
+        key[j] = key_of<EPL>(P, bias, e, lmax, inv_z, sc);
+        const float l = sc->val[e];
+        sc->key64[e] = score_groups && l != -INFINITY ? orderable64(score64(P.scoring, l, lmax, inv_z)) : key[j];
     }
     __syncwarp();
-    if (P.topk_group < P.n_group) {
-        double gs[2];
-        for (int q = 0; q < 2; ++q) {
-            const int g = lane + 32 * q;
-            double m1 = -INFINITY, m2 = -INFINITY;
-            if (g < P.n_group)
-                for (int i = 0; i < P.size; ++i) {
-                    const double x = sc->v64[g * P.size + i];
-                    m2 = x > m1 ? m1 : (x > m2 ? x : m2);
-                    m1 = x > m1 ? x : m1;
-                }
-            gs[q] = P.group_top == 2 ? m1 + m2 : m1;
-        }
-        unsigned long long kept = 0;
-        for (int g = 0; g < P.n_group; ++g) {
-            const double mine = __shfl_sync(0xffffffffu, g < 32 ? gs[0] : gs[1], g & 31);
-            const bool a0 = lane < P.n_group && (gs[0] > mine || (gs[0] == mine && lane < g));
-            const bool a1 = lane + 32 < P.n_group && (gs[1] > mine || (gs[1] == mine && lane + 32 < g));
-            const int rank = __popc(__ballot_sync(0xffffffffu, a0)) + __popc(__ballot_sync(0xffffffffu, a1));
-            if (rank < P.topk_group) kept |= 1ull << g;
-        }
+    unsigned long long gs[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < P.E && !((kept >> ((lane + 32 * j) / P.size)) & 1)) v[j] = NAN;
+    for (int q = 0; q < 2; ++q) {
+        const int g = lane + 32 * q;
+        if (g >= P.n_group) continue;
+        unsigned long long m1 = 0, m2 = 0;
+        for (int i = 0; i < P.size; ++i) {
+            const unsigned long long x = sc->key64[g * P.size + i];
+            m2 = max(m2, min(m1, x));
+            m1 = max(m1, x);
+        }
+        gs[q] = P.group_top == 2 ? orderable64(from_orderable64(m1) + from_orderable64(m2)) : m1;
     }
+    unsigned long long kept = 0;
+    for (int g = 0; g < P.n_group; ++g) {
+        const unsigned long long mine = __shfl_sync(0xffffffffu, g < 32 ? gs[0] : gs[1], g & 31);
+        const bool a0 = lane < P.n_group && (gs[0] > mine || (gs[0] == mine && lane < g));
+        const bool a1 = lane + 32 < P.n_group && (gs[1] > mine || (gs[1] == mine && lane + 32 < g));
+        const int rank = __popc(__ballot_sync(0xffffffffu, a0)) + __popc(__ballot_sync(0xffffffffu, a1));
+        if (rank < P.topk_group) kept |= 1ull << g;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        if (!((kept >> ((((lane + 32 * j) * P.size_inv) >> 20) & 63)) & 1)) key[j] = 0;
     int my_e = 0;
     for (int r = 0; r < P.k; ++r) {
-        double best = -INFINITY;
-        int be = 0x7fffffff;
+        unsigned long long m = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) m = max(m, key[j]);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(m >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
+        const unsigned long long top = ((unsigned long long)hi << 32) | lo;
+        uint32_t e = 0x7fffffffu;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (v[j] > best || (v[j] == best && lane + 32 * j < be)) {
-                best = v[j];
-                be = lane + 32 * j;
-            }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-            const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-            if (ob > best || (ob == best && oe < be)) {
-                best = ob;
-                be = oe;
-            }
-        }
+            if (key[j] == top) e = min(e, (uint32_t)(lane + 32 * j));
+        e = __reduce_min_sync(0xffffffffu, e);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j == be) v[j] = NAN;
-        if (lane == r) my_e = be;
+            if (lane + 32 * j == (int)e) key[j] = 0;
+        if (lane == r) my_e = (int)e;
     }
     return my_e;
+}
+
+// The K rounds over `count` candidates, N per lane: candidate r is expert r, or the r-th of the kept
+// groups.  Returns the pick of lane j < k, or sets `full` where the fp64 selection of all is needed.
+// tol(v): how far a value near v may be from the exact one (0: exact).
+template <int EPL, int N>
+__device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias, RouteScratch<EPL>* sc, int lane,
+                                           bool grouped, float tol_rel, float tol_abs, float lmax,
+                                           const float (&lg)[EPL], bool& full, bool& val_is_logit) {
+    const float* rank_val = reinterpret_cast<const float*>(sc->key64);
+    const int count = grouped ? P.topk_group * P.size : P.E;
+    uint32_t key[N];
+    int ee[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int r = lane + 32 * j;
+        key[j] = 0;  // below every value
+        ee[j] = 0x7fffffff;
+        if (r < count) {
+            const int q = (r * P.size_inv) >> 20;
+            ee[j] = grouped ? sc->kept[q] * P.size + r - q * P.size : r;
+            key[j] = orderable(rank_val[ee[j]]);
+        }
+    }
+    int my_e = 0, r = 0, want = P.k;
+    uint32_t my_key = 0;
+    for (bool again = false;; again = true) {
+        for (; r < want; ++r) {
+            uint32_t m = key[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) m = max(m, key[j]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+            uint32_t e = 0x7fffffffu;
+#pragma unroll
+            for (int j = 0; j < N; ++j) e = key[j] == top ? min(e, (uint32_t)ee[j]) : e;
+            e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+            for (int j = 0; j < N; ++j) key[j] = ee[j] == (int)e ? 0u : key[j];
+            if (lane == r) {
+                my_e = (int)e;
+                my_key = top;
+            }
+        }
+        if (P.by_logit) return my_e;
+        // neighbours too close, or one left behind too close to the last pick that counts?
+        const float v = from_orderable(my_key);
+        const float tol = 2.f * (tol_rel * fabsf(v) + tol_abs);
+        const float before = __shfl_up_sync(0xffffffffu, v, 1);
+        const bool near = lane > 0 && lane < P.k && v > -INFINITY && before - v <= tol;
+        const float bar = __shfl_sync(0xffffffffu, v - tol, P.k - 1);
+        bool left = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) left = left || (bar > -INFINITY && key[j] >= orderable(bar));
+        left = __any_sync(0xffffffffu, left);
+        if (!again) {
+            if (!left && !__any_sync(0xffffffffu, near)) return my_e;
+            // a few candidates more, and the order among all these in fp64
+            val_is_logit = true;
+            want = min(min(P.k + 4, 32), count);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (lane + 32 * j < P.E) sc->val[lane + 32 * j] = lg[j];
+            __syncwarp();
+        } else {
+            if (left) {  // more than those are that close
+                full = true;
+                return 0;
+            }
+            const double inv_z = inv_z64<EPL>(P, lmax, sc, lane);
+            const unsigned long long mine = lane < want ? key_of<EPL>(P, bias, my_e, lmax, inv_z, sc) : 0;
+            int rank = 0;
+            for (int i = 0; i < want; ++i) {
+                const unsigned long long o = __shfl_sync(0xffffffffu, mine, i);
+                const int oe = __shfl_sync(0xffffffffu, my_e, i);
+                rank += o > mine || (o == mine && oe < my_e) ? 1 : 0;
+            }
+            __syncwarp();
+            if (lane < want) sc->kept[rank] = my_e;
+            __syncwarp();
+            return lane < P.k ? sc->kept[lane] : 0;
+        }
+    }
 }
 
 // One warp routes one token: raw[j] is the logit of expert lane + 32 j (anything beyond E).
@@ -148,182 +295,192 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
                                             RouteScratch<EPL>* sc, int lane, int32_t* ids, float* wout,
                                             int32_t* status) {
     const bool softmax = is_softmax(P.scoring), grouped = P.topk_group < P.n_group;
-    float lg[EPL], v[EPL], lmax = -INFINITY;
+    float lg[EPL], lmax = -INFINITY;
     bool nonfinite = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 32 * j;
-        lg[j] = -INFINITY;
-        if (e < P.E) {
-            if (isfinite(raw[j])) lg[j] = raw[j];
-            else nonfinite = true;
-            sc->logit[e] = lg[j];
-        }
+        const bool in = lane + 32 * j < P.E, fin = fabsf(raw[j]) < INFINITY;
+        nonfinite = nonfinite || (in && !fin);
+        lg[j] = in && fin ? raw[j] : -INFINITY;
         lmax = fmaxf(lmax, lg[j]);
     }
     if (__any_sync(0xffffffffu, nonfinite) && lane == 0) status_or(status, MOE_DEV_NONFINITE);
-    lmax = from_orderable(__reduce_max_sync(0xffffffffu, orderable(lmax)));
 
     const bool need_score = !P.by_logit || (grouped && P.group_top == 2);
-    float zall = 1.f;  // softmax denominator: for the scores, or for weights that are not renormalised
-    if (softmax && (need_score || !P.renorm)) {
-        zall = 0.f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) zall += lg[j] == -INFINITY ? 0.f : expf(lg[j] - lmax);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) zall += __shfl_xor_sync(0xffffffffu, zall, o);
-    }
-    float* sv = reinterpret_cast<float*>(sc->v64);
     const bool score_groups = P.by_logit && P.group_top == 2;  // groups add scores, experts rank by logit
+    float s[EPL], inv_z = 1.f, smax = 0.f;
+    if (need_score || softmax) lmax = from_orderable(__reduce_max_sync(0xffffffffu, orderable(lmax)));
+    if (softmax && (need_score || !P.renorm)) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            s[j] = lg[j] == -INFINITY ? 0.f : expf(lg[j] - lmax);
+            z += s[j];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        inv_z = 1.f / z;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) s[j] *= inv_z;
+        smax = inv_z;
+    } else if (need_score) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) s[j] = score32(P.scoring, lg[j] == -INFINITY ? 0.f : lg[j], lmax, inv_z);
+        smax = score32(P.scoring, lmax == -INFINITY ? 0.f : lmax, lmax, inv_z);
+    }
+    float* rank_val = reinterpret_cast<float*>(sc->key64);
+    float bmax = 0.f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 32 * j;
-        v[j] = -INFINITY;
         if (e < P.E) {
-            float s = -INFINITY;
-            if (lg[j] != -INFINITY) {
-                if (need_score) s = score_of<float>(P.scoring, lg[j], lmax, zall);
-                if (P.by_logit) {
-                    v[j] = lg[j] + 0.f;  // -0 and +0 are equal
-                } else {
-                    const float b = bias ? __ldg(bias + e) : 0.f;
-                    v[j] = isfinite(b) ? s + b : -INFINITY;
-                }
+            float v = lg[j] + 0.f;  // -0 and +0 are equal
+            if (!P.by_logit) {
+                const float b = bias ? __ldg(bias + e) : 0.f;
+                const bool ok = fabsf(b) < INFINITY;
+                v = ok && lg[j] != -INFINITY ? s[j] + b : -INFINITY;
+                bmax = fmaxf(bmax, ok ? fabsf(b) : 0.f);
             }
-            sv[e] = score_groups ? s : v[j];
+            rank_val[e] = score_groups && grouped && lg[j] != -INFINITY ? s[j] : v;
+            sc->val[e] = need_score ? (lg[j] == -INFINITY ? 0.f : s[j]) : lg[j];
         }
     }
-    const float smax = need_score ? score_of<float>(P.scoring, lmax, lmax, zall) : 0.f;
-    const float eps = score_eps(P.scoring);
-    bool close = false;  // a deciding comparison fell inside the error bound
+    // Error bounds of a ranking value v: exp, sums and the reciprocal are within 2^-21 of the largest
+    // score and of |v|; an error of the softmax denominator (2^-19.7 for 512 logits) scales all scores
+    // alike, so between close values it counts only with what their biases differ by.
+    const float tol_rel = 0x1p-21f;
+    float tol_abs = 2.f * tol_rel * smax;
+    if (softmax && !P.by_logit)
+        tol_abs += 0x1p-19f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
 
-    uint32_t key[EPL];
-    int ee[EPL];
+    bool full = false, val_is_logit = !need_score;  // val_is_logit: sc->val holds logits
+    __syncwarp();
     if (grouped) {
-        __syncwarp();
         // 32 / n_group lanes (a power of two) share a group; above 32 groups a lane has two
-        int per = 1;
-        while (per * 2 * P.n_group <= 32) per *= 2;
+        const int per = P.group_lanes;
         const int slots = P.n_group > 32 ? 2 : 1;
         float gs[2] = {-INFINITY, -INFINITY}, tol[2] = {};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             if (q >= slots) break;
-            const int g = lane / per + 32 * q;
+            const int g = (lane >> P.group_shift) + 32 * q;
             float m1 = -INFINITY, m2 = -INFINITY;
-            if (g < P.n_group)
-                for (int i = lane % per; i < P.size; i += per) {
-                    const float x = sv[g * P.size + i];
+            if (g < P.n_group) {
+                const float* src = rank_val + g * P.size;
+                for (int i = lane & (per - 1); i < P.size; i += per) {
+                    const float x = src[i];
                     m2 = fmaxf(m2, fminf(m1, x));
                     m1 = fmaxf(m1, x);
                 }
-            for (int o = per / 2; o; o >>= 1) {
+            }
+            for (int o = per >> 1; o; o >>= 1) {
                 const float b1 = __shfl_xor_sync(0xffffffffu, m1, o);
                 const float b2 = __shfl_xor_sync(0xffffffffu, m2, o);
                 m2 = fmaxf(fminf(m1, b1), m1 > b1 ? m2 : b2);
                 m1 = fmaxf(m1, b1);
             }
             gs[q] = P.group_top == 2 ? m1 + m2 : m1;
-            if (need_score) tol[q] = eps * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f) + 4.f * smax);
-            if (lane % per == 0 && g < P.n_group) sc->group[g] = gs[q];
+            if (need_score) tol[q] = tol_rel * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f)) + 2.f * tol_abs;
+            if ((lane & (per - 1)) == 0 && g < P.n_group) sc->group[g] = gs[q];
         }
         __syncwarp();
-        unsigned before = 0;  // kept groups in earlier slots
+        unsigned long long kept = 0;
+        bool in[2] = {false, false}, keep[2] = {false, false};
         float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             if (q >= slots) break;
-            const int g = lane / per + 32 * q;
+            const int g = (lane >> P.group_shift) + 32 * q;
             int rank = 0;
             for (int i = 0; i < P.n_group; ++i) {
                 const float o = sc->group[i];
                 rank += o > gs[q] || (o == gs[q] && i < g) ? 1 : 0;
             }
-            const bool mine = lane % per == 0 && g < P.n_group, keep = mine && rank < P.topk_group;
-            const unsigned b = __ballot_sync(0xffffffffu, keep);
-            if (keep) sc->kept[before + __popc(b & ((1u << lane) - 1u))] = g;
-            before += __popc(b);
-            if (keep) lo = fminf(lo, gs[q] - tol[q]);
-            if (mine && !keep) hi = fmaxf(hi, gs[q] + tol[q]);
+            in[q] = (lane & (per - 1)) == 0 && g < P.n_group;
+            keep[q] = in[q] && rank < P.topk_group;
+            if (keep[q]) lo = fminf(lo, gs[q] - tol[q]);
+            else if (in[q]) hi = fmaxf(hi, gs[q] + tol[q]);
         }
         if (need_score) {
             lo = from_orderable(__reduce_min_sync(0xffffffffu, orderable(lo)));
             hi = from_orderable(__reduce_max_sync(0xffffffffu, orderable(hi)));
-            close = hi > -INFINITY && lo > -INFINITY && hi >= lo;
         }
-        __syncwarp();
-        if (score_groups) {
+        if (need_score && hi > -INFINITY && lo > -INFINITY && hi >= lo) {
+            // the border runs between groups too close to tell: those again in fp64
+            unsigned long long sure = 0, close = 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const bool c = in[q] && (keep[q] ? gs[q] - tol[q] <= hi : gs[q] + tol[q] >= lo);
+                const int g = (lane >> P.group_shift) + 32 * q;
+                const unsigned long long bit = 1ull << (g & 63);
+                close |= c ? bit : 0ull;
+                sure |= keep[q] && !c ? bit : 0ull;
+            }
+            close = __reduce_or_sync(0xffffffffu, (unsigned)close) |
+                    (unsigned long long)__reduce_or_sync(0xffffffffu, (unsigned)(close >> 32)) << 32;
+            sure = __reduce_or_sync(0xffffffffu, (unsigned)sure) |
+                   (unsigned long long)__reduce_or_sync(0xffffffffu, (unsigned)(sure >> 32)) << 32;
+            val_is_logit = true;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < P.E) sv[lane + 32 * j] = v[j];
+                if (lane + 32 * j < P.E) sc->val[lane + 32 * j] = lg[j];
             __syncwarp();
-        }
-        const int count = P.topk_group * P.size;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const int r = lane + 32 * j;
-            key[j] = 0;
-            ee[j] = 0x7fffffff;
-            if (r < count) {
-                const int q = (r * P.size_inv) >> 20;
-                ee[j] = sc->kept[q] * P.size + r - q * P.size;
-                key[j] = orderable(sv[ee[j]]);
+            kept = sure | kept_fp64<EPL>(P, bias, lmax, close, P.topk_group - __popcll(sure), sc, lane);
+            if (lane < P.n_group && ((kept >> lane) & 1)) sc->kept[__popcll(kept & ((1ull << lane) - 1))] = lane;
+            if (lane + 32 < P.n_group && ((kept >> (lane + 32)) & 1))
+                sc->kept[__popcll(kept & ((1ull << (lane + 32)) - 1))] = lane + 32;
+        } else {
+            const unsigned b0 = __ballot_sync(0xffffffffu, keep[0]), below = (1u << lane) - 1u;
+            if (keep[0]) sc->kept[__popc(b0 & below)] = lane >> P.group_shift;
+            if (slots == 2) {
+                const unsigned b1 = __ballot_sync(0xffffffffu, keep[1]);
+                if (keep[1]) sc->kept[__popc(b0) + __popc(b1 & below)] = lane + 32;
             }
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            ee[j] = lane + 32 * j;
-            key[j] = ee[j] < P.E ? orderable(v[j]) : 0u;
-        }
-    }
-    const int live = grouped ? (P.topk_group * P.size + 31) / 32 : EPL;  // values per lane
-    int my_e = 0;
-    float prev = INFINITY;
-    for (int r = 0; r < P.k; ++r) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (j < live) m = max(m, key[j]);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, m);
-        uint32_t e = 0x7fffffffu;
-        if (m == top) {
+        if (score_groups) {
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (j < live && key[j] == top) e = min(e, (uint32_t)ee[j]);
+                if (lane + 32 * j < P.E) rank_val[lane + 32 * j] = lg[j] + 0.f;
         }
-        e = __reduce_min_sync(0xffffffffu, e);
+        __syncwarp();
+    }
+    int my_e = 0;
+    if (!full) {
+        const int live = grouped ? (P.topk_group * P.size + 31) >> 5 : (P.E + 31) >> 5;  // candidates per lane
+        const auto run = [&](auto n) {
+            return pick_rounds<EPL, decltype(n)::value>(P, bias, sc, lane, grouped, tol_rel, tol_abs, lmax, lg, full,
+                                                          val_is_logit);
+        };
+        if (EPL == 1 || live == 1) my_e = run(Int<1>{});
+        else if (EPL == 2 || live == 2) my_e = run(Int<(EPL < 2 ? EPL : 2)>{});
+        else if (EPL == 4 || live <= 4) my_e = run(Int<(EPL < 4 ? EPL : 4)>{});
+        else if (EPL == 8 || live <= 8) my_e = run(Int<(EPL < 8 ? EPL : 8)>{});
+        else my_e = run(Int<EPL>{});
+    }
+    if (full) {
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (j < live && ee[j] == (int)e) key[j] = 0;
-        if (lane == r) my_e = (int)e;
-        if (!P.by_logit) {
-            const float best = from_orderable(top);
-            if (best > -INFINITY) close = close || prev - best <= 2.f * eps * (fabsf(best) + 2.f * smax);
-            prev = best;
-        }
+            if (lane + 32 * j < P.E) sc->val[lane + 32 * j] = lg[j];
+        __syncwarp();
+        val_is_logit = true;
+        my_e = select_fp64<EPL>(P, bias, lmax, sc, lane);
     }
-    if (!P.by_logit && prev > -INFINITY) {  // the best of those left behind
-        const uint32_t bar = orderable(prev - 2.f * eps * (fabsf(prev) + 2.f * smax));
-        bool amb = false;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) amb = amb || (j < live && key[j] >= bar);
-        close = __any_sync(0xffffffffu, close || amb);
+    float w = 0.f;
+    if (lane < P.k) {
+        w = sc->val[my_e];
+        if (val_is_logit) w = w == -INFINITY ? 0.f : score32(P.scoring, w, lmax, inv_z);
     }
-    __syncwarp();
-    if (close) my_e = select_fp64<EPL>(P, bias, lmax, sc, lane);
-
-    float s = 0.f;
-    if (lane < P.k) s = score_of<float>(P.scoring, sc->logit[my_e], lmax, zall);
     if (P.renorm) {
-        float den = s;
+        float den = w;
 #pragma unroll
         for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-        s = den > 0.f ? s / den : 0.f;
+        w = den > 0.f ? w / den : 0.f;
     }
     if (lane < P.k) {
         ids[lane] = my_e;
-        wout[lane] = s * P.scaling;
+        wout[lane] = w * P.scaling;
     }
     __syncwarp();  // the scratch is the next token's
 }
@@ -567,8 +724,10 @@ cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, in
 GroupRule make_rule(const float* bias, int E, int k, int scoring, int renorm, float scaling, int n_group,
                     int topk_group, int group_top) {
     const int size = E / n_group;
+    int shift = 0;
+    while ((2 << shift) * n_group <= 32) ++shift;
     return GroupRule{E, k, scoring, renorm, n_group, topk_group, group_top, bias == nullptr, size,
-                     ((1 << 20) + size - 1) / size, scaling};
+                     ((1 << 20) + size - 1) / size, 1 << shift, shift, scaling};
 }
 
 }  // namespace
