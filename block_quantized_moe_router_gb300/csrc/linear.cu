@@ -371,13 +371,15 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 if (n < a.N && (i & 1) * 64 < per_tile)
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
-    } else if (warp >= 2) {
+    }
+    {  // the two warps of a lane quarter take alternate 16 columns
+        __syncwarp();
         if (!mbar_wait_bounded(&acc_full, 0, kLinWaitLimit)) give_up();
         tc_fence_after();
         const int q = warp & 3;
         const uint32_t mine = smem_u32(landing + ((int)rank * 128 + 32 * q + lane) * pitch);
-        int owner = 0, at = 0;  // of the next four columns
-        for (int c = 0; c < ncols; c += 16) {
+        for (int c = 16 * (warp >> 2); c < ncols; c += 32) {
+            int owner = c / own, at = c - owner * own;  // of the next four columns
             uint32_t v[16];
             tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
             tmem_ld_wait();

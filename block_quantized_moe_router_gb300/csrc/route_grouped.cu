@@ -74,7 +74,7 @@ template <int EPL>
 struct alignas(16) RouteScratch {
     unsigned long long key64[32 * EPL];  // fp64 selection; the fp32 ranking values in the same place
     float val[32 * EPL];                 // scores (logits where no score was needed, or for fp64)
-    float group[64];
+    float group[68];
     int kept[64];
 };
 
@@ -224,11 +224,12 @@ __device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias
         ee[j] = 0x7fffffff;
         if (r < count) {
             const int q = (r * P.size_inv) >> 20;
-            ee[j] = grouped ? sc->kept[q] * P.size + r - q * P.size : r;
-            key[j] = orderable(rank_val[ee[j]]);
+            const int g = grouped ? sc->kept[q] : q;
+            ee[j] = g * P.size + r - q * P.size;
+            key[j] = orderable(rank_val[ee[j] + g]);  // a group takes size + 1 places: no bank conflicts
         }
     }
-    int my_e = 0, r = 0, want = P.k;
+    int r = 0, want = P.k, my_e = 0;
     uint32_t my_key = 0;
     for (bool again = false;; again = true) {
         for (; r < want; ++r) {
@@ -236,16 +237,14 @@ __device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias
 #pragma unroll
             for (int j = 1; j < N; ++j) m = max(m, key[j]);
             const uint32_t top = __reduce_max_sync(0xffffffffu, m);
-            uint32_t e = 0x7fffffffu;
+            uint32_t e = 0x7fffffffu;  // the lowest expert that reaches the top
 #pragma unroll
-            for (int j = 0; j < N; ++j) e = key[j] == top ? min(e, (uint32_t)ee[j]) : e;
+            for (int j = N - 1; j >= 0; --j) e = key[j] == top ? (uint32_t)ee[j] : e;
             e = __reduce_min_sync(0xffffffffu, e);
 #pragma unroll
             for (int j = 0; j < N; ++j) key[j] = ee[j] == (int)e ? 0u : key[j];
-            if (lane == r) {
-                my_e = (int)e;
-                my_key = top;
-            }
+            my_e = lane == r ? (int)e : my_e;
+            my_key = lane == r ? top : my_key;
         }
         if (P.by_logit) return my_e;
         // neighbours too close, or one left behind too close to the last pick that counts?
@@ -289,60 +288,71 @@ __device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias
     }
 }
 
-// One warp routes one token: raw[j] is the logit of expert lane + 32 j (anything beyond E).
+// One warp routes one token: raw[j] and bv[j] are the logit and the bias of expert lane + 32 j (anything
+// beyond E).  The branches on the kind of scores stand outside the loops over j: a warp on its own
+// spends some twenty cycles on each.
 template <int EPL>
-__device__ __forceinline__ void route_token(const GroupRule& P, const float (&raw)[EPL], const float* bias,
-                                            RouteScratch<EPL>* sc, int lane, int32_t* ids, float* wout,
-                                            int32_t* status) {
+__device__ __forceinline__ void route_token(const GroupRule& P, const float (&raw)[EPL], const float (&bv)[EPL],
+                                            const float* bias, RouteScratch<EPL>* sc, int lane, int32_t* ids,
+                                            float* wout, int32_t* status) {
     const bool softmax = is_softmax(P.scoring), grouped = P.topk_group < P.n_group;
     float lg[EPL], lmax = -INFINITY;
     bool nonfinite = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const bool in = lane + 32 * j < P.E, fin = fabsf(raw[j]) < INFINITY;
-        nonfinite = nonfinite || (in && !fin);
-        lg[j] = in && fin ? raw[j] : -INFINITY;
+        nonfinite |= in & !fin;
+        lg[j] = in & fin ? raw[j] : -INFINITY;
         lmax = fmaxf(lmax, lg[j]);
     }
     if (__any_sync(0xffffffffu, nonfinite) && lane == 0) status_or(status, MOE_DEV_NONFINITE);
 
     const bool need_score = !P.by_logit || (grouped && P.group_top == 2);
-    const bool score_groups = P.by_logit && P.group_top == 2;  // groups add scores, experts rank by logit
+    const bool score_groups = grouped && P.by_logit && P.group_top == 2;  // groups add scores, experts rank by logit
     float s[EPL], inv_z = 1.f, smax = 0.f;
     if (need_score || softmax) lmax = from_orderable(__reduce_max_sync(0xffffffffu, orderable(lmax)));
+    const float top_logit = lmax == -INFINITY ? 0.f : lmax;
     if (softmax && (need_score || !P.renorm)) {
         float z = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            s[j] = lg[j] == -INFINITY ? 0.f : expf(lg[j] - lmax);
+            s[j] = expf(lg[j] - top_logit);  // 0 for -inf
             z += s[j];
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        inv_z = 1.f / z;
+        inv_z = z > 0.f ? __fdividef(1.f, z) : 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) s[j] *= inv_z;
         smax = inv_z;
+    } else if (need_score && P.scoring == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) s[j] = __fdividef(1.f, 1.f + expf(-lg[j]));
+        smax = __fdividef(1.f, 1.f + expf(-top_logit));
     } else if (need_score) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] = score32(P.scoring, lg[j] == -INFINITY ? 0.f : lg[j], lmax, inv_z);
-        smax = score32(P.scoring, lmax == -INFINITY ? 0.f : lmax, lmax, inv_z);
+        for (int j = 0; j < EPL; ++j) s[j] = score32(P.scoring, lg[j], lmax, inv_z);
+        smax = score32(P.scoring, top_logit, lmax, inv_z);
     }
+    // places beyond E are written too: the arrays have room, and nothing reads them
     float* rank_val = reinterpret_cast<float*>(sc->key64);
     float bmax = 0.f;
+    if (P.by_logit) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 32 * j;
-        if (e < P.E) {
-            float v = lg[j] + 0.f;  // -0 and +0 are equal
-            if (!P.by_logit) {
-                const float b = bias ? __ldg(bias + e) : 0.f;
-                const bool ok = fabsf(b) < INFINITY;
-                v = ok && lg[j] != -INFINITY ? s[j] + b : -INFINITY;
-                bmax = fmaxf(bmax, ok ? fabsf(b) : 0.f);
-            }
-            rank_val[e] = score_groups && grouped && lg[j] != -INFINITY ? s[j] : v;
-            sc->val[e] = need_score ? (lg[j] == -INFINITY ? 0.f : s[j]) : lg[j];
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane + 32 * j;
+            const float v = lg[j] + 0.f;  // -0 and +0 are equal
+            rank_val[e + ((e * P.size_inv) >> 20)] = score_groups && lg[j] != -INFINITY ? s[j] : v;
+            sc->val[e] = need_score ? s[j] : lg[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane + 32 * j;
+            const bool ok = fabsf(bv[j]) < INFINITY;
+            rank_val[e + ((e * P.size_inv) >> 20)] = ok & (lg[j] != -INFINITY) ? s[j] + bv[j] : -INFINITY;
+            sc->val[e] = s[j];
+            bmax = fmaxf(bmax, ok ? fabsf(bv[j]) : 0.f);
         }
     }
     // Error bounds of a ranking value v: exp, sums and the reciprocal are within 2^-21 of the largest
@@ -358,20 +368,18 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
     if (grouped) {
         // 32 / n_group lanes (a power of two) share a group; above 32 groups a lane has two
         const int per = P.group_lanes;
-        const int slots = P.n_group > 32 ? 2 : 1;
+        const bool two = P.n_group > 32;
         float gs[2] = {-INFINITY, -INFINITY}, tol[2] = {};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (q >= slots) break;
+        const auto scan = [&](int q) {
             const int g = (lane >> P.group_shift) + 32 * q;
+            const bool in = g < P.n_group;
             float m1 = -INFINITY, m2 = -INFINITY;
-            if (g < P.n_group) {
-                const float* src = rank_val + g * P.size;
-                for (int i = lane & (per - 1); i < P.size; i += per) {
-                    const float x = src[i];
-                    m2 = fmaxf(m2, fminf(m1, x));
-                    m1 = fmaxf(m1, x);
-                }
+            const float* src = rank_val + (in ? g : 0) * (P.size + 1);
+#pragma unroll 4
+            for (int i = lane & (per - 1); i < P.size; i += per) {
+                const float x = src[i];
+                m2 = fmaxf(m2, fminf(m1, x));
+                m1 = fmaxf(m1, x);
             }
             for (int o = per >> 1; o; o >>= 1) {
                 const float b1 = __shfl_xor_sync(0xffffffffu, m1, o);
@@ -380,27 +388,34 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
                 m1 = fmaxf(m1, b1);
             }
             gs[q] = P.group_top == 2 ? m1 + m2 : m1;
-            if (need_score) tol[q] = tol_rel * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f)) + 2.f * tol_abs;
-            if ((lane & (per - 1)) == 0 && g < P.n_group) sc->group[g] = gs[q];
-        }
+            tol[q] = tol_rel * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f)) + 2.f * tol_abs;
+            if (in) sc->group[g] = gs[q];  // the lanes of a group write the same
+        };
+        scan(0);
+        if (two) scan(1);
+        if (lane < 3) sc->group[P.n_group + lane] = NAN;  // counts for nothing
         __syncwarp();
         unsigned long long kept = 0;
         bool in[2] = {false, false}, keep[2] = {false, false};
         float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (q >= slots) break;
+        const auto place = [&](int q) {
             const int g = (lane >> P.group_shift) + 32 * q;
-            int rank = 0;
-            for (int i = 0; i < P.n_group; ++i) {
-                const float o = sc->group[i];
-                rank += o > gs[q] || (o == gs[q] && i < g) ? 1 : 0;
+            int rank = 0;  // the lanes of a group share the comparisons
+            for (int i = 4 * (lane & (per - 1)); i < P.n_group; i += 4 * per) {
+                const float4 o = *reinterpret_cast<const float4*>(sc->group + i);
+                rank += (int)((o.x > gs[q]) | ((o.x == gs[q]) & (i < g)));
+                rank += (int)((o.y > gs[q]) | ((o.y == gs[q]) & (i + 1 < g)));
+                rank += (int)((o.z > gs[q]) | ((o.z == gs[q]) & (i + 2 < g)));
+                rank += (int)((o.w > gs[q]) | ((o.w == gs[q]) & (i + 3 < g)));
             }
-            in[q] = (lane & (per - 1)) == 0 && g < P.n_group;
-            keep[q] = in[q] && rank < P.topk_group;
-            if (keep[q]) lo = fminf(lo, gs[q] - tol[q]);
-            else if (in[q]) hi = fmaxf(hi, gs[q] + tol[q]);
-        }
+            for (int o = per >> 1; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+            in[q] = ((lane & (per - 1)) == 0) & (g < P.n_group);
+            keep[q] = in[q] & (rank < P.topk_group);
+            lo = keep[q] ? fminf(lo, gs[q] - tol[q]) : lo;
+            hi = in[q] & !keep[q] ? fmaxf(hi, gs[q] + tol[q]) : hi;
+        };
+        place(0);
+        if (two) place(1);
         if (need_score) {
             lo = from_orderable(__reduce_min_sync(0xffffffffu, orderable(lo)));
             hi = from_orderable(__reduce_max_sync(0xffffffffu, orderable(hi)));
@@ -432,7 +447,7 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
         } else {
             const unsigned b0 = __ballot_sync(0xffffffffu, keep[0]), below = (1u << lane) - 1u;
             if (keep[0]) sc->kept[__popc(b0 & below)] = lane >> P.group_shift;
-            if (slots == 2) {
+            if (two) {
                 const unsigned b1 = __ballot_sync(0xffffffffu, keep[1]);
                 if (keep[1]) sc->kept[__popc(b0) + __popc(b1 & below)] = lane + 32;
             }
@@ -441,7 +456,8 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < P.E) rank_val[lane + 32 * j] = lg[j] + 0.f;
+                if (lane + 32 * j < P.E)
+                    rank_val[lane + 32 * j + (((lane + 32 * j) * P.size_inv) >> 20)] = lg[j] + 0.f;
         }
         __syncwarp();
     }
@@ -475,8 +491,9 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
     if (P.renorm) {
         float den = w;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-        w = den > 0.f ? w / den : 0.f;
+        for (int o = 16; o; o >>= 1)
+            if (o < P.k) den += __shfl_xor_sync(0xffffffffu, den, o);  // lanes from k on hold 0
+        w = den > 0.f ? __fdividef(w, den) : 0.f;
     }
     if (lane < P.k) {
         ids[lane] = my_e;
@@ -493,7 +510,8 @@ constexpr int given_warps() { return EPL == 16 ? 4 : 8; }
 
 template <int EPL>
 __global__ void __launch_bounds__(given_warps<EPL>() * 32)
-topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, GroupRule P,
+topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T,
+                    const __grid_constant__ GroupRule P,
                     int32_t* __restrict__ ids, float* __restrict__ wout, int32_t* __restrict__ status) {
     __shared__ RouteScratch<EPL> scratch[given_warps<EPL>()];
     pdl_wait();  // logits come from the router kernel
@@ -505,7 +523,10 @@ topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ 
     float raw[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) raw[j] = lane + 32 * j < P.E ? __ldg(row + lane + 32 * j) : 0.f;
-    route_token<EPL>(P, raw, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
+    float bv[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bv[j] = bias && lane + 32 * j < P.E ? __ldg(bias + lane + 32 * j) : 0.f;
+    route_token<EPL>(P, raw, bv, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
 }
 
 template <int EPL>
@@ -551,7 +572,8 @@ struct FusedArgs {
 
 template <int EPL>
 __global__ void __launch_bounds__(kFusedThreads, 1)
-route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant__ FusedArgs a, const GroupRule P) {
+route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant__ FusedArgs a,
+                   const __grid_constant__ GroupRule P) {
     using namespace tc;
     extern __shared__ uint8_t rf_smem[];
     __shared__ uint64_t full[kFusedStagesMax], empty[kFusedStagesMax], acc_full;
@@ -635,14 +657,14 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         __syncthreads();
         cluster_sync();
     }
-    if (warp >= 2 && warp < 6) {  // warp's lane quarter: tokens 32 q + lane
+    {  // a warp's lane quarter: tokens 32 q + lane; the four warps of a quarter share the experts
         if (!mbar_wait_bounded(&acc_full, 0, kFusedWaitLimit)) give_up();
         tc_fence_after();
         const int q = warp & 3, row = 32 * q + lane;
         if (32 * q < rows) {
             const int owner = min(row / a.own, splits - 1), at = row - owner * a.own;
             const uint32_t dst = map_rank(smem_u32(landing + ((int64_t)rank * a.own + at) * pitch), owner);
-            for (int c = 0; c < a.n; c += 16) {
+            for (int c = 16 * (warp >> 2); c < a.n; c += 16 * (kFusedThreads / 128)) {
                 uint32_t v[16];
                 tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
                 tmem_ld_wait();
@@ -655,6 +677,9 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         }
         tc_fence_before();
     }
+    float bv[EPL];  // on its way while the parts land
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bv[j] = a.bias && lane + 32 * j < P.E ? __ldg(a.bias + lane + 32 * j) : 0.f;
     __syncthreads();
     cluster_sync();  // every part has landed
     if (warp == 1) {
@@ -668,6 +693,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         float raw[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) raw[j] = 0.f;
+#pragma unroll 2
         for (int s = 0; s < splits; ++s) {
             const float* src = landing + ((int64_t)s * a.own + i) * pitch + lane;
 #pragma unroll
@@ -677,7 +703,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (lane + 32 * j < P.E) a.logits[t * P.E + lane + 32 * j] = raw[j];
-        route_token<EPL>(P, raw, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
+        route_token<EPL>(P, raw, bv, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
     }
 }
 
