@@ -171,60 +171,6 @@ __device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int 
         if (i < rows) out[i * a.ldo] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
 }
 
-// C consecutive outputs of row t from feature n on: bias, function, factor, residual, one rounding.
-// u: the factor's sums (gated).  vec: every row starts at a multiple of 2 C bytes.
-template <int C>
-__device__ __forceinline__ void finish(const LinArgs& a, int64_t t, int n, float (&z)[C], const float (&u)[C],
-                                       bool vec) {
-    const bool f16 = a.f16;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ldo + n;
-    const uint16_t* res = a.res ? static_cast<const uint16_t*>(a.res) + t * a.ldr + n : nullptr;
-    const bool full = vec && n + C <= a.N;
-    uint32_t rw[C / 2] = {};
-    if (res && full) {
-#pragma unroll
-        for (int i = 0; i < C / 2; i += C >= 8 ? 4 : 2) {
-            if constexpr (C >= 8) {
-                const uint4 q = *reinterpret_cast<const uint4*>(res + 2 * i);
-                rw[i] = q.x; rw[i + 1] = q.y; rw[i + 2] = q.z; rw[i + 3] = q.w;
-            } else {
-                const uint2 q = *reinterpret_cast<const uint2*>(res + 2 * i);
-                rw[i] = q.x; rw[i + 1] = q.y;
-            }
-        }
-    } else if (res) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (n + i < a.N) rw[i / 2] |= (uint32_t)res[i] << (i & 1 ? 16 : 0);
-    }
-    if (a.bias) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) z[i] += n + i < a.N ? __ldg(a.bias + n + i) : 0.f;
-    }
-    apply_func(a.func, z);
-    if (a.gated) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            z[i] *= u[i] + (a.bias_mul && n + i < a.N ? __ldg(a.bias_mul + n + i) : 0.f);
-    }
-    if (res) add_packed(z, rw, f16);
-    uint32_t ow[C / 2];
-    pack_all(z, ow, f16);
-    if (full) {
-#pragma unroll
-        for (int i = 0; i < C / 2; i += C >= 8 ? 4 : 2) {
-            if constexpr (C >= 8)
-                *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(ow[i], ow[i + 1], ow[i + 2], ow[i + 3]);
-            else
-                *reinterpret_cast<uint2*>(out + 2 * i) = make_uint2(ow[i], ow[i + 1]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (n + i < a.N) out[i] = (uint16_t)(i & 1 ? ow[i / 2] >> 16 : ow[i / 2] & 0xFFFFu);
-    }
-}
-
 // 16 outputs of one row, biases in shared memory, the residual's 16 values packed in rw (zeros
 // without one), to packed results.
 __device__ __forceinline__ void combine16(const LinArgs& a, const float* bias, const float* bias_mul,
@@ -253,7 +199,7 @@ __device__ __forceinline__ void combine16(const LinArgs& a, const float* bias, c
 }
 
 // Whether rows of `p` (ld elements apart) all start at multiples of `bytes`.
-__host__ __device__ __forceinline__ bool rows_aligned(const void* p, int64_t ld, int bytes) {
+inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(2 * ld)) & (uintptr_t)(bytes - 1)) == 0;
 }
 
@@ -427,17 +373,20 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 // Many rows.  Clusters of two CTAs, one per SM; a pair's tile is 256 rows of x by `width` rows of W
 // (gated: width / 2 of W and of V), each CTA holding 128 rows of x and all columns.  Warp 0 loads,
 // warp 1 of the pair's first CTA issues the MMAs, warps 2-9 (two per lane quarter, alternate
-// columns) turn accumulators into rows and warp 10 moves rows: the residual comes in and results
-// go out by TMA through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per
-// row meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
-// meanwhile.  Rows that TMA cannot address (not 16-byte aligned) are read and written by the threads.
+// columns) turn accumulators into rows and warps 10-13 move rows: the residual comes in and results
+// go out through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per row
+// meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
+// meanwhile.  Warp 10 alone moves them by TMA; rows that TMA cannot address (not 16-byte aligned) are
+// copied element by element by the four warps, a warp's lanes along the row (8192 x 2047 x 2048: 169 us
+// with the epilogue's threads storing their own rows, 58 so, 48 at 2048 features).
 //
 // A stage is 128 elements of K: with 64 the commit and barrier round trips of twice as many stages
 // held the MMAs back (8192^3 without its epilogue 620 us, against 563 with 128, of 574 at the
 // measured cuBLAS rate).  Two pairs sharing x by multicast were no faster: clusters of four occupy
 // 144 of the 152 SMs.
 // ------------------------------------------------------------------------------------------
-constexpr int kManyThreads = 352;
+constexpr int kManyThreads = 448;
+constexpr int kManyMovers = 4;
 constexpr int kManyStages = 3;
 constexpr int kManyHalf = 2 * kLinA;             // 64 elements of K: 128 rows of x, at most 128 of W
 constexpr int kManyStageBytes = 2 * kManyHalf;
@@ -494,7 +443,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 16);  // the epilogue warps of both CTAs
-            mbar_init(&buf_ready[b], 1);
+            mbar_init(&buf_ready[b], by_tma ? 1 : kManyMovers);
             mbar_init(&buf_done[b], 8);
         }
         abort_flag = 0;
@@ -580,7 +529,6 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     } else if (warp >= 2 && warp < 10) {
         const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, parity of the columns' 16s
         const int row = 32 * q + lane, sw = (row >> 1) & 3;
-        const bool vec = rows_aligned(a.out, a.ldo, 16) && (!a.res || rows_aligned(a.res, a.ldr, 16));
         int n = 0;
         uint32_t pass = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
@@ -593,70 +541,84 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             }
             tc_fence_after();
             const uint32_t trow = tmem + 256 * b + ((uint32_t)(32 * q) << 16);
-            const int64_t t = (int64_t)r0 + row;
             for (int p = 0; p < passes; ++p, ++pass) {
                 const int buf = pass & 1;
-                if (by_tma && !__all_sync(0xffffffffu, mbar_wait_bounded(&buf_ready[buf], (pass >> 1) & 1,
-                                                                          kLinWaitLimit)))
-                    give_up();  // carries on: the row mover stops, and with it this loop
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&buf_ready[buf], (pass >> 1) & 1, kLinWaitLimit)))
+                    give_up();  // carries on: the row movers stop, and with them this loop
                 for (int c = 4 * p + side; c < min(4 * p + 4, 2 * subs); c += 2) {  // 16 features each
                     float z[16], u[16];
                     tmem_ld_16(trow + 16 * c, reinterpret_cast<uint32_t(&)[16]>(z));
                     if (a.gated) tmem_ld_16(trow + half + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
                     tmem_ld_wait();
-                    if (by_tma) {
-                        uint8_t* line = rows_s + buf * 2 * kManySub + ((c >> 1) & 1) * kManySub + row * 64;
-                        uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 1)) ^ sw) << 4));
-                        uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 1) + 1) ^ sw) << 4));
-                        uint32_t rw[8] = {};
-                        if (res_tma) {
-                            *reinterpret_cast<uint4*>(rw) = *p0;
-                            *reinterpret_cast<uint4*>(rw + 4) = *p1;
-                        }
-                        uint32_t ow[8];
-                        const float* bias = bias_s[buf] + 16 * (c & 3);
-                        combine16(a, bias, bias + 64, z, u, rw, ow);
-                        *p0 = *reinterpret_cast<uint4*>(ow);
-                        *p1 = *reinterpret_cast<uint4*>(ow + 4);
-                    } else if (t < a.T && f0 + 16 * c < a.N) {
-                        finish<16>(a, t, f0 + 16 * c, z, u, vec);
+                    uint8_t* line = rows_s + buf * 2 * kManySub + ((c >> 1) & 1) * kManySub + row * 64;
+                    uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 1)) ^ sw) << 4));
+                    uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 1) + 1) ^ sw) << 4));
+                    uint32_t rw[8] = {};
+                    if (a.res) {
+                        *reinterpret_cast<uint4*>(rw) = *p0;
+                        *reinterpret_cast<uint4*>(rw + 4) = *p1;
                     }
+                    uint32_t ow[8];
+                    const float* bias = bias_s[buf] + 16 * (c & 3);
+                    combine16(a, bias, bias + 64, z, u, rw, ow);
+                    *p0 = *reinterpret_cast<uint4*>(ow);
+                    *p1 = *reinterpret_cast<uint4*>(ow + 4);
                     __syncwarp();
                 }
-                if (by_tma) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&buf_done[buf]);
-                }
+                if (by_tma) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&buf_done[buf]);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[b]), 0));
         }
-    } else if (warp == 10 && by_tma) {  // row mover
+    } else if (warp >= 10 && (warp == 10 || !by_tma)) {  // row movers
         const int64_t tiles = pair < sched.total ? (sched.total - pair + pairs - 1) / pairs : 0;
         const int64_t all = tiles * passes;
+        const int first_row = 32 * (warp - 10);  // of this warp's share, without TMA
+        // row r, feature f < 64 of a buffer
+        const auto element = [&](int buf, int r, int f) {
+            uint8_t* line = rows_s + (2 * buf + (f >> 5)) * kManySub + r * 64;
+            return reinterpret_cast<uint16_t*>(line + ((((f & 31) >> 3) ^ ((r >> 1) & 3)) << 4) + (f & 7) * 2);
+        };
         // makes buffer g & 1 ready for pass g: its biases, and the residual if there is one
-        auto prepare = [&](int64_t g) {
+        const auto prepare = [&](int64_t g) {
             if (g >= all) return;
             const int buf = (int)(g & 1);
             int r0, f0;
             first(pair + g / passes * pairs, r0, f0);
-            const int p = (int)(g % passes), fp = f0 + 64 * p;
-            if (a.bias || a.bias_mul) {
+            const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
+            if ((a.bias || a.bias_mul) && warp == 10) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float* src = j < 2 ? a.bias : a.bias_mul;
                     const int f = fp + lane + 32 * (j & 1);
                     bias_s[buf][lane + 32 * j] = src && f < a.N ? __ldg(src + f) : 0.f;
                 }
-                __syncwarp();
             }
+            if (a.res && !by_tma) {
+                // all loads of the pass in flight at once
+                const int rows = min(32, a.T - r0 - first_row);
+                const uint16_t* src = static_cast<const uint16_t*>(a.res) + ((int64_t)r0 + first_row) * a.ldr + fp + lane;
+                const bool in0 = fp + lane < a.N, in1 = pieces == 2 && fp + 32 + lane < a.N;
+                uint16_t v0[32], v1[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r) {
+                    v0[r] = in0 && r < rows ? __ldcg(src + r * a.ldr) : (uint16_t)0;
+                    v1[r] = in1 && r < rows ? __ldcg(src + r * a.ldr + 32) : (uint16_t)0;
+                }
+#pragma unroll
+                for (int r = 0; r < 32; ++r) {
+                    *element(buf, first_row + r, lane) = v0[r];
+                    if (pieces == 2) *element(buf, first_row + r, 32 + lane) = v1[r];
+                }
+            }
+            __syncwarp();
             if (lane == 0) {
                 if (!res_tma) {
                     mbar_arrive(&buf_ready[buf]);
                 } else {
-                    const int pieces = min(2, subs - 2 * p);
                     mbar_arrive_expect_tx(&buf_ready[buf], pieces * kManySub);
                     for (int s = 0; s < pieces; ++s)
                         tma_load_2d(rows_s + (2 * buf + s) * kManySub, &maps.res, fp + 32 * s, r0, &buf_ready[buf]);
@@ -674,11 +636,19 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 give_up();
                 break;
             }
-            if (lane == 0) {
-                int r0, f0;
-                first(pair + g / passes * pairs, r0, f0);
-                const int p = (int)(g % passes), fp = f0 + 64 * p;
-                for (int s = 0; s < min(2, subs - 2 * p); ++s)
+            int r0, f0;
+            first(pair + g / passes * pairs, r0, f0);
+            const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
+            if (!by_tma) {
+                for (int i = 0; i < pieces; ++i) {
+                    const int f = 32 * i + lane, rows = min(32, a.T - r0 - first_row);
+                    uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp + f;
+                    if (fp + f < a.N)
+#pragma unroll 8
+                        for (int r = 0; r < rows; ++r) dst[r * a.ldo] = *element(buf, first_row + r, f);
+                }
+            } else if (lane == 0) {
+                for (int s = 0; s < pieces; ++s)
                     if (fp + 32 * s < a.N && r0 < a.T)
                         tma_store_2d(&maps.out, rows_s + (2 * buf + s) * kManySub, fp + 32 * s, r0);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -690,7 +660,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         if (g < all)  // gave up: wait (bounded) for the residual copies in flight
             for (int64_t j = g; j < g + 2 && j < all; ++j)
                 mbar_wait_bounded(&buf_ready[j & 1], (j >> 1) & 1, kLinWaitLimit);
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0 && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();
     cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done

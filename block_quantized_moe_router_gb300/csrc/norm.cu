@@ -1,8 +1,15 @@
 // norm.cu -- residual add and RMS norm: s = x + r, y = s * rsqrt(mean(s^2) + eps) * weight.
 //
-// One CTA per row.  The row stays in registers between the sum of squares and the scaling, so
-// every input is read once and every output written once; the kernel is bound by HBM.  The sum
-// s, its squares and the scaling are fp32; s and y are each rounded once, y from the unrounded s.
+// A CTA per row, or a warp per row for short ones.  The row stays in registers between the sum of
+// squares and the scaling, so every input is read once and every output written once; the kernel is
+// bound by HBM (32768 rows of 7168 with a residual, 1.88 GB: 287 us, 0.98 of the measured copy rate).
+// The sum s, its squares and the scaling are fp32; s and y are each rounded once, y from the unrounded s.
+//
+// Rows move in vectors of 8 elements (16 bytes).  Where rows start off a 16-byte boundary, but all
+// tensors' rows equally far off (an odd H, all contiguous), the vectors are laid over the row from
+// the boundary before it: whole ones move as 16 bytes, the two at the ends element by element, and
+// the weight, which does not shift with the row, as two vectors shifted into one.  Where they are not
+// equally far off, a vector is one element.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -10,11 +17,6 @@ namespace moe {
 
 namespace {
 
-// VEC elements of 2 bytes <-> fp32
-template <typename E, int VEC>
-struct alignas(2 * VEC) Pack {
-    E v[VEC];
-};
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_f32(float f, __nv_bfloat16& v) { v = __float2bfloat16_rn(f); }
@@ -24,117 +26,194 @@ struct NormArgs {
     const void *x, *r, *w;
     void *sum, *out;
     int64_t ldx, ldr, lds, ldo;
-    int H;
+    int T, H;
     float eps;
 };
 
-template <typename E, int VEC, int VPT>
-__global__ void __launch_bounds__(1024)
+enum { ROWS_ALIGNED, ROWS_SHIFTED, ROWS_SINGLE };
+
+template <typename E, int VEC>
+struct alignas(2 * VEC) Pack {
+    E v[VEC];
+};
+
+// VEC elements from column c0 on, those inside [0, H).
+template <typename E, int MODE, int VEC>
+__device__ __forceinline__ Pack<E, VEC> load_vec(const E* row, int c0, int H) {
+    Pack<E, VEC> p;
+    if (MODE != ROWS_SHIFTED || (c0 >= 0 && c0 + VEC <= H)) {
+        p = *reinterpret_cast<const Pack<E, VEC>*>(row + c0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            from_f32(0.f, p.v[j]);
+            if (c0 + j >= 0 && c0 + j < H) p.v[j] = row[c0 + j];
+        }
+    }
+    return p;
+}
+template <typename E, int MODE, int VEC>
+__device__ __forceinline__ void store_vec(E* row, int c0, int H, const Pack<E, VEC>& p) {
+    if (MODE != ROWS_SHIFTED || (c0 >= 0 && c0 + VEC <= H)) {
+        *reinterpret_cast<Pack<E, VEC>*>(row + c0) = p;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c0 + j >= 0 && c0 + j < H) row[c0 + j] = p.v[j];
+    }
+}
+
+// Elements w[c0 .. c0 + 7], clamped to [0, H), where c0 may be off a 16-byte boundary: two aligned
+// vectors shifted into one, or element by element where those reach beyond w.
+template <typename E>
+__device__ __forceinline__ Pack<E, 8> load_weight(const E* w, int c0, int H) {
+    const int ow = (int)((reinterpret_cast<uintptr_t>(w) >> 1) & 7);
+    const int shift = (c0 + ow) & 7, b0 = c0 - shift;  // w + b0 is aligned
+    Pack<E, 8> p;
+    if (b0 >= 0 && b0 + 16 <= H) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(w + b0), hi = *reinterpret_cast<const uint4*>(w + b0 + 8);
+        uint32_t q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) q[i] = shift & 4 ? q[i + 2] : q[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) q[i] = shift & 2 ? q[i + 1] : q[i];
+        uint4 r;
+        uint32_t* rw = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rw[i] = shift & 1 ? __funnelshift_r(q[i], q[i + 1], 16) : q[i];
+        p = *reinterpret_cast<Pack<E, 8>*>(&r);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p.v[j] = w[min(max(c0 + j, 0), H - 1)];
+    }
+    return p;
+}
+
+// WARPS: rows per CTA, a warp each; 0: one row per CTA, by all its warps.
+template <typename E, int MODE, int VPT, int WARPS>
+__global__ void __launch_bounds__(WARPS ? 32 * WARPS : 1024, !WARPS && VPT == 1 ? 2 : 1)
 add_rms_norm_kernel(NormArgs a) {
+    constexpr int VEC = MODE == ROWS_SINGLE ? 1 : 8;
     using P = Pack<E, VEC>;
     __shared__ float part[32];
     pdl_wait();
     pdl_trigger();
-    const int64_t row = blockIdx.x;
-    const int nvec = a.H / VEC, tid = threadIdx.x;
-    const P* x = reinterpret_cast<const P*>(static_cast<const E*>(a.x) + row * a.ldx);
-    const P* r = a.r ? reinterpret_cast<const P*>(static_cast<const E*>(a.r) + row * a.ldr) : nullptr;
-    const P* w = reinterpret_cast<const P*>(a.w);
-    P* sum = a.sum ? reinterpret_cast<P*>(static_cast<E*>(a.sum) + row * a.lds) : nullptr;
-    P* out = reinterpret_cast<P*>(static_cast<E*>(a.out) + row * a.ldo);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = WARPS ? (int64_t)blockIdx.x * WARPS + warp : blockIdx.x;
+    if (WARPS && t >= a.T) return;
+    const int tid = WARPS ? lane : threadIdx.x, step = WARPS ? 32 : blockDim.x;
+    const E* x = static_cast<const E*>(a.x) + t * a.ldx;
+    const E* r = a.r ? static_cast<const E*>(a.r) + t * a.ldr : nullptr;
+    const E* w = static_cast<const E*>(a.w);
+    E* sum = a.sum ? static_cast<E*>(a.sum) + t * a.lds : nullptr;
+    E* out = static_cast<E*>(a.out) + t * a.ldo;
+    // elements between the boundary before the row and its start (the same for all tensors)
+    const int off = MODE == ROWS_SHIFTED ? (int)((reinterpret_cast<uintptr_t>(x) >> 1) & 7) : 0;
+    const int nvec = (a.H + off + VEC - 1) / VEC;
     P xv[VPT], rv[VPT], wv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {  // every load issued before any is used
-        const int c = tid + i * blockDim.x;
+        const int c = tid + i * step, c0 = c * VEC - off;
         if (c < nvec) {
-            xv[i] = x[c];
-            if (r) rv[i] = r[c];
-            wv[i] = w[c];
+            xv[i] = load_vec<E, MODE, VEC>(x, c0, a.H);
+            if (r) rv[i] = load_vec<E, MODE, VEC>(r, c0, a.H);
+            if constexpr (MODE == ROWS_SHIFTED) wv[i] = load_weight<E>(w, c0, a.H);
+            else wv[i] = *reinterpret_cast<const P*>(w + c0);
         }
     }
     float s[VPT][VEC], sq = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = tid + i * blockDim.x;
+        const int c = tid + i * step;
         if (c < nvec) {
             P o;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 s[i][j] = to_f32(xv[i].v[j]);
                 if (r) s[i][j] += to_f32(rv[i].v[j]);
-                sq += s[i][j] * s[i][j];
+                sq += s[i][j] * s[i][j];  // elements outside the row are 0
                 from_f32(s[i][j], o.v[j]);
             }
-            if (sum) sum[c] = o;
+            if (sum) store_vec<E, MODE, VEC>(sum, c * VEC - off, a.H, o);
         }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    if ((tid & 31) == 0) part[tid >> 5] = sq;
-    __syncthreads();
-    sq = (tid & 31) < (blockDim.x >> 5) ? part[tid & 31] : 0.f;
+    if (!WARPS) {
+        if (lane == 0) part[warp] = sq;
+        __syncthreads();
+        sq = lane < (blockDim.x >> 5) ? part[lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    }
     const float scale = rsqrtf(sq / (float)a.H + a.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = tid + i * blockDim.x;
+        const int c = tid + i * step;
         if (c < nvec) {
             P o;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) from_f32(s[i][j] * scale * to_f32(wv[i].v[j]), o.v[j]);
-            out[c] = o;
+            store_vec<E, MODE, VEC>(out, c * VEC - off, a.H, o);
         }
     }
 }
 
-template <typename E, int VEC, int VPT>
-cudaError_t launch_vpt(const NormArgs& a, int T, int threads, cudaStream_t st) {
-    return launch_pdl(add_rms_norm_kernel<E, VEC, VPT>, dim3(T), dim3(threads), st, a);
+constexpr int kNormWarps = 8;
+
+template <typename E, int MODE, int VPT>
+cudaError_t launch_row_per_cta(const NormArgs& a, int nvec, cudaStream_t st) {
+    const int threads = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
+    return launch_pdl(add_rms_norm_kernel<E, MODE, VPT, 0>, dim3(a.T), dim3(threads), st, a);
+}
+template <typename E, int MODE, int VPT>
+cudaError_t launch_row_per_warp(const NormArgs& a, cudaStream_t st) {
+    return launch_pdl(add_rms_norm_kernel<E, MODE, VPT, kNormWarps>,
+                      dim3((unsigned)(((int64_t)a.T + kNormWarps - 1) / kNormWarps)), dim3(32 * kNormWarps), st, a);
 }
 
-template <typename E, int VEC>
-cudaError_t launch_vec(const NormArgs& a, int T, cudaStream_t st) {
-    const int nvec = a.H / VEC;
-    int vpt = 1;
-    while (vpt * 1024 < nvec) vpt *= 2;
-    const int threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
-    switch (vpt) {
-        case 1: return launch_vpt<E, VEC, 1>(a, T, threads, st);
-        case 2: return launch_vpt<E, VEC, 2>(a, T, threads, st);
+template <typename E, int MODE>
+cudaError_t launch_mode(const NormArgs& a, cudaStream_t st) {
+    const int nvec = MODE == ROWS_SINGLE ? a.H : (a.H + (MODE == ROWS_SHIFTED ? 7 : 0) + 7) / 8;
+    // Many short rows: a warp per row (32768 x 64: 6 us, against 33 with a CTA per row).  Few: a CTA per
+    // row has more loads in flight.
+    if (a.T >= 4 * kNormWarps) {
+        if (nvec <= 32) return launch_row_per_warp<E, MODE, 1>(a, st);
+        if (nvec <= 64) return launch_row_per_warp<E, MODE, 2>(a, st);
+        if (nvec <= 128) return launch_row_per_warp<E, MODE, 4>(a, st);
     }
-    if constexpr (VEC < 8) {
-        switch (vpt) {
-            case 4: return launch_vpt<E, VEC, 4>(a, T, threads, st);
-            case 8: return launch_vpt<E, VEC, 8>(a, T, threads, st);
-        }
-        if constexpr (VEC < 2) {
-            if (vpt == 16) return launch_vpt<E, VEC, 16>(a, T, threads, st);
-        }
+    if (nvec <= 1024) return launch_row_per_cta<E, MODE, 1>(a, nvec, st);
+    if (nvec <= 2048 || MODE == ROWS_ALIGNED) return launch_row_per_cta<E, MODE, 2>(a, nvec, st);
+    if constexpr (MODE == ROWS_SHIFTED) return launch_row_per_cta<E, MODE, 3>(a, nvec, st);
+    if constexpr (MODE == ROWS_SINGLE) {
+        if (nvec <= 4096) return launch_row_per_cta<E, MODE, 4>(a, nvec, st);
+        if (nvec <= 8192) return launch_row_per_cta<E, MODE, 8>(a, nvec, st);
+        return launch_row_per_cta<E, MODE, 16>(a, nvec, st);
     }
     return cudaErrorInvalidValue;
 }
 
 template <typename E>
-cudaError_t launch_type(const NormArgs& a, int T, cudaStream_t st) {
-    // The widest vector that every row's start and the row length allow.
-    uint64_t bits = (uint64_t)a.H | (uint64_t)(uintptr_t)a.x / 2 | (uint64_t)(uintptr_t)a.w / 2 |
-                    (uint64_t)(uintptr_t)a.out / 2;
-    if (T > 1) bits |= (uint64_t)a.ldx | (uint64_t)a.ldo;
-    if (a.r) bits |= (uint64_t)(uintptr_t)a.r / 2 | (T > 1 ? (uint64_t)a.ldr : 0);
-    if (a.sum) bits |= (uint64_t)(uintptr_t)a.sum / 2 | (T > 1 ? (uint64_t)a.lds : 0);
-    if (bits % 8 == 0) return launch_vec<E, 8>(a, T, st);
-    if (bits % 2 == 0) return launch_vec<E, 2>(a, T, st);
-    return launch_vec<E, 1>(a, T, st);
+cudaError_t launch_type(const NormArgs& a, cudaStream_t st) {
+    // how far each tensor's rows start off a 16-byte boundary, in elements: `first` of row 0, and
+    // `pitch` more with each row
+    const auto at = [](const void* p) { return (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 7); };
+    const bool many = a.T > 1;
+    const int first = at(a.x), pitch = many ? (int)(a.ldx & 7) : 0;
+    const auto alike = [&](const void* p, int64_t ld) {
+        return !p || (at(p) == first && (!many || (int)(ld & 7) == pitch));
+    };
+    if (!alike(a.r, a.ldr) || !alike(a.sum, a.lds) || !alike(a.out, a.ldo)) return launch_mode<E, ROWS_SINGLE>(a, st);
+    if (first == 0 && pitch == 0 && a.H % 8 == 0 && at(a.w) == 0) return launch_mode<E, ROWS_ALIGNED>(a, st);
+    return launch_mode<E, ROWS_SHIFTED>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const void* r, const void* w,
                                 void* sum, void* out, cudaStream_t st) {
-    const NormArgs a{x, r, w, sum, out, d.ldx, d.ldr, d.lds, d.ldo, d.H, d.eps};
-    return d.dtype == MOE_DT_F16 ? launch_type<__half>(a, d.T, st)
-                                 : launch_type<__nv_bfloat16>(a, d.T, st);
+    const NormArgs a{x, r, w, sum, out, d.ldx, d.ldr, d.lds, d.ldo, d.T, d.H, d.eps};
+    return d.dtype == MOE_DT_F16 ? launch_type<__half>(a, st) : launch_type<__nv_bfloat16>(a, st);
 }
 
 }  // namespace moe
