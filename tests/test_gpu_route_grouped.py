@@ -81,6 +81,25 @@ def test_from_logits(cuda_lib, E, groups, keep, top, k, scoring):
                 _agree(got, _ref(logits, k, scoring, renorm, scaling, groups, keep, top, bias), scaling)
 
 
+# E, groups, keep, top, k for many tokens, some of them odd ones
+@pytest.mark.parametrize("E,groups,keep,top,k", [(128, 8, 3, 2, 8), (256, 16, 6, 2, 8), (64, 4, 1, 1, 16), (256, 32, 9, 2, 16),
+                                                 (160, 8, 3, 1, 6), (8, 1, 1, 1, 8), (24, 6, 2, 2, 3), (96, 1, 1, 1, 9)])
+@pytest.mark.parametrize("scoring", [SOFTMAX, SIGMOID, SQRT, SOFT_BIAS])
+def test_many_tokens(cuda_lib, E, groups, keep, top, k, scoring):
+    T = 8200 + E % 37
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    logits = torch.randn(T, E, generator=g, device="cuda") * 2
+    logits[5] = 0.25  # all equal
+    logits[77, 3] = math.nan
+    logits[78] = -math.inf
+    logits[T - 1, 1] = -3.4e38
+    for bias in (None, torch.rand(E, generator=g, device="cuda") * 0.2 - 0.1, torch.zeros(E, device="cuda")):
+        for renorm, scaling in ((True, 2.5), (False, 1.0)):
+            got = _run(k, scoring, renorm, scaling, groups, keep, top, logits=logits, bias=bias)
+            assert got[3] == capi.MOE_DEV_NONFINITE
+            _agree(got, _ref(logits, k, scoring, renorm, scaling, groups, keep, top, bias), scaling)
+
+
 def _grid(T, E, H, seed):
     """Tokens and a router on fixed-point grids: the logits are exact in fp32 in any order."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -116,11 +135,12 @@ def test_random_router_logits(cuda_lib):
         _agree(got, _ref(got[2], 6, SIGMOID, True, 1.0, 8, 3, 2), 1.0)
 
 
+@pytest.mark.parametrize("tokens", [4000, 9000])
 @pytest.mark.parametrize("scoring", [SIGMOID, SQRT, SOFT_BIAS])
-def test_scores_closer_than_fp32_can_tell(cuda_lib, scoring):
+def test_scores_closer_than_fp32_can_tell(cuda_lib, scoring, tokens):
     """Pairs of experts (and of groups) whose exact values differ by less than fp32 rounding: the
     order is that of the exact values."""
-    T, E, groups = 4000, 64, 8
+    T, E, groups = tokens, 64, 8
     g = torch.Generator(device="cuda").manual_seed(11)
     bias = torch.rand(E, generator=g, device="cuda") * 0.2 - 0.1
     logits = torch.randn(T, E, generator=g, device="cuda") * 0.5
