@@ -253,7 +253,7 @@ def moe_route_grouped(*, T, E, H, top_k, scoring, renormalize, routed_scaling, n
                        None if given else _tptr(w_router, torch.bfloat16, (E, H), dev, "w_router"),
                        _tptr(correction_bias, torch.float32, (E,), dev, "correction_bias"),
                        None, 0, None, 0)
-    rc = load_library().moe_route_grouped(
+    rc = (_lib or load_library()).moe_route_grouped(
         ctypes.byref(d), n_group, topk_group, group_top,
         None if given else _tptr(x, torch.bfloat16, (T, H), dev, "x"),
         _tptr(logits_in, torch.float32, (T, E), dev, "logits_in"),
@@ -285,7 +285,7 @@ def moe_linear(x, w, out, *, w_mul=None, bias=None, bias_mul=None, residual=None
     if residual is not None:
         pr, ldr = _rows(residual, dt, T, N, dev, "residual")
     d = moe_linear_desc(T, N, K, _DTYPES.get(dt, -1), func, ldx, ldw, ldr, ldo)
-    rc = load_library().moe_linear(
+    rc = (_lib or load_library()).moe_linear(
         ctypes.byref(d), px, pw, pm, _tptr(bias, torch.float32, (N,), dev, "bias"),
         _tptr(bias_mul, torch.float32, (N,), dev, "bias_mul"), pr, po,
         _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
@@ -308,7 +308,7 @@ def moe_add_rms_norm(x, weight, out, *, residual=None, sum_out=None, eps=1e-6, s
     if sum_out is not None:
         ps, lds = _rows(sum_out, dt, T, H, dev, "sum_out")
     d = moe_norm_desc(T, H, _DTYPES.get(dt, -1), eps, ldx, ldr, lds, ldo)
-    rc = load_library().moe_add_rms_norm(ctypes.byref(d), px, pr, _tptr(weight, dt, (H,), dev, "weight"),
+    rc = (_lib or load_library()).moe_add_rms_norm(ctypes.byref(d), px, pr, _tptr(weight, dt, (H,), dev, "weight"),
                                          ps, po, st)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_add_rms_norm")

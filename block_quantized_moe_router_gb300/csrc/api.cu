@@ -293,6 +293,8 @@ moe_status_t moe_linear(const moe_linear_desc* d, const void* x, const void* w, 
     if (!valid_ld(d->ldx, d->K) || d->ldx % 8 || !valid_ld(d->ldw, d->K) || d->ldw % 8 ||
         !valid_ld(d->ldo, d->N) || (residual && !valid_ld(d->ldr, d->N)) || (bias_mul && !w_mul))
         return MOE_ERR_INVALID_ARG;
+    if (out && (out == x || out == w || out == w_mul || (out == residual && d->ldo != d->ldr)))
+        return MOE_ERR_INVALID_ARG;
     if (d->T == 0) return MOE_OK;
     if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(w_mul) || !aligned2(residual) ||
         !aligned2(out))
@@ -311,6 +313,12 @@ moe_status_t moe_add_rms_norm(const moe_norm_desc* d, const void* x, const void*
         (sum_out && !valid_ld(d->lds, d->H)))
         return MOE_ERR_INVALID_ARG;
     if (d->T == 0) return MOE_OK;
+    // in place means the same rows
+    const auto other_rows = [](const void* p, int64_t ldp, const void* q, int64_t ldq) { return p && p == q && ldp != ldq; };
+    if (other_rows(out, d->ldo, x, d->ldx) || other_rows(out, d->ldo, residual, d->ldr) ||
+        other_rows(sum_out, d->lds, x, d->ldx) || other_rows(sum_out, d->lds, residual, d->ldr) || weight == out ||
+        (sum_out && weight == sum_out))
+        return MOE_ERR_INVALID_ARG;
     if (!x || !weight || !out || sum_out == out || !aligned2(x) || !aligned2(residual) ||
         !aligned2(weight) || !aligned2(sum_out) || !aligned2(out))
         return MOE_ERR_INVALID_ARG;

@@ -4,7 +4,24 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
+
+// Lets `kernel` use `smem` bytes of dynamic shared memory (its largest need, so that no two calls differ)
+// and clusters of up to 16; once per device.
+template <typename K>
+inline cudaError_t allow_large_launch(K* kernel, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return err;
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

@@ -672,9 +672,9 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
 
 // ---- host ------------------------------------------------------------------------------------------
 template <typename K>
-cudaError_t launch_clusters(K* kernel, dim3 grid, int cluster, int threads, int smem, const LinMaps& m,
-                            const LinArgs& a, cudaStream_t st) {
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allowed, dim3 grid, int cluster,
+                            int threads, int smem, const LinMaps& m, const LinArgs& a, cudaStream_t st) {
+    const cudaError_t err = allow_large_launch(kernel, smem_max, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -777,7 +777,8 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
         a.rows_t = plan.rows_t;
         a.stages = plan.stages;
         const int tiles_n = (d.N + box_w - 1) / box_w, tiles_t = (d.T + plan.rows_t - 1) / plan.rows_t;
-        return launch_clusters(linear_few_kernel, dim3(tiles_n * plan.splits, tiles_t), plan.splits, kFewThreads,
+        static std::atomic<uint64_t> allowed{0};
+        return launch_clusters(linear_few_kernel, kFewSmemMax, allowed, dim3(tiles_n * plan.splits, tiles_t), plan.splits, kFewThreads,
                                few_smem(plan.rows_t, plan.splits, plan.stages), m, a, st);
     }
     // TMA addresses rows that start at multiples of 16 bytes
@@ -788,7 +789,8 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
         return cudaErrorInvalidValue;
     const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);
-    return launch_clusters(linear_many_kernel, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
+    static std::atomic<uint64_t> allowed{0};
+    return launch_clusters(linear_many_kernel, kManySmem, allowed, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
 }
 
 }  // namespace moe

@@ -727,9 +727,8 @@ cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, in
     smem += 1024;
     if (smem > kFusedSmemMax) return cudaErrorNotSupported;
     const auto kernel = route_fused_kernel<EPL>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err == cudaSuccess && splits > 8)
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t err = allow_large_launch(kernel, kFusedSmemMax, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * splits));

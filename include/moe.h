@@ -214,7 +214,8 @@ moe_status_t moe_route_grouped(const moe_route_desc* desc, int32_t n_group, int3
  * dev_status [device] int32 [1] or NULL (MOE_DEV_TIMEOUT: a wait inside the kernel gave up and out
  *           is invalid).
  * Needs no workspace.  T == 0 is a valid no-op.  Errors: MOE_ERR_INVALID_ARG for the checks of
- * moe_linear_desc, a NULL or misaligned pointer or bias_mul without w_mul; MOE_ERR_CUDA. */
+ * moe_linear_desc, a NULL or misaligned pointer, bias_mul without w_mul, out equal to x, w or
+ * w_mul, or out equal to residual with another row distance; MOE_ERR_CUDA. */
 moe_status_t moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const void* w_mul,
                         const float* bias, const float* bias_mul, const void* residual, void* out,
                         int32_t* dev_status, void* stream);
@@ -222,11 +223,12 @@ moe_status_t moe_linear(const moe_linear_desc* desc, const void* x, const void* 
 /* Residual add and RMS norm (qwen3_attention/init.rs and moe/init.rs, the `rms_norm` and
  * `bf16_residual_add` handles, in one pass): s = x + residual, out = s * weight / sqrt(mean(s^2) +
  * eps), over each of the T rows.  Computed in fp32 from the unrounded s; s and out are each
- * rounded once.
+ * rounded once.  The squares are added in fp32: a row whose sum of squares exceeds 3.4e38 gives zeros.
  * x, weight [H], out [device] desc->dtype; residual and sum_out [device] or NULL (s = x without
  * a residual).  out and sum_out may each be x or residual itself (same rows), but not one another.
  * T == 0 is a valid no-op.  Errors: MOE_ERR_INVALID_ARG for the checks of moe_norm_desc, a NULL
- * x, weight or out, or sum_out == out; MOE_ERR_CUDA. */
+ * x, weight or out, sum_out == out, out or sum_out equal to weight, or equal to x or residual with
+ * another row distance; MOE_ERR_CUDA. */
 moe_status_t moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const void* residual,
                               const void* weight, void* sum_out, void* out, void* stream);
 

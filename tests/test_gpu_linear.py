@@ -84,7 +84,8 @@ SIZES = [(1, 1, 8), (1, 2048, 7168), (2, 64, 64), (3, 130, 72), (5, 1, 4096), (8
          (16, 128, 512), (17, 129, 520), (31, 1000, 1544), (64, 512, 1032), (65, 65, 65 * 8), (100, 2048, 256),
          (128, 256, 128), (129, 257, 136), (200, 4096, 512), (255, 1000, 2056), (256, 512, 512), (257, 96, 64),
          (300, 7168, 264), (511, 384, 1536), (513, 1025, 520), (1000, 200, 8), (1024, 2048, 1024),
-         (2049, 640, 776), (4096, 1, 64), (4100, 300, 192)]
+         (2049, 640, 776), (4096, 1, 64), (4100, 300, 192), (1, 70000, 64), (3, 20001, 16), (600, 33, 8200),
+         (90, 64, 16384), (70000, 8, 8), (515, 1025, 64)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES)

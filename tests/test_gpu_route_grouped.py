@@ -112,16 +112,30 @@ def _grid(T, E, H, seed):
     (1, 256, 7168, 16, 6, 8), (1, 8, 32, 2, 1, 2), (3, 180, 1184, 12, 5, 6), (8, 512, 4096, 8, 3, 8), (9, 96, 96, 8, 2, 4),
     (17, 64, 2048, 4, 2, 6), (53, 180, 1184, 12, 5, 6), (64, 256, 7168, 16, 6, 8), (127, 128, 512, 8, 4, 8),
     (128, 128, 384, 8, 4, 8), (129, 256, 1152, 4, 2, 8), (300, 384, 256, 6, 3, 8), (511, 72, 800, 3, 2, 5),
-    (1000, 512, 640, 16, 4, 16), (4096, 256, 512, 16, 6, 8), (5000, 40, 32, 4, 2, 4)])
+    (1000, 512, 640, 16, 4, 16), (4096, 256, 512, 16, 6, 8), (5000, 40, 32, 4, 2, 4), (9900, 96, 64, 8, 3, 5),
+    (10100, 256, 128, 8, 3, 8), (2, 300, 96, 3, 2, 7), (900, 330, 160, 33, 4, 16), (7, 1, 64, 1, 1, 1)])
 def test_from_tokens(cuda_lib, T, E, H, groups, keep, k):
     x, w = _grid(T, E, H, T + E)
     bias = torch.rand(E, device="cuda") * 0.2 - 0.1
     logits = x.double() @ w.double().t()
-    for scoring, top in ((SIGMOID, 2), (SOFTMAX, 1)):
+    for scoring, top in ((SIGMOID, min(2, E // groups)), (SOFTMAX, 1)):
         got = _run(k, scoring, True, 2.5, groups, keep, top, x=x, w=w, bias=bias)
         assert got[3] == 0
         assert torch.equal(got[2].double(), logits)
         _agree(got, _ref(logits, k, scoring, True, 2.5, groups, keep, top, bias), 2.5)
+
+
+def test_tokens_that_are_not_finite(cuda_lib):
+    """They set the status bit and disturb no other token."""
+    for T in (3, 200):
+        x, w = _grid(T, 128, 256, T)
+        want = _run(6, SIGMOID, True, 1.0, 8, 3, 2, x=x, w=w)
+        x[1, 7] = math.nan
+        got = _run(6, SIGMOID, True, 1.0, 8, 3, 2, x=x, w=w)
+        assert got[3] == capi.MOE_DEV_NONFINITE
+        rows = [t for t in range(T) if t != 1]
+        assert torch.equal(got[0][rows], want[0][rows]) and torch.equal(got[1][rows], want[1][rows])
+        assert got[0][1].tolist() == [0, 1, 2, 3, 4, 5] and (got[1][1] == 0).all()
 
 
 def test_random_router_logits(cuda_lib):

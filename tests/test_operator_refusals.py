@@ -6,7 +6,7 @@ import pytest
 
 from block_quantized_moe_router_gb300 import build, capi
 
-P = ctypes.c_void_p(0x1000)
+P, Q = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x8000)
 
 
 @pytest.fixture(scope="module")
@@ -39,7 +39,7 @@ def test_route_grouped(lib):
     assert lib.moe_route_grouped(None, 1, 1, 1, P, P, P, P, P, None, None) == capi.MOE_ERR_INVALID_ARG
 
 
-def _linear(lib, x=P, w=P, w_mul=None, bias=None, bias_mul=None, residual=None, out=P, **kw):
+def _linear(lib, x=P, w=P, w_mul=None, bias=None, bias_mul=None, residual=None, out=Q, **kw):
     d = capi.moe_linear_desc(4, 32, 64, 0, 0, 64, 64, 32, 32)
     for name, value in kw.items():
         setattr(d, name, value)
@@ -53,7 +53,8 @@ def test_linear(lib):
            dict(dtype=-1), dict(func=5), dict(func=-1), dict(ldx=56), dict(ldx=68), dict(ldw=56), dict(ldw=65),
            dict(ldo=31), dict(ldr=31, residual=P), dict(ldx=1 << 38), dict(x=None), dict(w=None), dict(out=None), dict(x=odd),
            dict(w=odd), dict(w_mul=odd), dict(out=ctypes.c_void_p(0x1001)), dict(residual=ctypes.c_void_p(0x1001)),
-           dict(bias_mul=P)]
+           dict(bias_mul=P), dict(out=P, x=P), dict(out=P, x=Q, w=P), dict(out=P, x=Q, w=Q, w_mul=P),
+           dict(out=P, x=Q, w=Q, residual=P, ldr=40)]
     for kw in bad:
         assert _linear(lib, **kw) == capi.MOE_ERR_INVALID_ARG, kw
     assert lib.moe_linear(None, P, P, None, None, None, None, P, None, None) == capi.MOE_ERR_INVALID_ARG
@@ -72,7 +73,9 @@ def test_add_rms_norm(lib):
     bad = [dict(T=-1), dict(H=0), dict(H=16385, ldx=20000, ldo=20000), dict(dtype=2), dict(eps=-1e-6),
            dict(eps=float("nan")), dict(eps=float("inf")), dict(ldx=31), dict(ldo=31), dict(ldr=31, r=P),
            dict(lds=31, s=P), dict(x=None), dict(w=None), dict(out=None), dict(s=ctypes.c_void_p(0x2000)),
-           dict(x=odd), dict(r=odd), dict(w=odd), dict(s=odd), dict(out=odd), dict(ldo=1 << 38)]
+           dict(x=odd), dict(r=odd), dict(w=odd), dict(s=odd), dict(out=odd), dict(ldo=1 << 38),
+           dict(out=P, ldo=40), dict(x=Q, r=P, out=P, ldo=40), dict(s=P, lds=40), dict(x=Q, r=P, s=P, lds=40),
+           dict(out=P, x=Q), dict(s=P, x=Q)]
     for kw in bad:
         assert _norm(lib, **kw) == capi.MOE_ERR_INVALID_ARG, kw
     assert lib.moe_add_rms_norm(None, P, None, P, None, P, None) == capi.MOE_ERR_INVALID_ARG
