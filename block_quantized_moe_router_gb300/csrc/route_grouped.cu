@@ -72,8 +72,8 @@ __device__ __forceinline__ double from_orderable64(unsigned long long u) {
 // Shared memory of one routing warp.
 template <int EPL>
 struct alignas(16) RouteScratch {
-    unsigned long long key64[32 * EPL];  // fp64 selection; the fp32 ranking values in the same place
-    float val[32 * EPL];                 // scores (logits where no score was needed, or for fp64)
+    float rank[32 * EPL + (EPL > 1 ? 64 : 32)];  // ranking values, size + 1 places per group
+    float val[32 * EPL];  // scores (logits where no score was needed, or for fp64)
     float group[68];
     int kept[64];
 };
@@ -143,48 +143,26 @@ __device__ __noinline__ unsigned long long kept_fp64(const GroupRule& P, const f
     return kept;
 }
 
-// The whole selection in fp64 (more candidates are too close together than a warp's lanes rank), from
-// the logits in sc->val.  On return lane j < k holds pick j.
+// The K rounds in fp64 (more candidates are too close together than a warp's lanes rank), over the
+// kept groups, from the logits in sc->val.  On return lane j < k holds pick j.
 template <int EPL>
-__device__ __noinline__ int select_fp64(const GroupRule& P, const float* bias, float lmax, RouteScratch<EPL>* sc,
-                                        int lane) {
+__device__ __noinline__ int pick_fp64(const GroupRule& P, const float* bias, float lmax, RouteScratch<EPL>* sc,
+                                      int lane) {
     const double inv_z = inv_z64<EPL>(P, lmax, sc, lane);
-    const bool score_groups = P.by_logit && P.group_top == 2;
+    const bool grouped = P.topk_group < P.n_group;
+    const int count = grouped ? P.topk_group * P.size : P.E;
     unsigned long long key[EPL];
+    int ee[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 32 * j;
+        const int r = lane + 32 * j;
         key[j] = 0;
-        if (e >= P.E) continue;
-        key[j] = key_of<EPL>(P, bias, e, lmax, inv_z, sc);
-        const float l = sc->val[e];
-        sc->key64[e] = score_groups && l != -INFINITY ? orderable64(score64(P.scoring, l, lmax, inv_z)) : key[j];
+        ee[j] = 0x7fffffff;
+        if (r >= count) continue;
+        const int q = (r * P.size_inv) >> 20;
+        ee[j] = grouped ? sc->kept[q] * P.size + r - q * P.size : r;
+        key[j] = key_of<EPL>(P, bias, ee[j], lmax, inv_z, sc);
     }
-    __syncwarp();
-    unsigned long long gs[2] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int g = lane + 32 * q;
-        if (g >= P.n_group) continue;
-        unsigned long long m1 = 0, m2 = 0;
-        for (int i = 0; i < P.size; ++i) {
-            const unsigned long long x = sc->key64[g * P.size + i];
-            m2 = max(m2, min(m1, x));
-            m1 = max(m1, x);
-        }
-        gs[q] = P.group_top == 2 ? orderable64(from_orderable64(m1) + from_orderable64(m2)) : m1;
-    }
-    unsigned long long kept = 0;
-    for (int g = 0; g < P.n_group; ++g) {
-        const unsigned long long mine = __shfl_sync(0xffffffffu, g < 32 ? gs[0] : gs[1], g & 31);
-        const bool a0 = lane < P.n_group && (gs[0] > mine || (gs[0] == mine && lane < g));
-        const bool a1 = lane + 32 < P.n_group && (gs[1] > mine || (gs[1] == mine && lane + 32 < g));
-        const int rank = __popc(__ballot_sync(0xffffffffu, a0)) + __popc(__ballot_sync(0xffffffffu, a1));
-        if (rank < P.topk_group) kept |= 1ull << g;
-    }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-        if (!((kept >> ((((lane + 32 * j) * P.size_inv) >> 20) & 63)) & 1)) key[j] = 0;
     int my_e = 0;
     for (int r = 0; r < P.k; ++r) {
         unsigned long long m = 0;
@@ -196,24 +174,23 @@ __device__ __noinline__ int select_fp64(const GroupRule& P, const float* bias, f
         uint32_t e = 0x7fffffffu;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (key[j] == top) e = min(e, (uint32_t)(lane + 32 * j));
+            if (key[j] == top) e = min(e, (uint32_t)ee[j]);
         e = __reduce_min_sync(0xffffffffu, e);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j == (int)e) key[j] = 0;
+            if (ee[j] == (int)e) key[j] = 0;
         if (lane == r) my_e = (int)e;
     }
     return my_e;
 }
 
 // The K rounds over `count` candidates, N per lane: candidate r is expert r, or the r-th of the kept
-// groups.  Returns the pick of lane j < k, or sets `full` where the fp64 selection of all is needed.
-// tol(v): how far a value near v may be from the exact one (0: exact).
+// groups.  Returns the pick of lane j < k, or sets `full` where all candidates are needed in fp64.
 template <int EPL, int N>
 __device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias, RouteScratch<EPL>* sc, int lane,
                                            bool grouped, float tol_rel, float tol_abs, float lmax,
                                            const float (&lg)[EPL], bool& full, bool& val_is_logit) {
-    const float* rank_val = reinterpret_cast<const float*>(sc->key64);
+    const float* rank_val = sc->rank;
     const int count = grouped ? P.topk_group * P.size : P.E;
     uint32_t key[N];
     int ee[N];
@@ -335,7 +312,7 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
         smax = score32(P.scoring, top_logit, lmax, inv_z);
     }
     // places beyond E are written too: the arrays have room, and nothing reads them
-    float* rank_val = reinterpret_cast<float*>(sc->key64);
+    float* rank_val = sc->rank;
     float bmax = 0.f;
     if (P.by_logit) {
 #pragma unroll
@@ -363,7 +340,7 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
     if (softmax && !P.by_logit)
         tol_abs += 0x1p-19f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
 
-    bool full = false, val_is_logit = !need_score;  // val_is_logit: sc->val holds logits
+    bool full = false, val_is_logit = !need_score;  // full: see pick_rounds; val_is_logit: sc->val holds logits
     __syncwarp();
     if (grouped) {
         // 32 / n_group lanes (a power of two) share a group; above 32 groups a lane has two
@@ -462,7 +439,7 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
         __syncwarp();
     }
     int my_e = 0;
-    if (!full) {
+    {
         const int live = grouped ? (P.topk_group * P.size + 31) >> 5 : (P.E + 31) >> 5;  // candidates per lane
         const auto run = [&](auto n) {
             return pick_rounds<EPL, decltype(n)::value>(P, bias, sc, lane, grouped, tol_rel, tol_abs, lmax, lg, full,
@@ -475,13 +452,7 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
         else my_e = run(Int<EPL>{});
     }
     if (full) {
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < P.E) sc->val[lane + 32 * j] = lg[j];
-        __syncwarp();
-        val_is_logit = true;
-        my_e = select_fp64<EPL>(P, bias, lmax, sc, lane);
+        my_e = pick_fp64<EPL>(P, bias, lmax, sc, lane);
     }
     float w = 0.f;
     if (lane < P.k) {
@@ -712,7 +683,7 @@ cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, in
     // ring | landing | scratch, or the last two over the ring where they do not fit beside it
     const int stage = kFusedA + a.n * 128;
     const int landing = splits * a.own * (a.n + 4) * 4;
-    const int scratch = (int)sizeof(RouteScratch<EPL>) * (kFusedThreads / 32);
+    const int scratch = (int)sizeof(RouteScratch<EPL>) * (a.own < kFusedThreads / 32 ? a.own : kFusedThreads / 32);
     const int steps = (a.nk + splits - 1) / splits;
     const int landing16 = (landing + 15) / 16 * 16;
     a.stages = (kFusedSmemMax - 1024 - landing16 - scratch) / stage;
