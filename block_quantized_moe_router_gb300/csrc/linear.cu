@@ -268,7 +268,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         status_or(a.status, MOE_DEV_TIMEOUT);
     };
     const int steps = k_end - k_begin;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         int issued = 0;
         for (int i = 0; i < steps && !abort_flag; ++i) {
             const int s = i % a.stages;
@@ -287,7 +287,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         if (abort_flag)  // wait (bounded) for the copies still in flight
             for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
                 mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kLinWaitLimit);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
         int i = 0;
         for (; i < steps; ++i) {
@@ -297,11 +297,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 break;
             }
             tc_fence_after();
-            const uint32_t sb = smem_u32(smem + s * stage_bytes);
+            const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes along the swizzled row
-                mma_f16kind<0>(tmem, smem_desc(sb + 32 * j, 16, 1024, kLayoutSw128),
-                               smem_desc(sb + kLinA + 32 * j, 16, 1024, kLayoutSw128), idesc, (i | j) != 0);
+            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                mma_f16kind<0>(tmem, ad + 2 * j, ad + (kLinA >> 4) + 2 * j, idesc, (i | j) != 0);
             tc_commit(&empty[s]);
         }
         tc_commit(&acc_full);  // arrives when every MMA has completed
@@ -472,7 +471,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         r0 = tt * 256 + rank * 128;
         f0 = tn * per_tile;
     };
-    if (warp == 0 && lane == 0) {  // TMA producer of this CTA's halves
+    if (warp == 0 && elect_one()) {  // TMA producer of this CTA's halves
         const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
         int it = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs) {
@@ -497,7 +496,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         if (abort_flag && rank == 0)  // wait (bounded) for the pair's copies still in flight
             for (int j = it - 1; j >= 0 && j >= it - kManyStages; --j)
                 mbar_wait_bounded(&full[j % kManyStages], (j / kManyStages) & 1, kLinWaitLimit);
-    } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA issuer of the pair
+    } else if (warp == 1 && rank == 0 && elect_one()) {  // MMA issuer of the pair
         const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
         int it = 0, n = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
@@ -514,13 +513,12 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sb = smem_u32(smem + s * kManyStageBytes);
+                const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 1024, kLayoutSw128);
                 for (int h = 0; h < parts; ++h)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // K 16 per MMA: 32 bytes along the swizzled row
-                        const uint32_t at = sb + h * kManyHalf + 32 * j;
-                        mma_f16kind<1>(tmem + 256 * b, smem_desc(at, 16, 1024, kLayoutSw128),
-                                       smem_desc(at + kLinA, 16, 1024, kLayoutSw128), idesc, (k | h | j) != 0);
+                    for (int j = 0; j < 4; ++j) {  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                        const uint64_t at = ad + h * (kManyHalf >> 4) + 2 * j;
+                        mma_f16kind<1>(tmem + 256 * b, at, at + (kLinA >> 4), idesc, (k | h | j) != 0);
                     }
                 tc_commit_pair(&empty[s]);
             }

@@ -585,7 +585,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         abort_flag = 1;
         status_or(a.status, MOE_DEV_TIMEOUT);
     };
-    if (warp == 0 && lane == 0) {  // TMA producer
+    if (warp == 0 && elect_one()) {  // TMA producer
         const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
         int issued = 0;
         for (int i = 0; i < steps && !abort_flag; ++i) {
@@ -604,7 +604,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         if (abort_flag)  // wait (bounded) for the copies still in flight
             for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
                 mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kFusedWaitLimit);
-    } else if (warp == 1 && lane == 0) {  // MMA issuer
+    } else if (warp == 1 && elect_one()) {  // MMA issuer
         const uint32_t idesc = idesc_bf16(128, a.n);
         for (int i = 0; i < steps; ++i) {
             const int s = i % a.stages;
@@ -613,11 +613,10 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
                 break;
             }
             tc_fence_after();
-            const uint32_t sb = smem_u32(smem + s * stage_bytes);
+            const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes along the swizzled row
-                tc_mma_bf16(tmem, smem_desc(sb + 32 * j, 16, 1024, kLayoutSw128),
-                            smem_desc(sb + kFusedA + 32 * j, 16, 1024, kLayoutSw128), idesc, (i | j) != 0);
+            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                tc_mma_bf16(tmem, ad + 2 * j, ad + (kFusedA >> 4) + 2 * j, idesc, (i | j) != 0);
             tc_commit(&empty[s]);
         }
         tc_commit(&acc_full);  // arrives when every MMA has completed
