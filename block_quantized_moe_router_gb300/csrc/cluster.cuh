@@ -69,6 +69,19 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
+// Place in a ring of stages: the slot, and the parity of its phase.  Counted, not divided: a division by
+// a runtime number of stages took longer (600 cycles on a lone thread) than a stage's copies.
+struct RingPos {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
 // Tensor map of [rows][cols] 16-bit elements, rows ld apart: boxes of box_cols columns (64 or 32: 128
 // or 64 bytes, swizzled over as many) x box_rows rows; what lies beyond reads as zero.
 inline bool encode_rows16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,

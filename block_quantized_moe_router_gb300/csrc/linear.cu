@@ -270,9 +270,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     const int steps = k_end - k_begin;
     if (warp == 0 && elect_one()) {
         int issued = 0;
-        for (int i = 0; i < steps && !abort_flag; ++i) {
-            const int s = i % a.stages;
-            if (!mbar_wait_bounded(&empty[s], ((i / a.stages) & 1) ^ 1, kLinWaitLimit)) {
+        RingPos at;
+        for (int i = 0; i < steps && !abort_flag; ++i, at.next(a.stages)) {
+            const int s = at.slot;
+            if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kLinWaitLimit)) {
                 give_up();
                 break;
             }
@@ -289,10 +290,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kLinWaitLimit);
     } else if (warp == 1 && elect_one()) {
         const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
-        int i = 0;
-        for (; i < steps; ++i) {
-            const int s = i % a.stages;
-            if (!mbar_wait_bounded(&full[s], (i / a.stages) & 1, kLinWaitLimit) || abort_flag) {
+        RingPos at;
+        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+            const int s = at.slot;
+            if (!mbar_wait_bounded(&full[s], at.parity, kLinWaitLimit) || abort_flag) {
                 give_up();
                 break;
             }
@@ -474,13 +475,14 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     if (warp == 0 && elect_one()) {  // TMA producer of this CTA's halves
         const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
         int it = 0;
+        RingPos at;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs) {
             int t0, n0;
             first(i, t0, n0);
             if (!a.gated) n0 += rank * half;
-            for (int k = 0; k < a.nk; k += 2, ++it) {
-                const int s = it % kManyStages, parts = min(2, a.nk - k);
-                if (!mbar_wait_bounded(&empty[s], ((it / kManyStages) & 1) ^ 1, kLinWaitLimit) || abort_flag) {
+            for (int k = 0; k < a.nk; k += 2, ++it, at.next(kManyStages)) {
+                const int s = at.slot, parts = min(2, a.nk - k);
+                if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kLinWaitLimit) || abort_flag) {
                     give_up();
                     break;
                 }
@@ -498,7 +500,8 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 mbar_wait_bounded(&full[j % kManyStages], (j / kManyStages) & 1, kLinWaitLimit);
     } else if (warp == 1 && rank == 0 && elect_one()) {  // MMA issuer of the pair
         const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
-        int it = 0, n = 0;
+        int n = 0;
+        RingPos ring;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
             const int b = n & 1;
             if (!mbar_wait_bounded(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinWaitLimit)) {
@@ -506,9 +509,9 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 break;
             }
             tc_fence_after();
-            for (int k = 0; k < a.nk; k += 2, ++it) {
-                const int s = it % kManyStages, parts = min(2, a.nk - k);
-                if (!mbar_wait_bounded(&full[s], (it / kManyStages) & 1, kLinWaitLimit) || abort_flag) {
+            for (int k = 0; k < a.nk; k += 2, ring.next(kManyStages)) {
+                const int s = ring.slot, parts = min(2, a.nk - k);
+                if (!mbar_wait_bounded(&full[s], ring.parity, kLinWaitLimit) || abort_flag) {
                     give_up();
                     break;
                 }

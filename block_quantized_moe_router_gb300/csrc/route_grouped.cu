@@ -588,9 +588,10 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     if (warp == 0 && elect_one()) {  // TMA producer
         const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
         int issued = 0;
-        for (int i = 0; i < steps && !abort_flag; ++i) {
-            const int s = i % a.stages;
-            if (!mbar_wait_bounded(&empty[s], ((i / a.stages) & 1) ^ 1, kFusedWaitLimit)) {
+        RingPos at;
+        for (int i = 0; i < steps && !abort_flag; ++i, at.next(a.stages)) {
+            const int s = at.slot;
+            if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kFusedWaitLimit)) {
                 give_up();
                 break;
             }
@@ -606,9 +607,10 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
                 mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kFusedWaitLimit);
     } else if (warp == 1 && elect_one()) {  // MMA issuer
         const uint32_t idesc = idesc_bf16(128, a.n);
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % a.stages;
-            if (!mbar_wait_bounded(&full[s], (i / a.stages) & 1, kFusedWaitLimit) || abort_flag) {
+        RingPos at;
+        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+            const int s = at.slot;
+            if (!mbar_wait_bounded(&full[s], at.parity, kFusedWaitLimit) || abort_flag) {
                 give_up();
                 break;
             }
