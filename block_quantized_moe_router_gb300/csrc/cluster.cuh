@@ -69,6 +69,36 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
+// Bounded wait on a phase of an mbarrier: one poll here, then up to kWaitPolls more out of line, each of
+// which the hardware may suspend for up to kWaitHint ns; false when they run out.  Loops that feed
+// the tensor cores run on one thread, where every instruction between two waits counts: a loop of polls
+// in place, and a look at a flag besides, doubled the cost of a wait that has nothing to wait for.
+constexpr uint32_t kWaitHint = 1000000, kWaitPolls = 4000;  // 4 s in all
+static __device__ __noinline__ bool mbar_wait_long(uint32_t addr, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(kWaitHint)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity) {
+    const uint32_t addr = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return ok != 0 || mbar_wait_long(addr, parity);
+}
+
 // Place in a ring of stages: the slot, and the parity of its phase.  Counted, not divided: a division by
 // a runtime number of stages took longer (600 cycles on a lone thread) than a stage's copies.
 struct RingPos {

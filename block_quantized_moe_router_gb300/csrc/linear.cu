@@ -27,7 +27,6 @@ namespace {
 
 using namespace tc;
 
-constexpr uint64_t kLinWaitLimit = 1ull << 26;  // polls before a wait is declared stuck
 constexpr int kLinK = 64;                       // K elements per stage (128 bytes per row)
 constexpr int kLinA = 128 * 128;                // bytes of a 128-row operand stage
 
@@ -267,13 +266,14 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         abort_flag = 1;
         status_or(a.status, MOE_DEV_TIMEOUT);
     };
+    const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const int steps = k_end - k_begin;
     if (warp == 0 && elect_one()) {
         int issued = 0;
         RingPos at;
-        for (int i = 0; i < steps && !abort_flag; ++i, at.next(a.stages)) {
+        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
             const int s = at.slot;
-            if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kLinWaitLimit)) {
+            if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                 give_up();
                 break;
             }
@@ -287,13 +287,13 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         }
         if (abort_flag)  // wait (bounded) for the copies still in flight
             for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
-                mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kLinWaitLimit);
+                mbar_wait_suspended(&full[i % a.stages], (i / a.stages) & 1);
     } else if (warp == 1 && elect_one()) {
         const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
         RingPos at;
         for (int i = 0; i < steps; ++i, at.next(a.stages)) {
             const int s = at.slot;
-            if (!mbar_wait_bounded(&full[s], at.parity, kLinWaitLimit) || abort_flag) {
+            if (!mbar_wait_suspended(&full[s], at.parity)) {
                 give_up();
                 break;
             }
@@ -305,11 +305,9 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
             tc_commit(&empty[s]);
         }
         tc_commit(&acc_full);  // arrives when every MMA has completed
-        mbar_wait_bounded(&acc_full, 0, kLinWaitLimit);
-    }
-    cluster_wait();
-    const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
-    if (warp >= 6) {
+        if (!mbar_wait_suspended(&acc_full, 0)) give_up();
+        tc_fence_before();
+    } else if (warp >= 6) {
         // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
         if (a.res)
             for (int i = threadIdx.x - 192; i < my_cols * 2; i += 64) {
@@ -318,9 +316,9 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
     }
+    __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
+    cluster_wait();
     {  // the two warps of a lane quarter take alternate 16 columns
-        __syncwarp();
-        if (!mbar_wait_bounded(&acc_full, 0, kLinWaitLimit)) give_up();
         tc_fence_after();
         const int q = warp & 3;
         const uint32_t mine = smem_u32(landing + ((int)rank * 128 + 32 * q + lane) * pitch);
@@ -482,7 +480,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             if (!a.gated) n0 += rank * half;
             for (int k = 0; k < a.nk; k += 2, ++it, at.next(kManyStages)) {
                 const int s = at.slot, parts = min(2, a.nk - k);
-                if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kLinWaitLimit) || abort_flag) {
+                if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                     give_up();
                     break;
                 }
@@ -497,21 +495,21 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         }
         if (abort_flag && rank == 0)  // wait (bounded) for the pair's copies still in flight
             for (int j = it - 1; j >= 0 && j >= it - kManyStages; --j)
-                mbar_wait_bounded(&full[j % kManyStages], (j / kManyStages) & 1, kLinWaitLimit);
+                mbar_wait_suspended(&full[j % kManyStages], (j / kManyStages) & 1);
     } else if (warp == 1 && rank == 0 && elect_one()) {  // MMA issuer of the pair
         const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
         int n = 0;
         RingPos ring;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
             const int b = n & 1;
-            if (!mbar_wait_bounded(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinWaitLimit)) {
+            if (!mbar_wait_suspended(&acc_empty[b], ((n >> 1) & 1) ^ 1)) {
                 give_up();
                 break;
             }
             tc_fence_after();
             for (int k = 0; k < a.nk; k += 2, ring.next(kManyStages)) {
                 const int s = ring.slot, parts = min(2, a.nk - k);
-                if (!mbar_wait_bounded(&full[s], ring.parity, kLinWaitLimit) || abort_flag) {
+                if (!mbar_wait_suspended(&full[s], ring.parity)) {
                     give_up();
                     break;
                 }
@@ -536,7 +534,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             const int b = n & 1;
             int r0, f0;
             first(i, r0, f0);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], (n >> 1) & 1, kLinWaitLimit))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_suspended(&acc_full[b], (n >> 1) & 1))) {
                 give_up();
                 break;
             }
@@ -544,7 +542,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             const uint32_t trow = tmem + 256 * b + ((uint32_t)(32 * q) << 16);
             for (int p = 0; p < passes; ++p, ++pass) {
                 const int buf = pass & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&buf_ready[buf], (pass >> 1) & 1, kLinWaitLimit)))
+                if (!__all_sync(0xffffffffu, mbar_wait_suspended(&buf_ready[buf], (pass >> 1) & 1)))
                     give_up();  // carries on: the row movers stop, and with them this loop
                 for (int c = 4 * p + side; c < min(4 * p + 4, 2 * subs); c += 2) {  // 16 features each
                     float z[16], u[16];
@@ -632,7 +630,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         int64_t g = 0;
         for (; g < all; ++g) {
             const int buf = (int)(g & 1);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&buf_done[buf], (g >> 1) & 1, kLinWaitLimit)) ||
+            if (!__all_sync(0xffffffffu, mbar_wait_suspended(&buf_done[buf], (g >> 1) & 1)) ||
                 __any_sync(0xffffffffu, abort_flag)) {
                 give_up();
                 break;
@@ -660,7 +658,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         }
         if (g < all)  // gave up: wait (bounded) for the residual copies in flight
             for (int64_t j = g; j < g + 2 && j < all; ++j)
-                mbar_wait_bounded(&buf_ready[j & 1], (j >> 1) & 1, kLinWaitLimit);
+                mbar_wait_suspended(&buf_ready[j & 1], (j >> 1) & 1);
         if (lane == 0 && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();

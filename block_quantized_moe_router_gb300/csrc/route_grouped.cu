@@ -520,7 +520,6 @@ cudaError_t launch_given(const float* logits, const float* bias, int T, const Gr
 constexpr int kFusedThreads = 512;
 constexpr int kFusedK = 64;
 constexpr int kFusedA = 128 * 128;
-constexpr uint64_t kFusedWaitLimit = 1ull << 26;  // polls before a wait is declared stuck
 constexpr int kFusedSmemMax = 226 * 1024;
 constexpr int kFusedStagesMax = 8;
 
@@ -589,9 +588,9 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
         int issued = 0;
         RingPos at;
-        for (int i = 0; i < steps && !abort_flag; ++i, at.next(a.stages)) {
+        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
             const int s = at.slot;
-            if (!mbar_wait_bounded(&empty[s], at.parity ^ 1, kFusedWaitLimit)) {
+            if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                 give_up();
                 break;
             }
@@ -604,13 +603,13 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         }
         if (abort_flag)  // wait (bounded) for the copies still in flight
             for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
-                mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, kFusedWaitLimit);
+                mbar_wait_suspended(&full[i % a.stages], (i / a.stages) & 1);
     } else if (warp == 1 && elect_one()) {  // MMA issuer
         const uint32_t idesc = idesc_bf16(128, a.n);
         RingPos at;
         for (int i = 0; i < steps; ++i, at.next(a.stages)) {
             const int s = at.slot;
-            if (!mbar_wait_bounded(&full[s], at.parity, kFusedWaitLimit) || abort_flag) {
+            if (!mbar_wait_suspended(&full[s], at.parity)) {
                 give_up();
                 break;
             }
@@ -622,15 +621,13 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
             tc_commit(&empty[s]);
         }
         tc_commit(&acc_full);  // arrives when every MMA has completed
-        mbar_wait_bounded(&acc_full, 0, kFusedWaitLimit);
+        if (!mbar_wait_suspended(&acc_full, 0)) give_up();
+        tc_fence_before();
     }
+    __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
     cluster_wait();
-    if (a.landing_at == 0) {  // over the ring: no CTA's copies or MMAs may still use it
-        __syncthreads();
-        cluster_sync();
-    }
+    if (a.landing_at == 0) cluster_sync();  // over the ring: no CTA's copies or MMAs may still use it
     {  // a warp's lane quarter: tokens 32 q + lane; the four warps of a quarter share the experts
-        if (!mbar_wait_bounded(&acc_full, 0, kFusedWaitLimit)) give_up();
         tc_fence_after();
         const int q = warp & 3, row = 32 * q + lane;
         if (32 * q < rows) {
