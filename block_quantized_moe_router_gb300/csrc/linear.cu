@@ -1,10 +1,10 @@
 // linear.cu -- y = f(x W^T + b) [* (x V^T + c)] [+ r], fp32 sums, one rounding.
 //
-// Two kernels on tcgen05.mma.kind::f16, both fed by TMA (64 elements of K per stage, 128-byte
-// swizzled rows; what lies beyond a matrix reads as zero) into accumulators in tensor memory:
+// Two kernels on tcgen05.mma.kind::f16, both fed by TMA (boxes of 64 elements of K, 128-byte swizzled
+// rows; what lies beyond a matrix reads as zero) into accumulators in tensor memory:
 //
 //   linear_few_kernel   few rows.  The time is that of streaming the weights, so the weights are
-//       the MMA's 128-row operand and the rows of x its N side (16 to 256 columns): each weight
+//       the MMA's 128-row operand and the rows of x its N side (16 to 128 columns): each weight
 //       byte passes through shared memory once, however few rows there are.  K is split over the
 //       CTAs of a cluster so that a narrow matrix still occupies the SMs; the partial sums meet
 //       through distributed shared memory, added in rank order (equal calls give equal bits).
@@ -696,14 +696,14 @@ cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allo
 namespace {
 
 // Which kernel, and its tiles, by estimated time in microseconds (fitted to measurements over 1 to
-// 16384 rows, N 2048 to 8192, K 2048 to 8192; the estimates are within about 15 % of them).
+// 16384 rows, N 600 to 8192, K 600 to 8192; the fastest of the choices measured, or within 8 % of it).
 //   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.34 / 0.30 / 0.27 us
 //     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 1 us a tile
-//     besides, and 6 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.6 at 256.
-//   few rows: 64 elements cost a CTA 0.37 us and more with the rows of x, or what its SM's share of
+//     besides, and 6 us once.  512 x 7168 x 2048: 18.7 us at 192 columns (one wave), 20.2 at 256.
+//   few rows: 64 elements cost a CTA 0.27 us and more with the rows of x, or what its SM's share of
 //     the L2 rate (105 GB/s) allows; 4.5 us besides, and the exchange of the parts.
-//     64 rows of the gated 2 x 2048 x 7168: 17.2 us, against 37.7 for the other kernel; 256 rows of
-//     7168 x 2048: 27 against 15.0.
+//     64 rows of the gated 2 x 2048 x 7168: 15.7 us, against 37.2 for the other kernel; 256 rows of
+//     7168 x 2048: 24.4 against 15.3.
 struct LinPlan {
     bool few;
     int width;                   // many: columns per tile
@@ -740,9 +740,9 @@ LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
         const int64_t places = (int64_t)sms * fit * (splits < 4 ? 32 : splits == 4 ? 30 : fit == 1 ? 25 : 28) / 32;
         const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
         const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
-        const float per_k_lat = 0.37f + 0.0008f * (float)rows, per_k_bw = (float)on_sm * stage_kb / 105.f;
+        const float per_k_lat = 0.27f + 0.0003f * (float)rows, per_k_bw = (float)on_sm * stage_kb / 105.f;
         const float us = (float)waves * ((float)kbs * (per_k_lat > per_k_bw ? per_k_lat : per_k_bw) + 4.5f +
-                                         0.03f * (float)rows);
+                                         0.05f * (float)rows);
         if (us < best_us) {
             best_us = us;
             best = LinPlan{true, 0, splits, stages, rows};
