@@ -69,23 +69,17 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
-// Bounded wait on a phase of an mbarrier: one poll here, then up to kWaitPolls more out of line, each of
-// which the hardware may suspend for up to kWaitHint ns; false when they run out.  Loops that feed
-// the tensor cores run on one thread, where every instruction between two waits counts: a loop of polls
-// in place, and a look at a flag besides, doubled the cost of a wait that has nothing to wait for.
-constexpr uint32_t kWaitHint = 1000000, kWaitPolls = 4000;  // 4 s in all
-static __device__ __noinline__ bool mbar_wait_long(uint32_t addr, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity), "r"(kWaitHint)
-            : "memory");
-        if (ok) return true;
-    }
-    return false;
+// Bounded wait on a phase of an mbarrier; false after kWaitNs.  One poll, and only where it finds nothing a
+// loop with a clock: the loops that feed the tensor cores run on one thread, where every instruction
+// between two waits counts (a counted loop and a look at a flag doubled the cost of a wait that has nothing
+// to wait for).  The bound is a time and not a number of polls: a poll lasts up to 1 ms on a lone lane and
+// 4 us on a whole warp.  All of it is in place: no call is made where one lane of a warp runs.
+constexpr uint32_t kWaitHint = 1000000;  // ns that a poll may last
+constexpr uint64_t kWaitNs = 4000000000ull;
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
 }
 __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
@@ -96,7 +90,17 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
         : "=r"(ok)
         : "r"(addr), "r"(parity)
         : "memory");
-    return ok != 0 || mbar_wait_long(addr, parity);
+    if (__builtin_expect(ok != 0, 1)) return true;
+    const uint64_t began = global_ns();
+    do {
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(kWaitHint)
+            : "memory");
+    } while (ok == 0 && global_ns() - began < kWaitNs);
+    return ok != 0;
 }
 
 // Place in a ring of stages: the slot, and the parity of its phase.  Counted, not divided: a division by
@@ -107,6 +111,12 @@ struct RingPos {
     __device__ __forceinline__ void next(int stages) {
         if (++slot == stages) {
             slot = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void back(int stages) {
+        if (--slot < 0) {
+            slot = stages - 1;
             parity ^= 1u;
         }
     }

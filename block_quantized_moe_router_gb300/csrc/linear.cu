@@ -225,7 +225,6 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     extern __shared__ uint8_t lin_smem[];
     __shared__ uint64_t full[8], empty[8], acc_full;
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t splits = cluster_size();
@@ -248,7 +247,6 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
             mbar_init(&empty[s], 1);
         }
         mbar_init(&acc_full, 1);
-        abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.x);
         prefetch_tmap(&maps.w);
@@ -262,10 +260,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
-    auto give_up = [&]() {
-        abort_flag = 1;
-        status_or(a.status, MOE_DEV_TIMEOUT);
-    };
+    auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const int steps = k_end - k_begin;
     if (warp == 0 && elect_one()) {
@@ -285,9 +280,11 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
             tma_load_2d(base + kLinA, &maps.x, kx, t0, &full[s]);
             ++issued;
         }
-        if (abort_flag)  // wait (bounded) for the copies still in flight
-            for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
-                mbar_wait_suspended(&full[i % a.stages], (i / a.stages) & 1);
+        // whoever gives up, no copy is in flight when the CTA ends
+        for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
+            at.back(a.stages);
+            mbar_wait_suspended(&full[at.slot], at.parity);
+        }
     } else if (warp == 1 && elect_one()) {
         const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
         RingPos at;
@@ -493,9 +490,11 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 }
             }
         }
-        if (abort_flag && rank == 0)  // wait (bounded) for the pair's copies still in flight
-            for (int j = it - 1; j >= 0 && j >= it - kManyStages; --j)
-                mbar_wait_suspended(&full[j % kManyStages], (j / kManyStages) & 1);
+        if (rank == 0)  // whoever gives up, none of the pair's copies is in flight when its CTAs end
+            for (int i = it < kManyStages ? it : kManyStages; i > 0; --i) {
+                at.back(kManyStages);
+                mbar_wait_suspended(&full[at.slot], at.parity);
+            }
     } else if (warp == 1 && rank == 0 && elect_one()) {  // MMA issuer of the pair
         const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
         int n = 0;

@@ -548,7 +548,6 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     extern __shared__ uint8_t rf_smem[];
     __shared__ uint64_t full[kFusedStagesMax], empty[kFusedStagesMax], acc_full;
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rf_smem) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int splits = (int)cluster_size(), rank = (int)cluster_rank();
@@ -567,7 +566,6 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
             mbar_init(&empty[s], 1);
         }
         mbar_init(&acc_full, 1);
-        abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.x);
         prefetch_tmap(&maps.w);
@@ -580,10 +578,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
-    auto give_up = [&]() {
-        abort_flag = 1;
-        status_or(a.status, MOE_DEV_TIMEOUT);
-    };
+    auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     if (warp == 0 && elect_one()) {  // TMA producer
         const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
         int issued = 0;
@@ -601,9 +596,11 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
             tma_load_2d(base, &maps.x, kx, (int)t0, &full[s]);  // rows beyond the box: never read back
             ++issued;
         }
-        if (abort_flag)  // wait (bounded) for the copies still in flight
-            for (int i = issued - 1; i >= 0 && i >= issued - a.stages; --i)
-                mbar_wait_suspended(&full[i % a.stages], (i / a.stages) & 1);
+        // whoever gives up, no copy is in flight when the CTA ends
+        for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
+            at.back(a.stages);
+            mbar_wait_suspended(&full[at.slot], at.parity);
+        }
     } else if (warp == 1 && elect_one()) {  // MMA issuer
         const uint32_t idesc = idesc_bf16(128, a.n);
         RingPos at;
