@@ -72,7 +72,10 @@ __device__ __forceinline__ double from_orderable64(unsigned long long u) {
 // Shared memory of one routing warp.
 template <int EPL>
 struct alignas(16) RouteScratch {
-    float rank[32 * EPL + (EPL > 1 ? 64 : 32)];  // ranking values, size + 1 places per group
+    // Ranking values, size + 1 places per group: value e stands at e + e / size, also for e from E to
+    // 32 EPL - 1.  With at most 64 groups and E > 16 EPL the groups are of at least 2, 3 and 5 experts at EPL
+    // 4, 8 and 16, which puts the last place at 190, 340 and 613 (EPL 1 and 2: groups of one, 62 and 126).
+    float rank[32 * EPL + (EPL == 1 ? 32 : EPL <= 4 ? 64 : EPL == 8 ? 96 : 112)];
     float val[32 * EPL];  // scores (logits where no score was needed, or for fp64)
     float group[68];
     int kept[64];

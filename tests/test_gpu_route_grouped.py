@@ -81,6 +81,21 @@ def test_from_logits(cuda_lib, E, groups, keep, top, k, scoring):
                 _agree(got, _ref(logits, k, scoring, renorm, scaling, groups, keep, top, bias), scaling)
 
 
+# the smallest groups that a number of experts allows with up to 64 groups
+@pytest.mark.parametrize("E,groups,keep,top,k", [(33, 33, 6, 1, 6), (66, 33, 5, 2, 8), (129, 43, 5, 2, 6), (192, 64, 64, 2, 16),
+                                                 (189, 63, 9, 1, 8), (260, 52, 7, 2, 9), (320, 64, 64, 2, 32),
+                                                 (384, 64, 5, 1, 7), (448, 64, 9, 2, 16)])
+@pytest.mark.parametrize("scoring", [SOFTMAX, SIGMOID, SQRT, SOFT_BIAS])
+def test_small_groups(cuda_lib, E, groups, keep, top, k, scoring):
+    for T in (1, 40, 700):
+        g = torch.Generator(device="cuda").manual_seed(2 * E + T)
+        logits = torch.randn(T, E, generator=g, device="cuda") * 2
+        for bias in (None, torch.rand(E, generator=g, device="cuda") * 0.2 - 0.1):
+            got = _run(k, scoring, True, 1.5, groups, keep, top, logits=logits, bias=bias)
+            assert got[3] == 0
+            _agree(got, _ref(logits, k, scoring, True, 1.5, groups, keep, top, bias), 1.5)
+
+
 # E, groups, keep, top, k for many tokens, some of them odd ones
 @pytest.mark.parametrize("E,groups,keep,top,k", [(128, 8, 3, 2, 8), (256, 16, 6, 2, 8), (64, 4, 1, 1, 16), (256, 32, 9, 2, 16),
                                                  (160, 8, 3, 1, 6), (8, 1, 1, 1, 8), (24, 6, 2, 2, 3), (96, 1, 1, 1, 9)])
