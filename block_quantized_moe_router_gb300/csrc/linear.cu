@@ -143,16 +143,16 @@ __device__ __forceinline__ void pack_all(const float (&z)[C], uint32_t (&w)[C / 
     }
 }
 
-// Feature n of up to four consecutive rows from t on (the lanes of a warp hold consecutive features).
-__device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[4],
-                                               const float (&u)[4]) {
-    uint32_t rw[4] = {};
-    if (a.res) {
-        const uint16_t* res = static_cast<const uint16_t*>(a.res) + t * a.ldr + n;
+// The residual of feature n of up to four consecutive rows from t on, and these rows' results (the lanes of
+// a warp hold consecutive features).
+__device__ __forceinline__ void load_residual(const LinArgs& a, int64_t t, int rows, int n, uint32_t (&rw)[4]) {
+    const uint16_t* res = static_cast<const uint16_t*>(a.res) + t * a.ldr + n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < rows) rw[i] = res[i * a.ldr];
-    }
+    for (int i = 0; i < 4; ++i)
+        if (i < rows) rw[i] = res[i * a.ldr];
+}
+__device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[4],
+                                               const float (&u)[4], const uint32_t (&rw)[4]) {
     const float b = a.bias ? __ldg(a.bias + n) : 0.f, c = a.bias_mul ? __ldg(a.bias_mul + n) : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] += b;
@@ -337,12 +337,21 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         }
         tc_fence_before();
     }
+    // Items of 32 features x 4 rows of x, lane = feature.  The residual is read one item ahead, the first
+    // before the parts have landed (the compiler may not: out may be the residual).
+    const int shift = a.gated ? 1 : 2, items = ((my_cols + 3) / 4) << shift;  // per_tile / 32 blocks of features
+    uint32_t rw[4] = {};
+    const auto ahead = [&](int item) {
+        const int n = n0 + (item & ((1 << shift) - 1)) * 32 + lane, c = (item >> shift) * 4;
+        if (a.res && item < items && n < a.N) load_residual(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, rw);
+    };
+    ahead(warp);
     cluster_sync();  // every part has landed
-    // items of 32 features x 4 rows of x, lane = feature
-    const int blocks = per_tile / 32, items = blocks * ((my_cols + 3) / 4);
     for (int item = warp; item < items; item += kFewThreads / 32) {
-        const int r = (item % blocks) * 32 + lane, c = item / blocks * 4;
+        const int r = (item & ((1 << shift) - 1)) * 32 + lane, c = (item >> shift) * 4;
         const float* src = landing + r * pitch + c;
+        const uint32_t now[4] = {rw[0], rw[1], rw[2], rw[3]};
+        ahead(item + kFewThreads / 32);
         float z[4] = {}, u[4] = {};
 #pragma unroll
         for (int s = 0; s < kFewSplits; ++s)
@@ -355,7 +364,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 }
             }
         const int n = n0 + r;
-        if (n < a.N) finish_feature(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z, u);
+        if (n < a.N) finish_feature(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z, u, now);
     }
     __syncwarp();
     if (warp == 1) {
@@ -723,7 +732,6 @@ LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
             best = LinPlan{false, width, 0, 0, 0};
         }
     }
-    if (T > 4 * kFewRows) return best;
     const int tiles_t = (T + kFewRows - 1) / kFewRows;
     const int rows = ((T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
     const int64_t tiles = (int64_t)tiles_t * ((N + (gated ? 63 : 127)) / (gated ? 64 : 128));
