@@ -39,6 +39,7 @@ struct LinArgs {
     int func, gated, f16;
     int rows_t, stages; // few rows: rows of x per tile, stages of the ring
     int tma_rows;       // many rows: out and the residual go by TMA
+    int even_out, even_res;  // or their rows start at multiples of 4 bytes
     int width;          // many rows: rows of weights per tile
     int64_t ldr, ldo;
     const float *bias, *bias_mul;
@@ -89,13 +90,15 @@ __device__ __forceinline__ uint32_t idesc_f16kind(uint32_t M, uint32_t N, bool f
 
 // ---- epilogue arithmetic -------------------------------------------------------------------------
 // The function over C values: one branch for all of them (a branch per value, unrolled, costs more
-// in instruction fetch than the arithmetic).
+// in instruction fetch than the arithmetic).  __fdividef is off by 2 units of the last place of fp32, and 0
+// where the divisor passes 2^126, where the result is below 2^-119; the exact division has a branch of its
+// own per value (8192 x 4096 x 1024 with SiLU: 86 us, 53 so, 51 without a function).
 template <int C>
 __device__ __forceinline__ void apply_func(int func, float (&z)[C]) {
     switch (func) {
         case MOE_FUNC_SILU:
 #pragma unroll
-            for (int i = 0; i < C; ++i) z[i] = z[i] / (1.f + __expf(-z[i]));
+            for (int i = 0; i < C; ++i) z[i] = __fdividef(z[i], 1.f + __expf(-z[i]));
             break;
         case MOE_FUNC_GELU:
 #pragma unroll
@@ -104,7 +107,7 @@ __device__ __forceinline__ void apply_func(int func, float (&z)[C]) {
         case MOE_FUNC_GELU_TANH:  // 0.5 (1 + tanh u) = sigmoid(2 u)
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                z[i] = z[i] / (1.f + __expf(-1.5957691f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+                z[i] = __fdividef(z[i], 1.f + __expf(-1.5957691f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
             break;
         case MOE_FUNC_RELU:  // not fmaxf: a NaN stays
 #pragma unroll
@@ -381,8 +384,9 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 // go out through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per row
 // meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
 // meanwhile.  Warp 10 alone moves them by TMA; rows that TMA cannot address (not 16-byte aligned) are
-// copied element by element by the four warps, a warp's lanes along the row (8192 x 2047 x 2048: 169 us
-// with the epilogue's threads storing their own rows, 58 so, 48 at 2048 features).
+// copied by the four warps, a warp's lanes along the row: element by element (8192 x 2047 x 2048: 169 us with
+// the epilogue's threads storing their own rows, 58 so, 45 at 2048 features), or two features a lane where
+// rows start at multiples of 4 bytes (10744 x 3982 x 1808: 133 us element by element, 106 so, 96 at 3984).
 //
 // A stage is 128 elements of K: with 64 the commit and barrier round trips of twice as many stages
 // held the MMAs back (8192^3 without its epilogue 620 us, against 563 with 128, of 574 at the
@@ -604,7 +608,23 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                     bias_s[buf][lane + 32 * j] = src && f < a.N ? __ldg(src + f) : 0.f;
                 }
             }
-            if (a.res && !by_tma) {
+            if (a.res && !by_tma && a.even_res) {  // as below, two features a lane
+                const int rows = min(32, a.T - r0 - first_row), f = 2 * lane;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.res) +
+                                                                        ((int64_t)r0 + first_row) * a.ldr + fp + f);
+                const bool in = f < 32 * pieces && fp + f < a.N, both = fp + f + 1 < a.N;
+                uint32_t v[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r) {
+                    v[r] = 0;
+                    if (in && r < rows)
+                        v[r] = both ? __ldcg(src + r * (a.ldr >> 1))
+                                    : __ldcg(reinterpret_cast<const uint16_t*>(src + r * (a.ldr >> 1)));
+                }
+                if (f < 32 * pieces)
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) *reinterpret_cast<uint32_t*>(element(buf, first_row + r, f)) = v[r];
+            } else if (a.res && !by_tma) {
                 // all loads of the pass in flight at once
                 const int rows = min(32, a.T - r0 - first_row);
                 const uint16_t* src = static_cast<const uint16_t*>(a.res) + ((int64_t)r0 + first_row) * a.ldr + fp + lane;
@@ -646,7 +666,18 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             int r0, f0;
             first(pair + g / passes * pairs, r0, f0);
             const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
-            if (!by_tma) {
+            if (!by_tma && a.even_out) {
+                const int f = 2 * lane, rows = min(32, a.T - r0 - first_row);
+                uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp + f;
+                if (f < 32 * pieces && fp + f + 1 < a.N) {
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r)
+                        *reinterpret_cast<uint32_t*>(dst + r * a.ldo) =
+                            *reinterpret_cast<const uint32_t*>(element(buf, first_row + r, f));
+                } else if (f < 32 * pieces && fp + f < a.N) {
+                    for (int r = 0; r < rows; ++r) dst[r * a.ldo] = *element(buf, first_row + r, f);
+                }
+            } else if (!by_tma) {
                 for (int i = 0; i < pieces; ++i) {
                     const int f = 32 * i + lane, rows = min(32, a.T - r0 - first_row);
                     uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp + f;
@@ -703,15 +734,16 @@ cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allo
 
 namespace {
 
-// Which kernel, and its tiles, by estimated time in microseconds (fitted to measurements over 1 to
-// 16384 rows, N 600 to 8192, K 600 to 8192; the fastest of the choices measured, or within 8 % of it).
-//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.34 / 0.30 / 0.27 us
-//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 1 us a tile
-//     besides, and 6 us once.  512 x 7168 x 2048: 18.7 us at 192 columns (one wave), 20.2 at 256.
-//   few rows: 64 elements cost a CTA 0.27 us and more with the rows of x, or what its SM's share of
-//     the L2 rate (105 GB/s) allows; 4.5 us besides, and the exchange of the parts.
-//     64 rows of the gated 2 x 2048 x 7168: 15.7 us, against 37.2 for the other kernel; 256 rows of
-//     7168 x 2048: 24.4 against 15.3.
+// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all seven
+// choices at 156 sizes (1 to 11677 rows, N 88 to 7168, K 512 to 7168): the plan's choice takes 1 % longer
+// than the fastest one in the mean, 43 % at worst (64 x 2048 x 512: 7.2 us against 5.0).
+//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.36 / 0.29 / 0.22 us
+//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 1.2 us a tile
+//     besides, and 4.7 us once.  512 x 7168 x 2048: 18.0 us at 192 columns (one wave), 19.5 at 256.
+//   few rows: 64 elements cost a CTA 0.2 us, or what its SM's share of the L2 rate (102 GB/s) allows;
+//     1.4 us a wave and 0.9 us once besides, and the exchange and the sums of the parts.
+//     64 rows of the gated 2 x 2048 x 7168: 15.2 us, against 36.1 for the other kernel; 256 rows of
+//     7168 x 2048: 22.3 against 14.7; 1600 x 160 x 5848: 17.0 against 30.0.
 struct LinPlan {
     bool few;
     int width;                   // many: columns per tile
@@ -721,12 +753,12 @@ struct LinPlan {
 LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
     LinPlan best{};
     float best_us = 1e30f;
-    const float per_k[3] = {0.34f, 0.30f, 0.27f};
+    const float per_k[3] = {0.36f, 0.29f, 0.22f};
     for (int i = 0; i < 3; ++i) {
         const int width = 256 - 64 * i;
         const int64_t tiles = ManySched(T, N, gated ? width / 2 : width).total;
         const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-        const float us = (float)waves * ((float)nk * per_k[i] + 1.f) + 6.f;
+        const float us = (float)waves * ((float)nk * per_k[i] + 1.2f) + 4.7f;
         if (us < best_us) {
             best_us = us;
             best = LinPlan{false, width, 0, 0, 0};
@@ -741,15 +773,15 @@ LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
         const int stages = kbs < 4 ? (kbs < 2 ? 2 : kbs) : 4;
         const int smem = few_smem(rows, splits, stages);
         if (smem > kFewSmemMax) continue;
-        // CTAs an SM holds, and what clusters of 4 and 8 leave usable of these places (a device of
-        // 152 SMs holds 120 CTAs in clusters of 8 at one per SM, 288 at two)
+        // CTAs an SM holds, and how many of these places clusters of 4 and 8 leave usable (152 SMs hold 36
+        // clusters of 4 and 15 of 8 at one CTA per SM, 36 of 8 at two)
         const int fit = kSmSmem / (smem + 1024 + 256);
-        const int64_t places = (int64_t)sms * fit * (splits < 4 ? 32 : splits == 4 ? 30 : fit == 1 ? 25 : 28) / 32;
+        const int usable = splits < 4 ? 152 : splits == 8 && fit == 1 ? 120 : 144;
+        const int64_t places = (int64_t)sms * fit * usable / 152;
         const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
         const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
-        const float per_k_lat = 0.27f + 0.0003f * (float)rows, per_k_bw = (float)on_sm * stage_kb / 105.f;
-        const float us = (float)waves * ((float)kbs * (per_k_lat > per_k_bw ? per_k_lat : per_k_bw) + 4.5f +
-                                         0.05f * (float)rows);
+        const float per_k_bw = (float)on_sm * stage_kb / 102.f;
+        const float us = (float)waves * ((float)kbs * (per_k_bw > 0.2f ? per_k_bw : 0.2f) + 0.046f * (float)rows + 1.4f) + 0.9f;
         if (us < best_us) {
             best_us = us;
             best = LinPlan{true, 0, splits, stages, rows};
@@ -793,6 +825,8 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     if (a.tma_rows && (!encode_rows16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
                        (residual && !encode_rows16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
         return cudaErrorInvalidValue;
+    a.even_out = rows_aligned(out, d.ldo, 4);
+    a.even_res = residual && rows_aligned(residual, d.ldr, 4);
     const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);
     static std::atomic<uint64_t> allowed{0};

@@ -114,6 +114,23 @@ def test_functions(cuda_lib, T, func, dtype):
         _check(_run(a, func), ref, bound, DT[dtype])
 
 
+# many rows of few features; and rows at multiples of 4 bytes that are none of 16, with tiles that end in them
+@pytest.mark.parametrize("T,N,K", [(700, 96, 4096), (1300, 33, 2056), (2264, 160, 5848), (20000, 40, 512), (5000, 1002, 264),
+                                   (3001, 2052, 200), (2500, 1986, 520), (9000, 130, 64)])
+def test_tall_and_even(cuda_lib, T, N, K):
+    for gated in (False, True):
+        func = (T + gated) % 5
+        a = _make(T, N, K, DT["f16" if gated else "bf16"], gated=gated, bias=not gated, residual=True, seed=N)
+        ref, bound = _linear_ref(func=func, **a)
+        _check(_run(a, func), ref, bound, a["x"].dtype)
+        wide = torch.full((T, N + 6), 7.0, dtype=a["x"].dtype, device="cuda")
+        res = torch.zeros(T, N + 3, dtype=a["x"].dtype, device="cuda")  # out even, the residual's rows odd
+        res[:, 1:N + 1] = a["residual"]
+        out = _run({**a, "residual": res[:, 1:N + 1]}, func, out=wide[:, 2:N + 2])
+        _check(out, ref, bound, a["x"].dtype)
+        assert (wide[:, :2] == 7).all() and (wide[:, N + 2:] == 7).all()
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 300, 4096), (7, 130, 2056), (70, 257, 1000), (129, 128, 64),
                                    (300, 520, 776), (2000, 700, 520)])
 def test_whole_numbers_are_exact(cuda_lib, T, N, K):
