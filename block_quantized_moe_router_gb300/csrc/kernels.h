@@ -31,8 +31,8 @@ cudaError_t launch_hash_route(const int64_t* tid2eid, const int32_t* token_ids, 
 cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k, int scoring,
                                 int renorm, float scaling, int n_group, int topk_group, int group_top,
                                 int32_t* ids, float* w, int32_t* status, cudaStream_t st);
-// The router product and that selection in one launch: E <= 256, x and wr 16-byte aligned;
-// cudaErrorNotSupported (nothing launched) otherwise.
+// The router product and that selection, in one launch for E <= 256; x and wr 16-byte aligned.
+// cudaErrorNotSupported (nothing launched) where the router's own kernels are faster.
 cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias, int T, int E, int H, int k,
                                int scoring, int renorm, float scaling, int n_group, int topk_group,
                                int group_top, float* logits, int32_t* ids, float* w, int32_t* status,

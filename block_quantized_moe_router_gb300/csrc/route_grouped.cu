@@ -512,13 +512,16 @@ cudaError_t launch_given(const float* logits, const float* bias, int T, const Gr
 }
 
 // ------------------------------------------------------------------------------------------
-// From tokens: the router product and the selection in one launch, for E <= 256.
+// From tokens: the router product and the selection in one launch, for E <= 256.  More experts go through
+// the same kernel in blocks of up to 256 (grid y) that write their logits only; the selection follows.
 //
 // A cluster takes 128 tokens, its CTAs a part of K each: x (the MMA's 128 rows) and the router (all
 // experts as the N side) stream through a TMA ring into a TMEM accumulator.  Each CTA owns
 // 128 / splits of the tokens; the partial logits go from tensor memory to the owners' shared memory,
 // where a warp per token adds them in rank order, writes the logits and selects.  The logits never
-// come back from memory, and for few tokens a launch is saved.
+// come back from memory, and for few tokens a launch is saved.  Where K has fewer stages than there is
+// room for CTAs, the CTAs beyond add no part and only own tokens (178 x 72 x 160: 15.9 us with 2 CTAs a
+// tile, 8.1 with 16).
 // ------------------------------------------------------------------------------------------
 constexpr int kFusedThreads = 512;
 constexpr int kFusedK = 64;
@@ -531,7 +534,10 @@ struct FusedMaps {
 };
 
 struct FusedArgs {
-    int T, nk, n;           // n: experts rounded up to 16, the MMA's columns
+    int T, nk, n;           // n: experts of a block rounded up to 16, the MMA's columns
+    int E;                  // all experts, the length of a row of logits
+    int select;             // 0: write the logits only
+    int parts;              // CTAs of a cluster that have a part of K
     int own, stages;        // tokens per CTA of a tile; ring stages
     int box_x;              // token rows a TMA box brings
     int landing_at;         // byte offsets: of the landing area (0: over the ring)
@@ -557,8 +563,9 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     const int64_t t0 = (int64_t)(blockIdx.x / splits) * 128;
     const int rows = (int)min((int64_t)128, a.T - t0);  // tokens of this tile
     const int stage_bytes = kFusedA + a.n * 128;
-    const int k_begin = (int)((int64_t)a.nk * rank / splits), k_end = (int)((int64_t)a.nk * (rank + 1) / splits);
-    const int steps = k_end - k_begin;
+    const int k_begin = (int)((int64_t)a.nk * rank / a.parts), k_end = (int)((int64_t)a.nk * (rank + 1) / a.parts);
+    const int steps = rank < a.parts ? k_end - k_begin : 0;
+    const int e0 = (int)blockIdx.y * a.n, experts = min(a.n, a.E - e0);  // of this block
     const int pitch = a.n + 4;  // floats: 16-byte accesses of eight rows meet 32 banks
     float* landing = reinterpret_cast<float*>(smem + a.landing_at);  // [rank][own token][pitch]
     uint32_t tm_cols = 32;
@@ -595,7 +602,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
             uint8_t* base = smem + s * stage_bytes;
             const int kx = (k_begin + i) * kFusedK;
             mbar_arrive_expect_tx(&full[s], bytes);
-            tma_load_2d(base + kFusedA, &maps.w, kx, 0, &full[s]);
+            tma_load_2d(base + kFusedA, &maps.w, kx, e0, &full[s]);
             tma_load_2d(base, &maps.x, kx, (int)t0, &full[s]);  // rows beyond the box: never read back
             ++issued;
         }
@@ -630,7 +637,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     {  // a warp's lane quarter: tokens 32 q + lane; the four warps of a quarter share the experts
         tc_fence_after();
         const int q = warp & 3, row = 32 * q + lane;
-        if (32 * q < rows) {
+        if (32 * q < rows && rank < a.parts) {
             const int owner = min(row / a.own, splits - 1), at = row - owner * a.own;
             const uint32_t dst = map_rank(smem_u32(landing + ((int64_t)rank * a.own + at) * pitch), owner);
             for (int c = 16 * (warp >> 2); c < a.n; c += 16 * (kFusedThreads / 128)) {
@@ -648,7 +655,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     }
     float bv[EPL];  // on its way while the parts land
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) bv[j] = a.bias && lane + 32 * j < P.E ? __ldg(a.bias + lane + 32 * j) : 0.f;
+    for (int j = 0; j < EPL; ++j) bv[j] = a.bias && lane + 32 * j < experts ? __ldg(a.bias + lane + 32 * j) : 0.f;
     __syncthreads();
     cluster_sync();  // every part has landed
     if (warp == 1) {
@@ -663,16 +670,16 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
 #pragma unroll
         for (int j = 0; j < EPL; ++j) raw[j] = 0.f;
 #pragma unroll 2
-        for (int s = 0; s < splits; ++s) {
+        for (int s = 0; s < a.parts; ++s) {
             const float* src = landing + ((int64_t)s * a.own + i) * pitch + lane;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < P.E) raw[j] += src[32 * j];
+                if (lane + 32 * j < experts) raw[j] += src[32 * j];
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < P.E) a.logits[t * P.E + lane + 32 * j] = raw[j];
-        route_token<EPL>(P, raw, bv, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
+            if (lane + 32 * j < experts) a.logits[t * a.E + e0 + lane + 32 * j] = raw[j];
+        if (a.select) route_token<EPL>(P, raw, bv, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
     }
 }
 
@@ -680,9 +687,9 @@ template <int EPL>
 cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, int splits, cudaStream_t st) {
     // ring | landing | scratch, or the last two over the ring where they do not fit beside it
     const int stage = kFusedA + a.n * 128;
-    const int landing = splits * a.own * (a.n + 4) * 4;
-    const int scratch = (int)sizeof(RouteScratch<EPL>) * (a.own < kFusedThreads / 32 ? a.own : kFusedThreads / 32);
-    const int steps = (a.nk + splits - 1) / splits;
+    const int landing = a.parts * a.own * (a.n + 4) * 4;
+    const int scratch = a.select ? (int)sizeof(RouteScratch<EPL>) * (a.own < kFusedThreads / 32 ? a.own : kFusedThreads / 32) : 0;
+    const int steps = (a.nk + a.parts - 1) / a.parts;
     const int landing16 = (landing + 15) / 16 * 16;
     a.stages = (kFusedSmemMax - 1024 - landing16 - scratch) / stage;
     const bool beside = a.stages >= 3 || a.stages >= steps;
@@ -700,7 +707,7 @@ cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, in
     const cudaError_t err = allow_large_launch(kernel, kFusedSmemMax, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * splits));
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * splits), (unsigned)((a.E + a.n - 1) / a.n));
     cfg.blockDim = dim3(kFusedThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -741,19 +748,27 @@ cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias,
                                int scoring, int renorm, float scaling, int n_group, int topk_group,
                                int group_top, float* logits, int32_t* ids, float* w, int32_t* status,
                                cudaStream_t st) {
-    if (E > 256) return cudaErrorNotSupported;
     const GroupRule P = make_rule(bias, E, k, scoring, renorm, scaling, n_group, topk_group, group_top);
+    const int blocks = (E + 255) / 256;
+    // Two launches save none, and a small product is done sooner without clusters: 1 x 512 x 2048 7.5 us
+    // against 8.9 (1 x 384 x 7168 10.7 against 9.4), 161 x 466 x 352 9.9 against 15.6 (2702 tokens 28.8 against
+    // 20.9; 16 x 512 x 2048 33.3 against 9.5).
+    if (blocks > 1 && (T == 1 ? H <= 4096 : T <= 1024 && H <= 512)) return cudaErrorNotSupported;
     FusedArgs a{};
     a.T = T;
+    a.E = E;
+    a.select = blocks == 1;
     a.nk = (H + kFusedK - 1) / kFusedK;
-    a.n = (E + 15) / 16 * 16;
-    a.bias = bias; a.logits = logits; a.ids = ids; a.w = w; a.status = status;
+    a.n = ((E + blocks - 1) / blocks + 15) / 16 * 16;
+    a.bias = a.select ? bias : nullptr;
+    a.logits = logits; a.ids = ids; a.w = w; a.status = status;
     // as many CTAs per tile as keep every cluster resident at one CTA per SM (152 SMs hold 7, 15,
-    // 36 and 76 clusters of 16, 8, 4 and 2)
-    const int64_t tiles = ((int64_t)T + 127) / 128;
-    int splits = tiles <= 7 ? 16 : tiles <= 15 ? 8 : tiles <= 36 ? 4 : tiles <= 76 ? 2 : 1;
-    while (splits > a.nk) splits /= 2;
+    // 36 and 76 clusters of 16, 8, 4 and 2), but beyond one per stage only to share many tokens
+    const int64_t tiles = ((int64_t)T + 127) / 128 * blocks;
     const int rows = T < 128 ? T : 128;
+    int splits = tiles <= 7 ? 16 : tiles <= 15 ? 8 : tiles <= 36 ? 4 : tiles <= 76 ? 2 : 1;
+    while (splits > a.nk && rows <= splits / 2 * (kFusedThreads / 32)) splits /= 2;
+    a.parts = splits < a.nk ? splits : a.nk;
     a.own = (rows + splits - 1) / splits;
     a.box_x = (rows + 7) / 8 * 8;
     FusedMaps m{};
@@ -762,7 +777,10 @@ cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias,
     if (E <= 32) return launch_fused<1>(m, a, P, splits, st);
     if (E <= 64) return launch_fused<2>(m, a, P, splits, st);
     if (E <= 128) return launch_fused<4>(m, a, P, splits, st);
-    return launch_fused<8>(m, a, P, splits, st);
+    const cudaError_t err = launch_fused<8>(m, a, P, splits, st);
+    if (err != cudaSuccess || a.select) return err;
+    return launch_topk_grouped(logits, bias, T, E, k, scoring, renorm, scaling, n_group, topk_group, group_top, ids, w,
+                               status, st);
 }
 
 }  // namespace moe

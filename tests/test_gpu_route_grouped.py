@@ -128,7 +128,11 @@ def _grid(T, E, H, seed):
     (17, 64, 2048, 4, 2, 6), (53, 180, 1184, 12, 5, 6), (64, 256, 7168, 16, 6, 8), (127, 128, 512, 8, 4, 8),
     (128, 128, 384, 8, 4, 8), (129, 256, 1152, 4, 2, 8), (300, 384, 256, 6, 3, 8), (511, 72, 800, 3, 2, 5),
     (1000, 512, 640, 16, 4, 16), (4096, 256, 512, 16, 6, 8), (5000, 40, 32, 4, 2, 4), (9900, 96, 64, 8, 3, 5),
-    (10100, 256, 128, 8, 3, 8), (2, 300, 96, 3, 2, 7), (900, 330, 160, 33, 4, 16), (7, 1, 64, 1, 1, 1)])
+    (10100, 256, 128, 8, 3, 8), (2, 300, 96, 3, 2, 7), (900, 330, 160, 33, 4, 16), (7, 1, 64, 1, 1, 1),
+    # blocks of experts, the last one short or ending off 16; fewer stages of K than CTAs share the tokens
+    (1, 384, 7168, 8, 4, 8), (70, 272, 7584, 16, 11, 5), (161, 510, 2048, 3, 2, 9), (1500, 466, 352, 1, 1, 16),
+    (5000, 257, 64, 1, 1, 4), (12000, 512, 96, 8, 3, 8), (178, 72, 160, 8, 7, 13), (245, 120, 224, 12, 5, 14),
+    (128, 192, 32, 64, 9, 8), (100, 256, 64, 4, 3, 8), (640, 8, 32, 2, 1, 3)])
 def test_from_tokens(cuda_lib, T, E, H, groups, keep, k):
     x, w = _grid(T, E, H, T + E)
     bias = torch.rand(E, device="cuda") * 0.2 - 0.1
