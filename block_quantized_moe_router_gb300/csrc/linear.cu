@@ -67,11 +67,11 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t nco
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrive on `bar` of both CTAs of the pair once this thread's earlier MMAs have completed.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+// Arrive on `bar` of the CTAs in `mask` (both of the pair) once this thread's earlier MMAs have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint32_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)), "h"((uint16_t)3) : "memory");
+            smem_u32(bar)), "h"((uint16_t)mask) : "memory");
 }
 template <int PAIR>
 __device__ __forceinline__ void mma_f16kind(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
@@ -146,30 +146,32 @@ __device__ __forceinline__ void pack_all(const float (&z)[C], uint32_t (&w)[C / 
     }
 }
 
-// The residual of feature n of up to four consecutive rows from t on, and these rows' results (the lanes of
-// a warp hold consecutive features).
-__device__ __forceinline__ void load_residual(const LinArgs& a, int64_t t, int rows, int n, uint32_t (&rw)[4]) {
+// The residual of feature n of up to C consecutive rows from t on, and these rows' results (the lanes of a
+// warp hold consecutive features).
+template <int C>
+__device__ __forceinline__ void load_residual(const LinArgs& a, int64_t t, int rows, int n, uint32_t (&rw)[C]) {
     const uint16_t* res = static_cast<const uint16_t*>(a.res) + t * a.ldr + n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C; ++i)
         if (i < rows) rw[i] = res[i * a.ldr];
 }
-__device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[4],
-                                               const float (&u)[4], const uint32_t (&rw)[4]) {
+template <int C>
+__device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[C],
+                                               const float (&u)[C], const uint32_t (&rw)[C]) {
     const float b = a.bias ? __ldg(a.bias + n) : 0.f, c = a.bias_mul ? __ldg(a.bias_mul + n) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] += b;
+    for (int i = 0; i < C; ++i) z[i] += b;
     apply_func(a.func, z);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C; ++i) {
         if (a.gated) z[i] *= u[i] + c;
         if (a.res) z[i] += a.f16 ? __half2float(__ushort_as_half((unsigned short)rw[i])) : __uint_as_float(rw[i] << 16);
     }
-    uint32_t w[2];
+    uint32_t w[C / 2];
     pack_all(z, w, a.f16);
     uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.ldo + n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C; ++i)
         if (i < rows) out[i * a.ldo] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
 }
 
@@ -206,43 +208,70 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Few rows.  grid (tiles of W rows * splits of K, tiles of x rows), clusters of `splits` CTAs.  A tile
-// is 128 rows of W, or 64 of W and 64 of V.  Warp 0 loads, warp 1 issues the MMAs, warps 2-5 send the
-// accumulator (lane = W row, column = row of x) to its owners: each CTA of the cluster owns `own`
-// columns and has a landing area for every CTA's part of them.  After one cluster barrier each CTA
-// adds its columns' parts, in rank order, from its own shared memory.
+// Few rows.  grid (tiles of W rows * CTAs of a cluster, tiles of x rows).  A tile is 128 rows of W, or 64 of
+// W and 64 of V; `splits` parts of K make its cluster.  Warp 0 loads, warp 1 issues the MMAs, and the eight
+// warps send the accumulator (lane = W row, column = row of x) to its owners: each CTA owns `own` columns of
+// its features and has a landing area for every part of them.  After one cluster barrier each CTA adds its
+// columns' parts, in rank order, from its own shared memory.  Where a tile has one part of K and no gate, a lane
+// has all of its feature and the rows go out straight from tensor memory (pairs, 128 rows of 7168 x 2048: 11.8
+// us, 14.3 through the landing area).
+//
+// PAIR: a part of K belongs to two CTAs (cta_group::2), each with half of the tile's weight rows and half of
+// the rows of x, which both use.  An SM's share of the L2 rate bounds the loads, and of every 64 elements of
+// K a CTA then takes 64 (rows of W) + rows / 2 lines and not 128 + rows; its accumulator, and with it the
+// exchange, is half as large.  In tensor memory lanes 0 to 63 hold the CTA's 64 weight rows against the first
+// half of x, lanes 64 to 127 against the second.  128 rows of 7168 x 2048: 11.8 us against 15.7 in single CTAs;
+// 16 rows 9.9 against 8.8, where the latency of a stage counts and not its bytes.
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
-constexpr int kFewSplits = 8;    // CTAs per cluster at most (the portable cluster size)
-constexpr int kFewRows = 128;    // rows of x per tile at most
+constexpr int kFewSplits = 8;    // parts of K at most; CTAs of a cluster too (the portable cluster size)
+constexpr int kFewStages = 8;
 constexpr int kSmSmem = 228 * 1024, kFewSmemMax = 226 * 1024;  // shared memory of an SM, and of a CTA here
-__host__ __device__ constexpr int few_own(int rows, int splits) { return ((rows + splits - 1) / splits + 3) / 4 * 4; }
-__host__ __device__ constexpr int few_pitch(int own) { return own | 4; }  // own is a multiple of 4
-__host__ __device__ constexpr int few_smem(int rows, int splits, int stages) {
-    return stages * (kLinA + rows * 128) + splits * 128 * few_pitch(few_own(rows, splits)) * 4 + 1024;
-}
+template <bool PAIR>
+struct Few {
+    static constexpr int kRows = PAIR ? 256 : 128;   // rows of x per tile at most
+    static constexpr int kStep = PAIR ? 32 : 16;     // a tile's rows of x are a multiple of it
+    static constexpr int kW = PAIR ? 64 : 128;       // weight rows of a CTA
+    static constexpr int kA = kW * 128;              // bytes of them per stage
+    static constexpr int kCtas = PAIR ? 2 : 1;       // per part of K
+    __host__ __device__ static constexpr int own(int rows, int splits) { return ((rows + splits - 1) / splits + 3) / 4 * 4; }
+    __host__ __device__ static constexpr int pitch(int own) { return own | 4; }  // own is a multiple of 4
+    __host__ __device__ static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
+    // A pair takes all of tensor memory, so that its CTAs hold the same columns, and more than half of an SM's
+    // shared memory, so that no two pairs wait for each other's columns on shared SMs.
+    static constexpr int kSmemMin = PAIR ? 116 * 1024 : 0;
+    __host__ __device__ static constexpr int rest(int rows, int splits) {  // beside the stages
+        return splits * kW * pitch(own(rows, splits)) * 4 + 1024;
+    }
+    __host__ __device__ static constexpr int smem(int rows, int splits, int stages) {
+        const int need = stages * stage(rows) + rest(rows, splits);
+        return need > kSmemMin ? need : kSmemMin;
+    }
+};
 
-
+template <bool PAIR>
 __global__ void __launch_bounds__(kFewThreads)
 linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
+    using F = Few<PAIR>;
     extern __shared__ uint8_t lin_smem[];
-    __shared__ uint64_t full[8], empty[8], acc_full;
+    __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full;
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t splits = cluster_size();
-    const uint32_t rank = cluster_rank();
-    const int per_tile = a.gated ? 64 : 128;
-    const int n0 = (int)(blockIdx.x / splits) * per_tile;
+    const uint32_t ctas = cluster_size(), cta = cluster_rank();
+    const uint32_t splits = ctas / F::kCtas, rank = cta / F::kCtas;  // part of K
+    const uint32_t half = cta % F::kCtas, first = cta - half;        // CTA of the pair, and its first one
+    const int per_cta = a.gated ? F::kW / 2 : F::kW;                 // features
+    const int n0 = ((int)(blockIdx.x / ctas) * F::kCtas + (int)half) * per_cta;
     const int t0 = (int)blockIdx.y * a.rows_t;
-    const int NT = a.rows_t;
+    const int NT = a.rows_t, x_rows = NT / F::kCtas;  // of the tile, and of them here
     const int k_begin = (int)((int64_t)a.nk * rank / splits), k_end = (int)((int64_t)a.nk * (rank + 1) / splits);
-    const int stage_bytes = kLinA + NT * 128;
+    const int stage_bytes = F::stage(NT);
     const int ncols = min(NT, a.T - t0);
     // [rank][W row][own columns, padded so that 16-byte accesses of 8 rows meet 32 banks]
     float* landing = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
-    const int own = few_own(NT, (int)splits), pitch = few_pitch(own);
-    uint32_t tm_cols = 32;
+    const int own = F::own(NT, (int)splits), pitch = F::pitch(own);
+    uint32_t tm_cols = PAIR ? 512 : 32;
     while (tm_cols < (uint32_t)NT) tm_cols *= 2;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
@@ -255,18 +284,26 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         prefetch_tmap(&maps.w);
         if (a.gated) prefetch_tmap(&maps.v);
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, tm_cols);
+    if (warp == 1) {
+        if constexpr (PAIR) tmem_alloc_pair(&tmem_slot, tm_cols);
+        else tmem_alloc(&tmem_slot, tm_cols);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+    // This CTA runs: its shared memory may be written from the others.  A pair signals each other's barriers
+    // from the first stage on, single CTAs meet at the exchange.
+    cluster_arrive();
+    if constexpr (PAIR) cluster_wait();
     pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
+    const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
     const int steps = k_end - k_begin;
     if (warp == 0 && elect_one()) {
+        const uint32_t full0 = PAIR ? map_rank(smem_u32(&full[0]), first) : smem_u32(&full[0]);
         int issued = 0;
         RingPos at;
         for (int i = 0; i < steps; ++i, at.next(a.stages)) {
@@ -277,34 +314,48 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
             }
             uint8_t* base = smem + s * stage_bytes;
             const int kx = (k_begin + i) * kLinK;
-            mbar_arrive_expect_tx(&full[s], stage_bytes);
-            tma_load_2d(base, &maps.w, kx, n0, &full[s]);
-            if (a.gated) tma_load_2d(base + kLinA / 2, &maps.v, kx, n0, &full[s]);
-            tma_load_2d(base + kLinA, &maps.x, kx, t0, &full[s]);
+            if constexpr (PAIR) {
+                const uint32_t dst = smem_u32(base), bar = full0 + 8 * s;
+                if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+                tma_load_pair(dst, &maps.w, kx, n0, bar);
+                if (a.gated) tma_load_pair(dst + F::kA / 2, &maps.v, kx, n0, bar);
+                tma_load_pair(dst + F::kA, &maps.x, kx, t0 + (int)half * x_rows, bar);
+            } else {
+                mbar_arrive_expect_tx(&full[s], stage_bytes);
+                tma_load_2d(base, &maps.w, kx, n0, &full[s]);
+                if (a.gated) tma_load_2d(base + F::kA / 2, &maps.v, kx, n0, &full[s]);
+                tma_load_2d(base + F::kA, &maps.x, kx, t0, &full[s]);
+            }
             ++issued;
         }
-        // whoever gives up, no copy is in flight when the CTA ends
-        for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
-            at.back(a.stages);
-            mbar_wait_suspended(&full[at.slot], at.parity);
-        }
-    } else if (warp == 1 && elect_one()) {
-        const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
-        RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
-            const int s = at.slot;
-            if (!mbar_wait_suspended(&full[s], at.parity)) {
-                give_up();
-                break;
+        // whoever gives up, no copy is in flight when the CTA ends (the pair's arrive at its first CTA)
+        if (half == 0)
+            for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
+                at.back(a.stages);
+                mbar_wait_suspended(&full[at.slot], at.parity);
             }
-            tc_fence_after();
-            const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
+    } else if (warp == 1 && elect_one()) {
+        if (half == 0) {
+            const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
+            RingPos at;
+            for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+                const int s = at.slot;
+                if (!mbar_wait_suspended(&full[s], at.parity)) {
+                    give_up();
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
-                mma_f16kind<0>(tmem, ad + 2 * j, ad + (kLinA >> 4) + 2 * j, idesc, (i | j) != 0);
-            tc_commit(&empty[s]);
+                for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                    mma_f16kind<PAIR>(tmem, ad + 2 * j, ad + (F::kA >> 4) + 2 * j, idesc, (i | j) != 0);
+                if constexpr (PAIR) tc_commit_pair(&empty[s], 3u << first);
+                else tc_commit(&empty[s]);
+            }
+            // arrives when every MMA has completed
+            if constexpr (PAIR) tc_commit_pair(&acc_full, 3u << first);
+            else tc_commit(&acc_full);
         }
-        tc_commit(&acc_full);  // arrives when every MMA has completed
         if (!mbar_wait_suspended(&acc_full, 0)) give_up();
         tc_fence_before();
     } else if (warp >= 6) {
@@ -312,25 +363,37 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         if (a.res)
             for (int i = threadIdx.x - 192; i < my_cols * 2; i += 64) {
                 const int n = n0 + 64 * (i & 1);
-                if (n < a.N && (i & 1) * 64 < per_tile)
+                if (n < a.N && (i & 1) * 64 < per_cta)
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
-    cluster_wait();
+    if constexpr (!PAIR) cluster_wait();
     {  // the two warps of a lane quarter take alternate 16 columns
         tc_fence_after();
         const int q = warp & 3;
-        const uint32_t mine = smem_u32(landing + ((int)rank * 128 + 32 * q + lane) * pitch);
-        for (int c = 16 * (warp >> 2); c < ncols; c += 32) {
+        const int row = 32 * (PAIR ? q & 1 : q) + lane, c0 = PAIR && q >= 2 ? x_rows : 0;  // of tensor memory column 0
+        const uint32_t mine = smem_u32(landing + ((int)rank * F::kW + row) * pitch);
+        for (int c = c0 + 16 * (warp >> 2); c < min(ncols, c0 + x_rows); c += 32) {
+            if (direct) {
+                const int n = n0 + row, rows = min(16, ncols - c);
+                uint32_t rw[16] = {};
+                if (a.res && n < a.N) load_residual(a, (int64_t)t0 + c, rows, n, rw);
+                float z[16];
+                tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c - c0, reinterpret_cast<uint32_t(&)[16]>(z));
+                tmem_ld_wait();
+                if (n < a.N) finish_feature(a, (int64_t)t0 + c, rows, n, z, z, rw);
+                __syncwarp();
+                continue;
+            }
             int owner = c / own, at = c - owner * own;  // of the next four columns
             uint32_t v[16];
-            tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+            tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c - c0, v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 if (c + i < ncols) {
-                    st_cluster_v4(map_rank(mine + at * 4, owner), v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    st_cluster_v4(map_rank(mine + at * 4, owner * F::kCtas + half), v[i], v[i + 1], v[i + 2], v[i + 3]);
                     at += 4;
                     if (at == own) {
                         at = 0;
@@ -342,27 +405,28 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     }
     // Items of 32 features x 4 rows of x, lane = feature.  The residual is read one item ahead, the first
     // before the parts have landed (the compiler may not: out may be the residual).
-    const int shift = a.gated ? 1 : 2, items = ((my_cols + 3) / 4) << shift;  // per_tile / 32 blocks of features
+    const int blocks = per_cta / 32, shift = blocks >> 1;  // 1, 2 or 4 blocks of features
+    const int items = direct ? 0 : ((my_cols + 3) / 4) << shift;
     uint32_t rw[4] = {};
     const auto ahead = [&](int item) {
-        const int n = n0 + (item & ((1 << shift) - 1)) * 32 + lane, c = (item >> shift) * 4;
+        const int n = n0 + (item & (blocks - 1)) * 32 + lane, c = (item >> shift) * 4;
         if (a.res && item < items && n < a.N) load_residual(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, rw);
     };
     ahead(warp);
     cluster_sync();  // every part has landed
     for (int item = warp; item < items; item += kFewThreads / 32) {
-        const int r = (item & ((1 << shift) - 1)) * 32 + lane, c = (item >> shift) * 4;
+        const int r = (item & (blocks - 1)) * 32 + lane, c = (item >> shift) * 4;
         const float* src = landing + r * pitch + c;
         const uint32_t now[4] = {rw[0], rw[1], rw[2], rw[3]};
         ahead(item + kFewThreads / 32);
         float z[4] = {}, u[4] = {};
 #pragma unroll
-        for (int s = 0; s < kFewSplits; ++s)
+        for (int s = 0; s < kFewSplits / F::kCtas; ++s)
             if (s < (int)splits) {
-                const float4 p = *reinterpret_cast<const float4*>(src + s * 128 * pitch);
+                const float4 p = *reinterpret_cast<const float4*>(src + s * F::kW * pitch);
                 z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
                 if (a.gated) {
-                    const float4 g = *reinterpret_cast<const float4*>(src + (s * 128 + 64) * pitch);
+                    const float4 g = *reinterpret_cast<const float4*>(src + (s * F::kW + F::kW / 2) * pitch);
                     u[0] += g.x; u[1] += g.y; u[2] += g.z; u[3] += g.w;
                 }
             }
@@ -372,7 +436,8 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     __syncwarp();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, tm_cols);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, tm_cols);
+        else tmem_dealloc(tmem, tm_cols);
     }
 }
 
@@ -533,9 +598,9 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                         const uint64_t at = ad + h * (kManyHalf >> 4) + 2 * j;
                         mma_f16kind<1>(tmem + 256 * b, at, at + (kLinA >> 4), idesc, (k | h | j) != 0);
                     }
-                tc_commit_pair(&empty[s]);
+                tc_commit_pair(&empty[s], 3);
             }
-            tc_commit_pair(&acc_full[b]);
+            tc_commit_pair(&acc_full[b], 3);
         }
     } else if (warp >= 2 && warp < 10) {
         const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, parity of the columns' 16s
@@ -730,63 +795,81 @@ cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allo
     return cudaLaunchKernelEx(&cfg, kernel, m, a);
 }
 
-}  // namespace
+template <bool PAIR>
+cudaError_t launch_few(const LinMaps& m, const LinArgs& a, int splits, int N, cudaStream_t st) {
+    using F = Few<PAIR>;
+    const int per_tile = F::kW * F::kCtas / (a.gated ? 2 : 1), cluster = splits * F::kCtas;
+    const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
+    static std::atomic<uint64_t> allowed{0};
+    return launch_clusters(linear_few_kernel<PAIR>, kFewSmemMax, allowed, grid, cluster, kFewThreads,
+                           F::smem(a.rows_t, splits, a.stages), m, a, st);
+}
 
-namespace {
-
-// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all seven
-// choices at 156 sizes (1 to 11677 rows, N 88 to 7168, K 512 to 7168): the plan's choice takes 1 % longer
-// than the fastest one in the mean, 43 % at worst (64 x 2048 x 512: 7.2 us against 5.0).
-//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.36 / 0.29 / 0.22 us
-//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 1.2 us a tile
-//     besides, and 4.7 us once.  512 x 7168 x 2048: 18.0 us at 192 columns (one wave), 19.5 at 256.
-//   few rows: 64 elements cost a CTA 0.2 us, or what its SM's share of the L2 rate (102 GB/s) allows;
-//     1.4 us a wave and 0.9 us once besides, and the exchange and the sums of the parts.
-//     64 rows of the gated 2 x 2048 x 7168: 15.2 us, against 36.1 for the other kernel; 256 rows of
-//     7168 x 2048: 22.3 against 14.7; 1600 x 160 x 5848: 17.0 against 30.0.
+// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all ten
+// choices at 168 sizes (1 to 4096 rows, N 88 to 7168, K 512 to 7168): the plan's choice takes 1 % longer
+// than the fastest one in the mean, 19 % at worst.
+//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.38 / 0.31 / 0.25 us
+//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 0.95 us a tile
+//     besides, and 3.7 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.8 at 256.
+//   few rows: 64 elements cost a CTA 0.19 us, in pairs 0.24, or what its SM's share of the L2 rate (112 GB/s)
+//     allows; every row of x costs its exchange and sums, least where a part of K has a tile alone; 1.6 us
+//     a wave and 0.6 us once besides.  128 rows of the gated 2 x 2048 x 7168: 16.2 us in two parts by pairs,
+//     19.3 in four by single CTAs, 31.2 in the other kernel; 256 rows of 7168 x 2048: 15.4, 17.4 and 14.7.
 struct LinPlan {
-    bool few;
+    bool few, pair;
     int width;                   // many: columns per tile
-    int splits, stages, rows_t;  // few: CTAs per cluster, ring stages, rows of x per tile
+    int splits, stages, rows_t;  // few: parts of K, ring stages, rows of x per tile
 };
+
+template <bool PAIR>
+void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
+    using F = Few<PAIR>;
+    const int tiles_t = (T + F::kRows - 1) / F::kRows;
+    const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
+    const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
+    const int64_t tiles = (int64_t)tiles_t * ((N + per_tile - 1) / per_tile) * F::kCtas;
+    const float stage_kb = (float)F::stage(rows) / 1024.f;
+    for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
+        const int kbs = (nk + splits - 1) / splits;
+        int stages = PAIR ? (kFewSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
+        stages = stages < kFewStages ? stages : kFewStages;
+        stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
+        const int smem = F::smem(rows, splits, stages);
+        if (smem > kFewSmemMax) continue;
+        // CTAs an SM holds, and how many of these places clusters of 4 and 8 leave usable (152 SMs hold 36
+        // clusters of 4 and 15 of 8 at one CTA per SM, 36 of 8 at two)
+        const int fit = kSmSmem / (smem + 1024 + 256), cluster = splits * F::kCtas;
+        const int usable = cluster < 4 ? 152 : cluster == 8 && fit == 1 ? 120 : 144;
+        const int64_t places = (int64_t)sms * fit * usable / 152;
+        const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
+        const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
+        const float per_k_lat = PAIR ? 0.24f : 0.19f, per_k_bw = (float)on_sm * stage_kb / 112.f;
+        const float per_row = splits == 1 && !gated ? (PAIR ? 0.012f : 0.037f) : (PAIR ? 0.0175f : 0.051f);
+        const float us = (float)waves * ((float)kbs * (per_k_bw > per_k_lat ? per_k_bw : per_k_lat) +
+                                         per_row * (float)rows + 1.6f) + (PAIR ? 0.65f : 0.6f);
+        if (us < best_us) {
+            best_us = us;
+            best = LinPlan{true, PAIR, 0, splits, stages, rows};
+        }
+    }
+}
 
 LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
     LinPlan best{};
     float best_us = 1e30f;
-    const float per_k[3] = {0.36f, 0.29f, 0.22f};
+    const float per_k[3] = {0.38f, 0.31f, 0.25f};
     for (int i = 0; i < 3; ++i) {
         const int width = 256 - 64 * i;
         const int64_t tiles = ManySched(T, N, gated ? width / 2 : width).total;
         const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-        const float us = (float)waves * ((float)nk * per_k[i] + 1.2f) + 4.7f;
+        const float us = (float)waves * ((float)nk * per_k[i] + 0.95f) + 3.7f;
         if (us < best_us) {
             best_us = us;
-            best = LinPlan{false, width, 0, 0, 0};
+            best = LinPlan{false, false, width, 0, 0, 0};
         }
     }
-    const int tiles_t = (T + kFewRows - 1) / kFewRows;
-    const int rows = ((T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
-    const int64_t tiles = (int64_t)tiles_t * ((N + (gated ? 63 : 127)) / (gated ? 64 : 128));
-    const float stage_kb = (float)(kLinA + rows * 128) / 1024.f;
-    for (int splits = 1; splits <= kFewSplits && splits <= nk; splits *= 2) {
-        const int kbs = (nk + splits - 1) / splits;
-        const int stages = kbs < 4 ? (kbs < 2 ? 2 : kbs) : 4;
-        const int smem = few_smem(rows, splits, stages);
-        if (smem > kFewSmemMax) continue;
-        // CTAs an SM holds, and how many of these places clusters of 4 and 8 leave usable (152 SMs hold 36
-        // clusters of 4 and 15 of 8 at one CTA per SM, 36 of 8 at two)
-        const int fit = kSmSmem / (smem + 1024 + 256);
-        const int usable = splits < 4 ? 152 : splits == 8 && fit == 1 ? 120 : 144;
-        const int64_t places = (int64_t)sms * fit * usable / 152;
-        const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
-        const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
-        const float per_k_bw = (float)on_sm * stage_kb / 102.f;
-        const float us = (float)waves * ((float)kbs * (per_k_bw > 0.2f ? per_k_bw : 0.2f) + 0.046f * (float)rows + 1.4f) + 0.9f;
-        if (us < best_us) {
-            best_us = us;
-            best = LinPlan{true, 0, splits, stages, rows};
-        }
-    }
+    plan_few<false>(T, N, nk, gated, sms, best_us, best);
+    plan_few<true>(T, N, nk, gated, sms, best_us, best);
     return best;
 }
 
@@ -807,17 +890,15 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms);
     LinMaps m{};
     // rows of W per box, and rows of x
-    const int box_w = plan.few ? (a.gated ? 64 : 128) : plan.width / 2, box_x = plan.few ? plan.rows_t : 128;
+    const int box_w = plan.few ? (plan.pair ? 64 : 128) / (a.gated ? 2 : 1) : plan.width / 2;
+    const int box_x = !plan.few ? 128 : plan.pair ? plan.rows_t / 2 : plan.rows_t;
     if (!encode_rows16(&m.x, x, d.K, d.T, d.ldx, box_x, kLinK) || !encode_rows16(&m.w, w, d.K, d.N, d.ldw, box_w, kLinK) ||
         (a.gated && !encode_rows16(&m.v, w_mul, d.K, d.N, d.ldw, box_w, kLinK)))
         return cudaErrorInvalidValue;
     if (plan.few) {
         a.rows_t = plan.rows_t;
         a.stages = plan.stages;
-        const int tiles_n = (d.N + box_w - 1) / box_w, tiles_t = (d.T + plan.rows_t - 1) / plan.rows_t;
-        static std::atomic<uint64_t> allowed{0};
-        return launch_clusters(linear_few_kernel, kFewSmemMax, allowed, dim3(tiles_n * plan.splits, tiles_t), plan.splits, kFewThreads,
-                               few_smem(plan.rows_t, plan.splits, plan.stages), m, a, st);
+        return plan.pair ? launch_few<true>(m, a, plan.splits, d.N, st) : launch_few<false>(m, a, plan.splits, d.N, st);
     }
     // TMA addresses rows that start at multiples of 16 bytes
     a.width = plan.width;

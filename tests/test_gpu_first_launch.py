@@ -45,6 +45,7 @@ print("right")
 
 
 @pytest.mark.parametrize("what,T,N,K", [("gated", 1, 2048, 7168), ("gated", 300, 1024, 7168), ("plain", 5, 7168, 2048),
+                                        ("plain", 128, 7168, 2048), ("gated", 100, 2048, 7168),
                                         ("plain", 1000, 2048, 2048), ("route", 1, 256, 7168), ("route", 500, 64, 2048)])
 def test_first_launch(cuda_lib, what, T, N, K):
     done = subprocess.run([sys.executable, "-c", CHILD, what, str(T), str(N), str(K)], cwd=ROOT, capture_output=True,

@@ -131,6 +131,21 @@ def test_tall_and_even(cuda_lib, T, N, K):
         assert (wide[:, :2] == 7).all() and (wide[:, N + 2:] == 7).all()
 
 
+# the middle range, where pairs of CTAs share the rows of x: tiles of 32 to 256 rows, one, two and four parts
+# of K, odd ends of every kind
+@pytest.mark.parametrize("T", [33, 64, 95, 128, 129, 161, 200, 255, 256, 257, 384])
+@pytest.mark.parametrize("N,K", [(7168, 1024), (2048, 2056), (513, 1544), (320, 4096), (131, 264), (5001, 2048)])
+def test_middle(cuda_lib, T, N, K):
+    for gated in (False, True):
+        dt = DT["f16" if (T + N) % 2 else "bf16"]
+        func = (T + N // 7 + gated) % 5
+        a = _make(T, N, K, dt, gated=gated, bias=T % 3 == 0, residual=(T + gated) % 2 == 0, seed=T + K)
+        ref, bound = _linear_ref(func=func, **a)
+        out = _run(a, func)
+        _check(out, ref, bound, dt)
+        assert torch.equal(out, _run(a, func)), "equal calls give equal bits"
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 300, 4096), (7, 130, 2056), (70, 257, 1000), (129, 128, 64),
                                    (300, 520, 776), (2000, 700, 520)])
 def test_whole_numbers_are_exact(cuda_lib, T, N, K):
