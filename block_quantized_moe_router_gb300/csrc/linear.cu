@@ -237,9 +237,10 @@ struct Few {
     __host__ __device__ static constexpr int own(int rows, int splits) { return ((rows + splits - 1) / splits + 3) / 4 * 4; }
     __host__ __device__ static constexpr int pitch(int own) { return own | 4; }  // own is a multiple of 4
     __host__ __device__ static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
-    // A pair takes all of tensor memory, so that its CTAs hold the same columns, and more than half of an SM's
-    // shared memory, so that no two pairs wait for each other's columns on shared SMs.
-    static constexpr int kSmemMin = PAIR ? 116 * 1024 : 0;
+    // A pair takes all of tensor memory, so that its CTAs hold the same columns, and so it takes all of the
+    // shared memory too: another cluster's CTAs beside it (of another stream) could hold columns on one SM
+    // and wait for a CTA that waits for this pair's columns on the other, and both for ever.
+    static constexpr int kSmemMin = PAIR ? kFewSmemMax : 0;
     __host__ __device__ static constexpr int rest(int rows, int splits) {  // beside the stages
         return splits * kW * pitch(own(rows, splits)) * 4 + 1024;
     }
