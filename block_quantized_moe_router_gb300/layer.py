@@ -38,7 +38,6 @@ class MoeLayer:
             raise ValueError("a layer has one shared expert: FP4 (I_shared) or bf16 (shared)")
         self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
         self.shared, self.norm_weight, self.norm_eps = shared, norm_weight, norm_eps
-        self._shared_h = None
         self._weights = (gate, up, down, sh_gate, sh_up, sh_down)  # keep alive
         self.desc = capi.ffn_desc(E, H, I, top_k, I_shared, gate, up, down, sh_gate, sh_up, sh_down,
                                   zero_experts)
@@ -130,9 +129,8 @@ class MoeLayer:
             return
         s = self.shared
         T, I = x.shape[0], s["gate"].shape[0]
-        if self._shared_h is None or self._shared_h.shape[0] < T:
-            self._shared_h = torch.empty((T, I), dtype=torch.bfloat16, device="cuda")
-        h = self._shared_h[:T]
+        with torch.cuda.stream(stream):  # h is freed before it is used up: only that stream may have it next
+            h = torch.empty((T, I), dtype=torch.bfloat16, device="cuda")
         capi.moe_linear(x, s["gate"], h, w_mul=s["up"], bias=s.get("gate_bias"),
                         bias_mul=s.get("up_bias"), func=capi.MOE_FUNC_SILU, dev_status=self.status,
                         stream=stream)
@@ -141,14 +139,18 @@ class MoeLayer:
 
     def block(self, delta, residual=None, *, logits_in=None, stream=None):
         """The layer with the residual add and norm before it: r = delta + residual, n = RMS norm of
-        r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta."""
+        r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta.  The
+        results belong to `stream` (the current one by default)."""
         if self.norm_weight is None:
             raise ValueError("the layer was built without norm_weight")
+        if stream is not None:  # what is freed on return goes back to the stream that still uses it
+            with torch.cuda.stream(stream):
+                return self.block(delta, residual, logits_in=logits_in)
         n = torch.empty_like(delta)
         r = torch.empty_like(delta)
         capi.moe_add_rms_norm(delta, self.norm_weight, n, residual=residual, sum_out=r,
-                              eps=self.norm_eps, stream=stream)
-        return self.forward(n, logits_in=logits_in, stream=stream)[0], r
+                              eps=self.norm_eps)
+        return self.forward(n, logits_in=logits_in)[0], r
 
     def forward(self, x=None, *, token_ids=None, logits_in=None, out=None, topk_ids=None,
                 topk_w=None, logits_out=None, stream=None):

@@ -100,6 +100,68 @@ def test_block_in_a_graph(cuda_lib):
     layer.close()
 
 
+def test_block_on_another_stream(cuda_lib):
+    """What block() lets go of on its return is not handed out again while its stream still uses it."""
+    cfg = synth.MoeConfig("t", T=300, H=512, I=256, E=24, k=4, scoring=synth.SCORE_SIGMOID, act=capi.MOE_ACT_BF16)
+    layer, inp, shared = _layer(cfg, seed=3, n_group=6, topk_group=3, group_top=2)
+    delta = torch.randn(300, 512, device="cuda").bfloat16()
+    resid = torch.randn(300, 512, device="cuda").bfloat16()
+    want = layer.block(delta, resid)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, mess = [], []
+    for _ in range(30):
+        got.append(layer.block(delta, resid, stream=side))
+        mess.append([torch.full(shape, float("nan"), dtype=dt, device="cuda")  # on the current stream, at once
+                     for shape, dt in (((300, 512), torch.bfloat16), ((300, 192), torch.bfloat16), ((300, 4), torch.float32),
+                                       ((300, 24), torch.float32))])
+        mess.pop()
+    torch.cuda.synchronize()
+    assert int(layer.status.item()) == 0
+    for out, r in got:
+        assert torch.equal(out, want[0]) and torch.equal(r, want[1])
+    layer.close()
+
+
+def test_streams_side_by_side(cuda_lib):
+    """Every kind of kernel that waits within clusters, at once on streams of its own."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    mk = lambda *s: (torch.randn(s, generator=g, device="cuda") / s[-1] ** 0.25).bfloat16()
+    wg, wu, wd = mk(1024, 2048), mk(1024, 2048), mk(2048, 1024)
+    jobs = []
+    for T in (3, 128, 200, 700):  # one CTA per part of K, pairs, many rows
+        x = mk(T, 2048)
+        jobs.append(lambda o, x=x: capi.moe_linear(x, wg, o, w_mul=wu, func=capi.MOE_FUNC_SILU, stream=torch.cuda.current_stream()))
+        jobs[-1].shape = (T, 1024)
+        h = mk(T, 1024)
+        jobs.append(lambda o, h=h: capi.moe_linear(h, wd, o, stream=torch.cuda.current_stream()))
+        jobs[-1].shape = (T, 2048)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for T, E in ((40, 128), (500, 256), (300, 384)):
+        x, w = mk(T, 2048), mk(E, 2048)
+        logits, tw = torch.empty(T, E, device="cuda"), torch.empty(T, 6, device="cuda")
+        jobs.append(lambda o, x=x, w=w, T=T, E=E, l=logits, tw=tw: capi.moe_route_grouped(
+            T=T, E=E, H=2048, top_k=6, scoring=1, renormalize=True, routed_scaling=1.0, n_group=8, topk_group=3,
+            group_top=2, x=x, w_router=w, logits_out=l, topk_ids=o, topk_w=tw, dev_status=status))
+        jobs[-1].shape = (T, 6)
+    kinds = [torch.int32 if j.shape[1] == 6 else torch.bfloat16 for j in jobs]
+    want = [torch.empty(j.shape, dtype=t, device="cuda") for j, t in zip(jobs, kinds)]
+    for j, o in zip(jobs, want):
+        j(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = [[torch.empty_like(o) for _ in range(40)] for o in want]
+    torch.cuda.synchronize()
+    for i in range(40):
+        for j, s, o in zip(jobs, streams, outs):
+            with torch.cuda.stream(s):
+                j(o[i])
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for o, w in zip(outs, want):
+        assert all(torch.equal(t, w) for t in o)
+
+
 def test_refusals(cuda_lib):
     cfg = synth.MoeConfig("r", T=2, H=256, I=128, E=8, k=2, scoring=synth.SCORE_SOFTMAX)
     with pytest.raises(ValueError):
