@@ -285,7 +285,7 @@ moe_status_t moe_route_grouped(const moe_route_desc* d, int32_t n_group, int32_t
 moe_status_t moe_linear(const moe_linear_desc* d, const void* x, const void* w, const void* w_mul,
                         const float* bias, const float* bias_mul, const void* residual, void* out,
                         int32_t* dev_status, void* stream) {
-    if (!d || d->T < 0 || d->N < 1 || d->N > kMaxLinear || d->K < 8 || d->K > kMaxLinear || d->K % 8)
+    if (!d || d->T < 0 || d->T > kMaxLinearRows || d->N < 1 || d->N > kMaxLinear || d->K < 8 || d->K > kMaxLinear || d->K % 8)
         return MOE_ERR_INVALID_ARG;
     if ((d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16) || d->func < MOE_FUNC_NONE ||
         d->func > MOE_FUNC_RELU)

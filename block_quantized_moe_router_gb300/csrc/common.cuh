@@ -17,6 +17,7 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 64;
 constexpr int kMaxLinear = 1 << 20;  // N and K of moe_linear
+constexpr int kMaxLinearRows = 1 << 30;
 constexpr int kMaxNorm = 16384;      // H of moe_add_rms_norm
 
 // ---- loads --------------------------------------------------------------------------------

@@ -826,6 +826,7 @@ template <bool PAIR>
 void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int tiles_t = (T + F::kRows - 1) / F::kRows;
+    if (tiles_t > 65535) return;  // grid y
     const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
     const int64_t tiles = (int64_t)tiles_t * ((N + per_tile - 1) / per_tile) * F::kCtas;

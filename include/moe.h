@@ -123,7 +123,7 @@ typedef struct {
 } moe_route_desc;
 
 /* A dense layer over T rows (moe_linear): x [T][K], w and w_mul [N][K], residual and out [T][N].
- * The ld fields are the distances between rows in elements.  Constraints (checked): T >= 0;
+ * The ld fields are the distances between rows in elements.  Constraints (checked): 0 <= T <= 2^30;
  * 1 <= N <= 1048576; K a multiple of 8, 8 <= K <= 1048576; ldx, ldw >= K and multiples of 8;
  * ldr, ldo >= N; every ld below 2^38. */
 typedef struct {

@@ -229,6 +229,31 @@ def test_streams_and_graphs(cuda_lib, T):
     assert torch.equal(y, _run(dict(x=h, w=down, w_mul=None, bias=None, bias_mul=None, residual=b["x"]), 0))
 
 
+@pytest.mark.parametrize("T", [3, 40, 200, 600])
+def test_rows_far_apart(cuda_lib, T):
+    """Element offsets beyond 32 bits, in every matrix."""
+    N, K = 72, 128
+    a = _make(T, N, K, torch.bfloat16, residual=True, seed=T)
+    ld = (1 << 33) // T // 8 * 8  # 16 GB from the first row to the last
+    buf = torch.empty(ld * T, dtype=torch.bfloat16, device="cuda")
+    far = lambda cols, at: buf.as_strided((T, cols), (ld, 1), at)
+    x, res, out = far(K, 0), far(N, 1024), far(N, 2048)
+    x.copy_(a["x"])
+    res.copy_(a["residual"])
+    ref, bound = _linear_ref(func=1, **a)
+    capi.moe_linear(x, a["w"], out, residual=res, func=1)
+    _check(out.clone(), ref, bound, torch.bfloat16)
+    odd = far(N, 4097)  # off 16 bytes
+    capi.moe_linear(x, a["w"], odd, residual=res, func=1)
+    assert torch.equal(odd, out)
+    weight = torch.ones(N, device="cuda").bfloat16()
+    s, n = far(N, 6144), far(N, 8192)
+    capi.moe_add_rms_norm(out, weight, n, residual=res, sum_out=s)
+    s2, n2 = (torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    capi.moe_add_rms_norm(out.clone(), weight, n2, residual=res.clone(), sum_out=s2)
+    assert torch.equal(s, s2) and torch.equal(n, n2)
+
+
 def test_no_rows(cuda_lib):
     a = _make(0, 64, 64, torch.bfloat16)
     assert _run(a, 0).shape == (0, 64)

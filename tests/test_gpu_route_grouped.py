@@ -201,6 +201,18 @@ def test_scores_closer_than_fp32_can_tell(cuda_lib, scoring, tokens):
         _agree(got, _ref(logits, 8, scoring, True, 1.0, groups, 3, top, bias), 1.0)
 
 
+def test_offsets_beyond_32_bits(cuda_lib):
+    """The last of 4.3 million tokens' logits lie 2^31 elements from the first."""
+    T, E = (1 << 31) // 512 + 1000, 512
+    logits = torch.zeros(T, E, device="cuda")
+    rows = torch.randn(1000, E, device="cuda")
+    logits[-1000:] = rows
+    got = _run(3, SIGMOID, True, 1.0, 8, 2, 2, logits=logits)
+    assert got[3] == 0
+    assert (got[0][:-1000] == torch.tensor([0, 1, 2], device="cuda")).all()
+    _agree((got[0][-1000:], got[1][-1000:]), _ref(rows, 3, SIGMOID, True, 1.0, 8, 2, 2), 1.0)
+
+
 def test_ties_go_to_the_lowest(cuda_lib):
     for bias in (None, torch.zeros(64, device="cuda")):
         logits = torch.zeros(9, 64, device="cuda")

@@ -49,7 +49,7 @@ def _linear(lib, x=P, w=P, w_mul=None, bias=None, bias_mul=None, residual=None, 
 def test_linear(lib):
     assert _linear(lib, T=0) == capi.MOE_OK
     odd = ctypes.c_void_p(0x1008)
-    bad = [dict(T=-1), dict(N=0), dict(N=(1 << 20) + 1), dict(K=0), dict(K=60), dict(K=(1 << 20) + 8), dict(dtype=2),
+    bad = [dict(T=-1), dict(T=(1 << 30) + 1), dict(N=0), dict(N=(1 << 20) + 1), dict(K=0), dict(K=60), dict(K=(1 << 20) + 8), dict(dtype=2),
            dict(dtype=-1), dict(func=5), dict(func=-1), dict(ldx=56), dict(ldx=68), dict(ldw=56), dict(ldw=65),
            dict(ldo=31), dict(ldr=31, residual=P), dict(ldx=1 << 38), dict(x=None), dict(w=None), dict(out=None), dict(x=odd),
            dict(w=odd), dict(w_mul=odd), dict(out=ctypes.c_void_p(0x1001)), dict(residual=ctypes.c_void_p(0x1001)),
