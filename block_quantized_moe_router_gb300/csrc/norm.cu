@@ -2,7 +2,7 @@
 //
 // A CTA per row, or a warp per row for short ones.  The row stays in registers between the sum of
 // squares and the scaling, so every input is read once and every output written once; the kernel is
-// bound by HBM (32768 rows of 7168 with a residual, 1.88 GB: 287 us, 0.98 of the measured copy rate).
+// bound by HBM (32768 rows of 7168 with a residual, 1.88 GB: 290 us, 0.97 of the measured copy rate).
 // The sum s, its squares and the scaling are fp32; s and y are each rounded once, y from the unrounded s.
 //
 // Rows move in vectors of 8 elements (16 bytes).  Where rows start off a 16-byte boundary, but all
