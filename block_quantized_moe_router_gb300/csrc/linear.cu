@@ -806,13 +806,13 @@ cudaError_t launch_few(const LinMaps& m, const LinArgs& a, int splits, int N, cu
                            F::smem(a.rows_t, splits, a.stages), m, a, st);
 }
 
-// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all ten
-// choices at 168 sizes (1 to 4096 rows, N 88 to 7168, K 512 to 7168): the plan's choice takes 1 % longer
-// than the fastest one in the mean, 19 % at worst.
+// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all the choices
+// at 168 sizes (1 to 4096 rows, N 88 to 7168, K 512 to 7168); the choices that nearby constants make are 1 %
+// faster in the mean at best, 20 % at single sizes.
 //   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.38 / 0.31 / 0.25 us
 //     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 0.95 us a tile
-//     besides, and 3.7 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.8 at 256.
-//   few rows: 64 elements cost a CTA 0.19 us, in pairs 0.24, or what its SM's share of the L2 rate (112 GB/s)
+//     besides, and 3 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.8 at 256.
+//   few rows: 64 elements cost a CTA 0.2 us, in pairs 0.22, or what its SM's share of the L2 rate (106 GB/s)
 //     allows; every row of x costs its exchange and sums, least where a part of K has a tile alone; 1.6 us
 //     a wave and 0.6 us once besides.  128 rows of the gated 2 x 2048 x 7168: 16.2 us in two parts by pairs,
 //     19.3 in four by single CTAs, 31.2 in the other kernel; 256 rows of 7168 x 2048: 15.4, 17.4 and 14.7.
@@ -822,30 +822,34 @@ struct LinPlan {
     int splits, stages, rows_t;  // few: parts of K, ring stages, rows of x per tile
 };
 
+// Of 152 SMs, how many places for one CTA each clusters can use: 36 clusters of 4 and 15 of 8 are resident at
+// one CTA per SM, 36 of 8 at two.
+constexpr int few_usable(int cluster, int fit) { return cluster < 4 ? 152 : cluster == 8 && fit == 1 ? 120 : 144; }
+
+// The few-row choices with the rows of x in `tiles_t` tiles.
 template <bool PAIR>
-void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
+void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
-    const int tiles_t = (T + F::kRows - 1) / F::kRows;
-    if (tiles_t > 65535) return;  // grid y
     const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
-    const int64_t tiles = (int64_t)tiles_t * ((N + per_tile - 1) / per_tile) * F::kCtas;
+    const int64_t tiles = (int64_t)((T + rows - 1) / rows) * ((N + per_tile - 1) / per_tile) * F::kCtas;
     const float stage_kb = (float)F::stage(rows) / 1024.f;
     for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
         const int kbs = (nk + splits - 1) / splits;
-        int stages = PAIR ? (kFewSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
-        stages = stages < kFewStages ? stages : kFewStages;
+        // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
+        // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
+        const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
+        int stages = alone ? (kFewSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
+        const int most = PAIR ? kFewStages : alone ? 6 : 4;
+        stages = stages < most ? stages : most;
         stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
         const int smem = F::smem(rows, splits, stages);
-        if (smem > kFewSmemMax) continue;
-        // CTAs an SM holds, and how many of these places clusters of 4 and 8 leave usable (152 SMs hold 36
-        // clusters of 4 and 15 of 8 at one CTA per SM, 36 of 8 at two)
-        const int fit = kSmSmem / (smem + 1024 + 256), cluster = splits * F::kCtas;
-        const int usable = cluster < 4 ? 152 : cluster == 8 && fit == 1 ? 120 : 144;
-        const int64_t places = (int64_t)sms * fit * usable / 152;
+        if (stages < 2 || smem > kFewSmemMax) continue;
+        const int fit = kSmSmem / (smem + 1024 + 256);  // CTAs an SM holds
+        const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
         const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
         const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
-        const float per_k_lat = PAIR ? 0.24f : 0.19f, per_k_bw = (float)on_sm * stage_kb / 112.f;
+        const float per_k_lat = PAIR ? 0.22f : 0.2f, per_k_bw = (float)on_sm * stage_kb / 106.f;
         const float per_row = splits == 1 && !gated ? (PAIR ? 0.012f : 0.037f) : (PAIR ? 0.0175f : 0.051f);
         const float us = (float)waves * ((float)kbs * (per_k_bw > per_k_lat ? per_k_bw : per_k_lat) +
                                          per_row * (float)rows + 1.6f) + (PAIR ? 0.65f : 0.6f);
@@ -854,6 +858,15 @@ void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan
             best = LinPlan{true, PAIR, 0, splits, stages, rows};
         }
     }
+}
+// As few tiles of x as its rows need, or up to eight times as many where a narrow matrix leaves SMs idle
+// (256 x 2048 x 2048: 12.9 us with one, 10.0 with two; 128 x 256 x 7168: 9.5 with one, 5.9 with four).
+template <bool PAIR>
+void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
+    using F = Few<PAIR>;
+    const int least = (T + F::kRows - 1) / F::kRows;
+    for (int m = 1; m <= 8 && (m == 1 || least * m * F::kStep < T + F::kStep) && least * m <= 65535; m *= 2)
+        plan_few_tiles<PAIR>(T, N, nk, gated, sms, least * m, best_us, best);
 }
 
 LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
@@ -864,7 +877,7 @@ LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
         const int width = 256 - 64 * i;
         const int64_t tiles = ManySched(T, N, gated ? width / 2 : width).total;
         const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-        const float us = (float)waves * ((float)nk * per_k[i] + 0.95f) + 3.7f;
+        const float us = (float)waves * ((float)nk * per_k[i] + 0.95f) + 3.f;
         if (us < best_us) {
             best_us = us;
             best = LinPlan{false, false, width, 0, 0, 0};
