@@ -21,6 +21,8 @@
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -39,7 +41,6 @@ struct LinArgs {
     int func, gated, f16;
     int rows_t, stages; // few rows: rows of x per tile, stages of the ring
     int tma_rows;       // many rows: out and the residual go by TMA
-    int even_out, even_res;  // or their rows start at multiples of 4 bytes
     int width;          // many rows: rows of weights per tile
     int64_t ldr, ldo;
     const float *bias, *bias_mul;
@@ -450,9 +451,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 // go out through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per row
 // meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
 // meanwhile.  Warp 10 alone moves them by TMA; rows that TMA cannot address (not 16-byte aligned) are
-// copied by the four warps, a warp's lanes along the row: element by element (8192 x 2047 x 2048: 169 us with
-// the epilogue's threads storing their own rows, 58 so, 45 at 2048 features), or two features a lane where
-// rows start at multiples of 4 bytes (10744 x 3982 x 1808: 133 us element by element, 106 so, 96 at 3984).
+// copied by the four warps, a warp's lanes along the row in aligned words of two features, which start at the
+// second feature where a row starts off 4 bytes; which rows do is a choice made once per pass, so that the
+// copies carry no branch (8192 x 2047 x 2048: 169 us with the epilogue's threads storing their own rows, 58
+// feature by feature, 92 with the choice in every row, 49 so, 45 at 2048 features).
 //
 // A stage is 128 elements of K: with 64 the commit and barrier round trips of twice as many stages
 // held the MMAs back (8192^3 without its epilogue 620 us, against 563 with 128, of 574 at the
@@ -659,6 +661,20 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             uint8_t* line = rows_s + (2 * buf + (f >> 5)) * kManySub + r * 64;
             return reinterpret_cast<uint16_t*>(line + ((((f & 31) >> 3) ^ ((r >> 1) & 3)) << 4) + (f & 7) * 2);
         };
+        // whether an element stands at an odd multiple of 2 bytes
+        const auto odd_at = [](const uint16_t* at) { return (int)((reinterpret_cast<uintptr_t>(at) >> 1) & 1); };
+        // f with the oddness of the even and of the odd rows from one that starts `odd`, known when compiled
+        const auto with_parity = [](int odd, int64_t ld, auto&& f) {
+            using Is = std::integral_constant<int, 1>;
+            using Not = std::integral_constant<int, 0>;
+            if (ld & 1) {
+                if (odd) f(Is{}, Not{});
+                else f(Not{}, Is{});
+            } else {
+                if (odd) f(Is{}, Is{});
+                else f(Not{}, Not{});
+            }
+        };
         // makes buffer g & 1 ready for pass g: its biases, and the residual if there is one
         const auto prepare = [&](int64_t g) {
             if (g >= all) return;
@@ -674,38 +690,37 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                     bias_s[buf][lane + 32 * j] = src && f < a.N ? __ldg(src + f) : 0.f;
                 }
             }
-            if (a.res && !by_tma && a.even_res) {  // as below, two features a lane
-                const int rows = min(32, a.T - r0 - first_row), f = 2 * lane;
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.res) +
-                                                                        ((int64_t)r0 + first_row) * a.ldr + fp + f);
-                const bool in = f < 32 * pieces && fp + f < a.N, both = fp + f + 1 < a.N;
-                uint32_t v[32];
+            if (a.res && !by_tma) {
+                const uint16_t* src = static_cast<const uint16_t*>(a.res) + ((int64_t)r0 + first_row) * a.ldr + fp;
+                const int rows = min(32, a.T - r0 - first_row), in = min(32 * pieces, a.N - fp);
+                const int odd_lane = odd_at(src + lane * a.ldr);
+                // the single features at the ends, a row a lane; then two features a lane of every row: all in flight
+                const bool head = odd_lane && in > 0 && lane < rows, tail = ((in - odd_lane) & 1) && in > odd_lane && lane < rows;
+                const uint16_t h0 = head ? __ldcg(src + lane * a.ldr) : (uint16_t)0;
+                const uint16_t h1 = tail ? __ldcg(src + lane * a.ldr + in - 1) : (uint16_t)0;
+                with_parity(odd_at(src), a.ldr, [&](auto even_rows, auto odd_rows) {
+                    constexpr int O[2] = {even_rows.value, odd_rows.value};
+                    const bool pair[2] = {2 * lane + 1 < in, 2 * lane + 2 < in};
+                    uint32_t v[32];
 #pragma unroll
-                for (int r = 0; r < 32; ++r) {
-                    v[r] = 0;
-                    if (in && r < rows)
-                        v[r] = both ? __ldcg(src + r * (a.ldr >> 1))
-                                    : __ldcg(reinterpret_cast<const uint16_t*>(src + r * (a.ldr >> 1)));
-                }
-                if (f < 32 * pieces)
+                    for (int r = 0; r < 32; ++r) {
+                        const int odd = O[r & 1];
+                        v[r] = r < rows && pair[odd]
+                                   ? __ldcg(reinterpret_cast<const uint32_t*>(src + r * a.ldr + 2 * lane + odd)) : 0u;
+                    }
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) *reinterpret_cast<uint32_t*>(element(buf, first_row + r, f)) = v[r];
-            } else if (a.res && !by_tma) {
-                // all loads of the pass in flight at once
-                const int rows = min(32, a.T - r0 - first_row);
-                const uint16_t* src = static_cast<const uint16_t*>(a.res) + ((int64_t)r0 + first_row) * a.ldr + fp + lane;
-                const bool in0 = fp + lane < a.N, in1 = pieces == 2 && fp + 32 + lane < a.N;
-                uint16_t v0[32], v1[32];
-#pragma unroll
-                for (int r = 0; r < 32; ++r) {
-                    v0[r] = in0 && r < rows ? __ldcg(src + r * a.ldr) : (uint16_t)0;
-                    v1[r] = in1 && r < rows ? __ldcg(src + r * a.ldr + 32) : (uint16_t)0;
-                }
-#pragma unroll
-                for (int r = 0; r < 32; ++r) {
-                    *element(buf, first_row + r, lane) = v0[r];
-                    if (pieces == 2) *element(buf, first_row + r, 32 + lane) = v1[r];
-                }
+                    for (int r = 0; r < 32; ++r) {
+                        const int odd = O[r & 1], f = 2 * lane + odd;
+                        if (!odd) {
+                            if (pair[0]) *reinterpret_cast<uint32_t*>(element(buf, first_row + r, f)) = v[r];
+                        } else if (pair[1]) {
+                            *element(buf, first_row + r, f) = (uint16_t)v[r];
+                            *element(buf, first_row + r, f + 1) = (uint16_t)(v[r] >> 16);
+                        }
+                    }
+                });
+                if (head) *element(buf, first_row + lane, 0) = h0;
+                if (tail) *element(buf, first_row + lane, in - 1) = h1;
             }
             __syncwarp();
             if (lane == 0) {
@@ -732,25 +747,35 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             int r0, f0;
             first(pair + g / passes * pairs, r0, f0);
             const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
-            if (!by_tma && a.even_out) {
-                const int f = 2 * lane, rows = min(32, a.T - r0 - first_row);
-                uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp + f;
-                if (f < 32 * pieces && fp + f + 1 < a.N) {
-#pragma unroll 8
-                    for (int r = 0; r < rows; ++r)
-                        *reinterpret_cast<uint32_t*>(dst + r * a.ldo) =
-                            *reinterpret_cast<const uint32_t*>(element(buf, first_row + r, f));
-                } else if (f < 32 * pieces && fp + f < a.N) {
-                    for (int r = 0; r < rows; ++r) dst[r * a.ldo] = *element(buf, first_row + r, f);
+            if (!by_tma) {
+                uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp;
+                const int rows = min(32, a.T - r0 - first_row), in = min(32 * pieces, a.N - fp);
+                const int odd_lane = odd_at(dst + lane * a.ldo);
+                if (lane < rows) {
+                    if (odd_lane && in > 0) dst[lane * a.ldo] = *element(buf, first_row + lane, 0);
+                    if (((in - odd_lane) & 1) && in > odd_lane)
+                        dst[lane * a.ldo + in - 1] = *element(buf, first_row + lane, in - 1);
                 }
-            } else if (!by_tma) {
-                for (int i = 0; i < pieces; ++i) {
-                    const int f = 32 * i + lane, rows = min(32, a.T - r0 - first_row);
-                    uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp + f;
-                    if (fp + f < a.N)
-#pragma unroll 8
-                        for (int r = 0; r < rows; ++r) dst[r * a.ldo] = *element(buf, first_row + r, f);
-                }
+                with_parity(odd_at(dst), a.ldo, [&](auto even_rows, auto odd_rows) {
+                    constexpr int O[2] = {even_rows.value, odd_rows.value};
+                    const bool pair[2] = {2 * lane + 1 < in, 2 * lane + 2 < in};
+#pragma unroll
+                    for (int b = 0; b < 32; b += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = first_row + b + i, odd = O[i & 1], f = 2 * lane + odd;
+                            if (!odd) v[i] = *reinterpret_cast<const uint32_t*>(element(buf, r, f));
+                            else v[i] = *element(buf, r, f) | (uint32_t)*element(buf, r, min(f + 1, 63)) << 16;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int odd = O[i & 1];
+                            if (b + i < rows && pair[odd])
+                                *reinterpret_cast<uint32_t*>(dst + (b + i) * a.ldo + 2 * lane + odd) = v[i];
+                        }
+                    }
+                });
             } else if (lane == 0) {
                 for (int s = 0; s < pieces; ++s)
                     if (fp + 32 * s < a.N && r0 < a.T)
@@ -921,8 +946,6 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     if (a.tma_rows && (!encode_rows16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
                        (residual && !encode_rows16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
         return cudaErrorInvalidValue;
-    a.even_out = rows_aligned(out, d.ldo, 4);
-    a.even_res = residual && rows_aligned(residual, d.ldr, 4);
     const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);
     static std::atomic<uint64_t> allowed{0};

@@ -146,6 +146,26 @@ def test_middle(cuda_lib, T, N, K):
         assert torch.equal(out, _run(a, func)), "equal calls give equal bits"
 
 
+@pytest.mark.parametrize("T,N,K", [(5000, 1003, 264), (3000, 2051, 520), (2601, 515, 72), (4097, 4159, 64)])
+def test_many_odd_rows(cuda_lib, T, N, K):
+    """Rows at every second multiple of 2 bytes, out and residual alike, apart, and one of them aligned."""
+    for gated in (False, True):
+        func = (N + gated) % 5
+        a = _make(T, N, K, DT["bf16" if gated else "f16"], gated=gated, bias=True, residual=True, seed=T)
+        ref, bound = _linear_ref(func=func, **a)
+        want = _run(a, func)
+        _check(want, ref, bound, a["x"].dtype)
+        for pad_out, at_out, pad_res, at_res in ((0, 0, 1, 1), (1, 1, 0, 0), (2, 1, 3, 0), (5, 4, 2, 2)):
+            wide = torch.full((T, N + pad_out), 7.0, dtype=a["x"].dtype, device="cuda")
+            res = torch.full((T, N + pad_res), float("nan"), dtype=a["x"].dtype, device="cuda")
+            res[:, at_res:at_res + N] = a["residual"]
+            out = _run({**a, "residual": res[:, at_res:at_res + N]}, func, out=wide[:, at_out:at_out + N])
+            assert torch.equal(out, want)
+            assert (wide[:, :at_out] == 7).all() and (wide[:, at_out + N:] == 7).all()
+        own = a["residual"].clone()
+        assert torch.equal(_run({**a, "residual": own}, func, out=own), want)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 300, 4096), (7, 130, 2056), (70, 257, 1000), (129, 128, 64),
                                    (300, 520, 776), (2000, 700, 520)])
 def test_whole_numbers_are_exact(cuda_lib, T, N, K):
