@@ -19,6 +19,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_plan.h"
 #include "tc_ptx.cuh"
 
 #include <type_traits>
@@ -29,7 +30,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kLinK = 64;                       // K elements per stage (128 bytes per row)
 constexpr int kLinA = 128 * 128;                // bytes of a 128-row operand stage
 
 struct LinMaps {
@@ -225,31 +225,6 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // 16 rows 9.9 against 8.8, where the latency of a stage counts and not its bytes.
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
-constexpr int kFewSplits = 8;    // parts of K at most; CTAs of a cluster too (the portable cluster size)
-constexpr int kFewStages = 8;
-constexpr int kSmSmem = 228 * 1024, kFewSmemMax = 226 * 1024;  // shared memory of an SM, and of a CTA here
-template <bool PAIR>
-struct Few {
-    static constexpr int kRows = PAIR ? 256 : 128;   // rows of x per tile at most
-    static constexpr int kStep = PAIR ? 32 : 16;     // a tile's rows of x are a multiple of it
-    static constexpr int kW = PAIR ? 64 : 128;       // weight rows of a CTA
-    static constexpr int kA = kW * 128;              // bytes of them per stage
-    static constexpr int kCtas = PAIR ? 2 : 1;       // per part of K
-    __host__ __device__ static constexpr int own(int rows, int splits) { return ((rows + splits - 1) / splits + 3) / 4 * 4; }
-    __host__ __device__ static constexpr int pitch(int own) { return own | 4; }  // own is a multiple of 4
-    __host__ __device__ static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
-    // A pair takes all of tensor memory, so that its CTAs hold the same columns, and so it takes all of the
-    // shared memory too: another cluster's CTAs beside it (of another stream) could hold columns on one SM
-    // and wait for a CTA that waits for this pair's columns on the other, and both for ever.
-    static constexpr int kSmemMin = PAIR ? kFewSmemMax : 0;
-    __host__ __device__ static constexpr int rest(int rows, int splits) {  // beside the stages
-        return splits * kW * pitch(own(rows, splits)) * 4 + 1024;
-    }
-    __host__ __device__ static constexpr int smem(int rows, int splits, int stages) {
-        const int need = stages * stage(rows) + rest(rows, splits);
-        return need > kSmemMin ? need : kSmemMin;
-    }
-};
 
 template <bool PAIR>
 __global__ void __launch_bounds__(kFewThreads)
@@ -273,8 +248,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     // [rank][W row][own columns, padded so that 16-byte accesses of 8 rows meet 32 banks]
     float* landing = reinterpret_cast<float*>(smem + a.stages * stage_bytes);
     const int own = F::own(NT, (int)splits), pitch = F::pitch(own);
-    uint32_t tm_cols = PAIR ? 512 : 32;
-    while (tm_cols < (uint32_t)NT) tm_cols *= 2;
+    const uint32_t tm_cols = (uint32_t)F::columns(NT);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
@@ -468,6 +442,7 @@ constexpr int kManyHalf = 2 * kLinA;             // 64 elements of K: 128 rows o
 constexpr int kManyStageBytes = 2 * kManyHalf;
 constexpr int kManySub = 128 * 64;               // bytes of 32 features of 128 rows
 constexpr int kManySmem = kManyStages * kManyStageBytes + 4 * kManySub + 1024;
+static_assert(columns_covered(kManySmem, kTmemColumns));
 constexpr int kManyGroup = 8;  // row tiles that share a pass over the weights
 
 struct ManySched {
@@ -827,90 +802,8 @@ cudaError_t launch_few(const LinMaps& m, const LinArgs& a, int splits, int N, cu
     const int per_tile = F::kW * F::kCtas / (a.gated ? 2 : 1), cluster = splits * F::kCtas;
     const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
     static std::atomic<uint64_t> allowed{0};
-    return launch_clusters(linear_few_kernel<PAIR>, kFewSmemMax, allowed, grid, cluster, kFewThreads,
+    return launch_clusters(linear_few_kernel<PAIR>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
                            F::smem(a.rows_t, splits, a.stages), m, a, st);
-}
-
-// Which kernel, and its tiles, by estimated time in microseconds.  The constants are fitted to all the choices
-// at 168 sizes (1 to 4096 rows, N 88 to 7168, K 512 to 7168); the choices that nearby constants make are 1 %
-// faster in the mean at best, 20 % at single sizes.
-//   many rows: tiles go out in waves of one per CTA pair; 64 elements of K cost 0.38 / 0.31 / 0.25 us
-//     at 256 / 192 / 128 columns (the loads of x do not shrink with the columns), 0.95 us a tile
-//     besides, and 3 us once.  512 x 7168 x 2048: 18.2 us at 192 columns (one wave), 19.8 at 256.
-//   few rows: 64 elements cost a CTA 0.2 us, in pairs 0.22, or what its SM's share of the L2 rate (106 GB/s)
-//     allows; every row of x costs its exchange and sums, least where a part of K has a tile alone; 1.6 us
-//     a wave and 0.6 us once besides.  128 rows of the gated 2 x 2048 x 7168: 16.2 us in two parts by pairs,
-//     19.3 in four by single CTAs, 31.2 in the other kernel; 256 rows of 7168 x 2048: 15.4, 17.4 and 14.7.
-struct LinPlan {
-    bool few, pair;
-    int width;                   // many: columns per tile
-    int splits, stages, rows_t;  // few: parts of K, ring stages, rows of x per tile
-};
-
-// Of 152 SMs, how many places for one CTA each clusters can use: 36 clusters of 4 and 15 of 8 are resident at
-// one CTA per SM, 36 of 8 at two.
-constexpr int few_usable(int cluster, int fit) { return cluster < 4 ? 152 : cluster == 8 && fit == 1 ? 120 : 144; }
-
-// The few-row choices with the rows of x in `tiles_t` tiles.
-template <bool PAIR>
-void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, float& best_us, LinPlan& best) {
-    using F = Few<PAIR>;
-    const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
-    const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
-    const int64_t tiles = (int64_t)((T + rows - 1) / rows) * ((N + per_tile - 1) / per_tile) * F::kCtas;
-    const float stage_kb = (float)F::stage(rows) / 1024.f;
-    for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
-        const int kbs = (nk + splits - 1) / splits;
-        // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
-        // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
-        const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
-        int stages = alone ? (kFewSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
-        const int most = PAIR ? kFewStages : alone ? 6 : 4;
-        stages = stages < most ? stages : most;
-        stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
-        const int smem = F::smem(rows, splits, stages);
-        if (stages < 2 || smem > kFewSmemMax) continue;
-        const int fit = kSmSmem / (smem + 1024 + 256);  // CTAs an SM holds
-        const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
-        const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
-        const int64_t on_sm = waves > 1 ? fit : (ctas + sms - 1) / sms;
-        const float per_k_lat = PAIR ? 0.22f : 0.2f, per_k_bw = (float)on_sm * stage_kb / 106.f;
-        const float per_row = splits == 1 && !gated ? (PAIR ? 0.012f : 0.037f) : (PAIR ? 0.0175f : 0.051f);
-        const float us = (float)waves * ((float)kbs * (per_k_bw > per_k_lat ? per_k_bw : per_k_lat) +
-                                         per_row * (float)rows + 1.6f) + (PAIR ? 0.65f : 0.6f);
-        if (us < best_us) {
-            best_us = us;
-            best = LinPlan{true, PAIR, 0, splits, stages, rows};
-        }
-    }
-}
-// As few tiles of x as its rows need, or up to eight times as many where a narrow matrix leaves SMs idle
-// (256 x 2048 x 2048: 12.9 us with one, 10.0 with two; 128 x 256 x 7168: 9.5 with one, 5.9 with four).
-template <bool PAIR>
-void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
-    using F = Few<PAIR>;
-    const int least = (T + F::kRows - 1) / F::kRows;
-    for (int m = 1; m <= 8 && (m == 1 || least * m * F::kStep < T + F::kStep) && least * m <= 65535; m *= 2)
-        plan_few_tiles<PAIR>(T, N, nk, gated, sms, least * m, best_us, best);
-}
-
-LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
-    LinPlan best{};
-    float best_us = 1e30f;
-    const float per_k[3] = {0.38f, 0.31f, 0.25f};
-    for (int i = 0; i < 3; ++i) {
-        const int width = 256 - 64 * i;
-        const int64_t tiles = ManySched(T, N, gated ? width / 2 : width).total;
-        const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-        const float us = (float)waves * ((float)nk * per_k[i] + 0.95f) + 3.f;
-        if (us < best_us) {
-            best_us = us;
-            best = LinPlan{false, false, width, 0, 0, 0};
-        }
-    }
-    plan_few<false>(T, N, nk, gated, sms, best_us, best);
-    plan_few<true>(T, N, nk, gated, sms, best_us, best);
-    return best;
 }
 
 }  // namespace

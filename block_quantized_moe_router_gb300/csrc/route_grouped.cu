@@ -21,6 +21,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_plan.h"
 #include "tc_ptx.cuh"
 #include "topk.cuh"
 
@@ -68,18 +69,6 @@ __device__ __forceinline__ unsigned long long orderable64(double v) {
 __device__ __forceinline__ double from_orderable64(unsigned long long u) {
     return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
-
-// Shared memory of one routing warp.
-template <int EPL>
-struct alignas(16) RouteScratch {
-    // Ranking values, size + 1 places per group: value e stands at e + e / size, also for e from E to
-    // 32 EPL - 1.  With at most 64 groups and E > 16 EPL the groups are of at least 2, 3 and 5 experts at EPL
-    // 4, 8 and 16, which puts the last place at 190, 340 and 613 (EPL 1 and 2: groups of one, 62 and 126).
-    float rank[32 * EPL + (EPL == 1 ? 32 : EPL <= 4 ? 64 : EPL == 8 ? 96 : 112)];
-    float val[32 * EPL];  // scores (logits where no score was needed, or for fp64)
-    float group[68];
-    int kept[64];
-};
 
 // 1 / softmax denominator over the finite logits in sc->val, in fp64.
 template <int EPL>
@@ -523,25 +512,15 @@ cudaError_t launch_given(const float* logits, const float* bias, int T, const Gr
 // room for CTAs, the CTAs beyond add no part and only own tokens (178 x 72 x 160: 15.9 us with 2 CTAs a
 // tile, 8.1 with 16).
 // ------------------------------------------------------------------------------------------
-constexpr int kFusedThreads = 512;
-constexpr int kFusedK = 64;
-constexpr int kFusedA = 128 * 128;
-constexpr int kFusedSmemMax = 226 * 1024;
-constexpr int kFusedStagesMax = 8;
-
 struct FusedMaps {
     CUtensorMap x, w;
 };
 
 struct FusedArgs {
-    int T, nk, n;           // n: experts of a block rounded up to 16, the MMA's columns
+    int T;
     int E;                  // all experts, the length of a row of logits
     int select;             // 0: write the logits only
-    int parts;              // CTAs of a cluster that have a part of K
-    int own, stages;        // tokens per CTA of a tile; ring stages
-    int box_x;              // token rows a TMA box brings
-    int landing_at;         // byte offsets: of the landing area (0: over the ring)
-    int scratch_at;         // and of the warps' scratch
+    FusedPlan p;
     const float* bias;
     float* logits;
     int32_t* ids;
@@ -562,16 +541,15 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     const int splits = (int)cluster_size(), rank = (int)cluster_rank();
     const int64_t t0 = (int64_t)(blockIdx.x / splits) * 128;
     const int rows = (int)min((int64_t)128, a.T - t0);  // tokens of this tile
-    const int stage_bytes = kFusedA + a.n * 128;
-    const int k_begin = (int)((int64_t)a.nk * rank / a.parts), k_end = (int)((int64_t)a.nk * (rank + 1) / a.parts);
-    const int steps = rank < a.parts ? k_end - k_begin : 0;
-    const int e0 = (int)blockIdx.y * a.n, experts = min(a.n, a.E - e0);  // of this block
-    const int pitch = a.n + 4;  // floats: 16-byte accesses of eight rows meet 32 banks
-    float* landing = reinterpret_cast<float*>(smem + a.landing_at);  // [rank][own token][pitch]
-    uint32_t tm_cols = 32;
-    while (tm_cols < (uint32_t)a.n) tm_cols *= 2;
+    const int stage_bytes = kFusedA + a.p.n * 128;
+    const int k_begin = (int)((int64_t)a.p.nk * rank / a.p.parts), k_end = (int)((int64_t)a.p.nk * (rank + 1) / a.p.parts);
+    const int steps = rank < a.p.parts ? k_end - k_begin : 0;
+    const int e0 = (int)blockIdx.y * a.p.n, experts = min(a.p.n, a.E - e0);  // of this block
+    const int pitch = a.p.n + 4;  // floats: 16-byte accesses of eight rows meet 32 banks
+    float* landing = reinterpret_cast<float*>(smem + a.p.landing_at);  // [rank][own token][pitch]
+    const uint32_t tm_cols = (uint32_t)tmem_columns(a.p.n);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < a.p.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -590,10 +568,10 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     if (warp == 0 && elect_one()) {  // TMA producer
-        const uint32_t bytes = (uint32_t)(a.box_x * 128 + a.n * 128);
+        const uint32_t bytes = (uint32_t)(a.p.box_x * 128 + a.p.n * 128);
         int issued = 0;
         RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+        for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
             const int s = at.slot;
             if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                 give_up();
@@ -607,14 +585,14 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
             ++issued;
         }
         // whoever gives up, no copy is in flight when the CTA ends
-        for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
-            at.back(a.stages);
+        for (int i = issued < a.p.stages ? issued : a.p.stages; i > 0; --i) {
+            at.back(a.p.stages);
             mbar_wait_suspended(&full[at.slot], at.parity);
         }
     } else if (warp == 1 && elect_one()) {  // MMA issuer
-        const uint32_t idesc = idesc_bf16(128, a.n);
+        const uint32_t idesc = idesc_bf16(128, a.p.n);
         RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+        for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
             const int s = at.slot;
             if (!mbar_wait_suspended(&full[s], at.parity)) {
                 give_up();
@@ -633,14 +611,14 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
     cluster_wait();
-    if (a.landing_at == 0) cluster_sync();  // over the ring: no CTA's copies or MMAs may still use it
+    if (a.p.landing_at == 0) cluster_sync();  // over the ring: no CTA's copies or MMAs may still use it
     {  // a warp's lane quarter: tokens 32 q + lane; the four warps of a quarter share the experts
         tc_fence_after();
         const int q = warp & 3, row = 32 * q + lane;
-        if (32 * q < rows && rank < a.parts) {
-            const int owner = min(row / a.own, splits - 1), at = row - owner * a.own;
-            const uint32_t dst = map_rank(smem_u32(landing + ((int64_t)rank * a.own + at) * pitch), owner);
-            for (int c = 16 * (warp >> 2); c < a.n; c += 16 * (kFusedThreads / 128)) {
+        if (32 * q < rows && rank < a.p.parts) {
+            const int owner = min(row / a.p.own, splits - 1), at = row - owner * a.p.own;
+            const uint32_t dst = map_rank(smem_u32(landing + ((int64_t)rank * a.p.own + at) * pitch), owner);
+            for (int c = 16 * (warp >> 2); c < a.p.n; c += 16 * (kFusedThreads / 128)) {
                 uint32_t v[16];
                 tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
                 tmem_ld_wait();
@@ -662,16 +640,16 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, tm_cols);
     }
-    auto* scratch = reinterpret_cast<RouteScratch<EPL>*>(smem + a.scratch_at) + warp;
-    const int mine = min(a.own, rows - rank * a.own);  // tokens of this CTA (may be negative)
+    auto* scratch = reinterpret_cast<RouteScratch<EPL>*>(smem + a.p.scratch_at) + warp;
+    const int mine = min(a.p.own, rows - rank * a.p.own);  // tokens of this CTA (may be negative)
     for (int i = warp; i < mine; i += kFusedThreads / 32) {
-        const int64_t t = t0 + (int64_t)rank * a.own + i;
+        const int64_t t = t0 + (int64_t)rank * a.p.own + i;
         float raw[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) raw[j] = 0.f;
 #pragma unroll 2
-        for (int s = 0; s < a.parts; ++s) {
-            const float* src = landing + ((int64_t)s * a.own + i) * pitch + lane;
+        for (int s = 0; s < a.p.parts; ++s) {
+            const float* src = landing + ((int64_t)s * a.p.own + i) * pitch + lane;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 if (lane + 32 * j < experts) raw[j] += src[32 * j];
@@ -684,36 +662,19 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
 }
 
 template <int EPL>
-cudaError_t launch_fused(const FusedMaps& m, FusedArgs a, const GroupRule& P, int splits, cudaStream_t st) {
-    // ring | landing | scratch, or the last two over the ring where they do not fit beside it
-    const int stage = kFusedA + a.n * 128;
-    const int landing = a.parts * a.own * (a.n + 4) * 4;
-    const int scratch = a.select ? (int)sizeof(RouteScratch<EPL>) * (a.own < kFusedThreads / 32 ? a.own : kFusedThreads / 32) : 0;
-    const int steps = (a.nk + a.parts - 1) / a.parts;
-    const int landing16 = (landing + 15) / 16 * 16;
-    a.stages = (kFusedSmemMax - 1024 - landing16 - scratch) / stage;
-    const bool beside = a.stages >= 3 || a.stages >= steps;
-    if (!beside) a.stages = (kFusedSmemMax - 1024) / stage;
-    a.stages = a.stages < steps ? a.stages : steps;
-    a.stages = a.stages < 1 ? 1 : a.stages < kFusedStagesMax ? a.stages : kFusedStagesMax;
-    a.landing_at = beside ? a.stages * stage : 0;
-    a.scratch_at = a.landing_at + landing16;
-    int smem = a.scratch_at + scratch;
-    if (a.stages * stage > smem) smem = a.stages * stage;
-    smem += 1024;
-    if (smem > kFusedSmemMax) return cudaErrorNotSupported;
+cudaError_t launch_fused(const FusedMaps& m, const FusedArgs& a, const GroupRule& P, cudaStream_t st) {
     const auto kernel = route_fused_kernel<EPL>;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t err = allow_large_launch(kernel, kFusedSmemMax, allowed);
+    const cudaError_t err = allow_large_launch(kernel, kCtaSmemMax, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * splits), (unsigned)((a.E + a.n - 1) / a.n));
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.T + 127) / 128 * a.p.splits), (unsigned)a.p.blocks);
     cfg.blockDim = dim3(kFusedThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = a.p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.x = a.p.splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -749,35 +710,20 @@ cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias,
                                int group_top, float* logits, int32_t* ids, float* w, int32_t* status,
                                cudaStream_t st) {
     const GroupRule P = make_rule(bias, E, k, scoring, renorm, scaling, n_group, topk_group, group_top);
-    const int blocks = (E + 255) / 256;
-    // Two launches save none, and a small product is done sooner without clusters: 1 x 512 x 2048 7.5 us
-    // against 8.9 (1 x 384 x 7168 10.7 against 9.4), 161 x 466 x 352 9.9 against 15.6 (2702 tokens 28.8 against
-    // 20.9; 16 x 512 x 2048 33.3 against 9.5).
-    if (blocks > 1 && (T == 1 ? H <= 4096 : T <= 1024 && H <= 512)) return cudaErrorNotSupported;
     FusedArgs a{};
+    if (!plan_fused(T, E, H, a.p)) return cudaErrorNotSupported;
     a.T = T;
     a.E = E;
-    a.select = blocks == 1;
-    a.nk = (H + kFusedK - 1) / kFusedK;
-    a.n = ((E + blocks - 1) / blocks + 15) / 16 * 16;
+    a.select = a.p.blocks == 1;
     a.bias = a.select ? bias : nullptr;
     a.logits = logits; a.ids = ids; a.w = w; a.status = status;
-    // as many CTAs per tile as keep every cluster resident at one CTA per SM (152 SMs hold 7, 15,
-    // 36 and 76 clusters of 16, 8, 4 and 2), but beyond one per stage only to share many tokens
-    const int64_t tiles = ((int64_t)T + 127) / 128 * blocks;
-    const int rows = T < 128 ? T : 128;
-    int splits = tiles <= 7 ? 16 : tiles <= 15 ? 8 : tiles <= 36 ? 4 : tiles <= 76 ? 2 : 1;
-    while (splits > a.nk && rows <= splits / 2 * (kFusedThreads / 32)) splits /= 2;
-    a.parts = splits < a.nk ? splits : a.nk;
-    a.own = (rows + splits - 1) / splits;
-    a.box_x = (rows + 7) / 8 * 8;
     FusedMaps m{};
-    if (!encode_rows16(&m.x, x, H, T, H, a.box_x, 64) || !encode_rows16(&m.w, wr, H, E, H, a.n, 64))
+    if (!encode_rows16(&m.x, x, H, T, H, a.p.box_x, 64) || !encode_rows16(&m.w, wr, H, E, H, a.p.n, 64))
         return cudaErrorNotSupported;
-    if (E <= 32) return launch_fused<1>(m, a, P, splits, st);
-    if (E <= 64) return launch_fused<2>(m, a, P, splits, st);
-    if (E <= 128) return launch_fused<4>(m, a, P, splits, st);
-    const cudaError_t err = launch_fused<8>(m, a, P, splits, st);
+    if (E <= 32) return launch_fused<1>(m, a, P, st);
+    if (E <= 64) return launch_fused<2>(m, a, P, st);
+    if (E <= 128) return launch_fused<4>(m, a, P, st);
+    const cudaError_t err = launch_fused<8>(m, a, P, st);
     if (err != cudaSuccess || a.select) return err;
     return launch_topk_grouped(logits, bias, T, E, k, scoring, renorm, scaling, n_group, topk_group, group_top, ids, w,
                                status, st);
