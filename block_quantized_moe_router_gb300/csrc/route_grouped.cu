@@ -46,15 +46,18 @@ __device__ __forceinline__ bool is_softmax(int scoring) {
     return scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SOFTMAX_BIAS;
 }
 
-// Score of a finite logit.  fp32: expf within 2 units in the last place, the reciprocal within 1.
+// Score of a finite logit.  fp32: expf and __fdividef are within 2 units in the last place each, but the quotient is 0 where
+// its divisor passes 2^126, so a sigmoid below 2^-126 (a logit below -87.3) reads as 0; a softmax score below that
+// may be subnormal.  log(1 + e^l) is e^l to within e^l / 2 of itself, so far below 0 sqrt(softplus) is e^(l/2): e^l would
+// be subnormal, and its root off by more than fp32 holds, from l = -87 on.
 __device__ __forceinline__ float score32(int scoring, float l, float lmax, float inv_z) {
     if (is_softmax(scoring)) return expf(l - lmax) * inv_z;
-    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(l > 30.f ? l : log1pf(expf(l)));
+    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return l < -20.f ? expf(0.5f * l) : sqrtf(l > 30.f ? l : log1pf(expf(l)));
     return __fdividef(1.f, 1.f + expf(-l));
 }
 __device__ __forceinline__ double score64(int scoring, double l, double lmax, double inv_z) {
     if (is_softmax(scoring)) return exp(l - lmax) * inv_z;
-    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return sqrt(l > 40. ? l : log1p(exp(l)));
+    if (scoring == MOE_SCORE_SQRTSOFTPLUS) return l < -40. ? exp(0.5 * l) : sqrt(l > 40. ? l : log1p(exp(l)));
     return 1. / (1. + exp(-l));
 }
 
@@ -325,10 +328,10 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
         }
     }
     // Error bounds of a ranking value v: exp, sums and the reciprocal are within 2^-21 of the largest
-    // score and of |v|; an error of the softmax denominator (2^-19.7 for 512 logits) scales all scores
-    // alike, so between close values it counts only with what their biases differ by.
+    // score and of |v|, and what underflow takes is below 2^-126; an error of the softmax denominator (2^-19.7 for 512
+    // logits) scales all scores alike, so between close values it counts only with what their biases differ by.
     const float tol_rel = 0x1p-21f;
-    float tol_abs = 2.f * tol_rel * smax;
+    float tol_abs = 2.f * tol_rel * smax + 0x1p-125f;
     if (softmax && !P.by_logit)
         tol_abs += 0x1p-19f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
 
