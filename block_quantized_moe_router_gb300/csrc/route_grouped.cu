@@ -179,6 +179,16 @@ __device__ __noinline__ int pick_fp64(const GroupRule& P, const float* bias, flo
     return my_e;
 }
 
+// The score in fp64 of the pick with logit l (lanes below k) over the sum of them all; 0 where that sum is 0 too.  The
+// softmax's denominator drops out.
+__device__ __noinline__ float weight_fp64(int scoring, float l, float lmax, bool pick) {
+    const double s = pick && fabsf(l) < INFINITY ? score64(scoring, l, lmax, 1.) : 0.;
+    double den = s;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    return den > 0. ? (float)(s / den) : 0.f;
+}
+
 // The K rounds over `count` candidates, N per lane: candidate r is expert r, or the r-th of the kept
 // groups.  Returns the pick of lane j < k, or sets `full` where all candidates are needed in fp64.
 template <int EPL, int N>
@@ -261,12 +271,13 @@ __device__ __forceinline__ int pick_rounds(const GroupRule& P, const float* bias
 }
 
 // One warp routes one token: raw[j] and bv[j] are the logit and the bias of expert lane + 32 j (anything
-// beyond E).  The branches on the kind of scores stand outside the loops over j: a warp on its own
+// beyond E), `logits` its row in memory, read again where weights underflow (raw kept in registers until then: 26.1 -> 28.2
+// us for 8192 rows of 512, 26.3 so).  The branches on the kind of scores stand outside the loops over j: a warp on its own
 // spends some twenty cycles on each.
 template <int EPL>
 __device__ __forceinline__ void route_token(const GroupRule& P, const float (&raw)[EPL], const float (&bv)[EPL],
-                                            const float* bias, RouteScratch<EPL>* sc, int lane, int32_t* ids,
-                                            float* wout, int32_t* status) {
+                                            const float* logits, const float* bias, RouteScratch<EPL>* sc, int lane,
+                                            int32_t* ids, float* wout, int32_t* status) {
     const bool softmax = is_softmax(P.scoring), grouped = P.topk_group < P.n_group;
     float lg[EPL], lmax = -INFINITY;
     bool nonfinite = false;
@@ -459,7 +470,10 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             if (o < P.k) den += __shfl_xor_sync(0xffffffffu, den, o);  // lanes from k on hold 0
-        w = den > 0.f ? __fdividef(w, den) : 0.f;
+        // Underflow takes up to 2^-75 of a score (2^-126 where no root follows): nothing of a sum above 2^-50, but of a
+        // smaller one what fp32 could tell, down to all of it (every pick's logit below -87, or as far below the largest)
+        if (__shfl_sync(0xffffffffu, den, 0) >= 0x1p-50f) w = __fdividef(w, den);
+        else w = weight_fp64(P.scoring, lane < P.k ? logits[my_e] : 0.f, lmax, lane < P.k);
     }
     if (lane < P.k) {
         ids[lane] = my_e;
@@ -492,7 +506,7 @@ topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ 
     float bv[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) bv[j] = bias && lane + 32 * j < P.E ? __ldg(bias + lane + 32 * j) : 0.f;
-    route_token<EPL>(P, raw, bv, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
+    route_token<EPL>(P, raw, bv, row, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
 }
 
 template <int EPL>
@@ -660,7 +674,8 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (lane + 32 * j < experts) a.logits[t * a.E + e0 + lane + 32 * j] = raw[j];
-        if (a.select) route_token<EPL>(P, raw, bv, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
+        if (a.select)
+            route_token<EPL>(P, raw, bv, a.logits + t * a.E, a.bias, scratch, lane, a.ids + t * P.k, a.w + t * P.k, a.status);
     }
 }
 

@@ -188,7 +188,9 @@ moe_status_t moe_route(const moe_route_desc* desc, const void* x_bf16, const flo
  *   descending order; weight = s / sum(selected s) when renormalize, else s (for softmax kinds the
  *   probability over all E); times routed_scaling.
  * The order is that of the scores' exact values (fp32 scores too close to tell are compared again
- * in fp64), so it does not depend on how fp32 rounds them.  A non-finite logit ranks below every
+ * in fp64), so it does not depend on how fp32 rounds them.  Renormalised weights hold for scores of any
+ * size that fp64 holds (sigmoid: logits above -709; softmax kinds: within 745 of the largest); where
+ * every selected score is 0 so is every weight.  Without renormalize a weight below 1.2e-38 may be 0.  A non-finite logit ranks below every
  * finite one, counts as -infinity in its group's sum, weighs 0 and sets MOE_DEV_NONFINITE; a bias
  * that is not finite ranks its expert with those, but the expert keeps its weight if it is
  * selected for want of others.
