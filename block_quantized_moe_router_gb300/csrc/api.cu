@@ -126,6 +126,7 @@ moe_status_t validate_route(const moe_route_desc* d, const float* logits_in) {
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }  // NULL too
 bool aligned2(const void* p) { return reinterpret_cast<uintptr_t>(p) % 2 == 0; }
 
 constexpr int64_t kMaxLd = int64_t(1) << 38;  // 2-byte elements: row pitches below 2^39 bytes
@@ -259,12 +260,14 @@ moe_status_t moe_route_grouped(const moe_route_desc* d, int32_t n_group, int32_t
     if (group_top < 1 || group_top > 2 || group_top > size || d->top_k > topk_group * size)
         return MOE_ERR_INVALID_ARG;
     if (d->T == 0) return MOE_OK;
-    if (!topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const float* logits = logits_in;
     const float* bias = d->scoring != MOE_SCORE_SOFTMAX ? d->correction_bias : nullptr;
+    if (!topk_ids || !topk_w || !aligned4(topk_ids) || !aligned4(topk_w) || !aligned4(logits) || !aligned4(bias) ||
+        !aligned4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!logits) {
-        if (!d->w_router || !x_bf16 || !logits_out || !aligned16(x_bf16) || !aligned16(d->w_router))
+        if (!d->w_router || !x_bf16 || !logits_out || !aligned16(x_bf16) || !aligned16(d->w_router) || !aligned4(logits_out))
             return MOE_ERR_INVALID_ARG;
         cudaError_t err = launch_route_fused(x_bf16, d->w_router, bias, d->T, d->E, d->H, d->top_k, d->scoring,
                                              d->renormalize ? 1 : 0, d->routed_scaling, n_group, topk_group,
@@ -297,7 +300,7 @@ moe_status_t moe_linear(const moe_linear_desc* d, const void* x, const void* w, 
         return MOE_ERR_INVALID_ARG;
     if (d->T == 0) return MOE_OK;
     if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(w_mul) || !aligned2(residual) ||
-        !aligned2(out))
+        !aligned2(out) || !aligned4(bias) || !aligned4(bias_mul) || !aligned4(dev_status))
         return MOE_ERR_INVALID_ARG;
     return launch_linear(*d, x, w, w_mul, bias, bias_mul, residual, out, dev_status,
                          static_cast<cudaStream_t>(stream)) == cudaSuccess

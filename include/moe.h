@@ -197,7 +197,8 @@ moe_status_t moe_route(const moe_route_desc* desc, const void* x_bf16, const flo
  * Arguments, outputs and T == 0 as for moe_route.  Further checks: scoring is not a hash kind
  * (MOE_ERR_UNSUPPORTED); zero_experts == 0 (MOE_ERR_UNSUPPORTED); 1 <= n_group <= 64 divides E;
  * 1 <= topk_group <= n_group; group_top is 1 or 2 and at most E / n_group; top_k <= topk_group *
- * E / n_group; x_bf16 and w_router 16-byte aligned when the router GEMM runs. */
+ * E / n_group; x_bf16 and w_router 16-byte aligned when the router GEMM runs; every float and int32
+ * pointer that is used 4-byte aligned. */
 moe_status_t moe_route_grouped(const moe_route_desc* desc, int32_t n_group, int32_t topk_group,
                                int32_t group_top, const void* x_bf16, const float* logits_in,
                                float* logits_out, int32_t* topk_ids, float* topk_w,
