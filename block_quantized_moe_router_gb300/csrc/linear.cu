@@ -355,6 +355,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 const int n = n0 + row, rows = min(16, ncols - c);
                 uint32_t rw[16] = {};
                 if (a.res && n < a.N) load_residual(a, (int64_t)t0 + c, rows, n, rw);
+                __syncwarp();  // the read of tensor memory wants the whole warp, N may end inside it
                 float z[16];
                 tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c - c0, reinterpret_cast<uint32_t(&)[16]>(z));
                 tmem_ld_wait();
