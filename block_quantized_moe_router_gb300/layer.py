@@ -137,20 +137,21 @@ class MoeLayer:
         capi.moe_linear(h, s["down"], out, bias=s.get("down_bias"), residual=out,
                         dev_status=self.status, stream=stream)
 
-    def block(self, delta, residual=None, *, logits_in=None, stream=None):
+    def block(self, delta, residual=None, *, token_ids=None, logits_in=None, stream=None):
         """The layer with the residual add and norm before it: r = delta + residual, n = RMS norm of
-        r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta.  The
-        results belong to `stream` (the current one by default)."""
+        r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta.
+        token_ids: of the rows, for hash routing.  The results belong to `stream` (the current one
+        by default)."""
         if self.norm_weight is None:
             raise ValueError("the layer was built without norm_weight")
         if stream is not None:  # what is freed on return goes back to the stream that still uses it
             with torch.cuda.stream(stream):
-                return self.block(delta, residual, logits_in=logits_in)
+                return self.block(delta, residual, token_ids=token_ids, logits_in=logits_in)
         n = torch.empty_like(delta)
         r = torch.empty_like(delta)
         capi.moe_add_rms_norm(delta, self.norm_weight, n, residual=residual, sum_out=r,
                               eps=self.norm_eps)
-        return self.forward(n, logits_in=logits_in)[0], r
+        return self.forward(n, token_ids=token_ids, logits_in=logits_in)[0], r
 
     def forward(self, x=None, *, token_ids=None, logits_in=None, out=None, topk_ids=None,
                 topk_w=None, logits_out=None, stream=None):
