@@ -20,6 +20,43 @@ import torch
 from . import capi
 
 
+def _check_groups(E, top_k, scoring, zero_experts, n_group, topk_group, group_top):
+    """The rules of moe_route_grouped that do not depend on a call."""
+    if zero_experts or scoring in (capi.MOE_SCORE_HASH, capi.MOE_SCORE_HASH_SQRTSOFTPLUS):
+        raise ValueError("expert groups need a learned router without zero-computation experts")
+    if not 1 <= n_group <= 64 or E % n_group:
+        raise ValueError(f"n_group must be 1 to 64 and divide the {E} experts, got {n_group}")
+    if not 1 <= topk_group <= n_group:
+        raise ValueError(f"topk_group must be 1 to n_group ({n_group}), got {topk_group}")
+    size = E // n_group
+    if group_top not in (1, 2) or group_top > size:
+        raise ValueError(f"group_top must be 1 or 2 and at most the {size} experts of a group, got {group_top}")
+    if top_k > topk_group * size:
+        raise ValueError(f"top_k {top_k} exceeds the {topk_group * size} experts of {topk_group} groups")
+
+
+def _check_shared(s, H):
+    """The rules of moe_linear for the two products of the bf16 shared expert, before any kernel runs."""
+    missing = [key for key in ("gate", "up", "down") if s.get(key) is None]
+    if missing:
+        raise ValueError(f"the shared expert needs gate, up and down; {missing[0]} is missing")
+    I = s["gate"].shape[0]
+    if I < 8 or I % 8:
+        raise ValueError(f"the shared expert's width must be a multiple of 8, got {I}")
+    for key, shape in (("gate", (I, H)), ("up", (I, H)), ("down", (H, I))):
+        t = s[key]
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_cuda:
+            raise ValueError(f"shared {key} must be a bfloat16 CUDA matrix {shape}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < shape[1] or t.data_ptr() % 16:
+            raise ValueError(f"shared {key} must have contiguous rows that start at multiples of 16 bytes")
+    if s["up"].stride(0) != s["gate"].stride(0):
+        raise ValueError("shared up must have the row stride of gate")
+    for key, n in (("gate_bias", I), ("up_bias", I), ("down_bias", H)):
+        t = s.get(key)
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_cuda or not t.is_contiguous()):
+            raise ValueError(f"shared {key} must be a contiguous float32 CUDA tensor ({n},), got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 class MoeLayer:
     def __init__(self, *, E, H, I, top_k, scoring, gate, up, down, I_shared=0, sh_gate=None,
                  sh_up=None, sh_down=None, w_router=None, correction_bias=None, tid2eid=None,
@@ -31,11 +68,14 @@ class MoeLayer:
         self.scoring, self.renormalize, self.routed_scaling = scoring, renormalize, routed_scaling
         self.act, self.g_act1, self.g_act2 = act, g_act1, g_act2
         self.w_router, self.correction_bias, self.tid2eid = w_router, correction_bias, tid2eid
-        if n_group and (zero_experts or scoring in (capi.MOE_SCORE_HASH,
-                                                    capi.MOE_SCORE_HASH_SQRTSOFTPLUS)):
-            raise ValueError("expert groups need a learned router without zero-computation experts")
-        if shared is not None and I_shared:
-            raise ValueError("a layer has one shared expert: FP4 (I_shared) or bf16 (shared)")
+        if n_group:
+            _check_groups(E, top_k, scoring, zero_experts, n_group, topk_group, group_top)
+        if shared is not None:
+            if I_shared:
+                raise ValueError("a layer has one shared expert: FP4 (I_shared) or bf16 (shared)")
+            _check_shared(shared, H)
+        if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or tuple(norm_weight.shape) != (H,)):
+            raise ValueError(f"norm_weight must be a bfloat16 tensor ({H},), got {norm_weight.dtype} {tuple(norm_weight.shape)}")
         self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
         self.shared, self.norm_weight, self.norm_eps = shared, norm_weight, norm_eps
         self._weights = (gate, up, down, sh_gate, sh_up, sh_down)  # keep alive

@@ -1,4 +1,4 @@
-"""MoeLayer.block with hash routing, on the GPU."""
+"""MoeLayer.block with hash routing, and what the layer refuses when it is built, on the GPU."""
 import pytest
 import torch
 
@@ -36,4 +36,20 @@ def test_hash_routed_block(cuda_lib, scoring, T):
     torch.cuda.synchronize()
     assert int(layer.status.item()) == 0
     assert torch.equal(out, want) and torch.equal(r, s) and torch.equal(there, want)
+    layer.close()
+
+
+def test_shared_expert_is_checked_when_built(cuda_lib):
+    cfg = synth.MoeConfig("c", T=2, H=256, I=128, E=8, k=2, scoring=synth.SCORE_SOFTMAX)
+    inp = synth.make_inputs(cfg, seed=0, device="cuda")
+    mk = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    good = dict(gate=mk(64, 256), up=mk(64, 256), down=mk(256, 64))
+    for kw in (dict(gate=mk(64, 264)[:, 4:260]), dict(up=mk(64, 264)[:, :256]), dict(down=mk(256, 68)[:, :64]), dict(down=mk(64, 256).t()),
+               dict(gate_bias=torch.zeros(63, device="cuda")), dict(down_bias=mk(256))):
+        with pytest.raises(ValueError, match="shared"):
+            _layer(cfg, inp, shared={**good, **kw})
+    wide = dict(gate=mk(64, 264)[:, :256], up=mk(64, 264)[:, 8:], down=mk(256, 72)[:, 8:], gate_bias=torch.zeros(64, device="cuda"))
+    layer = _layer(cfg, inp, shared=wide)
+    x = inp["x"].cuda()
+    assert torch.isfinite(layer.forward(x)[0].float()).all()
     layer.close()
