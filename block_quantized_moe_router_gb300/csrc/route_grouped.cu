@@ -370,8 +370,9 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
                 m2 = fmaxf(fminf(m1, b1), m1 > b1 ? m2 : b2);
                 m1 = fmaxf(m1, b1);
             }
-            gs[q] = P.group_top == 2 ? m1 + m2 : m1;
-            tol[q] = tol_rel * (fabsf(m1) + (P.group_top == 2 ? fabsf(m2) : 0.f)) + 2.f * tol_abs;
+            // half of the sum, which does not pass the largest number (-infinity is for what is not finite)
+            gs[q] = P.group_top == 2 ? 0.5f * m1 + 0.5f * m2 : m1;
+            tol[q] = tol_rel * (P.group_top == 2 ? 0.5f * fabsf(m1) + 0.5f * fabsf(m2) : fabsf(m1)) + tol_abs;
             if (in) sc->group[g] = gs[q];  // the lanes of a group write the same
         };
         scan(0);
