@@ -340,11 +340,13 @@ __device__ __forceinline__ void route_token(const GroupRule& P, const float (&ra
     }
     // Error bounds of a ranking value v: exp, sums and the reciprocal are within 2^-21 of the largest
     // score and of |v|, and what underflow takes is below 2^-126; an error of the softmax denominator (2^-19.7 for 512
-    // logits) scales all scores alike, so between close values it counts only with what their biases differ by.
+    // logits) scales all scores alike, so between close values it counts only with what their scores differ by: no more than the
+    // largest score, nor than their biases differ (without the former a single bias of -1e9 sent every token to fp64,
+    // 32768 rows of 128 in 828 us).
     const float tol_rel = 0x1p-21f;
     float tol_abs = 2.f * tol_rel * smax + 0x1p-125f;
     if (softmax && !P.by_logit)
-        tol_abs += 0x1p-19f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+        tol_abs += 0x1p-19f * fminf(smax, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax))));
 
     bool full = false, val_is_logit = !need_score;  // full: see pick_rounds; val_is_logit: sc->val holds logits
     __syncwarp();

@@ -100,3 +100,44 @@ def test_ruled_out_experts_rank_above_logits_that_are_not_finite(cuda_lib, scori
     for keep, k in ((1, 8), (3, 20), (7, 32)):
         for top in (1, 2):
             _check(logits, k, scoring, 8, keep, top, bias, nonfinite=True)
+
+
+def test_softmax_bias_between_close_scores(cuda_lib):
+    """Pairs of experts whose biases make up for what their probabilities differ by, to within fp32's rounding, beside an
+    expert that a bias rules out: the order is that of the exact values."""
+    T, E = 4000, 512
+    g = torch.Generator(device="cuda").manual_seed(4)
+    logits = torch.randn(1, E, generator=g, device="cuda") * 0.3
+    p = torch.softmax(logits.double(), 1)[0]
+    bias = (p.amax() - p).float()  # every sum within half a step of the same value
+    bias[7] = -1e9
+    _check(logits.expand(T, E).contiguous(), 16, SOFT_BIAS, 8, 3, 2, bias)
+    wobble = logits + torch.randn(T, E, generator=g, device="cuda") * 1e-6
+    _check(wobble, 16, SOFT_BIAS, 8, 3, 2, bias)
+    _check(wobble, 8, SOFT_BIAS, 1, 1, 1, bias)
+
+
+def test_a_ruled_out_expert_costs_no_more(cuda_lib):
+    """One bias of -1e9 among 128: of the order of the time without it (1.07 of it measured; 27 where every token went to fp64)."""
+    logits = torch.randn(32768, 128, device="cuda")
+    ids, wt = torch.empty(32768, 8, dtype=torch.int32, device="cuda"), torch.empty(32768, 8, device="cuda")
+    bias = torch.rand(128, device="cuda") * 0.01
+    masked = bias.clone()
+    masked[5] = -1e9
+
+    def us(b):
+        best = math.inf
+        for _ in range(20):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            for _ in range(10):
+                capi.moe_route_grouped(T=32768, E=128, H=0, top_k=8, scoring=SOFT_BIAS, renormalize=True, routed_scaling=1.0,
+                                       n_group=8, topk_group=3, group_top=2, logits_in=logits, correction_bias=b,
+                                       topk_ids=ids, topk_w=wt)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, begin.elapsed_time(end) * 100)
+        return best
+
+    plain = us(bias)
+    assert us(masked) <= 4 * plain
