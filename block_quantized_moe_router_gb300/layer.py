@@ -84,6 +84,7 @@ class MoeLayer:
         self.handle = capi.moe_prepare_weights(self.desc)
         self._ws = None
         self._ws_host = None
+        self._outgrown = []
         self._host_route = {}
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
 
@@ -119,10 +120,19 @@ class MoeLayer:
             pass
 
     def workspace(self, T: int) -> torch.Tensor:
-        need = capi.moe_workspace_size(self.desc, T, self.act)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+        self._ws = self._grown(self._ws, capi.moe_workspace_size(self.desc, T, self.act))
         return self._ws
+
+    def _grown(self, ws, need):
+        """`ws`, or a larger one in its place.  The one that was outgrown stays with the layer: a captured graph keeps
+        its address, another stream may still be using it.  Steps of half of it at least bound the sum of them all."""
+        if ws is not None and ws.numel() >= need:
+            return ws
+        size = max(need, 256)
+        if ws is not None:
+            self._outgrown.append(ws)
+            size = max(size, ws.numel() + ws.numel() // 2)
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
 
     def route(self, x=None, *, token_ids=None, logits_in=None, topk_ids=None, topk_w=None,
               logits_out=None, stream=None):
@@ -242,8 +252,7 @@ class MoeLayer:
                                 zero_experts=self.zero_experts)
             cached = self._host_route[T] = (d, capi.moe_workspace_size_host(self.desc, T, self.act))
         d, need = cached
-        if self._ws_host is None or self._ws_host.numel() < need:
-            self._ws_host = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+        self._ws_host = self._grown(self._ws_host, need)
         capi.moe_forward_host(self.handle, d, self.act, self.g_act1, self.g_act2, x_host, out_host,
                               self._ws_host, token_ids_host=token_ids_host,
                               topk_ids_host=topk_ids_host, topk_w_host=topk_w_host,
