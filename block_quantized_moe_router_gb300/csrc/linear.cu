@@ -425,10 +425,10 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 // columns) turn accumulators into rows and warps 10-13 move rows: the residual comes in and results
 // go out through two 16 KB buffers of 64 features (64-byte swizzled halves, so a thread per row
 // meets no bank conflicts), a pass of 64 features at a time; the next passes' residual loads
-// meanwhile.  Warp 10 alone moves them by TMA; rows that TMA cannot address (not 16-byte aligned) are
-// copied by the four warps, a warp's lanes along the row in aligned words of two features, which start at the
-// second feature where a row starts off 4 bytes; which rows do is a choice made once per pass, so that the
-// copies carry no branch (8192 x 2047 x 2048: 169 us with the epilogue's threads storing their own rows, 58
+// meanwhile.  Warp 10 alone moves them by TMA; rows that TMA cannot address (not 16-byte aligned) or would
+// write beyond (their end is not) are copied by the four warps, a warp's lanes along the row in aligned
+// words of two features, which start at the second feature where a row starts off 4 bytes; which rows do is
+// a choice made once per pass, so that the copies carry no branch (8192 x 2047 x 2048: 169 us with the epilogue's threads storing their own rows, 58
 // feature by feature, 92 with the choice in every row, 49 so, 45 at 2048 features).
 //
 // A stage is 128 elements of K: with 64 the commit and barrier round trips of twice as many stages
@@ -834,9 +834,10 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
         a.stages = plan.stages;
         return plan.pair ? launch_few<true>(m, a, plan.splits, d.N, st) : launch_few<false>(m, a, plan.splits, d.N, st);
     }
-    // TMA addresses rows that start at multiples of 16 bytes
+    // TMA addresses rows that start at multiples of 16 bytes, and writes whole ones: where a row ends inside 16 bytes, what lies
+    // behind it is written too
     a.width = plan.width;
-    a.tma_rows = rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
+    a.tma_rows = d.N % 8 == 0 && rows_aligned(out, d.ldo, 16) && (!residual || rows_aligned(residual, d.ldr, 16));
     if (a.tma_rows && (!encode_rows16(&m.out, out, d.N, d.T, d.ldo, 128, 32) ||
                        (residual && !encode_rows16(&m.res, residual, d.N, d.T, d.ldr, 128, 32))))
         return cudaErrorInvalidValue;
