@@ -23,10 +23,13 @@ inline cudaError_t allow_large_launch(K* kernel, int smem, std::atomic<uint64_t>
     return err;
 }
 
+// The warp's index, known to the compiler as one value for the warp.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 // One lane of a converged warp.  Unlike a comparison with a lane number it tells the compiler that what
 // follows runs on one thread, so that TMA and MMA operands need no search for a common value
 // (4 % of moe_linear with few rows).
 __device__ __forceinline__ bool elect_one() {
+    __syncwarp();
     uint32_t p;
     asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
     return p != 0;

@@ -227,14 +227,14 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 constexpr int kFewThreads = 256;
 
 template <bool PAIR>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 4)
 linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
     using F = Few<PAIR>;
     extern __shared__ uint8_t lin_smem[];
     __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full;
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t ctas = cluster_size(), cta = cluster_rank();
     const uint32_t splits = ctas / F::kCtas, rank = cta / F::kCtas;  // part of K
     const uint32_t half = cta % F::kCtas, first = cta - half;        // CTA of the pair, and its first one
@@ -242,7 +242,7 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     const int n0 = ((int)(blockIdx.x / ctas) * F::kCtas + (int)half) * per_cta;
     const int t0 = (int)blockIdx.y * a.rows_t;
     const int NT = a.rows_t, x_rows = NT / F::kCtas;  // of the tile, and of them here
-    const int k_begin = (int)((int64_t)a.nk * rank / splits), k_end = (int)((int64_t)a.nk * (rank + 1) / splits);
+    const int k_begin = (int)((uint32_t)a.nk * rank / splits), k_end = (int)((uint32_t)a.nk * (rank + 1) / splits);  // nk < 2^15
     const int stage_bytes = F::stage(NT);
     const int ncols = min(NT, a.T - t0);
     // [rank][W row][own columns, padded so that 16-byte accesses of 8 rows meet 32 banks]
@@ -278,62 +278,70 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
     const int steps = k_end - k_begin;
-    if (warp == 0 && elect_one()) {
-        const uint32_t full0 = PAIR ? map_rank(smem_u32(&full[0]), first) : smem_u32(&full[0]);
-        int issued = 0;
-        RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.stages)) {
-            const int s = at.slot;
-            if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
-                give_up();
-                break;
-            }
-            uint8_t* base = smem + s * stage_bytes;
-            const int kx = (k_begin + i) * kLinK;
-            if constexpr (PAIR) {
-                const uint32_t dst = smem_u32(base), bar = full0 + 8 * s;
-                if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-                tma_load_pair(dst, &maps.w, kx, n0, bar);
-                if (a.gated) tma_load_pair(dst + F::kA / 2, &maps.v, kx, n0, bar);
-                tma_load_pair(dst + F::kA, &maps.x, kx, t0 + (int)half * x_rows, bar);
-            } else {
-                mbar_arrive_expect_tx(&full[s], stage_bytes);
-                tma_load_2d(base, &maps.w, kx, n0, &full[s]);
-                if (a.gated) tma_load_2d(base + F::kA / 2, &maps.v, kx, n0, &full[s]);
-                tma_load_2d(base + F::kA, &maps.x, kx, t0, &full[s]);
-            }
-            ++issued;
-        }
-        // whoever gives up, no copy is in flight when the CTA ends (the pair's arrive at its first CTA)
-        if (half == 0)
-            for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
-                at.back(a.stages);
-                mbar_wait_suspended(&full[at.slot], at.parity);
-            }
-    } else if (warp == 1 && elect_one()) {
-        if (half == 0) {
-            const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
+    // The elected lane's role is all that its warp does until the lane is done: the rest of the warp waits at the end of
+    // the role, so that nothing it might run shares the warp's uniform registers with the lane's copies and MMAs
+    if (warp == 0) {
+        if (elect_one()) {
+            const uint32_t full0 = PAIR ? map_rank(smem_u32(&full[0]), first) : smem_u32(&full[0]);
+            int issued = 0;
             RingPos at;
             for (int i = 0; i < steps; ++i, at.next(a.stages)) {
                 const int s = at.slot;
-                if (!mbar_wait_suspended(&full[s], at.parity)) {
+                if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                     give_up();
                     break;
                 }
-                tc_fence_after();
-                const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
-                    mma_f16kind<PAIR>(tmem, ad + 2 * j, ad + (F::kA >> 4) + 2 * j, idesc, (i | j) != 0);
-                if constexpr (PAIR) tc_commit_pair(&empty[s], 3u << first);
-                else tc_commit(&empty[s]);
+                uint8_t* base = smem + s * stage_bytes;
+                const int kx = (k_begin + i) * kLinK;
+                if constexpr (PAIR) {
+                    const uint32_t dst = smem_u32(base), bar = full0 + 8 * s;
+                    if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+                    tma_load_pair(dst, &maps.w, kx, n0, bar);
+                    if (a.gated) tma_load_pair(dst + F::kA / 2, &maps.v, kx, n0, bar);
+                    tma_load_pair(dst + F::kA, &maps.x, kx, t0 + (int)half * x_rows, bar);
+                } else {
+                    mbar_arrive_expect_tx(&full[s], stage_bytes);
+                    tma_load_2d(base, &maps.w, kx, n0, &full[s]);
+                    if (a.gated) tma_load_2d(base + F::kA / 2, &maps.v, kx, n0, &full[s]);
+                    tma_load_2d(base + F::kA, &maps.x, kx, t0, &full[s]);
+                }
+                ++issued;
             }
-            // arrives when every MMA has completed
-            if constexpr (PAIR) tc_commit_pair(&acc_full, 3u << first);
-            else tc_commit(&acc_full);
+            // whoever gives up, no copy is in flight when the CTA ends (the pair's arrive at its first CTA)
+            if (half == 0)
+                for (int i = issued < a.stages ? issued : a.stages; i > 0; --i) {
+                    at.back(a.stages);
+                    mbar_wait_suspended(&full[at.slot], at.parity);
+                }
         }
-        if (!mbar_wait_suspended(&acc_full, 0)) give_up();
-        tc_fence_before();
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            if (half == 0) {
+                const uint32_t idesc = idesc_f16kind(128, NT, a.f16);
+                RingPos at;
+                for (int i = 0; i < steps; ++i, at.next(a.stages)) {
+                    const int s = at.slot;
+                    if (!mbar_wait_suspended(&full[s], at.parity)) {
+                        give_up();
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                        mma_f16kind<PAIR>(tmem, ad + 2 * j, ad + (F::kA >> 4) + 2 * j, idesc, (i | j) != 0);
+                    if constexpr (PAIR) tc_commit_pair(&empty[s], 3u << first);
+                    else tc_commit(&empty[s]);
+                }
+                // arrives when every MMA has completed
+                if constexpr (PAIR) tc_commit_pair(&acc_full, 3u << first);
+                else tc_commit(&acc_full);
+            }
+            if (!mbar_wait_suspended(&acc_full, 0)) give_up();
+            tc_fence_before();
+        }
+        __syncwarp();
     } else if (warp >= 6) {
         // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
         if (a.res)
@@ -454,13 +462,28 @@ struct ManySched {
         tiles_n = (N + features - 1) / features;
         total = (int64_t)tiles_t * tiles_n;
     }
-    // tile i: its row tile and column tile; kManyGroup row tiles run through all columns together
-    __device__ __forceinline__ void tile(int64_t i, int& tt, int& tn) const {
-        const int64_t per = (int64_t)kManyGroup * tiles_n;
-        const int g = (int)(i / per), rest = (int)(i % per);
-        const int rows = min(kManyGroup, tiles_t - g * kManyGroup);
-        tt = g * kManyGroup + rest % rows;
-        tn = rest / rows;
+    // A tile's place: kManyGroup row tiles run through all columns together.  Counted on from tile to tile in 32 bits (a
+    // group has fewer than 2^18 tiles): a 64-bit division would be a call, and the thread that issues copies makes none.
+    struct Place {
+        int64_t tile;
+        uint32_t group, rest;
+    };
+    __device__ __forceinline__ Place begin(int pair) const {
+        const uint32_t per = (uint32_t)(kManyGroup * tiles_n);
+        return Place{pair, (uint32_t)pair / per, (uint32_t)pair % per};
+    }
+    __device__ __forceinline__ void next(Place& at, int pairs) const {
+        const uint32_t per = (uint32_t)(kManyGroup * tiles_n);
+        at.tile += pairs;
+        at.rest += (uint32_t)pairs;
+        at.group += at.rest / per;
+        at.rest %= per;
+    }
+    // its row tile and column tile
+    __device__ __forceinline__ void tiles(const Place& at, int& tt, int& tn) const {
+        const uint32_t rows = (uint32_t)min(kManyGroup, tiles_t - (int)at.group * kManyGroup);
+        tt = (int)at.group * kManyGroup + (int)(at.rest % rows);
+        tn = (int)(at.rest / rows);
     }
 };
 
@@ -479,7 +502,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
     uint8_t* rows_s = smem + kManyStages * kManyStageBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int half = a.width / 2;
@@ -518,69 +541,75 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         abort_flag = 1;
         status_or(a.status, MOE_DEV_TIMEOUT);
     };
-    auto first = [&](int64_t i, int& r0, int& f0) {  // this CTA's first row, the first feature of tile i
+    auto first = [&](const ManySched::Place& i, int& r0, int& f0) {  // this CTA's first row, the first feature of tile i
         int tt, tn;
-        sched.tile(i, tt, tn);
+        sched.tiles(i, tt, tn);
         r0 = tt * 256 + rank * 128;
         f0 = tn * per_tile;
     };
-    if (warp == 0 && elect_one()) {  // TMA producer of this CTA's halves
-        const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
-        int it = 0;
-        RingPos at;
-        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs) {
-            int t0, n0;
-            first(i, t0, n0);
-            if (!a.gated) n0 += rank * half;
-            for (int k = 0; k < a.nk; k += 2, ++it, at.next(kManyStages)) {
-                const int s = at.slot, parts = min(2, a.nk - k);
-                if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
-                    give_up();
-                    break;
-                }
-                const uint32_t base = smem_u32(smem + s * kManyStageBytes);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * parts * (kLinA + half * 128));
-                const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-                for (int h = 0; h < parts; ++h) {
-                    tma_load_pair(base + h * kManyHalf, &maps.x, (k + h) * kLinK, t0, bar);
-                    tma_load_pair(base + h * kManyHalf + kLinA, wmap, (k + h) * kLinK, n0, bar);
+    if (warp == 0) {  // roles of elected lanes as in the other kernel
+        if (elect_one()) {  // TMA producer of this CTA's halves
+            const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
+            int it = 0;
+            RingPos at;
+            for (auto i = sched.begin(pair); i.tile < sched.total && !abort_flag; sched.next(i, pairs)) {
+                int t0, n0;
+                first(i, t0, n0);
+                if (!a.gated) n0 += rank * half;
+                for (int k = 0; k < a.nk; k += 2, ++it, at.next(kManyStages)) {
+                    const int s = at.slot, parts = min(2, a.nk - k);
+                    if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
+                        give_up();
+                        break;
+                    }
+                    const uint32_t base = smem_u32(smem + s * kManyStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * parts * (kLinA + half * 128));
+                    const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+                    for (int h = 0; h < parts; ++h) {
+                        tma_load_pair(base + h * kManyHalf, &maps.x, (k + h) * kLinK, t0, bar);
+                        tma_load_pair(base + h * kManyHalf + kLinA, wmap, (k + h) * kLinK, n0, bar);
+                    }
                 }
             }
+            if (rank == 0)  // whoever gives up, none of the pair's copies is in flight when its CTAs end
+                for (int i = it < kManyStages ? it : kManyStages; i > 0; --i) {
+                    at.back(kManyStages);
+                    mbar_wait_suspended(&full[at.slot], at.parity);
+                }
         }
-        if (rank == 0)  // whoever gives up, none of the pair's copies is in flight when its CTAs end
-            for (int i = it < kManyStages ? it : kManyStages; i > 0; --i) {
-                at.back(kManyStages);
-                mbar_wait_suspended(&full[at.slot], at.parity);
-            }
-    } else if (warp == 1 && rank == 0 && elect_one()) {  // MMA issuer of the pair
-        const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
-        int n = 0;
-        RingPos ring;
-        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
-            const int b = n & 1;
-            if (!mbar_wait_suspended(&acc_empty[b], ((n >> 1) & 1) ^ 1)) {
-                give_up();
-                break;
-            }
-            tc_fence_after();
-            for (int k = 0; k < a.nk; k += 2, ring.next(kManyStages)) {
-                const int s = ring.slot, parts = min(2, a.nk - k);
-                if (!mbar_wait_suspended(&full[s], ring.parity)) {
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {  // MMA issuer of the pair
+            const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
+            int n = 0;
+            RingPos ring;
+            for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
+                const int b = n & 1;
+                if (!mbar_wait_suspended(&acc_empty[b], ((n >> 1) & 1) ^ 1)) {
                     give_up();
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 1024, kLayoutSw128);
-                for (int h = 0; h < parts; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // K 16 per MMA: 32 bytes (two units) along the swizzled row
-                        const uint64_t at = ad + h * (kManyHalf >> 4) + 2 * j;
-                        mma_f16kind<1>(tmem + 256 * b, at, at + (kLinA >> 4), idesc, (k | h | j) != 0);
+                for (int k = 0; k < a.nk; k += 2, ring.next(kManyStages)) {
+                    const int s = ring.slot, parts = min(2, a.nk - k);
+                    if (!mbar_wait_suspended(&full[s], ring.parity)) {
+                        give_up();
+                        break;
                     }
-                tc_commit_pair(&empty[s], 3);
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 1024, kLayoutSw128);
+                    for (int h = 0; h < parts; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                            const uint64_t at = ad + h * (kManyHalf >> 4) + 2 * j;
+                            mma_f16kind<1>(tmem + 256 * b, at, at + (kLinA >> 4), idesc, (k | h | j) != 0);
+                        }
+                    tc_commit_pair(&empty[s], 3);
+                }
+                tc_commit_pair(&acc_full[b], 3);
             }
-            tc_commit_pair(&acc_full[b], 3);
         }
+        __syncwarp();
     } else if (warp >= 2 && warp < 10) {
         const int q = warp & 3, side = (warp - 2) >> 2;  // lane quarter, parity of the columns' 16s
         const int row = 32 * q + lane, sw = (row >> 1) & 3;
@@ -588,8 +617,6 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         uint32_t pass = 0;
         for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
             const int b = n & 1;
-            int r0, f0;
-            first(i, r0, f0);
             if (!__all_sync(0xffffffffu, mbar_wait_suspended(&acc_full[b], (n >> 1) & 1))) {
                 give_up();
                 break;
@@ -629,8 +656,18 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[b]), 0));
         }
     } else if (warp >= 10 && (warp == 10 || !by_tma)) {  // row movers
-        const int64_t tiles = pair < sched.total ? (sched.total - pair + pairs - 1) / pairs : 0;
-        const int64_t all = tiles * passes;
+        struct {
+            ManySched::Place at;
+            int p;             // pass of the tile
+            uint32_t pass;     // of all this CTA's
+        } next_in{sched.begin(pair), 0, 0}, out_of = next_in;  // the pass to make a buffer ready for, and to move out
+        const auto go_on = [&](auto& to) {
+            ++to.pass;
+            if (++to.p == passes) {
+                to.p = 0;
+                sched.next(to.at, pairs);
+            }
+        };
         const int first_row = 32 * (warp - 10);  // of this warp's share, without TMA
         // row r, feature f < 64 of a buffer
         const auto element = [&](int buf, int r, int f) {
@@ -651,13 +688,13 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 else f(Not{}, Not{});
             }
         };
-        // makes buffer g & 1 ready for pass g: its biases, and the residual if there is one
-        const auto prepare = [&](int64_t g) {
-            if (g >= all) return;
-            const int buf = (int)(g & 1);
+        // makes a buffer ready for the next pass, if there is one: its biases, and the residual if there is one
+        const auto prepare = [&]() {
+            if (next_in.at.tile >= sched.total) return;
+            const int buf = (int)(next_in.pass & 1);
             int r0, f0;
-            first(pair + g / passes * pairs, r0, f0);
-            const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
+            first(next_in.at, r0, f0);
+            const int p = next_in.p, fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
             if ((a.bias || a.bias_mul) && warp == 10) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -709,20 +746,22 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 }
             }
             __syncwarp();
+            go_on(next_in);
         };
-        prepare(0);
-        prepare(1);
-        int64_t g = 0;
-        for (; g < all; ++g) {
-            const int buf = (int)(g & 1);
-            if (!__all_sync(0xffffffffu, mbar_wait_suspended(&buf_done[buf], (g >> 1) & 1)) ||
+        prepare();
+        prepare();
+        bool gave_up = false;
+        for (; out_of.at.tile < sched.total; go_on(out_of)) {
+            const int buf = (int)(out_of.pass & 1);
+            if (!__all_sync(0xffffffffu, mbar_wait_suspended(&buf_done[buf], (out_of.pass >> 1) & 1)) ||
                 __any_sync(0xffffffffu, abort_flag)) {
                 give_up();
+                gave_up = true;
                 break;
             }
             int r0, f0;
-            first(pair + g / passes * pairs, r0, f0);
-            const int p = (int)(g % passes), fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
+            first(out_of.at, r0, f0);
+            const int p = out_of.p, fp = f0 + 64 * p, pieces = min(2, subs - 2 * p);
             if (!by_tma) {
                 uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)r0 + first_row) * a.ldo + fp;
                 const int rows = min(32, a.T - r0 - first_row), in = min(32 * pieces, a.N - fp);
@@ -760,11 +799,10 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             }
             __syncwarp();
-            prepare(g + 2);
+            prepare();
         }
-        if (g < all)  // gave up: wait (bounded) for the residual copies in flight
-            for (int64_t j = g; j < g + 2 && j < all; ++j)
-                mbar_wait_suspended(&buf_ready[j & 1], (j >> 1) & 1);
+        if (gave_up)  // wait (bounded) for the residual copies in flight
+            for (uint32_t j = out_of.pass; j != next_in.pass; ++j) mbar_wait_suspended(&buf_ready[j & 1], (j >> 1) & 1);
         if (lane == 0 && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();

@@ -557,12 +557,12 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     __shared__ uint64_t full[kFusedStagesMax], empty[kFusedStagesMax], acc_full;
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rf_smem) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int splits = (int)cluster_size(), rank = (int)cluster_rank();
     const int64_t t0 = (int64_t)(blockIdx.x / splits) * 128;
     const int rows = (int)min((int64_t)128, a.T - t0);  // tokens of this tile
     const int stage_bytes = kFusedA + a.p.n * 128;
-    const int k_begin = (int)((int64_t)a.p.nk * rank / a.p.parts), k_end = (int)((int64_t)a.p.nk * (rank + 1) / a.p.parts);
+    const int k_begin = a.p.nk * rank / a.p.parts, k_end = a.p.nk * (rank + 1) / a.p.parts;  // nk < 2^26, rank < 16
     const int steps = rank < a.p.parts ? k_end - k_begin : 0;
     const int e0 = (int)blockIdx.y * a.p.n, experts = min(a.p.n, a.E - e0);  // of this block
     const int pitch = a.p.n + 4;  // floats: 16-byte accesses of eight rows meet 32 banks
@@ -587,47 +587,54 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
-    if (warp == 0 && elect_one()) {  // TMA producer
-        const uint32_t bytes = (uint32_t)(a.p.box_x * 128 + a.p.n * 128);
-        int issued = 0;
-        RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
-            const int s = at.slot;
-            if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
-                give_up();
-                break;
+    // the rest of an elected lane's warp waits at the end of its role (linear.cu says why)
+    if (warp == 0) {
+        if (elect_one()) {  // TMA producer
+            const uint32_t bytes = (uint32_t)(a.p.box_x * 128 + a.p.n * 128);
+            int issued = 0;
+            RingPos at;
+            for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
+                const int s = at.slot;
+                if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
+                    give_up();
+                    break;
+                }
+                uint8_t* base = smem + s * stage_bytes;
+                const int kx = (k_begin + i) * kFusedK;
+                mbar_arrive_expect_tx(&full[s], bytes);
+                tma_load_2d(base + kFusedA, &maps.w, kx, e0, &full[s]);
+                tma_load_2d(base, &maps.x, kx, (int)t0, &full[s]);  // rows beyond the box: never read back
+                ++issued;
             }
-            uint8_t* base = smem + s * stage_bytes;
-            const int kx = (k_begin + i) * kFusedK;
-            mbar_arrive_expect_tx(&full[s], bytes);
-            tma_load_2d(base + kFusedA, &maps.w, kx, e0, &full[s]);
-            tma_load_2d(base, &maps.x, kx, (int)t0, &full[s]);  // rows beyond the box: never read back
-            ++issued;
-        }
-        // whoever gives up, no copy is in flight when the CTA ends
-        for (int i = issued < a.p.stages ? issued : a.p.stages; i > 0; --i) {
-            at.back(a.p.stages);
-            mbar_wait_suspended(&full[at.slot], at.parity);
-        }
-    } else if (warp == 1 && elect_one()) {  // MMA issuer
-        const uint32_t idesc = idesc_bf16(128, a.p.n);
-        RingPos at;
-        for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
-            const int s = at.slot;
-            if (!mbar_wait_suspended(&full[s], at.parity)) {
-                give_up();
-                break;
+            // whoever gives up, no copy is in flight when the CTA ends
+            for (int i = issued < a.p.stages ? issued : a.p.stages; i > 0; --i) {
+                at.back(a.p.stages);
+                mbar_wait_suspended(&full[at.slot], at.parity);
             }
-            tc_fence_after();
-            const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {  // MMA issuer
+            const uint32_t idesc = idesc_bf16(128, a.p.n);
+            RingPos at;
+            for (int i = 0; i < steps; ++i, at.next(a.p.stages)) {
+                const int s = at.slot;
+                if (!mbar_wait_suspended(&full[s], at.parity)) {
+                    give_up();
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = smem_desc(smem_u32(smem + s * stage_bytes), 16, 1024, kLayoutSw128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
-                tc_mma_bf16(tmem, ad + 2 * j, ad + (kFusedA >> 4) + 2 * j, idesc, (i | j) != 0);
-            tc_commit(&empty[s]);
+                for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
+                    tc_mma_bf16(tmem, ad + 2 * j, ad + (kFusedA >> 4) + 2 * j, idesc, (i | j) != 0);
+                tc_commit(&empty[s]);
+            }
+            tc_commit(&acc_full);  // arrives when every MMA has completed
+            if (!mbar_wait_suspended(&acc_full, 0)) give_up();
+            tc_fence_before();
         }
-        tc_commit(&acc_full);  // arrives when every MMA has completed
-        if (!mbar_wait_suspended(&acc_full, 0)) give_up();
-        tc_fence_before();
+        __syncwarp();
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
     cluster_wait();
