@@ -8,7 +8,9 @@ synchronisation.
 Optional parts around the expert FFN:
   n_group / topk_group / group_top   routing limited to expert groups (moe_route_grouped)
   shared   a bf16 shared expert {gate, up [I][H], down [H][I], and float biases gate_bias, up_bias
-           [I], down_bias [H] if it has them}, added through moe_linear; instead of an FP4 one
+           [I], down_bias [H] if it has them}, added through moe_linear; instead of an FP4 one.
+           It is added to the routed experts' sum as that was rounded to bf16, and the result is
+           rounded again; an FP4 shared expert joins the sum in fp32
   norm_weight / norm_eps   the RMS norm before the layer, with the residual add (block())
 """
 from __future__ import annotations

@@ -208,7 +208,9 @@ moe_status_t moe_route_grouped(const moe_route_desc* desc, int32_t n_group, int3
  * shared expert of the pages (moe/init.rs, the bf16 shared-expert handle lookups) and for plain
  * layers next to the MoE ones.  Products accumulate in fp32; bias, function, the second factor
  * and the residual are applied in fp32 and the result is rounded once (fp16 overflows to
- * infinity).  The order of the sums depends on the sizes alone: equal calls give equal bits.
+ * infinity).  The order of the sums depends on the sizes alone: equal calls give equal bits.  SiLU and
+ * tanh GELU are within 2^-15 of themselves (0 below 2^-119); erf GELU within 2^-23 |z|, which far below
+ * 0 is more than its own size.
  * x, w      [device] desc->dtype, 16-byte aligned.
  * w_mul     [device] or NULL: the second matrix of the gated form, 16-byte aligned.
  * bias, bias_mul [device] float [N] or NULL; bias_mul needs w_mul.
