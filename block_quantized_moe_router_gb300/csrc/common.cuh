@@ -15,10 +15,6 @@ namespace moe {
 
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
-constexpr int kMaxGroups = 64;
-constexpr int kMaxLinear = 1 << 20;  // N and K of moe_linear
-constexpr int kMaxLinearRows = 1 << 30;
-constexpr int kMaxNorm = 16384;      // H of moe_add_rms_norm
 
 // ---- loads --------------------------------------------------------------------------------
 // 16-byte read-only streaming load (weights are read once per launch: keep them out of L1).

@@ -28,6 +28,7 @@ cudaError_t launch_hash_route(const int64_t* tid2eid, const int32_t* token_ids, 
                               int32_t* ids, float* w, int32_t* status, cudaStream_t st);
 
 // Top-K limited to expert groups (route_grouped.cu).
+constexpr int kMaxGroups = 64;
 cudaError_t launch_topk_grouped(const float* logits, const float* bias, int T, int E, int k, int scoring,
                                 int renorm, float scaling, int n_group, int topk_group, int group_top,
                                 int32_t* ids, float* w, int32_t* status, cudaStream_t st);
@@ -39,6 +40,9 @@ cudaError_t launch_route_fused(const void* x, const void* wr, const float* bias,
                                cudaStream_t st);
 
 // ---- dense layers around the experts (linear.cu, norm.cu) -----------------------------------
+constexpr int kMaxLinear = 1 << 20;  // N and K of moe_linear
+constexpr int kMaxLinearRows = 1 << 30;
+constexpr int kMaxNorm = 16384;      // H of moe_add_rms_norm
 cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
                           const float* bias, const float* bias_mul, const void* residual, void* out,
                           int32_t* status, cudaStream_t st);

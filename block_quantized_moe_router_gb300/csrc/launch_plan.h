@@ -12,6 +12,7 @@ namespace moe {
 // columns for, clusters of several streams could each hold columns on one and wait for the other's on the
 // other, for ever.  So a CTA that takes a share of the columns takes at least that share of the SM's shared memory: CTAs
 // that fit by shared memory fit by columns, whatever their kernels and registers.
+// CTAs without a cluster (prefill_tc.cu) hold theirs only while they run on, and wait for nobody then.
 constexpr int kSmSmem = 228 * 1024;       // shared memory of an SM
 constexpr int kCtaSmemMax = 226 * 1024;   // dynamic shared memory of a CTA here
 constexpr int kSmemReserved = 1024;       // taken per CTA besides

@@ -38,7 +38,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "launch_plan.h"
 #include "quant.cuh"
 #include "tc_ptx.cuh"
 
@@ -66,7 +65,6 @@ constexpr int kTcSfbBytes = 4096;
 constexpr int kTcSfbOff = kTcSfaOff + kTcSfaBytes;
 constexpr int kTcStageBytes = kTcSfbOff + kTcSfbBytes;  // 55296 (54 KiB, 1 KiB multiple)
 constexpr int kTcSmemBytes = kTcStages * kTcStageBytes + 1024 + 256;
-static_assert(columns_covered(kTcSmemBytes, kTcTmemCols));
 constexpr int kTcThreads = 448;    // producer warp, MMA warp, 8 epilogue warps, 4 scale warps
 constexpr int kTcScaleWarp0 = 10;
 // Registers: each of the SM's four sub-partitions holds 16384, and 14 warps put four warps on
@@ -881,7 +879,6 @@ void tc_release(TcWeights* tw) {
 constexpr int kRtStages = 4;
 constexpr int kRtStageBytes = 2 * 128 * 128;  // A and B: 128 rows x 128 B each
 constexpr int kRtSmemBytes = kRtStages * kRtStageBytes + 1024 + 256;
-static_assert(columns_covered(kRtSmemBytes, 128));
 constexpr int kRtThreads = 192;
 
 struct RtMaps {
