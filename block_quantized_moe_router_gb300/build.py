@@ -26,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 SOURCES = ["api.cu", "route.cu", "route_grouped.cu", "ffn.cu", "decode.cu", "decode_t1.cu",
-           "prefill_tc.cu", "noalloc.cu", "linear.cu", "norm.cu"]
+           "prefill_tc.cu", "noalloc.cu", "linear.cu", "norm.cu", "adapters.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

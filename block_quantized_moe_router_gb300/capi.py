@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_WORKSPACE = range(5)
 MOE_DEV_BAD_EXPERT_ID, MOE_DEV_BAD_TOKEN_ID, MOE_DEV_NONFINITE, MOE_DEV_TIMEOUT = 1, 2, 4, 8
+MOE_DEV_BAD_ADAPTER_ID = 16
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_HASH, MOE_SCORE_SQRTSOFTPLUS = 0, 1, 2, 3
 MOE_SCORE_SOFTMAX_BIAS, MOE_SCORE_HASH_SQRTSOFTPLUS = 4, 5
 MOE_FMT_NVFP4, MOE_FMT_MXFP4 = 0, 1
@@ -29,7 +30,7 @@ MOE_FUNC_NONE, MOE_FUNC_SILU, MOE_FUNC_GELU, MOE_FUNC_GELU_TANH, MOE_FUNC_RELU =
 EXPORTED = ["moe_route", "moe_workspace_size", "moe_prepare_weights", "moe_release_weights",
             "moe_ffn_forward", "moe_forward", "moe_workspace_size_host", "moe_forward_host",
             "moe_ffn_forward_noalloc", "moe_quantize_act_nvfp4", "moe_route_grouped", "moe_linear",
-            "moe_add_rms_norm",
+            "moe_add_rms_norm", "moe_linear_adapters", "moe_adapter_workspace_size", "moe_sandwich_norm",
             "moe_set_wait_limit", "moe_skew_barrier", "moe_profile_enable", "moe_profile_read",
             "moe_status_string"]
 
@@ -74,6 +75,21 @@ class moe_norm_desc(ctypes.Structure):
                 ("lds", ctypes.c_int64), ("ldo", ctypes.c_int64)]
 
 
+class moe_adapter_desc(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("R", ctypes.c_int32), ("lda", ctypes.c_int64),
+                ("sa", ctypes.c_int64), ("ldb", ctypes.c_int64), ("sb", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("a_mul", ctypes.c_void_p),
+                ("b_mul", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ids", ctypes.c_void_p)]
+
+
+class moe_sandwich_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("wide", ctypes.c_int32), ("row_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("lds", ctypes.c_int64),
+                ("ldo", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -97,6 +113,13 @@ def load_library(path: str = LIB_PATH):
     lib.moe_linear.restype = ctypes.c_int
     lib.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_desc), vp, vp, vp, vp, vp, vp]
     lib.moe_add_rms_norm.restype = ctypes.c_int
+    lib.moe_linear_adapters.argtypes = [ctypes.POINTER(moe_linear_desc), ctypes.POINTER(moe_adapter_desc), vp, vp,
+                                        vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.moe_linear_adapters.restype = ctypes.c_int
+    lib.moe_adapter_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+    lib.moe_adapter_workspace_size.restype = ctypes.c_int
+    lib.moe_sandwich_norm.argtypes = [ctypes.POINTER(moe_sandwich_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_sandwich_norm.restype = ctypes.c_int
     lib.moe_workspace_size.argtypes = [ctypes.POINTER(moe_ffn_desc), i32, i32, ctypes.POINTER(sz)]
     lib.moe_workspace_size.restype = ctypes.c_int
     lib.moe_prepare_weights.argtypes = [ctypes.POINTER(moe_ffn_desc), ctypes.POINTER(vp), vp]
@@ -312,6 +335,103 @@ def moe_add_rms_norm(x, weight, out, *, residual=None, sum_out=None, eps=1e-6, s
                                          ps, po, st)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_add_rms_norm")
+
+
+def _adapters(t, dtype, L, rows, cols, dev, name):
+    """Pointer, row and adapter stride of stacked adapter matrices [L][rows][cols]."""
+    if t.dtype != dtype or t.shape != (L, rows, cols) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor {(L, rows, cols)} on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    step, ld, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (ld if rows > 1 else cols), step
+
+
+def moe_adapter_workspace_size(T: int, R: int, matrices: int) -> int:
+    n = ctypes.c_size_t(0)
+    rc = (_lib or load_library()).moe_adapter_workspace_size(T, R, matrices, ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_adapter_workspace_size")
+    return n.value
+
+
+def moe_linear_adapters(x, w, out, ids, *, a=None, b=None, a_mul=None, b_mul=None, scale=None, w_mul=None,
+                        bias=None, bias_mul=None, residual=None, func=MOE_FUNC_NONE, workspace,
+                        dev_status=None, stream=None):
+    """moe_linear with low-rank adapters: x w^T gains scale[j] (x a[j]^T) b[j]^T for the adapter j = ids[t] of
+    each row (-1: none), x w_mul^T the same of a_mul and b_mul.  ids int32 [T]; a and a_mul [L][R][K], b and b_mul
+    [L][N][R], of the layer's type; scale float [L]; workspace: moe_adapter_workspace_size(T, R, matrices) bytes."""
+    st, dev = _stream_device(stream)
+    dt = x.dtype
+    T, K = x.shape
+    N = w.shape[0]
+    first = a if a is not None else a_mul
+    if first is None or first.dim() != 3:
+        raise ValueError("adapters must be given as a and b, or a_mul and b_mul, of three dimensions")
+    L, R = first.shape[:2]
+    px, ldx = _rows(x, dt, T, K, dev, "x")
+    pw, ldw = _rows(w, dt, N, K, dev, "w")
+    po, ldo = _rows(out, dt, T, N, dev, "out")
+    pm = pr = None
+    ldr = N
+    if w_mul is not None:
+        pm, ldm = _rows(w_mul, dt, N, K, dev, "w_mul")
+        if ldm != ldw:
+            raise ValueError("w_mul must have the row stride of w")
+    if residual is not None:
+        pr, ldr = _rows(residual, dt, T, N, dev, "residual")
+    ptr = {}
+    strides = {}
+    for name, t, rows, cols in (("a", a, R, K), ("b", b, N, R), ("a_mul", a_mul, R, K), ("b_mul", b_mul, N, R)):
+        if t is None:
+            ptr[name] = None
+            continue
+        ptr[name], ld, step = _adapters(t, dt, L, rows, cols, dev, name)
+        if strides.setdefault(name[0], (ld, step)) != (ld, step):
+            raise ValueError(f"{name} must have the strides of {name[0]}")
+    lda, sa = strides.get("a", (K, 0))
+    ldb, sb = strides.get("b", (R, 0))
+    if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
+    d = moe_linear_desc(T, N, K, _DTYPES.get(dt, -1), func, ldx, ldw, ldr, ldo)
+    ad = moe_adapter_desc(L, R, lda, sa, ldb, sb, ptr["a"], ptr["b"], ptr["a_mul"], ptr["b_mul"],
+                          _tptr(scale, torch.float32, (L,), dev, "scale"), _tptr(ids, torch.int32, (T,), dev, "ids"))
+    rc = (_lib or load_library()).moe_linear_adapters(
+        ctypes.byref(d), ctypes.byref(ad), px, pw, pm, _tptr(bias, torch.float32, (N,), dev, "bias"),
+        _tptr(bias_mul, torch.float32, (N,), dev, "bias_mul"), pr, po, workspace.data_ptr(), workspace.numel(),
+        _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_linear_adapters")
+
+
+def moe_sandwich_norm(x, sum_out, *, residual=None, post_weight=None, gate=None, row_gate=None, row_sigmoid=False,
+                      weight=None, out=None, residual_scale=1.0, weight_offset=0.0, eps=1e-6, stream=None):
+    """p = norm(x) * (post_weight + weight_offset), or x without post_weight; sum_out = residual_scale * residual +
+    row_gate * gate * p; out = norm(sum) * (weight + weight_offset).  x and out [T][H], post_weight, gate and weight [H]
+    of one type (bf16 or f16); residual and sum_out [T][H] of that type or float32; row_gate float32 [T], with
+    row_sigmoid its logits; rows of any stride."""
+    st, dev = _stream_device(stream)
+    dt = x.dtype
+    T, H = x.shape
+    stream_dt = sum_out.dtype
+    if stream_dt != dt and stream_dt != torch.float32:
+        raise ValueError(f"sum_out must be of the type of x or float32, got {stream_dt}")
+    px, ldx = _rows(x, dt, T, H, dev, "x")
+    ps, lds = _rows(sum_out, stream_dt, T, H, dev, "sum_out")
+    pr = po = None
+    ldr = ldo = H
+    if residual is not None:
+        pr, ldr = _rows(residual, stream_dt, T, H, dev, "residual")
+    if out is not None:
+        po, ldo = _rows(out, dt, T, H, dev, "out")
+    d = moe_sandwich_desc(T, H, _DTYPES.get(dt, -1), stream_dt == torch.float32, row_sigmoid, eps, residual_scale,
+                          weight_offset, ldx, ldr, lds, ldo)
+    rc = (_lib or load_library()).moe_sandwich_norm(
+        ctypes.byref(d), px, pr, _tptr(post_weight, dt, (H,), dev, "post_weight"), _tptr(gate, dt, (H,), dev, "gate"),
+        _tptr(row_gate, torch.float32, (T,), dev, "row_gate"), _tptr(weight, dt, (H,), dev, "weight"), ps, po, st)
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_sandwich_norm")
 
 
 def moe_workspace_size(desc: moe_ffn_desc, T: int, act: int) -> int:

@@ -193,6 +193,26 @@ struct HostStage {
     }
 };
 
+// The checks of moe_linear; MOE_OK with T == 0 for a valid call that does nothing.
+moe_status_t validate_linear(const moe_linear_desc* d, const void* x, const void* w, const void* w_mul, const float* bias,
+                             const float* bias_mul, const void* residual, const void* out, const int32_t* dev_status) {
+    if (!d || d->T < 0 || d->T > kMaxLinearRows || d->N < 1 || d->N > kMaxLinear || d->K < 8 || d->K > kMaxLinear || d->K % 8)
+        return MOE_ERR_INVALID_ARG;
+    if ((d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16) || d->func < MOE_FUNC_NONE ||
+        d->func > MOE_FUNC_RELU)
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_ld(d->ldx, d->K) || d->ldx % 8 || !valid_ld(d->ldw, d->K) || d->ldw % 8 ||
+        !valid_ld(d->ldo, d->N) || (residual && !valid_ld(d->ldr, d->N)) || (bias_mul && !w_mul))
+        return MOE_ERR_INVALID_ARG;
+    if (out && (out == x || out == w || out == w_mul || (out == residual && d->ldo != d->ldr)))
+        return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(w_mul) || !aligned2(residual) ||
+        !aligned2(out) || !aligned4(bias) || !aligned4(bias_mul) || !aligned4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -288,22 +308,41 @@ moe_status_t moe_route_grouped(const moe_route_desc* d, int32_t n_group, int32_t
 moe_status_t moe_linear(const moe_linear_desc* d, const void* x, const void* w, const void* w_mul,
                         const float* bias, const float* bias_mul, const void* residual, void* out,
                         int32_t* dev_status, void* stream) {
-    if (!d || d->T < 0 || d->T > kMaxLinearRows || d->N < 1 || d->N > kMaxLinear || d->K < 8 || d->K > kMaxLinear || d->K % 8)
-        return MOE_ERR_INVALID_ARG;
-    if ((d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16) || d->func < MOE_FUNC_NONE ||
-        d->func > MOE_FUNC_RELU)
-        return MOE_ERR_INVALID_ARG;
-    if (!valid_ld(d->ldx, d->K) || d->ldx % 8 || !valid_ld(d->ldw, d->K) || d->ldw % 8 ||
-        !valid_ld(d->ldo, d->N) || (residual && !valid_ld(d->ldr, d->N)) || (bias_mul && !w_mul))
-        return MOE_ERR_INVALID_ARG;
-    if (out && (out == x || out == w || out == w_mul || (out == residual && d->ldo != d->ldr)))
-        return MOE_ERR_INVALID_ARG;
-    if (d->T == 0) return MOE_OK;
-    if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(w_mul) || !aligned2(residual) ||
-        !aligned2(out) || !aligned4(bias) || !aligned4(bias_mul) || !aligned4(dev_status))
-        return MOE_ERR_INVALID_ARG;
+    const moe_status_t v = validate_linear(d, x, w, w_mul, bias, bias_mul, residual, out, dev_status);
+    if (v != MOE_OK || d->T == 0) return v;
     return launch_linear(*d, x, w, w_mul, bias, bias_mul, residual, out, dev_status,
                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_adapter_workspace_size(int32_t T, int32_t R, int32_t matrices, size_t* bytes) {
+    if (!bytes || T < 0 || T > kMaxLinearRows || R < 8 || R > kMaxRank || R % 8 || matrices < 1 || matrices > 2)
+        return MOE_ERR_INVALID_ARG;
+    *bytes = AdapterProducts::plan(T, R, matrices).total;
+    return MOE_OK;
+}
+
+moe_status_t moe_linear_adapters(const moe_linear_desc* d, const moe_adapter_desc* ad, const void* x, const void* w,
+                                 const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
+                                 void* out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    const moe_status_t v = validate_linear(d, x, w, w_mul, bias, bias_mul, residual, out, dev_status);
+    if (v != MOE_OK) return v;
+    if (!ad || ad->L < 1 || ad->L > kMaxAdapters || ad->R < 8 || ad->R > kMaxRank || ad->R % 8 || !ad->a != !ad->b ||
+        !ad->a_mul != !ad->b_mul || (!ad->a && !ad->a_mul) || (ad->a_mul && !w_mul))
+        return MOE_ERR_INVALID_ARG;
+    // rows and adapters that do not overlap; an adapter alone has no distance
+    const auto distances = [&](int64_t ld, int64_t n, int64_t rows, int64_t step) {
+        return valid_ld(ld, n) && ld % 8 == 0 && (ad->L == 1 || (valid_ld(step, n) && step % 8 == 0 && step >= (rows - 1) * ld + n));
+    };
+    if (!distances(ad->lda, d->K, ad->R, ad->sa) || !distances(ad->ldb, ad->R, d->N, ad->sb)) return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    if (!ad->ids || !aligned4(ad->ids) || !aligned4(ad->scale) || !aligned16(ad->a) || !aligned16(ad->b) ||
+        !aligned16(ad->a_mul) || !aligned16(ad->b_mul) || !workspace || !aligned16(workspace) || out == workspace ||
+        out == ad->a || out == ad->b || out == ad->a_mul || out == ad->b_mul)
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < AdapterProducts::plan(d->T, ad->R, ad->a && ad->a_mul ? 2 : 1).total) return MOE_ERR_WORKSPACE;
+    return launch_linear_adapters(*d, *ad, x, w, w_mul, bias, bias_mul, residual, out, workspace, dev_status,
+                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -327,6 +366,35 @@ moe_status_t moe_add_rms_norm(const moe_norm_desc* d, const void* x, const void*
         return MOE_ERR_INVALID_ARG;
     return launch_add_rms_norm(*d, x, residual, weight, sum_out, out,
                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_sandwich_norm(const moe_sandwich_desc* d, const void* x, const void* residual, const void* post_weight,
+                               const void* gate, const float* row_gate, const void* weight, void* sum_out, void* out,
+                               void* stream) {
+    if (!d || d->T < 0 || d->H < 1 || d->H > kMaxNorm || !(d->eps >= 0.f) || !std::isfinite(d->eps) ||
+        !std::isfinite(d->residual_scale) || !std::isfinite(d->weight_offset) ||
+        (d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16) || (d->wide != 0 && d->wide != 1) ||
+        (d->row_sigmoid != 0 && d->row_sigmoid != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_ld(d->ldx, d->H) || !valid_ld(d->lds, d->H) || (residual && !valid_ld(d->ldr, d->H)) ||
+        (out && !valid_ld(d->ldo, d->H)))
+        return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    const auto other_rows = [](const void* p, int64_t ldp, const void* q, int64_t ldq, bool same_type) {
+        return p && p == q && (ldp != ldq || !same_type);
+    };
+    if (other_rows(sum_out, d->lds, x, d->ldx, !d->wide) || other_rows(sum_out, d->lds, residual, d->ldr, true) ||
+        other_rows(out, d->ldo, x, d->ldx, true) || other_rows(out, d->ldo, residual, d->ldr, !d->wide) || sum_out == out)
+        return MOE_ERR_INVALID_ARG;
+    for (const void* p : {post_weight, gate, static_cast<const void*>(row_gate), weight})
+        if (p && (p == sum_out || p == out)) return MOE_ERR_INVALID_ARG;
+    const auto aligned_stream = [&](const void* p) { return d->wide ? aligned4(p) : aligned2(p); };
+    if (!x || !sum_out || !weight != !out || (d->row_sigmoid && !row_gate) || !aligned2(x) || !aligned_stream(residual) || !aligned_stream(sum_out) || !aligned2(out) ||
+        !aligned2(post_weight) || !aligned2(gate) || !aligned2(weight) || !aligned4(row_gate))
+        return MOE_ERR_INVALID_ARG;
+    return launch_sandwich_norm(*d, x, residual, post_weight, gate, row_gate, weight, sum_out, out,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
 }
 

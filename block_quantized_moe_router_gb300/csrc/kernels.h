@@ -49,6 +49,26 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
 cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const void* r, const void* w,
                                 void* sum, void* out, cudaStream_t st);
 
+// ---- low-rank adapters (adapters.cu), norms around a block (block_norm.cu) -------------------
+constexpr int kMaxRank = 256;
+constexpr int kMaxAdapters = 1 << 20;
+// The low-rank products v = scale x a^T of every row, in the workspace: [T][R] float for each matrix.
+struct AdapterProducts {
+    size_t plane, total;  // bytes of one matrix's, and of all
+    static AdapterProducts plan(int64_t T, int R, int matrices) {
+        AdapterProducts p;
+        p.plane = ((size_t)T * R * sizeof(float) + 255) / 256 * 256;
+        p.total = p.plane * matrices;
+        return p;
+    }
+};
+cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
+                                   const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
+                                   void* out, void* workspace, int32_t* status, cudaStream_t st);
+cudaError_t launch_sandwich_norm(const moe_sandwich_desc& d, const void* x, const void* residual, const void* post_weight,
+                                 const void* gate, const float* row_gate, const void* weight, void* sum_out, void* out,
+                                 cudaStream_t st);
+
 // ---- expert FFN (ffn.cu) --------------------------------------------------------------------
 // One projection as the kernels see it: packed codes, block scales, and a per-expert fp32
 // post-scale (the NVFP4 global, or 2^offset for MXFP4) plus, for MXFP4, the per-expert

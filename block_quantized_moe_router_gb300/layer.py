@@ -11,7 +11,12 @@ Optional parts around the expert FFN:
            [I], down_bias [H] if it has them}, added through moe_linear; instead of an FP4 one.
            It is added to the routed experts' sum as that was rounded to bf16, and the result is
            rounded again; an FP4 shared expert joins the sum in fp32
+  shared["adapters"]   low-rank adapters of many requests on the shared expert (moe_linear_adapters):
+           {gate_a, up_a [L][R][H], gate_b, up_b [L][I][R], down_a [L][R][I], down_b [L][H][R]}, each pair
+           or not, all of one rank, and a float scale [L]; calls name each row's adapter in adapter_ids
   norm_weight / norm_eps   the RMS norm before the layer, with the residual add (block())
+  post_norm_weight / block_gate / residual_scale / norm_offset   the norm behind the layer, its gate per
+           channel, the scale of the residual and what is added to the norms' weights (joined_block())
 """
 from __future__ import annotations
 
@@ -59,12 +64,37 @@ def _check_shared(s, H):
             raise ValueError(f"shared {key} must be a contiguous float32 CUDA tensor ({n},), got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _check_adapters(ad, s, H):
+    """The rules of moe_linear_adapters for the shared expert's adapters, before any kernel runs."""
+    I = s["gate"].shape[0]
+    sizes = None
+    for key, rows, cols in (("gate", I, H), ("up", I, H), ("down", H, I)):
+        a, b = ad.get(key + "_a"), ad.get(key + "_b")
+        if (a is None) != (b is None):
+            raise ValueError(f"adapters of {key} need {key}_a and {key}_b")
+        if a is None:
+            continue
+        if sizes is None:
+            sizes = tuple(a.shape[:2])
+            if len(sizes) < 2 or sizes[0] < 1 or sizes[1] % 8 or not 8 <= sizes[1] <= 256:
+                raise ValueError(f"adapters need ranks that are multiples of 8 up to 256, got {key}_a {tuple(a.shape)}")
+        for name, t, shape in ((key + "_a", a, sizes + (cols,)), (key + "_b", b, (sizes[0], rows, sizes[1]))):
+            if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor {shape}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if sizes is None:
+        raise ValueError("adapters hold none of gate, up and down")
+    scale = ad.get("scale")
+    if scale is not None and (scale.dtype != torch.float32 or tuple(scale.shape) != sizes[:1] or not scale.is_cuda or not scale.is_contiguous()):
+        raise ValueError(f"adapters' scale must be a contiguous float32 CUDA tensor {sizes[:1]}, got {scale.dtype} {tuple(scale.shape)} on {scale.device}")
+
+
 class MoeLayer:
     def __init__(self, *, E, H, I, top_k, scoring, gate, up, down, I_shared=0, sh_gate=None,
                  sh_up=None, sh_down=None, w_router=None, correction_bias=None, tid2eid=None,
                  renormalize=True, routed_scaling=1.0, act=capi.MOE_ACT_BF16, g_act1=1.0,
                  g_act2=1.0, zero_experts=0, n_group=0, topk_group=0, group_top=2, shared=None,
-                 norm_weight=None, norm_eps=1e-6):
+                 norm_weight=None, norm_eps=1e-6, post_norm_weight=None, block_gate=None,
+                 residual_scale=1.0, norm_offset=0.0):
         self.E, self.H, self.I, self.top_k, self.I_shared = E, H, I, top_k, I_shared
         self.zero_experts = zero_experts
         self.scoring, self.renormalize, self.routed_scaling = scoring, renormalize, routed_scaling
@@ -76,16 +106,24 @@ class MoeLayer:
             if I_shared:
                 raise ValueError("a layer has one shared expert: FP4 (I_shared) or bf16 (shared)")
             _check_shared(shared, H)
-        if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or tuple(norm_weight.shape) != (H,)):
-            raise ValueError(f"norm_weight must be a bfloat16 tensor ({H},), got {norm_weight.dtype} {tuple(norm_weight.shape)}")
+            if shared.get("adapters") is not None:
+                _check_adapters(shared["adapters"], shared, H)
+        for name, w in (("norm_weight", norm_weight), ("post_norm_weight", post_norm_weight), ("block_gate", block_gate)):
+            if w is not None and (w.dtype != torch.bfloat16 or tuple(w.shape) != (H,)):
+                raise ValueError(f"{name} must be a bfloat16 tensor ({H},), got {w.dtype} {tuple(w.shape)}")
+        if norm_weight is not None and norm_offset:
+            raise ValueError("norm_offset belongs to joined_block, whose caller norms the first rows; a layer with norm_weight has none")
         self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
         self.shared, self.norm_weight, self.norm_eps = shared, norm_weight, norm_eps
+        self.post_norm_weight, self.block_gate = post_norm_weight, block_gate
+        self.residual_scale, self.norm_offset = residual_scale, norm_offset
         self._weights = (gate, up, down, sh_gate, sh_up, sh_down)  # keep alive
         self.desc = capi.ffn_desc(E, H, I, top_k, I_shared, gate, up, down, sh_gate, sh_up, sh_down,
                                   zero_experts)
         self.handle = capi.moe_prepare_weights(self.desc)
         self._ws = None
         self._ws_host = None
+        self._ws_adapters = None
         self._outgrown = []
         self._host_route = {}
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -166,30 +204,53 @@ class MoeLayer:
                        dev_status=self.status, stream=stream, zero_experts=self.zero_experts)
         return topk_ids, topk_w, logits_out
 
-    def ffn(self, x, topk_ids, topk_w, out=None, stream=None):
+    def ffn(self, x, topk_ids, topk_w, out=None, stream=None, adapter_ids=None):
+        self._adapters(adapter_ids)
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
         capi.moe_ffn_forward(self.handle, T, self.act, self.g_act1, self.g_act2, x, topk_ids,
                              topk_w, out, self.workspace(T), dev_status=self.status, stream=stream)
-        self._add_shared(x, out, stream)
+        self._add_shared(x, out, stream, adapter_ids)
         return out
 
-    def _add_shared(self, x, out, stream):
+    def _add_shared(self, x, out, stream, adapter_ids=None):
         """out += down(SiLU(gate x) * up x) of the bf16 shared expert, if the layer has one."""
+        ad = self._adapters(adapter_ids)
         if self.shared is None:
             return
         s = self.shared
         T, I = x.shape[0], s["gate"].shape[0]
         with torch.cuda.stream(stream):  # h is freed before it is used up: only that stream may have it next
             h = torch.empty((T, I), dtype=torch.bfloat16, device="cuda")
-        capi.moe_linear(x, s["gate"], h, w_mul=s["up"], bias=s.get("gate_bias"),
-                        bias_mul=s.get("up_bias"), func=capi.MOE_FUNC_SILU, dev_status=self.status,
-                        stream=stream)
-        capi.moe_linear(h, s["down"], out, bias=s.get("down_bias"), residual=out,
-                        dev_status=self.status, stream=stream)
+        self._linear(ad, "gate", "up", adapter_ids, x, s["gate"], h, w_mul=s["up"], bias=s.get("gate_bias"),
+                     bias_mul=s.get("up_bias"), func=capi.MOE_FUNC_SILU, stream=stream)
+        self._linear(ad, "down", None, adapter_ids, h, s["down"], out, bias=s.get("down_bias"), residual=out,
+                     stream=stream)
 
-    def block(self, delta, residual=None, *, token_ids=None, logits_in=None, stream=None):
+    def _adapters(self, adapter_ids):
+        """The shared expert's adapters for a call that names them, None for one that does not."""
+        if adapter_ids is None:
+            return None
+        ad = None if self.shared is None else self.shared.get("adapters")
+        if ad is None:
+            raise ValueError("the layer was built without adapters")
+        return ad
+
+    def _linear(self, ad, key, mul, ids, x, w, out, **kw):
+        """moe_linear of the shared expert, with the adapters of `key` (and `mul`) where there are some."""
+        pairs = {} if ad is None else {"a": ad.get(key + "_a"), "b": ad.get(key + "_b")}
+        if ad is not None and mul is not None:
+            pairs.update(a_mul=ad.get(mul + "_a"), b_mul=ad.get(mul + "_b"))
+        given = [t for t in (pairs.get("a"), pairs.get("a_mul")) if t is not None]
+        if not given:
+            return capi.moe_linear(x, w, out, dev_status=self.status, **kw)
+        self._ws_adapters = self._grown(self._ws_adapters,
+                                        capi.moe_adapter_workspace_size(x.shape[0], given[0].shape[1], len(given)))
+        capi.moe_linear_adapters(x, w, out, ids, scale=ad.get("scale"), workspace=self._ws_adapters,
+                                 dev_status=self.status, **pairs, **kw)
+
+    def block(self, delta, residual=None, *, token_ids=None, logits_in=None, adapter_ids=None, stream=None):
         """The layer with the residual add and norm before it: r = delta + residual, n = RMS norm of
         r, and (FFN of n, r), the next layer's delta and residual.  Without a residual r = delta.
         token_ids: of the rows, for hash routing.  The results belong to `stream` (the current one
@@ -198,17 +259,37 @@ class MoeLayer:
             raise ValueError("the layer was built without norm_weight")
         if stream is not None:  # what is freed on return goes back to the stream that still uses it
             with torch.cuda.stream(stream):
-                return self.block(delta, residual, token_ids=token_ids, logits_in=logits_in)
+                return self.block(delta, residual, token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)
         n = torch.empty_like(delta)
         r = torch.empty_like(delta)
         capi.moe_add_rms_norm(delta, self.norm_weight, n, residual=residual, sum_out=r,
                               eps=self.norm_eps)
-        return self.forward(n, token_ids=token_ids, logits_in=logits_in)[0], r
+        return self.forward(n, token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)[0], r
+
+    def joined_block(self, n, residual, next_weight=None, *, row_gate=None, row_sigmoid=False, token_ids=None,
+                     logits_in=None, adapter_ids=None, stream=None):
+        """The layer on rows n that are normed already, and what stands between it and the next block in one pass
+        (moe_sandwich_norm): the norm behind it (post_norm_weight), its gates, the residual add and, with next_weight,
+        the norm before the next block.  residual is bf16 or float32 and stays so.  Returns (the next block's n or
+        None, its residual).  The results belong to `stream` (the current one by default)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.joined_block(n, residual, next_weight, row_gate=row_gate, row_sigmoid=row_sigmoid,
+                                         token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)
+        y = self.forward(n, token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)[0]
+        s = torch.empty(residual.shape, dtype=residual.dtype, device=residual.device)
+        out = None if next_weight is None else y
+        capi.moe_sandwich_norm(y, s, residual=residual, post_weight=self.post_norm_weight, gate=self.block_gate,
+                               row_gate=row_gate, row_sigmoid=row_sigmoid, weight=next_weight, out=out,
+                               residual_scale=self.residual_scale, weight_offset=self.norm_offset, eps=self.norm_eps)
+        return out, s
 
     def forward(self, x=None, *, token_ids=None, logits_in=None, out=None, topk_ids=None,
-                topk_w=None, logits_out=None, stream=None):
+                topk_w=None, logits_out=None, adapter_ids=None, stream=None):
         """Route + FFN through moe_forward (one launch for a few tokens; with expert groups the
-        routing runs first on its own).  Returns (out, topk_ids, topk_w, logits_out)."""
+        routing runs first on its own).  adapter_ids: int32, each row's adapter of the shared expert, -1
+        for none.  Returns (out, topk_ids, topk_w, logits_out)."""
+        self._adapters(adapter_ids)
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
@@ -216,7 +297,7 @@ class MoeLayer:
             topk_ids, topk_w, logits_out = self.route(
                 x, logits_in=logits_in, topk_ids=topk_ids, topk_w=topk_w, logits_out=logits_out,
                 stream=stream)
-            return self.ffn(x, topk_ids, topk_w, out=out, stream=stream), topk_ids, topk_w, logits_out
+            return self.ffn(x, topk_ids, topk_w, out=out, stream=stream, adapter_ids=adapter_ids), topk_ids, topk_w, logits_out
         if topk_ids is None:
             topk_ids = torch.empty((T, self.top_k), dtype=torch.int32, device="cuda")
         if topk_w is None:
@@ -233,7 +314,7 @@ class MoeLayer:
         capi.moe_forward(self.handle, d, self.act, self.g_act1, self.g_act2, x, topk_ids, topk_w,
                          out, self.workspace(T), logits_in=logits_in, logits_out=logits_out,
                          dev_status=self.status, stream=stream)
-        self._add_shared(x, out, stream)
+        self._add_shared(x, out, stream, adapter_ids)
         return out, topk_ids, topk_w, logits_out
 
     def forward_host(self, x_host, out_host, *, token_ids_host=None, topk_ids_host=None,

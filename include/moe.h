@@ -54,6 +54,7 @@ typedef enum {
 #define MOE_DEV_BAD_TOKEN_ID 0x2  /* a token id outside [0,vocab): the token's pairs dropped */
 #define MOE_DEV_NONFINITE 0x4     /* a NaN/Inf router logit: ranked below every finite one   */
 #define MOE_DEV_TIMEOUT 0x8       /* a bounded device-side wait gave up                      */
+#define MOE_DEV_BAD_ADAPTER_ID 0x10 /* an adapter id that is neither -1 nor in [0,L): the row has none */
 
 typedef enum {
     MOE_SCORE_SOFTMAX = 0,
@@ -142,6 +143,33 @@ typedef struct {
     float eps;
     int64_t ldx, ldr, lds, ldo;
 } moe_norm_desc;
+
+/* Low-rank adapters of a dense layer (moe_linear_adapters): a [L][R][K] and b [L][N][R] of the layer's
+ * type for w, a_mul and b_mul of the same shapes and distances for w_mul.  lda and ldb are the distances
+ * between rows in elements, sa and sb those between adapters (not used with one).  Constraints (checked):
+ * 1 <= L <= 2^20; R a multiple of 8, 8 <= R <= 256; lda >= K, ldb >= R, sa and sb so large that adapters do
+ * not overlap, all multiples of 8 below 2^38; a, b, a_mul and b_mul 16-byte aligned; a with b, a_mul with
+ * b_mul, and one of the pairs at least. */
+typedef struct {
+    int32_t L, R;
+    int64_t lda, sa, ldb, sb;
+    const void *a, *b;         /* [device] adapters of w, or both NULL                     */
+    const void *a_mul, *b_mul; /* [device] adapters of w_mul, or both NULL                 */
+    const float* scale;        /* [device] float [L] or NULL (every scale 1)               */
+    const int32_t* ids;        /* [device] int32 [T]: each row's adapter, -1 for none      */
+} moe_adapter_desc;
+
+/* Rows of moe_sandwich_norm: x and out are [T][H] of type dtype, residual and sum [T][H] of the same or
+ * of float (wide).  Constraints (checked): T >= 0; 1 <= H <= 16384; every ld in use >= H and below 2^38;
+ * eps >= 0; eps, residual_scale and weight_offset finite. */
+typedef struct {
+    int32_t T, H;
+    int32_t dtype;             /* moe_dtype_t                                              */
+    int32_t wide;              /* 1: residual and sum are float                            */
+    int32_t row_sigmoid;       /* 1: row_gate holds logits                                 */
+    float eps, residual_scale, weight_offset;
+    int64_t ldx, ldr, lds, ldo;
+} moe_sandwich_desc;
 
 /* Router GEMM + top-K (every rule below runs over the E + zero_experts router outputs).
  *   Softmax: p = softmax(logits) over all E; the top_k largest are selected; weight =
@@ -236,6 +264,51 @@ moe_status_t moe_linear(const moe_linear_desc* desc, const void* x, const void* 
  * another row distance; MOE_ERR_CUDA. */
 moe_status_t moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const void* residual,
                               const void* weight, void* sum_out, void* out, void* stream);
+
+/* moe_linear with low-rank adapters of many requests at once (moe/mod.rs, the `MoeLoraWeights` and
+ * `lora_gateup` fields, which the pages' layer applies to one request's prompt at a time):
+ *   z[t] = x[t] w^T + bias + scale[j] (x[t] a[j]^T) b[j]^T,  j = ids[t], nothing added for j = -1;
+ *   u[t] the same of w_mul, bias_mul, a_mul and b_mul;  out = f(z) [* u] [+ residual].
+ * x a^T is summed in fp32 and multiplied by the scale; it enters the second product as two numbers of the
+ * layer's type whose sum holds 16 bits of it (bf16; f16: 22, as long as it stays within f16's range, where a
+ * magnitude beyond 65504 is infinite).  All else as in moe_linear.  A row depends on its own adapter alone:
+ * a NaN or an infinity in one adapter stays in the rows that have it.  Rows of one adapter need not be
+ * neighbours; what is read of the adapters are those that occur in ids.  An id outside [-1, L) sets
+ * MOE_DEV_BAD_ADAPTER_ID, and its row has no adapter.
+ * workspace [device] 16-byte aligned, ws_bytes >= moe_adapter_workspace_size(T, R, matrices), matrices 2
+ * where both pairs are given and else 1.  It holds nothing between calls; calls that overlap on the GPU
+ * need one each.
+ * Other arguments, errors and T == 0 as for moe_linear, and MOE_ERR_INVALID_ARG for the checks of
+ * moe_adapter_desc, NULL ids, a_mul without w_mul, or out equal to a pointer of the adapters or the
+ * workspace; MOE_ERR_WORKSPACE for too small a workspace. */
+moe_status_t moe_linear_adapters(const moe_linear_desc* desc, const moe_adapter_desc* adapters, const void* x,
+                                 const void* w, const void* w_mul, const float* bias, const float* bias_mul,
+                                 const void* residual, void* out, void* workspace, size_t ws_bytes,
+                                 int32_t* dev_status, void* stream);
+/* Bytes of its workspace: the low-rank products of T rows (no counterpart on the pages, whose layer
+ * allocates its own).  Host-only.  Errors: MOE_ERR_INVALID_ARG for a NULL `bytes`, T < 0 or above
+ * 2^30, an R out of its range, or matrices other than 1 and 2. */
+moe_status_t moe_adapter_workspace_size(int32_t T, int32_t R, int32_t matrices, size_t* bytes);
+
+/* The norm behind a block, its gate and residual scale, the residual add and the norm before the next
+ * block, in one pass (moe/mod.rs, the `pre_expert_norm` field and the norm handles of moe/init.rs, whose
+ * kernels run one by one):
+ *   p = x / sqrt(mean(x^2) + eps) * (post_weight + weight_offset), or x without post_weight;
+ *   s = residual_scale * residual + row_gate * gate * p   (without a residual, or a gate: not that factor);
+ *   out = s / sqrt(mean(s^2) + eps) * (weight + weight_offset).
+ * Computed in fp32; s and out are each rounded once, out from the unrounded s.  The squares are added in
+ * fp32: a row whose sum of squares exceeds 3.4e38 counts as zeros in the norm's output.
+ * x [device]; residual [device] or NULL; post_weight, gate and weight [device] [H] of type dtype, each or
+ * NULL; row_gate [device] float [T] or NULL, with row_sigmoid the logits of the gate; sum_out [device]:
+ * s; out [device], with weight (both or neither).
+ * sum_out and out may each be x or residual itself where type and rows are the same, but not one another.
+ * T == 0 is a valid no-op.  Errors: MOE_ERR_INVALID_ARG for the checks of moe_sandwich_desc, a NULL x or
+ * sum_out, weight without out or out without weight, row_sigmoid without row_gate, a misaligned pointer,
+ * sum_out equal to out, either equal to a weight or gate, or equal to x or residual with another row
+ * distance or type; MOE_ERR_CUDA. */
+moe_status_t moe_sandwich_norm(const moe_sandwich_desc* desc, const void* x, const void* residual,
+                               const void* post_weight, const void* gate, const float* row_gate,
+                               const void* weight, void* sum_out, void* out, void* stream);
 
 /* Bytes of device workspace moe_ffn_forward needs for T tokens in activation mode act.
  * Source: the spark_model MoE pages, moe/mod.rs, `zero_accum_dev` field doc (the layer's
