@@ -1,86 +1,224 @@
-// adapters.cu -- a dense layer with low-rank adapters of many requests:
-// out = f(x W^T + b + v_w B_w^T) [* (x V^T + c + v_v B_v^T)] [+ r], v = scale x A^T, each row with its own adapter.
+// adapters.cu -- the low-rank products of moe_linear_adapters: v[t] = scale[j] x[t] a[j]^T, j = ids[t].
 //
-// Two launches: the low-rank products of every row (a warp each), and the layer, a thread per output.
+// Rows are taken in groups of 256.  In a group the rows of one adapter form batches of up to 32 in their order,
+// and an item is a batch and 32 of the stacked ranks (both matrices' in the gated form): D = A x^T by mma.sync,
+// ranks on the M side, rows of x on the N side (8 where the batch has no more, or 32).  Each byte of a that a batch needs
+// is read once for all of its rows, in 16-byte loads straight into the fragments: the sum may take K in any
+// order, so a lane's four 16-bit pairs of one 16-byte load serve as the operands of two MMAs, the same way on both sides.
+// K is split over the warps of a CTA and the CTAs of a cluster; the parts meet in shared memory and are added in
+// order.  A batch of one token costs its adapter's bytes, a prompt's its rows of x, read here before the layer
+// reads them again from L2: neither has work for tcgen05 (16 to 64 ranks of 128 lanes).
+//
+// Which adapters occur is known on the device alone: every CTA of a group finds the batches by itself (a comparison
+// with the ids before it per row), so that no launch has to sort them.
+#include "cluster.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 #include "rows.cuh"
 
 namespace moe {
 
 namespace {
 
-struct AdapterArgs {
-    int T, N, K, R, L, func;
-    int64_t ldx, ldw, ldr, ldo, lda, sa, ldb, sb;
-    const void *x, *w[2], *a[2], *b[2], *res;
-    const float *bias[2], *scale;
+constexpr int kGroup = 256;      // rows of a group, and threads
+constexpr int kBatch = 32;       // rows of a batch
+constexpr int kRanks = 32;       // ranks of an item
+constexpr int kLowSplits = 8;    // CTAs of a cluster at most
+constexpr int kLandingMax = 24 * 1024;  // bytes: with the static shared memory below the 48 KB that need no permission
+
+struct LowRankArgs {
+    int T, K, R, L, f16, matrices, slots, landing_rows;  // landing_rows: of a batch at most
+    int64_t ldx, lda, sa, plane;  // plane: elements of a plane of v
+    const uint16_t *x, *a[2];
+    const float* scale;
     const int32_t* ids;
-    float* v[2];  // [T][R]
-    void* out;
+    uint16_t* v;
     int32_t* status;
 };
 
-__device__ __forceinline__ int adapter_of(const AdapterArgs& g, int64_t t) {
-    const int j = __ldg(g.ids + t);
-    return j >= 0 && j < g.L ? j : -1;
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (F16) mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
+    else mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
-// grid (rows, matrices): a warp per low-rank product.
-template <typename E>
-__global__ void low_rank_kernel(AdapterArgs g) {
-    pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int m = g.a[0] ? (int)blockIdx.y : 1, j = adapter_of(g, t);
-    if (j < 0) {
-        if (threadIdx.x == 0 && __ldg(g.ids + t) != -1) status_or(g.status, MOE_DEV_BAD_ADAPTER_ID);
-        return;
-    }
-    const E* x = static_cast<const E*>(g.x) + t * g.ldx;
-    for (int r = threadIdx.x / 32; r < g.R; r += blockDim.x / 32) {
-        const E* a = static_cast<const E*>(g.a[m]) + j * g.sa + r * g.lda;
-        float s = 0.f;
-        for (int k = threadIdx.x % 32; k < g.K; k += 32) s += to_f32(x[k]) * to_f32(a[k]);
+// This warp's part of an item's sums, over the steps of 32 elements of K from `step` on, `stride` apart: NB blocks of 8
+// rows.  rows: where this lane's ranks of a begin (nullptr: none), their ranks being g, g + 8, g + 16 and g + 24.
+template <bool F16, int NB, int UNROLL>
+__device__ __forceinline__ void low_rank_sums(float (&d)[2][4][4], const uint16_t* const (&rank)[4],
+                                              const uint16_t* const (&row)[4], int step, int stride, int end, int K) {
+    const int c8 = 8 * (threadIdx.x & 3);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (; step < end; step += UNROLL * stride) {
+        uint4 w[UNROLL][4], x[UNROLL][NB];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (threadIdx.x % 32 == 0) g.v[m][t * g.R + r] = s * (g.scale ? __ldg(g.scale + j) : 1.f);
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = 32 * (step + u * stride) + c8;
+            const bool in = step + u * stride < end && k < K;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[u][i] = in && rank[i] ? ldg_stream128(rank[i] + k) : zero;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) x[u][i] = in && row[i] ? ldg_cached128(row[i] + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const uint4 p = w[u][2 * m], q = w[u][2 * m + 1];
+                    mma16<F16>(d[m][i], p.x, q.x, p.y, q.y, x[u][i].x, x[u][i].y);
+                    mma16<F16>(d[m][i], p.z, q.z, p.w, q.w, x[u][i].z, x[u][i].w);
+                }
     }
 }
 
-template <typename E>
-__global__ void layer_kernel(AdapterArgs g) {
+// grid (slots * CTAs of a cluster, groups): slot s takes the group's items s, s + slots, ...
+template <bool F16>
+__global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
+    __shared__ __align__(16) int id_s[kGroup];
+    __shared__ int batch_row[kBatch], leaders[kGroup / 32], item_id, item_first;
+    __shared__ __align__(16) float part[4][kBatch][kRanks + 4];     // sums of a warp: [row][rank]
+    extern __shared__ __align__(16) float landing[];                // [CTA][row][rank]
     pdl_wait();
-    const int64_t t = (int64_t)blockIdx.y * 16 + threadIdx.y;
-    const int n = blockIdx.x * 16 + threadIdx.x;
-    if (t >= g.T || n >= g.N) return;
-    const int j = adapter_of(g, t);
-    const E* x = static_cast<const E*>(g.x) + t * g.ldx;
-    float z[2] = {0.f, 0.f};
-    for (int m = 0; m < 2; ++m) {
-        if (!g.w[m]) continue;
-        const E* w = static_cast<const E*>(g.w[m]) + n * g.ldw;
-        for (int k = 0; k < g.K; ++k) z[m] += to_f32(x[k]) * to_f32(w[k]);
-        if (g.bias[m]) z[m] += g.bias[m][n];
-        if (j < 0 || !g.b[m]) continue;
-        const E* b = static_cast<const E*>(g.b[m]) + j * g.sb + n * g.ldb;
-        for (int r = 0; r < g.R; ++r) z[m] += g.v[m][t * g.R + r] * to_f32(b[r]);
+    pdl_trigger();  // the layer's launch may start: whatever came before this one is done
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = (int)cluster_size(), cta = (int)cluster_rank(), slot = (int)blockIdx.x / ctas;
+    if (ctas > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+    const int64_t t0 = (int64_t)blockIdx.y * kGroup;
+    int id = t0 + tid < g.T ? __ldg(g.ids + t0 + tid) : -1;
+    if (id < -1 || id >= g.L) {
+        if (blockIdx.x == 0) status_or(g.status, MOE_DEV_BAD_ADAPTER_ID);
+        id = -1;
     }
-    float y = z[0];
-    switch (g.func) {
-        case MOE_FUNC_SILU: y = y / (1.f + __expf(-y)); break;
-        case MOE_FUNC_GELU: y = 0.5f * y * (1.f + erff(y * 0.70710678f)); break;
-        case MOE_FUNC_GELU_TANH: y = y / (1.f + __expf(-1.5957691f * (y + 0.044715f * y * y * y))); break;
-        case MOE_FUNC_RELU: y = y < 0.f ? 0.f : y; break;
+    id_s[tid] = id;
+    __syncthreads();
+    int before = 0;  // rows of this adapter before this one
+    if (id >= 0) {
+        for (int i = 0; i < (tid & ~3); i += 4) {
+            const int4 p = *reinterpret_cast<const int4*>(id_s + i);
+            before += (p.x == id) + (p.y == id) + (p.z == id) + (p.w == id);
+        }
+        for (int i = tid & ~3; i < tid; ++i) before += id_s[i] == id;
     }
-    if (g.w[1]) y *= z[1];
-    if (g.res) y += to_f32(static_cast<const E*>(g.res)[t * g.ldr + n]);
-    from_f32(y, static_cast<E*>(g.out)[t * g.ldo + n]);
+    const bool leads = id >= 0 && before % kBatch == 0;
+    const unsigned lead_mask = __ballot_sync(0xffffffffu, leads);
+    if (lane == 0) leaders[warp] = __popc(lead_mask);
+    __syncthreads();
+    int batches = 0, batch = __popc(lead_mask & ((1u << lane) - 1u));  // of the group; the one this row leads
+#pragma unroll
+    for (int w = 0; w < kGroup / 32; ++w) {
+        if (w < warp) batch += leaders[w];
+        batches += leaders[w];
+    }
+    const int per_matrix = (g.R + 15) / 16, passes = (per_matrix * g.matrices + 1) / 2;  // blocks of 16 ranks, items of a batch
+    const int steps = (g.K + 31) / 32;
+    const int begin = (int)((int64_t)steps * cta / ctas), end = (int)((int64_t)steps * (cta + 1) / ctas);
+    if (ctas > 1) cluster_wait();
+    for (int item = slot; item < batches * passes; item += g.slots) {
+        const int pass = item % passes;
+        if (leads && batch == item / passes) {
+            item_id = id;
+            item_first = before;
+        }
+        __syncthreads();
+        const int j = item_id, first = item_first;
+        const bool here = id == j && before >= first && before < first + kBatch;
+        if (here) batch_row[before - first] = tid;
+        const int rows = __syncthreads_count(here);
+        const uint16_t *rank[4], *row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int block = 2 * pass + (i >> 1), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + 8 * (i & 1) + (lane >> 2);
+            rank[i] = block < per_matrix * g.matrices && r < g.R ? g.a[m] + j * g.sa + r * g.lda : nullptr;
+            row[i] = 8 * i + (lane >> 2) < rows ? g.x + (t0 + batch_row[8 * i + (lane >> 2)]) * g.ldx : nullptr;
+        }
+        float d[2][4][4] = {};
+        if (rows <= 8) low_rank_sums<F16, 1, 4>(d, rank, row, begin + warp, kGroup / 32, end, g.K);
+        else low_rank_sums<F16, 4, 2>(d, rank, row, begin + warp, kGroup / 32, end, g.K);
+        const int blocks = rows <= 8 ? 1 : 4;
+        // warps 4 to 7 hand theirs to warps 0 to 3, these add them to their own, and those four are added
+        const auto place = [&](int m, int b, int e) -> float& {
+            return part[warp & 3][8 * b + 2 * (lane & 3) + (e & 1)][16 * m + (lane >> 2) + 8 * (e >> 1)];
+        };
+        const auto each = [&](auto&& f) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (b < blocks) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f(d[m][b][e], place(m, b, e));
+                    }
+        };
+        if (warp >= 4) each([](float v, float& at) { at = v; });
+        __syncthreads();
+        if (warp < 4) each([](float v, float& at) { at = v + at; });
+        __syncthreads();
+        // a thread: one row of the batch (of 32), four ranks
+        const int at_row = tid >> 3, at_rank = 4 * (tid & 7);
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at_row < rows)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 p = *reinterpret_cast<const float4*>(&part[w][at_row][at_rank]);
+                z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
+            }
+        if (ctas > 1) {
+            const uint32_t there = tc::smem_u32(landing + (cta * g.landing_rows + at_row) * kRanks + at_rank);
+            if (at_row < rows)
+                st_cluster_v4(map_rank(there, 0), __float_as_uint(z.x), __float_as_uint(z.y), __float_as_uint(z.z), __float_as_uint(z.w));
+            cluster_sync();
+            if (cta == 0 && at_row < rows) {
+                z = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = 0; c < ctas; ++c) {
+                    const float4 p = *reinterpret_cast<const float4*>(landing + (c * g.landing_rows + at_row) * kRanks + at_rank);
+                    z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
+                }
+            }
+        }
+        const int block = 2 * pass + (at_rank >> 4), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + (at_rank & 15);
+        if (cta == 0 && at_row < rows && block < per_matrix * g.matrices && r < g.R) {  // R is a multiple of 8: all four or none
+            const float s = g.scale ? __ldg(g.scale + j) : 1.f;
+            const float v[4] = {z.x * s, z.y * s, z.z * s, z.w * s};
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // an infinite hi has no rest
+                if constexpr (F16) {
+                    const __half h = __float2half_rn(v[i]);
+                    hi[i] = __half_as_ushort(h);
+                    lo[i] = (hi[i] & 0x7C00u) == 0x7C00u ? 0 : __half_as_ushort(__float2half_rn(v[i] - __half2float(h)));
+                } else {
+                    const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+                    hi[i] = __bfloat16_as_ushort(h);
+                    lo[i] = (hi[i] & 0x7F80u) == 0x7F80u ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(v[i] - __bfloat162float(h)));
+                }
+            }
+            uint16_t* to = g.v + 2 * m * g.plane + (t0 + batch_row[at_row]) * g.R + r;
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+            *reinterpret_cast<uint2*>(to + g.plane) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+        }
+        if (ctas > 1) cluster_sync();  // the landing area is free
+        __syncthreads();               // and the batch's rows
+    }
 }
 
-template <typename E>
-cudaError_t launch(const AdapterArgs& g, cudaStream_t st) {
-    const cudaError_t err = launch_pdl(low_rank_kernel<E>, dim3(g.T, g.a[0] && g.a[1] ? 2 : 1), dim3(256), st, g);
-    if (err != cudaSuccess) return err;
-    return launch_pdl(layer_kernel<E>, dim3((g.N + 15) / 16, (g.T + 15) / 16), dim3(16, 16), st, g);
+template <bool F16>
+cudaError_t launch_low_rank(const LowRankArgs& g, int groups, int splits, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.slots * splits), (unsigned)groups);
+    cfg.blockDim = dim3(kGroup);
+    cfg.dynamicSmemBytes = splits > 1 ? splits * g.landing_rows * kRanks * sizeof(float) : 0;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, low_rank_kernel<F16>, g);
 }
 
 }  // namespace
@@ -89,12 +227,39 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
                                    const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                    void* out, void* workspace, int32_t* status, cudaStream_t st) {
     const AdapterProducts p = AdapterProducts::plan(d.T, ad.R, ad.a && ad.a_mul ? 2 : 1);
-    float* v0 = static_cast<float*>(workspace);
-    float* v1 = ad.a ? v0 + p.plane / sizeof(float) : v0;
-    const AdapterArgs g{d.T, d.N, d.K, ad.R, ad.L, d.func, d.ldx, d.ldw, d.ldr, d.ldo, ad.lda, ad.sa, ad.ldb, ad.sb,
-                        x, {w, w_mul}, {ad.a, ad.a_mul}, {ad.b, ad.b_mul}, residual, {bias, bias_mul}, ad.scale, ad.ids,
-                        {v0, v1}, out, status};
-    return d.dtype == MOE_DT_F16 ? launch<__half>(g, st) : launch<__nv_bfloat16>(g, st);
+    LowRankArgs g{};
+    g.T = d.T; g.K = d.K; g.R = ad.R; g.L = ad.L; g.f16 = d.dtype == MOE_DT_F16; g.matrices = p.matrices;
+    g.ldx = d.ldx; g.lda = ad.lda; g.sa = ad.sa; g.plane = (int64_t)(p.plane / 2);
+    g.x = static_cast<const uint16_t*>(x);
+    g.a[0] = static_cast<const uint16_t*>(ad.a ? ad.a : ad.a_mul);
+    g.a[1] = static_cast<const uint16_t*>(ad.a_mul);
+    g.scale = ad.scale; g.ids = ad.ids;
+    g.v = static_cast<uint16_t*>(workspace);
+    g.status = status;
+    // Slots for all the items that a group can have, a cluster of CTAs for each as long as the SMs have room for
+    // them and every warp a step of K.
+    const int rows = d.T < kGroup ? d.T : kGroup;
+    const int batches = (ad.L < rows ? ad.L : rows) + rows / kBatch, passes = ((ad.R + 15) / 16 * p.matrices + 1) / 2;
+    const int groups = (d.T + kGroup - 1) / kGroup, steps = (d.K + 31) / 32;
+    int slots = (batches < rows ? batches : rows) * passes;
+    if (slots > 32 && (int64_t)slots * groups > 1024) slots = 1024 / groups > 32 ? 1024 / groups : 32;
+    g.landing_rows = d.T < kBatch ? d.T : kBatch;
+    int splits = 1;
+    while (splits < kLowSplits && 2 * splits * g.landing_rows * kRanks * (int)sizeof(float) <= kLandingMax && 2 * splits * (kGroup / 32) <= steps && (int64_t)slots * groups * splits * 2 <= 512) splits *= 2;
+    g.slots = slots;
+    // groups are the grid's second dimension: at most 65535 a launch
+    for (int first = 0; first < groups; first += 65535) {
+        const int n = groups - first < 65535 ? groups - first : 65535;
+        LowRankArgs h = g;
+        const int64_t t = (int64_t)first * kGroup;
+        h.x += t * g.ldx;
+        h.ids += t;
+        h.v += t * g.R;
+        h.T = (int)(g.T - t);
+        const cudaError_t err = g.f16 ? launch_low_rank<true>(h, n, splits, st) : launch_low_rank<false>(h, n, splits, st);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_adapted_linear(d, ad, x, w, w_mul, bias, bias_mul, residual, out, workspace, status, st);
 }
 
 }  // namespace moe

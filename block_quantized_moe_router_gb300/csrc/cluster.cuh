@@ -125,10 +125,11 @@ struct RingPos {
     }
 };
 
-// Tensor map of [rows][cols] 16-bit elements, rows ld apart: boxes of box_cols columns (64 or 32: 128
-// or 64 bytes, swizzled over as many) x box_rows rows; what lies beyond reads as zero.
-inline bool encode_rows16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
-                          int box_cols) {
+// Tensor map of 16-bit elements in two dimensions or three (strides of the outer ones in elements): boxes of
+// box_cols columns (64 or 32: 128 or 64 bytes, swizzled over as many) x box_rows rows of one matrix; what lies
+// beyond reads as zero.
+inline bool encode_boxes16(CUtensorMap* m, const void* base, int rank, const int64_t (&size)[3], int64_t ld, int64_t step,
+                           int box_rows, int box_cols) {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
         void* ptr = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -138,14 +139,24 @@ inline bool encode_rows16(CUtensorMap* m, const void* base, int64_t cols, int64_
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
     }();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint64_t dims[3] = {(cuuint64_t)size[0], (cuuint64_t)size[1], (cuuint64_t)size[2]};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)step * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
               box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [rows][cols], rows ld apart.
+inline bool encode_rows16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
+                          int box_cols) {
+    return encode_boxes16(m, base, 2, {cols, rows, 1}, ld, 0, box_rows, box_cols);
+}
+// [count][rows][cols], rows ld and matrices step apart: boxes of 64 columns.
+inline bool encode_stack16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                           int64_t step, int box_rows) {
+    return encode_boxes16(m, base, 3, {cols, rows, count}, ld, step, box_rows, 64);
 }
 
 }  // namespace moe

@@ -52,16 +52,24 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const voi
 // ---- low-rank adapters (adapters.cu), norms around a block (block_norm.cu) -------------------
 constexpr int kMaxRank = 256;
 constexpr int kMaxAdapters = 1 << 20;
-// The low-rank products v = scale x a^T of every row, in the workspace: [T][R] float for each matrix.
+// The low-rank products v = scale x a^T of every row, in the workspace: for each matrix two planes [T][R] of the
+// layer's type, whose sum is v.
 struct AdapterProducts {
-    size_t plane, total;  // bytes of one matrix's, and of all
+    int matrices;
+    size_t plane, total;  // bytes of a plane, and of all
     static AdapterProducts plan(int64_t T, int R, int matrices) {
         AdapterProducts p;
-        p.plane = ((size_t)T * R * sizeof(float) + 255) / 256 * 256;
-        p.total = p.plane * matrices;
+        p.matrices = matrices;
+        p.plane = ((size_t)T * R * 2 + 255) / 256 * 256;
+        p.total = p.plane * 2 * matrices;
         return p;
     }
 };
+// The layer, given v (linear.cu).  It starts before the launch that computes v ends, which has to wait for all before
+// it before it triggers.
+cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
+                                  const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
+                                  void* out, const void* v, int32_t* status, cudaStream_t st);
 cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                    const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                    void* out, void* workspace, int32_t* status, cudaStream_t st);

@@ -51,15 +51,20 @@ struct Few {
     static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
     // A pair takes all of tensor memory, so that its CTAs hold the same columns.
     static constexpr int columns(int rows) { return PAIR ? kTmemColumns : tmem_columns(rows); }
-    static constexpr int rest(int rows, int splits) {  // beside the stages
-        return splits * kW * pitch(own(rows, splits)) * 4 + 1024;
-    }
-    static constexpr int smem(int rows, int splits, int stages) {
-        const int need = stages * stage(rows) + rest(rows, splits);
+    // beside the stages: landing areas of `parts` parts
+    static constexpr int rest(int rows, int splits, int parts) { return parts * kW * pitch(own(rows, splits)) * 4 + 1024; }
+    static constexpr int rest(int rows, int splits) { return rest(rows, splits, splits); }
+    static constexpr int smem(int rows, int splits, int stages) { return smem(rows, splits, stages, splits); }
+    static constexpr int smem(int rows, int splits, int stages, int parts) {
+        const int need = stages * stage(rows) + rest(rows, splits, parts);
         const int least = smem_for_columns(columns(rows));
         return need > least ? need : least;
     }
 };
+
+// Landing areas of a CTA: one for each part of K, and one for the adapters' addends; a single ungated part is not
+// exchanged, and the addends take its place.
+constexpr int few_parts(int splits, bool gated, bool adapters) { return splits + (adapters && (splits > 1 || gated)); }
 
 // Tiles of the many-row kernel: 256 rows by `features`.
 constexpr int64_t many_tiles(int T, int N, int features) {
@@ -88,7 +93,7 @@ constexpr int few_usable(int cluster, int fit) { return cluster < 4 ? 152 : clus
 
 // The few-row choices with the rows of x in `tiles_t` tiles.
 template <bool PAIR>
-void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, float& best_us, LinPlan& best) {
+void plan_few_tiles(int T, int N, int nk, bool gated, int sms, bool adapters, int tiles_t, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
@@ -99,11 +104,12 @@ void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, floa
         // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
         // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
         const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
-        int stages = alone ? (kCtaSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
+        const int parts = few_parts(splits, gated, adapters);
+        int stages = alone ? (kCtaSmemMax - F::rest(rows, splits, parts)) / F::stage(rows) : 4;
         const int most = PAIR ? kFewStages : alone ? 6 : 4;
         stages = stages < most ? stages : most;
         stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
-        const int smem = F::smem(rows, splits, stages);
+        const int smem = F::smem(rows, splits, stages, parts);
         if (stages < 2 || smem > kCtaSmemMax) continue;
         const int fit = kSmSmem / (smem + kSmemReserved + 256);  // CTAs an SM holds
         const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
@@ -122,14 +128,14 @@ void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, floa
 // As few tiles of x as its rows need, or up to eight times as many where a narrow matrix leaves SMs idle
 // (256 x 2048 x 2048: 12.9 us with one, 10.0 with two; 128 x 256 x 7168: 9.5 with one, 5.9 with four).
 template <bool PAIR>
-void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
+void plan_few(int T, int N, int nk, bool gated, int sms, bool adapters, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int least = (T + F::kRows - 1) / F::kRows;
     for (int m = 1; m <= 8 && (m == 1 || least * m * F::kStep < T + F::kStep) && least * m <= 65535; m *= 2)
-        plan_few_tiles<PAIR>(T, N, nk, gated, sms, least * m, best_us, best);
+        plan_few_tiles<PAIR>(T, N, nk, gated, sms, adapters, least * m, best_us, best);
 }
 
-inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
+inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, bool adapters = false) {
     LinPlan best{};
     float best_us = 1e30f;
     const float per_k[3] = {0.38f, 0.31f, 0.25f};
@@ -143,8 +149,8 @@ inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
             best = LinPlan{false, false, width, 0, 0, 0};
         }
     }
-    plan_few<false>(T, N, nk, gated, sms, best_us, best);
-    plan_few<true>(T, N, nk, gated, sms, best_us, best);
+    plan_few<false>(T, N, nk, gated, sms, adapters, best_us, best);
+    plan_few<true>(T, N, nk, gated, sms, adapters, best_us, best);
     return best;
 }
 

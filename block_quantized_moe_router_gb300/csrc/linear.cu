@@ -16,6 +16,16 @@
 // The gated form takes its weight rows half from W and half from V, so z and its factor meet in one
 // accumulator and neither goes through memory.  Every wait is bounded: one that gives up sets
 // MOE_DEV_TIMEOUT and the CTA winds down.
+//
+// With low-rank adapters (ADAPT) each row's product gains v b[j]^T, v = scale x a[j]^T, before the function.  v comes
+// from the launch before (adapters.cu), which lets this one start before it ends: x and the weights are not
+// its results, so only what reads v waits for it, and v takes no time where the weights take longer.  v is held as
+// two numbers of the layer's type, hi + lo: one rounding to bf16 would cost as much as the result's own.
+//   few rows   the warps that neither load nor issue MMAs compute the addends of this CTA's results meanwhile, by
+//              mma.sync over 8 rows and one adapter at a time, straight from global memory.
+//   many rows  a tile's accumulator takes further stages of K, hi and lo against b[j], for each adapter j that
+//              occurs in it; the MMAs leave out the lanes of the other rows (disable-output-lane).
+// Neither multiplies a row by another row's adapter, so that what is not finite in one stays in its rows.
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -36,6 +46,10 @@ struct LinMaps {
     CUtensorMap x, w, v, res, out;
 };
 
+struct AdaptMaps : LinMaps {
+    CUtensorMap b[2], v_low;  // many rows: [L][N][R] of each matrix, [planes][T][R] of v
+};
+
 struct LinArgs {
     int T, N, nk;       // nk: stages of K in all
     int func, gated, f16;
@@ -49,6 +63,26 @@ struct LinArgs {
     int32_t* status;
 };
 
+struct AdaptArgs : LinArgs {
+    int L, R;
+    int planes[2];         // of v: the first of each matrix's two (hi, lo), -1 for a matrix without adapters
+    int64_t plane, ldb, sb;  // elements of a plane of v; between rows of b and between its adapters
+    const void* b[2];
+    const uint16_t* v;
+    const int32_t* ids;
+};
+
+template <bool ADAPT>
+using MapsOf = std::conditional_t<ADAPT, AdaptMaps, LinMaps>;
+template <bool ADAPT>
+using ArgsOf = std::conditional_t<ADAPT, AdaptArgs, LinArgs>;
+
+// The adapter of row t; -1 for none (an id out of its range was reported by the launch before).
+__device__ __forceinline__ int adapter_of(const AdaptArgs& a, int64_t t) {
+    const int j = t < a.T ? __ldg(a.ids + t) : -1;
+    return j >= 0 && j < a.L ? j : -1;
+}
+
 // ---- CTA-pair primitives -------------------------------------------------------------------------
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // TMA load of a CTA pair: the bytes land here, the count on the mapped barrier of either CTA.
@@ -58,6 +92,14 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(mapped_bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                                 uint32_t mapped_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(mapped_bar)
         : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
@@ -83,6 +125,16 @@ __device__ __forceinline__ void mma_f16kind(uint32_t d, uint64_t ad, uint64_t bd
             "r"(idesc), "r"(acc) : "memory");
     else
         tc_mma_bf16(d, ad, bd, idesc, acc);
+}
+// The pair's MMA into the lanes whose bit of `off` is 0 (first CTA's 128, second CTA's).
+__device__ __forceinline__ void mma_f16kind_lanes(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                                  const uint32_t (&off)[8]) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.b32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
+        "r"(off[6]), "r"(off[7])
+        : "memory");
 }
 // kind::f16: fp32 D, A and B both bf16 (format 1) or both f16 (format 0), K-major.
 __device__ __forceinline__ uint32_t idesc_f16kind(uint32_t M, uint32_t N, bool f16) {
@@ -226,9 +278,70 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 
-template <bool PAIR>
-__global__ void __launch_bounds__(kFewThreads, 4)
-linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
+// The addends of `rows` (a multiple of 32) weight rows and `own` columns, rows t .. t + cols - 1 of x, to dst [row][pitch].
+// Weight rows from `half` on are those of the second matrix.  Items of 32 weight rows x 8 columns, one to a warp of
+// the `warps` that call this as number `warp`; in an item the adapters of its columns one after the other, each
+// into its own columns.
+__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, float* dst, int pitch, int rows, int half, int own, int n0, int64_t t,
+                                                int cols, int warp, int warps) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int blocks = rows / 32, items = (own + 7) / 8 * blocks;
+    for (int item = warp; item < items; item += warps) {
+        const int r0 = item % blocks * 32, c0 = item / blocks * 8, m = r0 >= half;
+        const int n = n0 + r0 - (m ? half : 0) + g;  // this lane's features: n, n + 8, n + 16, n + 24
+        const int plane = a.planes[m];
+        const int mine = c0 + g < cols && plane >= 0 ? adapter_of(a, t + c0 + g) : -1;
+        const uint16_t* hi = a.v + plane * a.plane + (t + c0 + g) * a.R + 4 * c;
+        float sum[2][4] = {};
+        for (int j = -1;;) {
+            j = (int)__reduce_min_sync(0xffffffffu, mine > j ? (unsigned)mine : 0x7fffffffu);
+            if (j == 0x7fffffff) break;
+            const unsigned match = __ballot_sync(0xffffffffu, mine == j);
+            const uint16_t* b = static_cast<const uint16_t*>(a.b[m]) + j * a.sb + n * a.ldb + 4 * c;
+            float d[2][4] = {};
+#pragma unroll 2
+            for (int r = 0; r < a.R; r += 16) {  // this lane's ranks: r + 4 c and the three after it, on both sides
+                const bool in = r + 4 * c < a.R;
+                uint2 w[4], vh = {0u, 0u}, vl = {0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = make_uint2(0u, 0u);
+                    if (in && n + 8 * i < a.N) w[i] = __ldg(reinterpret_cast<const uint2*>(b + 8 * i * a.ldb + r));
+                }
+                if (in && mine == j) {
+                    vh = __ldcg(reinterpret_cast<const uint2*>(hi + r));
+                    vl = __ldcg(reinterpret_cast<const uint2*>(hi + a.plane + r));
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (a.f16) {
+                        mma_f16_16816(d[i], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, vh.x, vh.y);
+                        mma_f16_16816(d[i], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, vl.x, vl.y);
+                    } else {
+                        mma_bf16_16816(d[i], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, vh.x, vh.y);
+                        mma_bf16_16816(d[i], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, vl.x, vl.y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // columns 2 c and 2 c + 1
+                if (match >> (4 * (2 * c + (i & 1))) & 1u) {
+                    sum[0][i] = d[0][i];
+                    sum[1][i] = d[1][i];
+                }
+        }
+        if (c0 + 2 * c < own) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float2*>(dst + (r0 + g + 8 * i) * pitch + c0 + 2 * c) =
+                    make_float2(sum[i >> 1][2 * (i & 1)], sum[i >> 1][2 * (i & 1) + 1]);
+        }
+    }
+}
+
+template <bool PAIR, bool ADAPT>
+__global__ void __launch_bounds__(kFewThreads, ADAPT ? 3 : 4)
+linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_constant__ ArgsOf<ADAPT> a) {
     using F = Few<PAIR>;
     extern __shared__ uint8_t lin_smem[];
     __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full;
@@ -272,11 +385,13 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
     // from the first stage on, single CTAs meet at the exchange.
     cluster_arrive();
     if constexpr (PAIR) cluster_wait();
-    pdl_wait();
+    // With adapters the launch before this one has waited for all before it before it let this one start
+    if constexpr (!ADAPT) pdl_wait();
     pdl_trigger();  // after the allocation, so that a waiting successor cannot hold the columns
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
+    [[maybe_unused]] float* const addends = landing + (direct ? 0 : (int)splits * F::kW * pitch);
     const int steps = k_end - k_begin;
     // The elected lane's role is all that its warp does until the lane is done: the rest of the warp waits at the end of
     // the role, so that nothing it might run shares the warp's uniform registers with the lane's copies and MMAs
@@ -342,14 +457,18 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
             tc_fence_before();
         }
         __syncwarp();
-    } else if (warp >= 6) {
+    } else if (warp >= (ADAPT ? 2 : 6)) {
         // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
         if (a.res)
-            for (int i = threadIdx.x - 192; i < my_cols * 2; i += 64) {
+            for (int i = threadIdx.x - (ADAPT ? 64 : 192); i < my_cols * 2; i += (ADAPT ? 192 : 64)) {
                 const int n = n0 + 64 * (i & 1);
                 if (n < a.N && (i & 1) * 64 < per_cta)
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
+        if constexpr (ADAPT) {
+            pdl_wait();  // v
+            adapter_addends(a, addends, pitch, F::kW, per_cta, own, n0, (int64_t)t0 + my_c0, my_cols, warp - 2, 6);
+        }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
     if constexpr (!PAIR) cluster_wait();
@@ -367,6 +486,13 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
                 float z[16];
                 tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c - c0, reinterpret_cast<uint32_t(&)[16]>(z));
                 tmem_ld_wait();
+                if constexpr (ADAPT) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 p = *reinterpret_cast<const float4*>(addends + row * pitch + c + i);
+                        z[i] += p.x; z[i + 1] += p.y; z[i + 2] += p.z; z[i + 3] += p.w;
+                    }
+                }
                 if (n < a.N) finish_feature(a, (int64_t)t0 + c, rows, n, z, z, rw);
                 __syncwarp();
                 continue;
@@ -406,8 +532,8 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
         ahead(item + kFewThreads / 32);
         float z[4] = {}, u[4] = {};
 #pragma unroll
-        for (int s = 0; s < kFewSplits / F::kCtas; ++s)
-            if (s < (int)splits) {
+        for (int s = 0; s < kFewSplits / F::kCtas + ADAPT; ++s)
+            if (s < (int)splits + ADAPT) {
                 const float4 p = *reinterpret_cast<const float4*>(src + s * F::kW * pitch);
                 z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
                 if (a.gated) {
@@ -444,7 +570,8 @@ linear_few_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ 
 // measured cuBLAS rate).  Two pairs sharing x by multicast were no faster: clusters of four occupy
 // 144 of the 152 SMs.
 // ------------------------------------------------------------------------------------------
-constexpr int kManyThreads = 448;
+template <bool ADAPT>
+constexpr int kManyThreads = ADAPT ? 480 : 448;  // with adapters one more warp lists them, tile by tile
 constexpr int kManyMovers = 4;
 constexpr int kManyStages = 3;
 constexpr int kManyHalf = 2 * kLinA;             // 64 elements of K: 128 rows of x, at most 128 of W
@@ -492,12 +619,22 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
                      reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
-__global__ void __launch_bounds__(kManyThreads, 1)
-linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
+// An adapter of a tile, and the tile's rows that have another one or none; id -1 behind the last.
+struct TileAdapter {
+    int id;
+    uint32_t off[8];
+};
+constexpr int kTileAdapters = 8;  // of the ring that hands them on
+
+template <bool ADAPT>
+__global__ void __launch_bounds__(kManyThreads<ADAPT>, 1)
+linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_constant__ ArgsOf<ADAPT> a) {
     extern __shared__ uint8_t lin_smem[];
     __shared__ uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2];
     __shared__ uint64_t buf_ready[2], buf_done[2];  // row buffers: usable by the epilogue; written by it
     __shared__ __align__(16) float bias_s[2][128];  // per buffer: 64 of bias, 64 of bias_mul
+    __shared__ TileAdapter tile_adapters[ADAPT ? kTileAdapters : 1];
+    __shared__ uint64_t listed[ADAPT ? kTileAdapters : 1], taken[ADAPT ? kTileAdapters : 1];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
@@ -521,6 +658,11 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             mbar_init(&buf_ready[b], by_tma ? 1 : kManyMovers);
             mbar_init(&buf_done[b], 8);
         }
+        if constexpr (ADAPT)
+            for (int i = 0; i < kTileAdapters; ++i) {
+                mbar_init(&listed[i], 1);
+                mbar_init(&taken[i], rank == 0 ? 2 : 1);  // who loads, and who issues the MMAs
+            }
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.x);
@@ -535,7 +677,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     cluster_sync();  // both CTAs' barriers exist before either is signalled from the other
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();
+    if constexpr (!ADAPT) pdl_wait();  // with adapters as in the other kernel
     pdl_trigger();
     auto give_up = [&]() {
         abort_flag = 1;
@@ -551,7 +693,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         if (elect_one()) {  // TMA producer of this CTA's halves
             const CUtensorMap* wmap = a.gated && rank == 1 ? &maps.v : &maps.w;
             int it = 0;
-            RingPos at;
+            RingPos at, list;
             for (auto i = sched.begin(pair); i.tile < sched.total && !abort_flag; sched.next(i, pairs)) {
                 int t0, n0;
                 first(i, t0, n0);
@@ -570,6 +712,39 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                         tma_load_pair(base + h * kManyHalf + kLinA, wmap, (k + h) * kLinK, n0, bar);
                     }
                 }
+                if constexpr (ADAPT) {
+                    // Stages of 64 ranks: hi and lo of the rows, and the adapter's rows of b.  In the gated form a
+                    // CTA's half of the columns belongs to one matrix: for the other's adapters it takes zeros,
+                    // from behind row N.
+                    for (bool more = !abort_flag; more; list.next(kTileAdapters)) {
+                        if (!mbar_wait_suspended(&listed[list.slot], list.parity)) {
+                            give_up();
+                            break;
+                        }
+                        const int j = tile_adapters[list.slot].id;
+                        mbar_arrive(&taken[list.slot]);
+                        more = j >= 0;
+                        if (more) pdl_wait();  // v
+                        for (int m = 0; m < 2 && more; ++m) {
+                            if (a.planes[m] < 0) continue;
+                            const int y = a.gated && m != rank ? a.N : n0;
+                            for (int r = 0; r < a.R && more; r += kLinK, ++it, at.next(kManyStages)) {
+                                const int s = at.slot;
+                                if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
+                                    give_up();
+                                    more = false;
+                                    break;
+                                }
+                                const uint32_t base = smem_u32(smem + s * kManyStageBytes);
+                                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (2 * kLinA + half * 128));
+                                const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+                                tma_load_pair_3d(base, &maps.v_low, r, t0, a.planes[m], bar);
+                                tma_load_pair_3d(base + kManyHalf, &maps.v_low, r, t0, a.planes[m] + 1, bar);
+                                tma_load_pair_3d(base + kLinA, &maps.b[m], r, y, j, bar);
+                            }
+                        }
+                    }
+                }
             }
             if (rank == 0)  // whoever gives up, none of the pair's copies is in flight when its CTAs end
                 for (int i = it < kManyStages ? it : kManyStages; i > 0; --i) {
@@ -582,7 +757,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
         if (rank == 0 && elect_one()) {  // MMA issuer of the pair
             const uint32_t idesc = idesc_f16kind(256, a.width, a.f16);
             int n = 0;
-            RingPos ring;
+            RingPos ring, list;
             for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
                 const int b = n & 1;
                 if (!mbar_wait_suspended(&acc_empty[b], ((n >> 1) & 1) ^ 1)) {
@@ -605,6 +780,36 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
                             mma_f16kind<1>(tmem + 256 * b, at, at + (kLinA >> 4), idesc, (k | h | j) != 0);
                         }
                     tc_commit_pair(&empty[s], 3);
+                }
+                if constexpr (ADAPT) {
+                    for (bool more = !abort_flag; more; list.next(kTileAdapters)) {
+                        if (!mbar_wait_suspended(&listed[list.slot], list.parity)) {
+                            give_up();
+                            break;
+                        }
+                        const TileAdapter of = tile_adapters[list.slot];
+                        mbar_arrive(&taken[list.slot]);
+                        more = of.id >= 0;
+                        for (int m = 0; m < 2 && more; ++m) {
+                            if (a.planes[m] < 0) continue;
+                            for (int r = 0; r < a.R && more; r += kLinK, ring.next(kManyStages)) {
+                                const int s = ring.slot;
+                                if (!mbar_wait_suspended(&full[s], ring.parity)) {
+                                    give_up();
+                                    more = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 1024, kLayoutSw128);
+                                for (int k = 0; k < kLinK && r + k < a.R; k += 16) {  // 32 bytes along the swizzled row
+                                    const uint64_t hi = ad + (k >> 3);
+                                    mma_f16kind_lanes(tmem + 256 * b, hi, hi + (kLinA >> 4), idesc, of.off);
+                                    mma_f16kind_lanes(tmem + 256 * b, hi + (kManyHalf >> 4), hi + (kLinA >> 4), idesc, of.off);
+                                }
+                                tc_commit_pair(&empty[s], 3);
+                            }
+                        }
+                    }
                 }
                 tc_commit_pair(&acc_full[b], 3);
             }
@@ -654,6 +859,40 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[b]), 0));
+        }
+    } else if (ADAPT && warp == 14) {  // lists each tile's adapters, in ascending order
+        if constexpr (ADAPT) {
+            RingPos list;
+            bool go = true;
+            for (auto i = sched.begin(pair); i.tile < sched.total && go && !abort_flag; sched.next(i, pairs)) {
+                int tt, tn;
+                sched.tiles(i, tt, tn);
+                int mine[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) mine[w] = adapter_of(a, (int64_t)tt * 256 + 32 * w + lane);
+                for (int j = -1; j != 0x7fffffff; list.next(kTileAdapters)) {
+                    unsigned next = 0x7fffffffu;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) next = mine[w] > j ? min(next, (unsigned)mine[w]) : next;
+                    j = (int)__reduce_min_sync(0xffffffffu, next);
+                    if (!__all_sync(0xffffffffu, mbar_wait_suspended(&taken[list.slot], list.parity ^ 1))) {
+                        give_up();
+                        go = false;
+                        break;
+                    }
+                    TileAdapter& to = tile_adapters[list.slot];
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) {
+                        const uint32_t off = __ballot_sync(0xffffffffu, mine[w] != j);
+                        if (lane == 0) to.off[w] = off;
+                    }
+                    if (lane == 0) {
+                        to.id = j == 0x7fffffff ? -1 : j;
+                        mbar_arrive(&listed[list.slot]);
+                    }
+                    __syncwarp();
+                }
+            }
         }
     } else if (warp >= 10 && (warp == 10 || !by_tma)) {  // row movers
         struct {
@@ -805,6 +1044,7 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             for (uint32_t j = out_of.pass; j != next_in.pass; ++j) mbar_wait_suspended(&buf_ready[j & 1], (j >> 1) & 1);
         if (lane == 0 && by_tma) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if constexpr (ADAPT) pdl_wait();  // whoever waits for this launch waits for the one before it too
     __syncthreads();
     cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done
     if (warp == 1) {
@@ -814,9 +1054,9 @@ linear_many_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
 }
 
 // ---- host ------------------------------------------------------------------------------------------
-template <typename K>
+template <typename K, typename M, typename A>
 cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allowed, dim3 grid, int cluster,
-                            int threads, int smem, const LinMaps& m, const LinArgs& a, cudaStream_t st) {
+                            int threads, int smem, const M& m, const A& a, cudaStream_t st) {
     const cudaError_t err = allow_large_launch(kernel, smem_max, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -835,42 +1075,56 @@ cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allo
     return cudaLaunchKernelEx(&cfg, kernel, m, a);
 }
 
-template <bool PAIR>
-cudaError_t launch_few(const LinMaps& m, const LinArgs& a, int splits, int N, cudaStream_t st) {
+template <bool PAIR, bool ADAPT>
+cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int splits, int N, cudaStream_t st) {
     using F = Few<PAIR>;
     const int per_tile = F::kW * F::kCtas / (a.gated ? 2 : 1), cluster = splits * F::kCtas;
     const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
     static std::atomic<uint64_t> allowed{0};
-    return launch_clusters(linear_few_kernel<PAIR>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
-                           F::smem(a.rows_t, splits, a.stages), m, a, st);
+    return launch_clusters(linear_few_kernel<PAIR, ADAPT>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
+                           F::smem(a.rows_t, splits, a.stages, few_parts(splits, a.gated, ADAPT)), m, a, st);
 }
 
-}  // namespace
-
-cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
-                          const float* bias, const float* bias_mul, const void* residual, void* out,
-                          int32_t* status, cudaStream_t st) {
+template <bool ADAPT>
+cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
+                         const float* bias, const float* bias_mul, const void* residual, void* out,
+                         const moe_adapter_desc* ad, const void* v, int32_t* status, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    LinArgs a{};
+    ArgsOf<ADAPT> a{};
     a.T = d.T; a.N = d.N; a.nk = (d.K + kLinK - 1) / kLinK;
     a.func = d.func; a.gated = w_mul != nullptr; a.f16 = d.dtype == MOE_DT_F16;
     a.ldr = d.ldr; a.ldo = d.ldo;
     a.bias = bias; a.bias_mul = bias_mul; a.res = residual; a.out = out; a.status = status;
-    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms);
-    LinMaps m{};
+    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms, ADAPT);
+    MapsOf<ADAPT> m{};
     // rows of W per box, and rows of x
     const int box_w = plan.few ? (plan.pair ? 64 : 128) / (a.gated ? 2 : 1) : plan.width / 2;
     const int box_x = !plan.few ? 128 : plan.pair ? plan.rows_t / 2 : plan.rows_t;
     if (!encode_rows16(&m.x, x, d.K, d.T, d.ldx, box_x, kLinK) || !encode_rows16(&m.w, w, d.K, d.N, d.ldw, box_w, kLinK) ||
         (a.gated && !encode_rows16(&m.v, w_mul, d.K, d.N, d.ldw, box_w, kLinK)))
         return cudaErrorInvalidValue;
+    if constexpr (ADAPT) {
+        const AdapterProducts p = AdapterProducts::plan(d.T, ad->R, ad->a && ad->a_mul ? 2 : 1);
+        a.L = ad->L; a.R = ad->R; a.ldb = ad->ldb; a.sb = ad->L > 1 ? ad->sb : d.N * ad->ldb;
+        a.b[0] = ad->b; a.b[1] = ad->b_mul;
+        a.planes[0] = ad->a ? 0 : -1;
+        a.planes[1] = ad->a_mul ? (ad->a ? 2 : 0) : -1;
+        a.plane = (int64_t)(p.plane / sizeof(uint16_t));
+        a.v = static_cast<const uint16_t*>(v);
+        a.ids = ad->ids;
+        if (!plan.few) {
+            if (!encode_stack16(&m.v_low, v, ad->R, d.T, p.matrices * 2, ad->R, a.plane, 128)) return cudaErrorInvalidValue;
+            for (int i = 0; i < 2; ++i)
+                if (a.b[i] && !encode_stack16(&m.b[i], a.b[i], ad->R, d.N, ad->L, ad->ldb, a.sb, box_w)) return cudaErrorInvalidValue;
+        }
+    }
     if (plan.few) {
         a.rows_t = plan.rows_t;
         a.stages = plan.stages;
-        return plan.pair ? launch_few<true>(m, a, plan.splits, d.N, st) : launch_few<false>(m, a, plan.splits, d.N, st);
+        return plan.pair ? launch_few<true, ADAPT>(m, a, plan.splits, d.N, st) : launch_few<false, ADAPT>(m, a, plan.splits, d.N, st);
     }
     // TMA addresses rows that start at multiples of 16 bytes, and writes whole ones: where a row ends inside 16 bytes, what lies
     // behind it is written too
@@ -882,7 +1136,20 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
     const int64_t total = ManySched(d.T, d.N, a.gated ? a.width / 2 : a.width).total;
     const int pairs = (int)(total < sms / 2 ? total : sms / 2);
     static std::atomic<uint64_t> allowed{0};
-    return launch_clusters(linear_many_kernel, kManySmem, allowed, dim3(2 * pairs), 2, kManyThreads, kManySmem, m, a, st);
+    return launch_clusters(linear_many_kernel<ADAPT>, kManySmem, allowed, dim3(2 * pairs), 2, kManyThreads<ADAPT>, kManySmem, m, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
+                          const float* bias, const float* bias_mul, const void* residual, void* out,
+                          int32_t* status, cudaStream_t st) {
+    return launch_layer<false>(d, x, w, w_mul, bias, bias_mul, residual, out, nullptr, nullptr, status, st);
+}
+cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
+                                  const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
+                                  void* out, const void* v, int32_t* status, cudaStream_t st) {
+    return launch_layer<true>(d, x, w, w_mul, bias, bias_mul, residual, out, &ad, v, status, st);
 }
 
 }  // namespace moe
