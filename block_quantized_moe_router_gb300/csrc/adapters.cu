@@ -26,8 +26,8 @@ struct LowMaps {
     CUtensorMap x, a[2];
 };
 struct LowArgs {
-    int T, R, L, matrices, steps, f16, halves;  // steps of K in all; halves: v as hi and lo of the layer's type, else fp32
-    int rows, own_log2, unit_log2, per_adapter, tile, width, slots, stages, stage;
+    int T, R, L, matrices, steps, f16;  // steps of K in all
+    int rows, own_log2, unit_log2, per_adapter_log2, tile, width, slots, stages, stage, loaders;
     int64_t plane;  // elements of 16 bits
     const float* scale;
     const int32_t* ids;
@@ -35,8 +35,7 @@ struct LowArgs {
     int32_t* status;
 };
 constexpr int kLowThreads = 256;
-constexpr int kLowLoaders = 6;  // warps that load adapters: of a tile's units one or two each
-static_assert(kLowTile / 16 <= 2 * kLowLoaders && kLowThreads == 32 * (kLowLoaders + 2));
+static_assert(kLowThreads / 32 - 2 == kLowLoaders);
 
 // kind::f16: fp32 D of 128 rows, A and B both bf16 (format 1) or both f16 (format 0), K-major.
 __device__ __forceinline__ uint32_t low_idesc(uint32_t N, bool f16) {
@@ -62,12 +61,11 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
     const int k_begin = (int)((int64_t)g.steps * cta / ctas), steps = (int)((int64_t)g.steps * (cta + 1) / ctas) - k_begin;
     const int unit = 1 << g.unit_log2, own = 1 << g.own_log2;
     const int x_at = g.tile * unit * 128;  // of a stage
-    const int loaders = min(g.tile, kLowLoaders);
     uint32_t tm_cols = kTmemLeast;
     while ((int)tm_cols < g.rows) tm_cols *= 2;
     if (tid == 0) {
         for (int s = 0; s < g.stages; ++s) {
-            mbar_init(&full[s], 1 + loaders);
+            mbar_init(&full[s], 1 + g.tile);  // x, and every unit
             mbar_init(&empty[s], 1);
         }
         mbar_init(&acc_full, 1);
@@ -83,7 +81,9 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
     const uint32_t tmem = tmem_slot;
     cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     pdl_wait();
-    pdl_trigger();  // the layer's launch may start: whatever came before this one is done
+    // The layer's launch may start: whatever came before this one is done.  (Once the first loads are here, so that they are
+    // not behind the layer's: 8 rows 16.6 us for 12.4.)
+    pdl_trigger();
     auto give_up = [&]() { status_or(g.status, MOE_DEV_TIMEOUT); };
     const auto load_x = [&](int s, int i) {
         mbar_arrive_expect_tx(&full[s], g.rows * 128);
@@ -91,9 +91,9 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
     };
     // roles of elected lanes as in linear.cu: the rest of their warps waits at the end of the role
     const int ahead = min(steps, g.stages);  // stages whose x comes before the adapters are known
-    if (warp == 0) {
+    if (warp >= kLowRows / 32) {  // the others find the adapters meanwhile
         if (elect_one())
-            for (int i = 0; i < ahead; ++i) load_x(i, i);
+            for (int i = warp - kLowRows / 32; i < ahead; i += kLowThreads / 32 - kLowRows / 32) load_x(i, i);
         __syncwarp();
     }
     // the group's adapters
@@ -141,7 +141,7 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
     if (tid < kLowRows && !leads) place[tid] = id >= 0 ? place[first] : (int8_t)-1;
     __syncthreads();
     cluster_wait();
-    const int units = adapters * g.per_adapter, per_matrix = g.per_adapter / g.matrices;
+    const int per_adapter = 1 << g.per_adapter_log2, units = adapters << g.per_adapter_log2, per_matrix = per_adapter / g.matrices;
     const int my_c0 = cta * own, my_cols = min(own, ncols - my_c0);  // this CTA's rows of x
     int done = 0;  // tiles
     for (int tile = blockIdx.z; tile * g.tile < units; tile += g.slots, ++done) {
@@ -149,13 +149,6 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
         RingPos ring;  // `done` tiles of `steps` stages on
         ring.slot = (done * steps) % g.stages;
         ring.parity = (uint32_t)((done * steps) / g.stages) & 1u;
-        // whoever gives up, no copy is in flight when the CTA ends
-        const auto drain = [&](RingPos at, int issued) {
-            for (int i = issued < g.stages ? issued : g.stages; i > 0; --i) {
-                at.back(g.stages);
-                mbar_wait_suspended(&full[at.slot], at.parity);
-            }
-        };
         if (warp == 0) {
             if (elect_one()) {
                 int i = 0;
@@ -168,35 +161,37 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
                     }
                     load_x(at.slot, i);
                 }
-                drain(at, i);
+                // whoever gives up, no copy is in flight when the CTA ends
+                for (int left = i < g.stages ? i : g.stages; left > 0; --left) {
+                    at.back(g.stages);
+                    mbar_wait_suspended(&full[at.slot], at.parity);
+                }
             }
             __syncwarp();
-        } else if (warp >= 2 && warp < 2 + loaders) {
-            // this warp's units of the tile, the second behind the last where there is none
-            const int k0 = warp - 2, k1 = k0 + kLowLoaders;
-            int of = (u0 + k0) / g.per_adapter, u = u0 + k0 - of * g.per_adapter;
-            const CUtensorMap* const map0 = u >= per_matrix ? &maps.a[1] : &maps.a[0];
-            const int y0 = (u >= per_matrix ? u - per_matrix : u) << g.unit_log2, z0 = id_s[min(of, kLowRows - 1)];
-            of = (u0 + k1) / g.per_adapter;
-            u = u0 + k1 - of * g.per_adapter;
-            const CUtensorMap* const map1 = u >= per_matrix ? &maps.a[1] : &maps.a[0];
-            const int y1 = (u >= per_matrix ? u - per_matrix : u) << g.unit_log2, z1 = id_s[min(of, kLowRows - 1)];
-            const uint32_t bytes = (uint32_t)((k0 < here) + (k1 < here)) * unit * 128;
-            if (elect_one()) {
-                int i = 0;
+        } else if (warp >= 2) {
+            // Units of stages in turn, so that all loaders have some however few units there are; a unit that a short tile
+            // lacks arrives without bytes.  A loader goes on by a lap of the ring at most: a barrier's parity tells the
+            // lap before from this one, not from the one before that.
+            if (warp - 2 < g.loaders && elect_one()) {
                 RingPos at = ring;
-                for (; i < steps; ++i, at.next(g.stages)) {
+                int i = 0;  // stage
+                for (int k = warp - 2;; k += g.loaders) {
+                    for (; k >= g.tile; k -= g.tile) {
+                        ++i;
+                        at.next(g.stages);
+                    }
+                    if (i >= steps) break;
                     if (!mbar_wait_suspended(&empty[at.slot], at.parity ^ 1)) {
                         give_up();
                         break;
                     }
                     uint64_t* const bar = &full[at.slot];
-                    uint8_t* const base = smem + at.slot * g.stage;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (k0 < here) tma_load_3d(base + k0 * unit * 128, map0, (k_begin + i) * kLowK, y0, z0, bar);
-                    if (k1 < here) tma_load_3d(base + k1 * unit * 128, map1, (k_begin + i) * kLowK, y1, z1, bar);
+                    mbar_arrive_expect_tx(bar, k < here ? unit * 128 : 0);
+                    if (k >= here) continue;
+                    const int of = (u0 + k) >> g.per_adapter_log2, u = (u0 + k) & (per_adapter - 1), second = u >= per_matrix;
+                    tma_load_3d(smem + at.slot * g.stage + k * unit * 128, &maps.a[second], (k_begin + i) * kLowK,
+                                (u - (second ? per_matrix : 0)) << g.unit_log2, id_s[of], bar);
                 }
-                drain(at, i);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -223,37 +218,35 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
             __syncwarp();
         }
         __syncthreads();  // all wait here for that
-        {  // the two warps of a lane quarter take alternate 16 columns; a lane is a rank
+        {  // A lane is a rank; the two warps of a lane quarter take alternate 32 columns, of those the ones with an adapter of this
+           // tile: two or three of 64 tokens with one each, all of a prompt.
             tc_fence_after();
-            const int q = warp & 3, u = u0 + ((32 * q + lane) >> g.unit_log2), of = u / g.per_adapter;  // adapter of the lane
-            const int rank = 32 * q + lane - ((max(of * g.per_adapter, u0) - u0) << g.unit_log2);       // of those of that adapter here
+            const int q = warp & 3, u = u0 + ((32 * q + lane) >> g.unit_log2), of = u >> g.per_adapter_log2;  // adapter of the lane
+            const int rank = 32 * q + lane - ((max(of << g.per_adapter_log2, u0) - u0) << g.unit_log2);       // of those of that adapter here
             const int mine = u < u0 + here ? of : kLowRows;
+            const int low = u0 >> g.per_adapter_log2, high = (u0 + here - 1) >> g.per_adapter_log2;  // adapters of the tile
             const uint32_t to = smem_u32(landing + (cta << g.own_log2) * g.width + rank);
-            if (32 * q < here * unit)
-                for (int c = 16 * (warp >> 2); c < ncols; c += 32) {
-                    uint32_t v[16];
-                    tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-                    const uint4 p = *reinterpret_cast<const uint4*>(place + c);
-                    const uint32_t places[4] = {p.x, p.y, p.z, p.w};
+            for (int c0 = 32 * (warp >> 2); 32 * q < here * unit && c0 < ncols; c0 += 64) {
+                const int at = place[c0 + lane];
+#pragma unroll 1
+                for (unsigned left = __ballot_sync(0xffffffffu, at >= low && at <= high); left; left &= left - 1) {
+                    const int c = c0 + __ffs(left) - 1;
+                    const uint32_t v = tmem_ld_1(tmem + ((uint32_t)(32 * q) << 16) + c);
+                    const uint32_t there = map_rank(to + (c & (own - 1)) * g.width * 4, c >> g.own_log2);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const int owner = (c + i) >> g.own_log2, at = (c + i) & (own - 1);
-                        const uint32_t there = map_rank(to + at * g.width * 4, owner);  // columns behind the last have no place
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if ((int)(places[i / 4] >> (8 * k) & 0xFFu) == mine) st_cluster(there + k * g.width * 4, v[i + k]);
-                    }
+                    if (place[c] == mine) st_cluster(there, v);
+                    __syncwarp();
                 }
+            }
             tc_fence_before();
         }
         cluster_sync();  // every part has landed
-        const int fours = g.width / 4;  // a power of two
-        for (int i = tid; i < my_cols * fours; i += kLowThreads) {  // a row's four ranks
-            const int c = i / fours, n = 4 * (i & (fours - 1)), of = place[my_c0 + c];
-            const int from = max(of * g.per_adapter, u0), end = min((of + 1) * g.per_adapter, u0 + g.tile);  // its units here
+        const int fours_log2 = 29 - __clz(g.width);  // width is a power of two
+        for (int i = tid; i < my_cols << fours_log2; i += kLowThreads) {  // a row's four ranks
+            const int c = i >> fours_log2, n = 4 * (i & ((1 << fours_log2) - 1)), of = place[my_c0 + c];
+            const int from = max(of << g.per_adapter_log2, u0), end = min((of + 1) << g.per_adapter_log2, u0 + g.tile);  // its units here
             if (of < 0 || n >= (end - from) << g.unit_log2) continue;
-            const int u = from - of * g.per_adapter + (n >> g.unit_log2), m = u >= per_matrix;  // of the adapter
+            const int u = from - (of << g.per_adapter_log2) + (n >> g.unit_log2), m = u >= per_matrix;  // of the adapter
             const int r = ((u - (m ? per_matrix : 0)) << g.unit_log2) + (n & (unit - 1));
             if (r >= g.R) continue;  // R is a multiple of 8: all four or none
             const float* src = landing + c * g.width + n;
@@ -268,10 +261,6 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
             const float v[4] = {z.x * times, z.y * times, z.z * times, z.w * times};
             uint16_t* const to_v = g.v + 2 * m * g.plane;
             const int64_t at = (t0 + my_c0 + c) * g.R + r;
-            if (!g.halves) {
-                *reinterpret_cast<float4*>(reinterpret_cast<float*>(to_v) + at) = make_float4(v[0], v[1], v[2], v[3]);
-                continue;
-            }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // an infinite hi has no rest
@@ -288,12 +277,12 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
             *reinterpret_cast<uint2*>(to_v + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
             *reinterpret_cast<uint2*>(to_v + g.plane + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
-        cluster_sync();  // the landing areas and tensor memory are free
+        if ((tile + g.slots) * g.tile < units) cluster_sync();  // the landing areas and tensor memory are free
     }
     if (done == 0 && warp == 0) {  // nothing used the x that came ahead
         if (elect_one())
             for (int i = 0; i < ahead; ++i) {
-                for (int k = 0; k < loaders; ++k) mbar_arrive(&full[i]);
+                for (int k = 0; k < g.tile; ++k) mbar_arrive(&full[i]);
                 mbar_wait_suspended(&full[i], 0);
             }
         __syncwarp();
@@ -313,8 +302,6 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    bool halves = false;
-    if (err == cudaSuccess) err = adapted_linear_halves(d, ad.R, w_mul != nullptr, halves);
     static std::atomic<uint64_t> allowed{0};
     if (err == cudaSuccess) err = allow_large_launch(low_rank_kernel, kCtaSmemMax, allowed);
     if (err != cudaSuccess) return err;
@@ -326,8 +313,8 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
     for (int i = 0; i < products.matrices; ++i)
         if (!encode_stack16(&m.a[i], of[i], d.K, ad.R, ad.L, ad.lda, ad.L > 1 ? ad.sa : ad.R * ad.lda, 1 << p.unit_log2)) return cudaErrorInvalidValue;
     LowArgs g{};
-    g.T = d.T; g.R = ad.R; g.L = ad.L; g.matrices = products.matrices; g.steps = (d.K + kLowK - 1) / kLowK; g.f16 = d.dtype == MOE_DT_F16; g.halves = halves;
-    g.rows = p.rows; g.own_log2 = p.own_log2; g.unit_log2 = p.unit_log2; g.tile = p.tile; g.width = p.width; g.per_adapter = p.per_adapter; g.slots = p.slots; g.stages = p.stages; g.stage = p.stage;
+    g.T = d.T; g.R = ad.R; g.L = ad.L; g.matrices = products.matrices; g.steps = (d.K + kLowK - 1) / kLowK; g.f16 = d.dtype == MOE_DT_F16;
+    g.rows = p.rows; g.own_log2 = p.own_log2; g.unit_log2 = p.unit_log2; g.tile = p.tile; g.width = p.width; g.per_adapter_log2 = p.per_adapter_log2; g.slots = p.slots; g.stages = p.stages; g.stage = p.stage; g.loaders = p.loaders;
     g.plane = (int64_t)(products.plane / 2);
     g.scale = ad.scale; g.ids = ad.ids; g.v = static_cast<uint16_t*>(workspace); g.status = status;
     // groups are the grid's second dimension: at most 65535 a launch
@@ -339,7 +326,7 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
             if (!encode_rows16(&m.x, static_cast<const uint16_t*>(x) + t * d.ldx, d.K, d.T - t, d.ldx, p.rows, kLowK)) return cudaErrorInvalidValue;
             h.T = (int)(d.T - t);
             h.ids += t;
-            h.v += t * g.R * (halves ? 1 : 2);
+            h.v += t * g.R;
         }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)p.splits, (unsigned)n, (unsigned)p.slots);

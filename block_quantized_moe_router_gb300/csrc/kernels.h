@@ -53,7 +53,7 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const voi
 constexpr int kMaxRank = 256;
 constexpr int kMaxAdapters = 1 << 20;
 // The low-rank products v = scale x a^T of every row, in the workspace: for each matrix two planes [T][R] of the
-// layer's type, whose sum is v; or in their place [T][R] float, where the layer takes v so.
+// layer's type, whose sum is v.
 struct AdapterProducts {
     int matrices;
     size_t plane, total;  // bytes of a plane, and of all
@@ -67,7 +67,6 @@ struct AdapterProducts {
 };
 // The layer, given v (linear.cu).  It starts before the launch that computes v ends, which has to wait for all before
 // it before it triggers.
-cudaError_t adapted_linear_halves(const moe_linear_desc& d, int R, bool gated, bool& halves);
 cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                   const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                   void* out, const void* v, int32_t* status, cudaStream_t st);

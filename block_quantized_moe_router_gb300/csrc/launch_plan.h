@@ -39,6 +39,7 @@ constexpr bool columns_covered(int smem, int columns) {
 constexpr int kLinK = 64;        // K elements per stage (128 bytes per row)
 constexpr int kFewSplits = 8;    // parts of K at most; CTAs of a cluster too (the portable cluster size)
 constexpr int kFewStages = 8;
+constexpr int kLowSmemFew = 76 * 1024;  // of a CTA that computes the low-rank products of few rows
 template <bool PAIR>
 struct Few {
     static constexpr int kRows = PAIR ? 256 : 128;   // rows of x per tile at most
@@ -51,16 +52,20 @@ struct Few {
     static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
     // A pair takes all of tensor memory, so that its CTAs hold the same columns.
     static constexpr int columns(int rows) { return PAIR ? kTmemColumns : tmem_columns(rows); }
-    // beside the stages: the landing area, and `column` bytes for each of a CTA's columns
-    static constexpr int rest(int rows, int splits, int column = 0) {
-        return splits * kW * pitch(own(rows, splits)) * 4 + own(rows, splits) * column + 1024;
-    }
-    static constexpr int smem(int rows, int splits, int stages, int column = 0) {
-        const int need = stages * stage(rows) + rest(rows, splits, column);
+    // beside the stages: landing areas of `parts` parts
+    static constexpr int rest(int rows, int splits, int parts) { return parts * kW * pitch(own(rows, splits)) * 4 + 1024; }
+    static constexpr int rest(int rows, int splits) { return rest(rows, splits, splits); }
+    static constexpr int smem(int rows, int splits, int stages) { return smem(rows, splits, stages, splits); }
+    static constexpr int smem(int rows, int splits, int stages, int parts) {
+        const int need = stages * stage(rows) + rest(rows, splits, parts);
         const int least = smem_for_columns(columns(rows));
         return need > least ? need : least;
     }
 };
+
+// Landing areas of a CTA: one for each part of K, and one for the adapters' addends; a single ungated part is not
+// exchanged, and the addends take its place.
+constexpr int few_parts(int splits, bool gated, bool adapters) { return splits + (adapters && (splits > 1 || gated)); }
 
 // Tiles of the many-row kernel: 256 rows by `features`.
 constexpr int64_t many_tiles(int T, int N, int features) {
@@ -87,25 +92,28 @@ struct LinPlan {
 // one CTA per SM, 36 of 8 at two.
 constexpr int few_usable(int cluster, int fit) { return cluster < 4 ? 152 : cluster == 8 && fit == 1 ? 120 : 144; }
 
-// The few-row choices with the rows of x in `tiles_t` tiles.  column: shared memory per column besides.
+// The few-row choices with the rows of x in `tiles_t` tiles.
 template <bool PAIR>
-void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int column, int tiles_t, float& best_us, LinPlan& best) {
+void plan_few_tiles(int T, int N, int nk, bool gated, int sms, bool adapters, int tiles_t, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
     const int64_t tiles = (int64_t)((T + rows - 1) / rows) * ((N + per_tile - 1) / per_tile) * F::kCtas;
     const float stage_kb = (float)F::stage(rows) / 1024.f;
+    // With adapters a CTA leaves room for one of the launch that computes their products, so that both run at once
+    const int smem_max = adapters ? kSmSmem - kLowSmemFew - 2 * (kSmemReserved + 256) : kCtaSmemMax;
     for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
         const int kbs = (nk + splits - 1) / splits;
         // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
         // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
         const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
-        int stages = alone ? (kCtaSmemMax - F::rest(rows, splits, column)) / F::stage(rows) : 4;
+        const int parts = few_parts(splits, gated, adapters);
+        int stages = alone ? (smem_max - F::rest(rows, splits, parts)) / F::stage(rows) : 4;
         const int most = PAIR ? kFewStages : alone ? 6 : 4;
         stages = stages < most ? stages : most;
         stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
-        const int smem = F::smem(rows, splits, stages, column);
-        if (stages < 2 || smem > kCtaSmemMax) continue;
+        const int smem = F::smem(rows, splits, stages, parts);
+        if (stages < 2 || smem > (F::columns(rows) == kTmemColumns ? kCtaSmemMax : smem_max)) continue;
         const int fit = kSmSmem / (smem + kSmemReserved + 256);  // CTAs an SM holds
         const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
         const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
@@ -123,14 +131,14 @@ void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int column, int t
 // As few tiles of x as its rows need, or up to eight times as many where a narrow matrix leaves SMs idle
 // (256 x 2048 x 2048: 12.9 us with one, 10.0 with two; 128 x 256 x 7168: 9.5 with one, 5.9 with four).
 template <bool PAIR>
-void plan_few(int T, int N, int nk, bool gated, int sms, int column, float& best_us, LinPlan& best) {
+void plan_few(int T, int N, int nk, bool gated, int sms, bool adapters, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int least = (T + F::kRows - 1) / F::kRows;
     for (int m = 1; m <= 8 && (m == 1 || least * m * F::kStep < T + F::kStep) && least * m <= 65535; m *= 2)
-        plan_few_tiles<PAIR>(T, N, nk, gated, sms, column, least * m, best_us, best);
+        plan_few_tiles<PAIR>(T, N, nk, gated, sms, adapters, least * m, best_us, best);
 }
 
-inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, int column = 0) {
+inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, bool adapters = false) {
     LinPlan best{};
     float best_us = 1e30f;
     const float per_k[3] = {0.38f, 0.31f, 0.25f};
@@ -144,8 +152,8 @@ inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, int column
             best = LinPlan{false, false, width, 0, 0, 0};
         }
     }
-    plan_few<false>(T, N, nk, gated, sms, column, best_us, best);
-    plan_few<true>(T, N, nk, gated, sms, column, best_us, best);
+    plan_few<false>(T, N, nk, gated, sms, adapters, best_us, best);
+    plan_few<true>(T, N, nk, gated, sms, adapters, best_us, best);
     return best;
 }
 
@@ -155,12 +163,15 @@ constexpr int kLowTile = 128;     // ranks of a tile at most, the MMA's rows
 constexpr int kLowRows = 128;     // rows of x of a group at most, the MMA's columns
 constexpr int kLowStages = 16;
 constexpr int kLowSplits = 8;
+constexpr int kLowLoaders = 6;    // warps that load adapters
 
 struct LowPlan {
     int rows, groups, own_log2;  // rows of x per group (a multiple of 16); rows of a CTA of the cluster
-    int unit_log2, per_adapter;  // ranks that are loaded as one; units of one adapter, both matrices'
+    int unit_log2;               // ranks that are loaded as one
+    int per_adapter_log2;        // units of one adapter, both matrices'
     int tile, width;             // units of a tile; ranks of a row's landing place
     int splits, slots;           // CTAs of a cluster, each with a part of K; clusters of a group, which share its tiles
+    int loaders;                 // warps that share the units of the stages: not more than the ring has
     int stages, stage, smem;     // smem: the ring, the landing places and the adapters' scales
 };
 // T rows, L adapters of rank R on `matrices` matrices, K in stages of 64.
@@ -170,15 +181,16 @@ inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices, int sms) 
     p.groups = (int)(((int64_t)T + p.rows - 1) / p.rows);
     p.unit_log2 = R <= 16 ? 4 : R <= 32 ? 5 : R <= 64 ? 6 : 7;
     const int unit = 1 << p.unit_log2;
-    p.per_adapter = (R + unit - 1) / unit * matrices;
+    const int per_adapter = (R + unit - 1) / unit * matrices;  // 1, 2 or 4
+    p.per_adapter_log2 = per_adapter >> 1;
     const int steps = (K + kLowK - 1) / kLowK, here = T < p.rows ? T : p.rows;
     // Long inputs are prompts, whose groups have an adapter or two: a tile for each, and many stages.  Short ones
     // may have one to each row: eight units to a tile.
     const bool prompt = T > 1024;
-    const int64_t units = prompt ? p.per_adapter : (int64_t)(L < here ? L : here) * p.per_adapter;
+    const int64_t units = prompt ? per_adapter : (int64_t)(L < here ? L : here) * per_adapter;
     p.tile = kLowTile / unit < units ? kLowTile / unit : (int)units;
     const int tiles = (int)((units + p.tile - 1) / p.tile);  // of a group, as far as that goes
-    p.width = (p.per_adapter < p.tile ? p.per_adapter : p.tile) * unit;
+    p.width = (per_adapter < p.tile ? per_adapter : p.tile) * unit;
     p.stage = (p.tile * unit + p.rows) * 128;
     // A round of tiles takes 4 us besides its stages, and those what an SM's share of the L2 rate allows (106 GB/s).
     float best = 1e30f;
@@ -197,9 +209,13 @@ inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices, int sms) 
     p.own_log2 = 2;
     while ((p.splits << p.own_log2) < p.rows) ++p.own_log2;
     const int landing = (p.splits << p.own_log2) * p.width * 4 + kLowRows * 4, share = (steps + p.splits - 1) / p.splits;
-    p.stages = (kCtaSmemMax - 1024 - landing) / p.stage;
+    // beside the layer's launch where that is of few rows and does not take all of an SM
+    const int room = p.groups > 1 ? kCtaSmemMax : kLowSmemFew;
+    p.stages = (room - 1024 - landing) / p.stage;
+    p.stages = p.stages < 2 ? 2 : p.stages;
     p.stages = p.stages < kLowStages ? p.stages : kLowStages;
     p.stages = p.stages < share ? p.stages : share;
+    p.loaders = p.stages * p.tile < kLowLoaders ? p.stages * p.tile : kLowLoaders;
     p.smem = p.stages * p.stage + landing + 1024;
     // the MMA reads 128 rows of a stage, however few of them are ranks
     const int reach = (p.stages - 1) * p.stage + kLowTile * 128 + 1024, least = smem_for_columns(tmem_columns(p.rows));

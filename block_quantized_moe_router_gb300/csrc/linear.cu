@@ -65,10 +65,10 @@ struct LinArgs {
 
 struct AdaptArgs : LinArgs {
     int L, R;
-    int planes[2];    // many rows: the first of each matrix's two planes of v, -1 for a matrix without adapters
-    int64_t ldb, sb;  // elements between rows of b and between its adapters
-    const void* b[2];  // nullptr for a matrix without adapters
-    const float* v[2]; // few rows: [T][R]
+    int planes[2];           // of v: the first of each matrix's two (hi, lo), -1 for a matrix without adapters
+    int64_t plane, ldb, sb;  // elements of a plane of v; between rows of b and between its adapters
+    const void* b[2];        // nullptr for a matrix without adapters
+    const uint16_t* v;
     const int32_t* ids;
 };
 
@@ -278,62 +278,95 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 
-// What the addends of `rows` weight rows from feature n0 on (those from `half` on of the second matrix) and `cols` rows of
-// x from t on read of b comes to L2, by 128-byte lines.
-__device__ __forceinline__ void prefetch_adapters(const AdaptArgs& a, int rows, int half, int n0, int64_t t, int cols, int warp, int warps) {
-    const int of_line = a.ldb >= 64 ? 1 : 64 / (int)a.ldb;  // rows of b in a line
-    for (int c = warp; c < cols; c += warps) {
-        const int j = adapter_of(a, t + c);
-        if (j < 0) continue;
-        for (int r = (threadIdx.x & 31) * of_line; r < rows; r += 32 * of_line) {
-            const int m = r >= half, n = n0 + r - (m ? half : 0);
-            if (n >= a.N || !a.b[m]) continue;
-            const uint16_t* row = static_cast<const uint16_t*>(a.b[m]) + j * a.sb + n * a.ldb;
-            for (int k = 0; k < a.R; k += 64) prefetch_l2(row + k);
-        }
-    }
-}
-
-// Eight 16-bit values.
-__device__ __forceinline__ void unpack8(const uint4& w, bool f16, float (&f)[8]) {
-    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+// The addends v b[j]^T of `rows` weight rows (a multiple of 16; from feature n0 on, those from `half` on of the second
+// matrix) and `own` columns (a multiple of 4; rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
+//
+// By mma.sync, a column's adapter at a time: A is 16 rows of its b, B the low-rank products of the eight columns of the
+// group, and of D only that column is kept, so that a column sees no other one's adapter.  That leaves seven eighths of
+// an MMA unused and still takes half the instructions of plain FMAs, which count: few warps run here, each through code that
+// it meets for the first time.  K may be in any order, so that one 16-byte load a lane serves two MMAs (ranks 8 c to
+// 8 c + 7 for lane c of four, the first four of each in the first MMA).
+//
+// While the launch before computes v, the first items are done without it, which brings these instructions to the SM and
+// their rows of b; those of the others are brought to L2.
+__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, float* dst, int pitch, int rows, int half, int own, int n0, int64_t t,
+                                                int cols) {
+    constexpr int kWarps = 6;
+    const int warp = (int)(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+    const int blocks = rows / 16, items = (own + 7) / 8 * blocks;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        if (round == 1) pdl_wait();  // v
+#pragma unroll 1
+        for (int item = warp; item < items; item += kWarps) {
+            const int r0 = item % blocks * 16, c0 = item / blocks * 8, m = r0 >= half;
+            const int n = n0 + r0 - (m ? half : 0) + g;  // this lane's features: n and n + 8
+            const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb + 8 * c4;
+            const int id = a.b[m] && lane < 8 && c0 + lane < cols ? adapter_of(a, t + c0 + lane) : -1;  // column `lane`
+            if (round == 0 && item >= kWarps) {
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const int j = __shfl_sync(0xffffffffu, id, c);
+                    if (j >= 0 && n < a.N)  // a line of 64 ranks a lane
+                        for (int r = 64 * c4; r < a.R; r += 256) {
+                            prefetch_l2(b - 8 * c4 + j * a.sb + r);
+                            if (n + 8 < a.N) prefetch_l2(b - 8 * c4 + 8 * a.ldb + j * a.sb + r);
+                        }
+                }
+                continue;
+            }
+            const bool mine = __shfl_sync(0xffffffffu, id, g) >= 0 && round == 1;
+            const uint16_t* const v = a.v + a.planes[m] * a.plane + (t + c0 + g) * a.R + 8 * c4;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int r = 0; r < a.R; r += 32) {
+                const bool ranks = r + 8 * c4 < a.R;
+                uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+                if (mine && ranks) {
+                    hi = __ldcg(reinterpret_cast<const uint4*>(v + r));
+                    lo = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + r));
+                }
+#pragma unroll 1
+                for (int first = 0; first < 8; first += 4) {  // four columns' loads in flight
+                    if (c0 + first >= cols) break;
+                    uint4 p[4], q[4];
+                    int j[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (f16) {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-            f[2 * i] = h.x;
-            f[2 * i + 1] = h.y;
-        } else {
-            f[2 * i] = __uint_as_float(p[i] << 16);
-            f[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
-        }
-    }
-}
-
-// s += the addends v b[j]^T of feature n for up to 4 rows from t on; v (of the first row, shared memory) is the same for
-// all lanes, and a row of b is loaded once for neighbouring rows with one adapter.  Plain FMAs: with an adapter to each
-// row an MMA has one useful column of eight, and what it takes to hand it that column is more than these.
-__device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int n, int64_t t, int rows, const float* v, float (&s)[4]) {
-    int j[4];
+                    for (int c = 0; c < 4; ++c) {
+                        j[c] = __shfl_sync(0xffffffffu, id, first + c);
+                        p[c] = q[c] = make_uint4(0u, 0u, 0u, 0u);
+                        if (j[c] >= 0 && ranks) {
+                            const uint16_t* const from = b + j[c] * a.sb + r;
+                            if (n < a.N) p[c] = __ldg(reinterpret_cast<const uint4*>(from));
+                            if (n + 8 < a.N) q[c] = __ldg(reinterpret_cast<const uint4*>(from + 8 * a.ldb));
+                        }
+                    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) j[i] = i < rows ? adapter_of(a, t + i) : -1;
-    const uint16_t* b = static_cast<const uint16_t*>(a.b[m]) + (int64_t)min(n, a.N - 1) * a.ldb;  // what a lane behind N computes goes nowhere
-#pragma unroll 2
-    for (int r = 0; r < a.R; r += 8) {
-        uint4 w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (i > 0 && j[i] == j[i - 1]) w[i] = w[i - 1];
-            else if (j[i] >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>(b + j[i] * a.sb + r));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (j[i] < 0) continue;
-            float f[8];
-            unpack8(w[i], a.f16, f);
-            const float4 p = *reinterpret_cast<const float4*>(v + i * a.R + r), q = *reinterpret_cast<const float4*>(v + i * a.R + r + 4);
-            s[i] += p.x * f[0] + p.y * f[1] + p.z * f[2] + p.w * f[3] + q.x * f[4] + q.y * f[5] + q.z * f[6] + q.w * f[7];
+                    for (int c = 0; c < 4; ++c) {
+                        if (j[c] < 0) continue;
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (a.f16) {
+                            mma_f16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, hi.x, hi.y);
+                            mma_f16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, hi.z, hi.w);
+                            mma_f16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, lo.x, lo.y);
+                            mma_f16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, lo.z, lo.w);
+                        } else {
+                            mma_bf16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, hi.x, hi.y);
+                            mma_bf16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, hi.z, hi.w);
+                            mma_bf16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, lo.x, lo.y);
+                            mma_bf16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, lo.z, lo.w);
+                        }
+                        if (c4 == (first + c) / 2) {  // columns 2 c4 and 2 c4 + 1 are this lane's
+                            sum[c & 1] += d[c & 1];
+                            sum[2 + (c & 1)] += d[2 + (c & 1)];
+                        }
+                    }
+                }
+            }
+            if (c0 + 2 * c4 < own) {
+                *reinterpret_cast<float2*>(dst + (r0 + g) * pitch + c0 + 2 * c4) = make_float2(sum[0], sum[1]);
+                *reinterpret_cast<float2*>(dst + (r0 + g + 8) * pitch + c0 + 2 * c4) = make_float2(sum[2], sum[3]);
+            }
         }
     }
 }
@@ -390,8 +423,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
-    // with adapters: v of this CTA's columns, [matrix][column][rank]
-    [[maybe_unused]] float* const v_s = landing + (int)splits * F::kW * pitch;
+    // with adapters: the addends of this CTA's columns
+    [[maybe_unused]] float* const addends = landing + (direct ? 0 : (int)splits * F::kW * pitch);
     const int steps = k_end - k_begin;
     // The elected lane's role is all that its warp does until the lane is done: the rest of the warp waits at the end of
     // the role, so that nothing it might run shares the warp's uniform registers with the lane's copies and MMAs
@@ -466,14 +499,7 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
         if constexpr (ADAPT) {
-            prefetch_adapters(a, F::kW, per_cta, n0, (int64_t)t0 + my_c0, my_cols, warp - 2, 6);
-            pdl_wait();  // v
-            for (int m = 0; m < 2; ++m)
-                if (a.b[m]) {
-                    const float4* from = reinterpret_cast<const float4*>(a.v[m] + ((int64_t)t0 + my_c0) * a.R);
-                    float4* to = reinterpret_cast<float4*>(v_s + m * own * a.R);
-                    for (int i = threadIdx.x - 64; i < my_cols * a.R / 4; i += 192) to[i] = __ldcg(from + i);
-                }
+            adapter_addends(a, addends, pitch, F::kW, per_cta, own, n0, (int64_t)t0 + my_c0, my_cols);
         }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
@@ -495,10 +521,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                 if constexpr (ADAPT) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        float add[4] = {};
-                        add_adapters(a, 0, n, (int64_t)t0 + c + i, rows - i, v_s + (c + i) * a.R, add);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) z[i + k] += add[k];
+                        const float4 p = *reinterpret_cast<const float4*>(addends + row * pitch + c + i);
+                        z[i] += p.x; z[i + 1] += p.y; z[i + 2] += p.z; z[i + 3] += p.w;
                     }
                 }
                 if (n < a.N) finish_feature(a, (int64_t)t0 + c, rows, n, z, z, rw);
@@ -532,21 +556,7 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
         if (a.res && item < items && n < a.N) load_residual(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, rw);
     };
     ahead(warp);
-    // an item's addends, the first one's before the parts have landed
-    float dz[4] = {}, du[4] = {};
-    const auto addends = [&](int item) {
-        if constexpr (ADAPT) {
-            const int n = n0 + (item & (blocks - 1)) * 32 + lane, c = (item >> shift) * 4;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dz[i] = du[i] = 0.f;
-            if (item >= items) return;
-            if (a.b[0]) add_adapters(a, 0, n, (int64_t)t0 + my_c0 + c, my_cols - c, v_s + c * a.R, dz);
-            if (a.b[1]) add_adapters(a, 1, n, (int64_t)t0 + my_c0 + c, my_cols - c, v_s + (own + c) * a.R, du);
-        }
-    };
-    cluster_arrive();
-    addends(warp);
-    cluster_wait();  // every part has landed
+    cluster_sync();  // every part has landed
     for (int item = warp; item < items; item += kFewThreads / 32) {
         const int r = (item & (blocks - 1)) * 32 + lane, c = (item >> shift) * 4;
         const float* src = landing + r * pitch + c;
@@ -554,8 +564,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
         ahead(item + kFewThreads / 32);
         float z[4] = {}, u[4] = {};
 #pragma unroll
-        for (int s = 0; s < kFewSplits / F::kCtas; ++s)
-            if (s < (int)splits) {
+        for (int s = 0; s < kFewSplits / F::kCtas + ADAPT; ++s)
+            if (s < (int)splits + ADAPT) {
                 const float4 p = *reinterpret_cast<const float4*>(src + s * F::kW * pitch);
                 z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
                 if (a.gated) {
@@ -563,16 +573,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                     u[0] += g.x; u[1] += g.y; u[2] += g.z; u[3] += g.w;
                 }
             }
-        if constexpr (ADAPT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[i] += dz[i];
-                u[i] += du[i];
-            }
-        }
         const int n = n0 + r;
         if (n < a.N) finish_feature(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z, u, now);
-        if (ADAPT && item + kFewThreads / 32 < items) addends(item + kFewThreads / 32);
     }
     __syncwarp();
     if (warp == 1) {
@@ -1105,17 +1107,14 @@ cudaError_t launch_clusters(K* kernel, int smem_max, std::atomic<uint64_t>& allo
     return cudaLaunchKernelEx(&cfg, kernel, m, a);
 }
 
-// Shared memory for v of one column.
-constexpr int adapter_column(int R, bool gated) { return R * (int)sizeof(float) * (gated ? 2 : 1); }
-
 template <bool PAIR, bool ADAPT>
-cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int splits, int N, int column, cudaStream_t st) {
+cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int splits, int N, cudaStream_t st) {
     using F = Few<PAIR>;
     const int per_tile = F::kW * F::kCtas / (a.gated ? 2 : 1), cluster = splits * F::kCtas;
     const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
     static std::atomic<uint64_t> allowed{0};
     return launch_clusters(linear_few_kernel<PAIR, ADAPT>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
-                           F::smem(a.rows_t, splits, a.stages, column), m, a, st);
+                           F::smem(a.rows_t, splits, a.stages, few_parts(splits, a.gated, ADAPT)), m, a, st);
 }
 
 template <bool ADAPT>
@@ -1131,9 +1130,7 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
     a.func = d.func; a.gated = w_mul != nullptr; a.f16 = d.dtype == MOE_DT_F16;
     a.ldr = d.ldr; a.ldo = d.ldo;
     a.bias = bias; a.bias_mul = bias_mul; a.res = residual; a.out = out; a.status = status;
-    int column = 0;  // bytes per column of few rows
-    if constexpr (ADAPT) column = adapter_column(ad->R, w_mul != nullptr);
-    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms, column);
+    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms, ADAPT);
     MapsOf<ADAPT> m{};
     // rows of W per box, and rows of x
     const int box_w = plan.few ? (plan.pair ? 64 : 128) / (a.gated ? 2 : 1) : plan.width / 2;
@@ -1147,11 +1144,11 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
         a.b[0] = ad->b; a.b[1] = ad->b_mul;
         a.planes[0] = ad->a ? 0 : -1;
         a.planes[1] = ad->a_mul ? (ad->a ? 2 : 0) : -1;
-        for (int i = 0; i < 2; ++i)
-            a.v[i] = reinterpret_cast<const float*>(static_cast<const char*>(v) + (a.planes[i] > 0 ? a.planes[i] * p.plane : 0));
+        a.plane = (int64_t)(p.plane / sizeof(uint16_t));
+        a.v = static_cast<const uint16_t*>(v);
         a.ids = ad->ids;
         if (!plan.few) {
-            if (!encode_stack16(&m.v_low, v, ad->R, d.T, p.matrices * 2, ad->R, (int64_t)(p.plane / 2), 128)) return cudaErrorInvalidValue;
+            if (!encode_stack16(&m.v_low, v, ad->R, d.T, p.matrices * 2, ad->R, a.plane, 128)) return cudaErrorInvalidValue;
             for (int i = 0; i < 2; ++i)
                 if (a.b[i] && !encode_stack16(&m.b[i], a.b[i], ad->R, d.N, ad->L, ad->ldb, a.sb, box_w)) return cudaErrorInvalidValue;
         }
@@ -1159,7 +1156,7 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
     if (plan.few) {
         a.rows_t = plan.rows_t;
         a.stages = plan.stages;
-        return plan.pair ? launch_few<true, ADAPT>(m, a, plan.splits, d.N, column, st) : launch_few<false, ADAPT>(m, a, plan.splits, d.N, column, st);
+        return plan.pair ? launch_few<true, ADAPT>(m, a, plan.splits, d.N, st) : launch_few<false, ADAPT>(m, a, plan.splits, d.N, st);
     }
     // TMA addresses rows that start at multiples of 16 bytes, and writes whole ones: where a row ends inside 16 bytes, what lies
     // behind it is written too
@@ -1180,13 +1177,6 @@ cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w
                           const float* bias, const float* bias_mul, const void* residual, void* out,
                           int32_t* status, cudaStream_t st) {
     return launch_layer<false>(d, x, w, w_mul, bias, bias_mul, residual, out, nullptr, nullptr, status, st);
-}
-cudaError_t adapted_linear_halves(const moe_linear_desc& d, int R, bool gated, bool& halves) {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    halves = !plan_linear(d.T, d.N, (d.K + kLinK - 1) / kLinK, gated, sms, adapter_column(R, gated)).few;
-    return err;
 }
 cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                   const void* w_mul, const float* bias, const float* bias_mul, const void* residual,

@@ -1,5 +1,5 @@
-"""The launches of the layer with adapters, over all kinds of sizes, without a GPU: tiles, stages and shared memory
-within their limits, with the low-rank products beside the parts of K, and those of the products themselves, and columns of tensor memory covered."""
+"""The launches of the layer with adapters and of its low-rank products, over all kinds of sizes, without a GPU: tiles,
+stages and shared memory within their limits, with the adapters' addends beside the parts of K, and columns of tensor memory covered."""
 import os
 import shutil
 import subprocess
@@ -17,12 +17,13 @@ using namespace moe;
 
 static long cases = 0, wrong = 0;
 template <bool PAIR>
-static void few(int T, int N, int K, const LinPlan& p, int column) {
+static void few(int T, int N, int K, const LinPlan& p, bool gated) {
     using F = Few<PAIR>;
     ++cases;
-    const int own = F::own(p.rows_t, p.splits), smem = F::smem(p.rows_t, p.splits, p.stages, column);
-    const int inner = 1024 + p.stages * F::stage(p.rows_t) + p.splits * F::kW * F::pitch(own) * 4 + own * column;
-    if (inner > smem || smem > kCtaSmemMax || !columns_covered(smem, F::columns(p.rows_t)) || p.rows_t > F::kRows ||
+    const int own = F::own(p.rows_t, p.splits), parts = few_parts(p.splits, gated, true);
+    const int smem = F::smem(p.rows_t, p.splits, p.stages, parts);
+    const int inner = 1024 + p.stages * F::stage(p.rows_t) + parts * F::kW * F::pitch(own) * 4;
+    if (parts < 1 || inner > smem || smem > kCtaSmemMax || !columns_covered(smem, F::columns(p.rows_t)) || p.rows_t > F::kRows ||
         p.rows_t % F::kStep || p.stages < 2 || p.stages > kFewStages || p.splits * F::kCtas > kFewSplits) {
         ++wrong;
         printf("plan of %d %d %d: %d bytes of %d\n", T, N, K, inner, smem);
@@ -36,12 +37,11 @@ int main() {
     for (int T : Ts)
         for (int N : Ns)
             for (int K : Ks)
-                for (int R : Rs)
                     for (int gated = 0; gated < 2; ++gated) {
-                        const int nk = (K + kLinK - 1) / kLinK, column = R * 4 * (gated + 1);
-                        const LinPlan p = plan_linear(T, N, nk, gated, 152, column);
-                        if (p.few && p.pair) few<true>(T, N, K, p, column);
-                        if (p.few && !p.pair) few<false>(T, N, K, p, column);
+                        const int nk = (K + kLinK - 1) / kLinK;
+                        const LinPlan p = plan_linear(T, N, nk, gated, 152, true);
+                        if (p.few && p.pair) few<true>(T, N, K, p, gated);
+                        if (p.few && !p.pair) few<false>(T, N, K, p, gated);
                         if (!p.few && p.width != 128 && p.width != 192 && p.width != 256) ++wrong;
                     }
     for (int T : Ts)
@@ -56,11 +56,12 @@ int main() {
                         const int reach = 1024 + (p.stages - 1) * p.stage + 128 * 128;
                         const int unit = 1 << p.unit_log2;
                         const bool units = unit >= 16 && p.tile >= 1 && p.tile * unit <= kLowTile && !(p.width & (p.width - 1)) && p.width <= p.tile * unit &&
-                                           p.per_adapter * unit >= R * matrices && (p.per_adapter > p.tile || p.width == p.per_adapter * unit);
+                                           (1 << p.per_adapter_log2) * unit >= R * matrices && ((1 << p.per_adapter_log2) > p.tile || p.width == (1 << p.per_adapter_log2) * unit);
                         const bool sizes = p.rows % 16 == 0 && p.rows >= 16 && p.rows <= kLowRows && (long)p.rows * p.groups >= T &&
                                            (p.splits << p.own_log2) >= p.rows && p.own_log2 >= 2;
                         const bool ring = p.stages >= 1 && p.stages <= kLowStages && p.splits >= 1 && p.splits <= kLowSplits &&
-                                          p.splits <= steps && p.slots >= 1 && p.slots <= 65535;
+                                          p.splits <= steps && p.slots >= 1 && p.slots <= 65535 &&
+                                          p.loaders >= 1 && p.loaders <= kLowLoaders && p.loaders <= p.stages * p.tile;
                         if (sizes && ring && units && reach <= p.smem && inner <= p.smem && p.smem <= kCtaSmemMax && columns_covered(p.smem, tmem_columns(p.rows))) continue;
                         if (++wrong <= 20) printf("products of %d rows, K %d, %d adapters of %d, %d: %d bytes of %d\n", T, K, L, R, matrices, inner, p.smem);
                     }
