@@ -311,7 +311,7 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
     LowMaps m{};
     if (!encode_rows16(&m.x, x, d.K, d.T, d.ldx, p.rows, kLowK)) return cudaErrorInvalidValue;
     for (int i = 0; i < products.matrices; ++i)
-        if (!encode_stack16(&m.a[i], of[i], d.K, ad.R, ad.L, ad.lda, ad.L > 1 ? ad.sa : ad.R * ad.lda, 1 << p.unit_log2)) return cudaErrorInvalidValue;
+        if (!encode_stack16(&m.a[i], of[i], d.K, ad.R, ad.L, ad.lda, ad.L > 1 ? ad.sa : ad.R * ad.lda, 1 << p.unit_log2, kLowK)) return cudaErrorInvalidValue;
     LowArgs g{};
     g.T = d.T; g.R = ad.R; g.L = ad.L; g.matrices = products.matrices; g.steps = (d.K + kLowK - 1) / kLowK; g.f16 = d.dtype == MOE_DT_F16;
     g.rows = p.rows; g.own_log2 = p.own_log2; g.unit_log2 = p.unit_log2; g.tile = p.tile; g.width = p.width; g.per_adapter_log2 = p.per_adapter_log2; g.slots = p.slots; g.stages = p.stages; g.stage = p.stage; g.loaders = p.loaders;

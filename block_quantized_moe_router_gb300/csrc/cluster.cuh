@@ -129,7 +129,7 @@ struct RingPos {
 };
 
 // Tensor map of 16-bit elements in two dimensions or three (strides of the outer ones in elements): boxes of
-// box_cols columns (64 or 32: 128 or 64 bytes, swizzled over as many) x box_rows rows of one matrix; what lies
+// box_cols columns (64, 32 or 16: 128, 64 or 32 bytes, swizzled over as many) x box_rows rows of one matrix; what lies
 // beyond reads as zero.
 inline bool encode_boxes16(CUtensorMap* m, const void* base, int rank, const int64_t (&size)[3], int64_t ld, int64_t step,
                            int box_rows, int box_cols) {
@@ -148,7 +148,7 @@ inline bool encode_boxes16(CUtensorMap* m, const void* base, int rank, const int
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // [rows][cols], rows ld apart.
@@ -165,10 +165,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
         "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar)))
         : "memory");
 }
-// [count][rows][cols], rows ld and matrices step apart: boxes of 64 columns.
+// [count][rows][cols], rows ld and matrices step apart.
 inline bool encode_stack16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
-                           int64_t step, int box_rows) {
-    return encode_boxes16(m, base, 3, {cols, rows, count}, ld, step, box_rows, 64);
+                           int64_t step, int box_rows, int box_cols) {
+    return encode_boxes16(m, base, 3, {cols, rows, count}, ld, step, box_rows, box_cols);
 }
 
 }  // namespace moe

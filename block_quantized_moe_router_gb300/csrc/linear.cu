@@ -65,6 +65,8 @@ struct LinArgs {
 
 struct AdaptArgs : LinArgs {
     int L, R;
+    int ranks, batch;        // many rows: ranks of a stage, adapters that share one
+    uint32_t ranks_layout;   // and how their rows are swizzled
     int planes[2];           // of v: the first of each matrix's two (hi, lo), -1 for a matrix without adapters
     int64_t plane, ldb, sb;  // elements of a plane of v; between rows of b and between its adapters
     const void* b[2];        // nullptr for a matrix without adapters
@@ -653,10 +655,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
 
 // An adapter of a tile, and the tile's rows that have another one or none; id -1 behind the last.
 struct TileAdapter {
+    uint2 off[4];
     int id;
-    uint32_t off[8];
 };
-constexpr int kTileAdapters = 8;  // of the ring that hands them on
+constexpr int kTileAdapters = 14;  // of the ring that hands them on
+constexpr int kTileBatch = 7;      // that share a stage at most: two such batches are under way
 
 template <bool ADAPT>
 __global__ void __launch_bounds__(kManyThreads<ADAPT>, 1)
@@ -745,36 +748,46 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                     }
                 }
                 if constexpr (ADAPT) {
-                    // Stages of 64 ranks: hi and lo of the rows, and the adapter's rows of b.  In the gated form a
-                    // CTA's half of the columns belongs to one matrix: for the other's adapters it takes zeros,
-                    // from behind row N.
-                    for (bool more = !abort_flag; more; list.next(kTileAdapters)) {
-                        if (!mbar_wait_suspended(&listed[list.slot], list.parity)) {
-                            give_up();
-                            break;
+                    // Stages of up to 64 ranks: hi and lo of the rows, and the rows of b of as many adapters as have room.
+                    // In the gated form a CTA's half of the columns belongs to one matrix: for the other's adapters it
+                    // takes zeros, from behind row N.
+                    const int row_bytes = a.ranks * 2, slot = 128 * row_bytes;
+                    for (bool more = !abort_flag; more;) {
+                        int n = 0;
+                        for (RingPos of = list; n < a.batch; ++n, of.next(kTileAdapters)) {
+                            if (!mbar_wait_suspended(&listed[of.slot], of.parity)) {
+                                give_up();
+                                n = 0;
+                                more = false;
+                                break;
+                            }
+                            if (tile_adapters[of.slot].id < 0) break;
                         }
-                        const int j = tile_adapters[list.slot].id;
-                        mbar_arrive(&taken[list.slot]);
-                        more = j >= 0;
-                        if (more) pdl_wait();  // v
-                        for (int m = 0; m < 2 && more; ++m) {
-                            if (a.planes[m] < 0) continue;
+                        if (!more) break;
+                        more = n == a.batch;
+                        if (n > 0) pdl_wait();  // v
+                        for (int m = 0; m < 2; ++m) {
+                            if (a.planes[m] < 0 || n == 0) continue;
                             const int y = a.gated && m != rank ? a.N : n0;
-                            for (int r = 0; r < a.R && more; r += kLinK, ++it, at.next(kManyStages)) {
+                            for (int r = 0; r < a.R; r += a.ranks, ++it, at.next(kManyStages)) {
                                 const int s = at.slot;
                                 if (!mbar_wait_suspended(&empty[s], at.parity ^ 1)) {
                                     give_up();
+                                    m = 2;
                                     more = false;
                                     break;
                                 }
                                 const uint32_t base = smem_u32(smem + s * kManyStageBytes);
-                                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (2 * kLinA + half * 128));
+                                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (2 * slot + n * half * row_bytes));
                                 const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
                                 tma_load_pair_3d(base, &maps.v_low, r, t0, a.planes[m], bar);
-                                tma_load_pair_3d(base + kManyHalf, &maps.v_low, r, t0, a.planes[m] + 1, bar);
-                                tma_load_pair_3d(base + kLinA, &maps.b[m], r, y, j, bar);
+                                tma_load_pair_3d(base + slot, &maps.v_low, r, t0, a.planes[m] + 1, bar);
+                                RingPos of = list;
+                                for (int i = 0; i < n; ++i, of.next(kTileAdapters))
+                                    tma_load_pair_3d(base + (2 + i) * slot, &maps.b[m], r, y, tile_adapters[of.slot].id, bar);
                             }
                         }
+                        for (int i = n + (n < a.batch); i > 0; --i, list.next(kTileAdapters)) mbar_arrive(&taken[list.slot]);
                     }
                 }
             }
@@ -814,33 +827,53 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                     tc_commit_pair(&empty[s], 3);
                 }
                 if constexpr (ADAPT) {
-                    for (bool more = !abort_flag; more; list.next(kTileAdapters)) {
-                        if (!mbar_wait_suspended(&listed[list.slot], list.parity)) {
-                            give_up();
-                            break;
+                    const int row_bytes = a.ranks * 2;
+                    const uint64_t slot = (uint64_t)(128 * row_bytes) >> 4;
+                    for (bool more = !abort_flag; more;) {  // the same batches
+                        int n = 0;
+                        for (RingPos of = list; n < a.batch; ++n, of.next(kTileAdapters)) {
+                            if (!mbar_wait_suspended(&listed[of.slot], of.parity)) {
+                                give_up();
+                                n = 0;
+                                more = false;
+                                break;
+                            }
+                            if (tile_adapters[of.slot].id < 0) break;
                         }
-                        const TileAdapter of = tile_adapters[list.slot];
-                        mbar_arrive(&taken[list.slot]);
-                        more = of.id >= 0;
-                        for (int m = 0; m < 2 && more; ++m) {
-                            if (a.planes[m] < 0) continue;
-                            for (int r = 0; r < a.R && more; r += kLinK, ring.next(kManyStages)) {
+                        if (!more) break;
+                        more = n == a.batch;
+                        for (int m = 0; m < 2; ++m) {
+                            if (a.planes[m] < 0 || n == 0) continue;
+                            for (int r = 0; r < a.R; r += a.ranks, ring.next(kManyStages)) {
                                 const int s = ring.slot;
                                 if (!mbar_wait_suspended(&full[s], ring.parity)) {
                                     give_up();
+                                    m = 2;
                                     more = false;
                                     break;
                                 }
                                 tc_fence_after();
-                                const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 1024, kLayoutSw128);
-                                for (int k = 0; k < kLinK && r + k < a.R; k += 16) {  // 32 bytes along the swizzled row
-                                    const uint64_t hi = ad + (k >> 3);
-                                    mma_f16kind_lanes(tmem + 256 * b, hi, hi + (kLinA >> 4), idesc, of.off);
-                                    mma_f16kind_lanes(tmem + 256 * b, hi + (kManyHalf >> 4), hi + (kLinA >> 4), idesc, of.off);
+                                const uint64_t ad = smem_desc(smem_u32(smem + s * kManyStageBytes), 16, 8 * row_bytes, a.ranks_layout);
+                                const int slices = min(a.ranks, a.R - r + 15) >> 4;  // of 16 ranks: 32 bytes along the swizzled row
+                                RingPos of = list;
+                                for (int i = 0; i < n; ++i, of.next(kTileAdapters)) {
+                                    uint32_t off[8];
+#pragma unroll
+                                    for (int w = 0; w < 4; ++w) {
+                                        const uint2 p = tile_adapters[of.slot].off[w];
+                                        off[2 * w] = p.x;
+                                        off[2 * w + 1] = p.y;
+                                    }
+                                    for (int k = 0; k < slices; ++k) {
+                                        const uint64_t hi = ad + 2 * k, of_b = ad + (2 + i) * slot + 2 * k;
+                                        mma_f16kind_lanes(tmem + 256 * b, hi, of_b, idesc, off);
+                                        mma_f16kind_lanes(tmem + 256 * b, hi + slot, of_b, idesc, off);
+                                    }
                                 }
                                 tc_commit_pair(&empty[s], 3);
                             }
                         }
+                        for (int i = n + (n < a.batch); i > 0; --i, list.next(kTileAdapters)) mbar_arrive(&taken[list.slot]);
                     }
                 }
                 tc_commit_pair(&acc_full[b], 3);
@@ -912,13 +945,13 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                         go = false;
                         break;
                     }
-                    TileAdapter& to = tile_adapters[list.slot];
+                    uint32_t off[8];
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        const uint32_t off = __ballot_sync(0xffffffffu, mine[w] != j);
-                        if (lane == 0) to.off[w] = off;
-                    }
+                    for (int w = 0; w < 8; ++w) off[w] = __ballot_sync(0xffffffffu, mine[w] != j);
                     if (lane == 0) {
+                        TileAdapter& to = tile_adapters[list.slot];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) to.off[w] = make_uint2(off[2 * w], off[2 * w + 1]);
                         to.id = j == 0x7fffffff ? -1 : j;
                         mbar_arrive(&listed[list.slot]);
                     }
@@ -1148,9 +1181,15 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
         a.v = static_cast<const uint16_t*>(v);
         a.ids = ad->ids;
         if (!plan.few) {
-            if (!encode_stack16(&m.v_low, v, ad->R, d.T, p.matrices * 2, ad->R, a.plane, 128)) return cudaErrorInvalidValue;
+            // Rows of 16, 32 or 64 ranks, swizzled over as many bytes: a stage has room for hi and lo of the rows and 14, 6
+            // or 2 adapters' rows of b (512 rows of 7168 x 2048 with 32 adapters of rank 16: 56 us with one to a stage)
+            a.ranks = ad->R <= 16 ? 16 : ad->R <= 32 ? 32 : 64;
+            a.batch = kManyStageBytes / (256 * a.ranks) - 2;
+            a.batch = a.batch < kTileBatch ? a.batch : kTileBatch;
+            a.ranks_layout = a.ranks == 16 ? kLayoutSw32 : a.ranks == 32 ? kLayoutSw64 : kLayoutSw128;
+            if (!encode_stack16(&m.v_low, v, ad->R, d.T, p.matrices * 2, ad->R, a.plane, 128, a.ranks)) return cudaErrorInvalidValue;
             for (int i = 0; i < 2; ++i)
-                if (a.b[i] && !encode_stack16(&m.b[i], a.b[i], ad->R, d.N, ad->L, ad->ldb, a.sb, box_w)) return cudaErrorInvalidValue;
+                if (a.b[i] && !encode_stack16(&m.b[i], a.b[i], ad->R, d.N, ad->L, ad->ldb, a.sb, box_w, a.ranks)) return cudaErrorInvalidValue;
         }
     }
     if (plan.few) {

@@ -181,7 +181,7 @@ __device__ __forceinline__ void tmem_st_wait() {
 
 // Shared-memory matrix descriptor: start address, leading/stride byte offsets (>> 4),
 // descriptor version 1 (bits 46-47), layout type in bits 61-63.
-enum : uint32_t { kLayoutNone = 0, kLayoutSw128 = 2 };
+enum : uint32_t { kLayoutNone = 0, kLayoutSw128 = 2, kLayoutSw64 = 4, kLayoutSw32 = 6 };
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes,
                                               uint32_t sbo_bytes, uint32_t layout) {
     uint64_t d = 0;
