@@ -133,6 +133,159 @@ sandwich_norm_kernel(BlockNormArgs a) {
     }
 }
 
+// Eight elements as fp32, from memory's form and back, rounded.
+__device__ __forceinline__ void to_floats(const uint4& p, float (&v)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void to_floats(const uint4& p, float (&v)[8], __half) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint32_t round_two(float lo, float hi, __nv_bfloat16) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+__device__ __forceinline__ uint32_t round_two(float lo, float hi, __half) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+// A vector of the stream: as it lies in memory, and as fp32.
+template <typename S>
+struct Raw {
+    uint4 v[sizeof(S) / 2];
+};
+template <typename S>
+__device__ __forceinline__ Raw<S> load_raw(const S* at) {
+    Raw<S> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(S) / 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(at)[i];
+    return r;
+}
+template <typename S>
+__device__ __forceinline__ void to_floats(const Raw<S>& r, float (&v)[8]) {
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.v[i].x); v[4 * i + 1] = __uint_as_float(r.v[i].y);
+            v[4 * i + 2] = __uint_as_float(r.v[i].z); v[4 * i + 3] = __uint_as_float(r.v[i].w);
+        }
+    } else {
+        to_floats(r.v[0], v, S{});
+    }
+}
+template <typename S>
+__device__ __forceinline__ void store_rounded(S* at, const float (&v)[8]) {
+    if constexpr (sizeof(S) == 4) {
+        reinterpret_cast<float4*>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(at) = make_uint4(round_two(v[0], v[1], S{}), round_two(v[2], v[3], S{}), round_two(v[4], v[5], S{}),
+                                                   round_two(v[6], v[7], S{}));
+    }
+}
+
+// Many long rows, all on their boundaries: a CTA per row, V vectors to a thread.  What bounds it are the instructions beside
+// the loads, of which each warp's sums are a large part: fewer warps to a row, as many rows to an SM as their registers allow
+// (us, 32768 rows of 7168 / 4096 of 4096 with an fp32 stream: V 1 by two rows to an SM 382 / 32.4, V 2 by three 293 / 32.4, V 4 by
+// four 269 / 36.4, by five 297 / 41; rows in pairs by CTAs that stay, the next ones brought ahead, 383 / 50).
+template <typename E, typename S, int V>
+__global__ void __launch_bounds__(V == 2 ? 512 : 256, V == 2 ? 3 : 4) sandwich_row_kernel(BlockNormArgs a) {
+    __shared__ float part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = blockIdx.x;
+    const E* const y = static_cast<const E*>(a.y) + t * a.ldy;
+    const S* const r = a.r ? static_cast<const S*>(a.r) + t * a.ldr : nullptr;
+    const float mean = 1.f / (float)a.H;
+    uint4 yv[V];
+    Raw<S> rv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+        yv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c0 < a.H) {
+            yv[i] = *reinterpret_cast<const uint4*>(y + c0);
+            if (r) rv[i] = load_raw(r + c0);
+        }
+    }
+    float g = a.row_gate ? __ldg(a.row_gate + t) : 1.f;
+    if (a.sigmoid) g = 1.f / (1.f + __expf(-g));
+    if (a.post) {
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f[8];
+            to_floats(yv[i], f, E{});
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq += f[j] * f[j];
+        }
+        g *= rsqrtf(row_sum<0>(sq, part[0], lane, warp) * mean + a.eps);
+    }
+    float s[V][8], sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+        if (c0 < a.H) {
+            float f[8];
+            to_floats(yv[i], s[i], E{});
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[i][j] *= g;
+            if (a.post) {
+                to_floats(*reinterpret_cast<const uint4*>(static_cast<const E*>(a.post) + c0), f, E{});
+                if (a.offset != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] += a.offset;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i][j] *= f[j];
+            }
+            if (a.gate) {
+                to_floats(*reinterpret_cast<const uint4*>(static_cast<const E*>(a.gate) + c0), f, E{});
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i][j] *= f[j];
+            }
+            if (r) {
+                to_floats(rv[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i][j] += a.scale * f[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq += s[i][j] * s[i][j];
+            store_rounded(static_cast<S*>(a.sum) + t * a.lds + c0, s[i]);
+        }
+    }
+    if (!a.out) return;
+    const float scale = rsqrtf(row_sum<0>(sq, part[1], lane, warp) * mean + a.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+        if (c0 < a.H) {
+            float f[8];
+            to_floats(*reinterpret_cast<const uint4*>(static_cast<const E*>(a.w) + c0), f, E{});
+            if (a.offset != 0.f) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] += a.offset;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[i][j] *= scale * f[j];
+            store_rounded(static_cast<E*>(a.out) + t * a.ldo + c0, s[i]);
+        }
+    }
+}
+
 constexpr int kBlockNormWarps = 8;
 
 template <typename E, typename S, int MODE, int VPT>
@@ -154,6 +307,13 @@ cudaError_t launch_mode(const BlockNormArgs& a, cudaStream_t st) {
         if (nvec <= 32) return launch_row_per_warp<E, S, MODE, 1>(a, st);
         if (nvec <= 64) return launch_row_per_warp<E, S, MODE, 2>(a, st);
         if (nvec <= 128) return launch_row_per_warp<E, S, MODE, 4>(a, st);
+    }
+    if constexpr (MODE == ROWS_ALIGNED) {
+        const auto row = [&](auto kernel, int v) {
+            return launch_pdl(kernel, dim3(a.T), dim3(((nvec + v - 1) / v + 31) / 32 * 32), st, a);
+        };
+        if (a.T >= 512 && nvec <= 1024)
+            return nvec > 512 && sizeof(S) == 2 ? row(sandwich_row_kernel<E, S, 4>, 4) : row(sandwich_row_kernel<E, S, 2>, 2);
     }
     if (nvec <= 1024) return launch_row_per_cta<E, S, MODE, 1>(a, nvec, st);
     if (nvec <= 2048 || MODE == ROWS_ALIGNED) return launch_row_per_cta<E, S, MODE, 2>(a, nvec, st);

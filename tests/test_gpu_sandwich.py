@@ -80,7 +80,7 @@ def _run(c, scale=1.0, eps=1e-6, sum_out=None, out=None):
 
 
 SIZES = [(1, 1), (1, 8), (2, 7), (3, 64), (1, 7168), (5, 2050), (31, 255), (32, 256), (33, 257), (40, 512), (64, 1000), (301, 2050),
-         (100, 1024), (7, 4099), (9, 8192), (3, 8200), (2, 16384), (2, 16383), (1, 12289), (5000, 64), (70001, 16), (600, 7168)]
+         (100, 1024), (7, 4099), (9, 8192), (3, 8200), (2, 16384), (2, 16383), (1, 12289), (5000, 64), (70001, 16), (600, 7168), (513, 1032), (520, 4096), (700, 5000), (512, 8192), (530, 2048)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
