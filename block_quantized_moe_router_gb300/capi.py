@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -113,12 +114,11 @@ def load_library(path: str = LIB_PATH):
     lib.moe_linear.restype = ctypes.c_int
     lib.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_desc), vp, vp, vp, vp, vp, vp]
     lib.moe_add_rms_norm.restype = ctypes.c_int
-    lib.moe_linear_adapters.argtypes = [ctypes.POINTER(moe_linear_desc), ctypes.POINTER(moe_adapter_desc), vp, vp,
-                                        vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.moe_linear_adapters.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]  # descriptors as bytes, or by reference
     lib.moe_linear_adapters.restype = ctypes.c_int
     lib.moe_adapter_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
     lib.moe_adapter_workspace_size.restype = ctypes.c_int
-    lib.moe_sandwich_norm.argtypes = [ctypes.POINTER(moe_sandwich_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_sandwich_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.moe_sandwich_norm.restype = ctypes.c_int
     lib.moe_workspace_size.argtypes = [ctypes.POINTER(moe_ffn_desc), i32, i32, ctypes.POINTER(sz)]
     lib.moe_workspace_size.restype = ctypes.c_int
@@ -337,7 +337,16 @@ def moe_add_rms_norm(x, weight, out, *, residual=None, sum_out=None, eps=1e-6, s
         raise MoeError(rc, "moe_add_rms_norm")
 
 
-def _adapters(t, dtype, L, rows, cols, dev, name):
+# The descriptors of the two calls below as bytes, in the order of the structures' fields: a ctypes structure of
+# as many costs 1 us of host time.
+_LINEAR = struct.Struct("5i4x4q")
+_ADAPTER = struct.Struct("2i4q6P")
+_SANDWICH = struct.Struct("5i3f4q")
+assert _LINEAR.size == ctypes.sizeof(moe_linear_desc) and _ADAPTER.size == ctypes.sizeof(moe_adapter_desc)
+assert _SANDWICH.size == ctypes.sizeof(moe_sandwich_desc)
+
+
+def _stack(t, dtype, L, rows, cols, dev, name):
     """Pointer, row and adapter stride of stacked adapter matrices [L][rows][cols]."""
     if t.dtype != dtype or t.shape != (L, rows, cols) or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor {(L, rows, cols)} on the current CUDA device, "
@@ -346,6 +355,17 @@ def _adapters(t, dtype, L, rows, cols, dev, name):
     if one != 1:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), (ld if rows > 1 else cols), step
+
+
+def _pair(a, b, dtype, L, R, N, K, dev, name):
+    """Pointers and strides of the adapters of one matrix, zeros without any."""
+    if a is None and b is None:
+        return 0, 0, None
+    if a is None or b is None:
+        raise ValueError(f"adapters need a{name} and b{name}")
+    pa, lda, sa = _stack(a, dtype, L, R, K, dev, "a" + name)
+    pb, ldb, sb = _stack(b, dtype, L, N, R, dev, "b" + name)
+    return pa, pb, (lda, sa, ldb, sb)
 
 
 def moe_adapter_workspace_size(T: int, R: int, matrices: int) -> int:
@@ -369,7 +389,7 @@ def moe_linear_adapters(x, w, out, ids, *, a=None, b=None, a_mul=None, b_mul=Non
     first = a if a is not None else a_mul
     if first is None or first.dim() != 3:
         raise ValueError("adapters must be given as a and b, or a_mul and b_mul, of three dimensions")
-    L, R = first.shape[:2]
+    L, R, _ = first.shape
     px, ldx = _rows(x, dt, T, K, dev, "x")
     pw, ldw = _rows(w, dt, N, K, dev, "w")
     po, ldo = _rows(out, dt, T, N, dev, "out")
@@ -381,26 +401,23 @@ def moe_linear_adapters(x, w, out, ids, *, a=None, b=None, a_mul=None, b_mul=Non
             raise ValueError("w_mul must have the row stride of w")
     if residual is not None:
         pr, ldr = _rows(residual, dt, T, N, dev, "residual")
-    ptr = {}
-    strides = {}
-    for name, t, rows, cols in (("a", a, R, K), ("b", b, N, R), ("a_mul", a_mul, R, K), ("b_mul", b_mul, N, R)):
-        if t is None:
-            ptr[name] = None
-            continue
-        ptr[name], ld, step = _adapters(t, dt, L, rows, cols, dev, name)
-        if strides.setdefault(name[0], (ld, step)) != (ld, step):
-            raise ValueError(f"{name} must have the strides of {name[0]}")
-    lda, sa = strides.get("a", (K, 0))
-    ldb, sb = strides.get("b", (R, 0))
+    pa, pb, strides = _pair(a, b, dt, L, R, N, K, dev, "")
+    pa_mul, pb_mul, strides_mul = _pair(a_mul, b_mul, dt, L, R, N, K, dev, "_mul")
+    if strides is None:
+        strides = strides_mul
+    elif strides_mul is not None and strides != strides_mul:
+        raise ValueError("a_mul and b_mul must have the strides of a and b")
     if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
-    d = moe_linear_desc(T, N, K, _DTYPES.get(dt, -1), func, ldx, ldw, ldr, ldo)
-    ad = moe_adapter_desc(L, R, lda, sa, ldb, sb, ptr["a"], ptr["b"], ptr["a_mul"], ptr["b_mul"],
-                          _tptr(scale, torch.float32, (L,), dev, "scale"), _tptr(ids, torch.int32, (T,), dev, "ids"))
+    if max(L, R, N, K, T) > 0x7FFFFFFF:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_linear_adapters")
     rc = (_lib or load_library()).moe_linear_adapters(
-        ctypes.byref(d), ctypes.byref(ad), px, pw, pm, _tptr(bias, torch.float32, (N,), dev, "bias"),
-        _tptr(bias_mul, torch.float32, (N,), dev, "bias_mul"), pr, po, workspace.data_ptr(), workspace.numel(),
-        _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
+        _LINEAR.pack(T, N, K, _DTYPES.get(dt, -1), func, ldx, ldw, ldr, ldo),
+        _ADAPTER.pack(L, R, *strides, pa, pb, pa_mul, pb_mul, _tptr(scale, torch.float32, (L,), dev, "scale") or 0,
+                      _tptr(ids, torch.int32, (T,), dev, "ids") or 0),
+        px, pw, pm, None if bias is None else _tptr(bias, torch.float32, (N,), dev, "bias"),
+        None if bias_mul is None else _tptr(bias_mul, torch.float32, (N,), dev, "bias_mul"), pr, po, workspace.data_ptr(),
+        workspace.numel(), None if dev_status is None else _tptr(dev_status, torch.int32, (1,), dev, "dev_status"), st)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_linear_adapters")
 
@@ -425,11 +442,15 @@ def moe_sandwich_norm(x, sum_out, *, residual=None, post_weight=None, gate=None,
         pr, ldr = _rows(residual, stream_dt, T, H, dev, "residual")
     if out is not None:
         po, ldo = _rows(out, dt, T, H, dev, "out")
-    d = moe_sandwich_desc(T, H, _DTYPES.get(dt, -1), stream_dt == torch.float32, row_sigmoid, eps, residual_scale,
-                          weight_offset, ldx, ldr, lds, ldo)
+    if max(T, H) > 0x7FFFFFFF:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_sandwich_norm")
     rc = (_lib or load_library()).moe_sandwich_norm(
-        ctypes.byref(d), px, pr, _tptr(post_weight, dt, (H,), dev, "post_weight"), _tptr(gate, dt, (H,), dev, "gate"),
-        _tptr(row_gate, torch.float32, (T,), dev, "row_gate"), _tptr(weight, dt, (H,), dev, "weight"), ps, po, st)
+        _SANDWICH.pack(T, H, _DTYPES.get(dt, -1), stream_dt == torch.float32, bool(row_sigmoid), eps, residual_scale,
+                       weight_offset, ldx, ldr, lds, ldo),
+        px, pr, None if post_weight is None else _tptr(post_weight, dt, (H,), dev, "post_weight"),
+        None if gate is None else _tptr(gate, dt, (H,), dev, "gate"),
+        None if row_gate is None else _tptr(row_gate, torch.float32, (T,), dev, "row_gate"),
+        None if weight is None else _tptr(weight, dt, (H,), dev, "weight"), ps, po, st)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_sandwich_norm")
 
