@@ -39,7 +39,8 @@ constexpr bool columns_covered(int smem, int columns) {
 constexpr int kLinK = 64;        // K elements per stage (128 bytes per row)
 constexpr int kFewSplits = 8;    // parts of K at most; CTAs of a cluster too (the portable cluster size)
 constexpr int kFewStages = 8;
-constexpr int kLowSmemFew = 76 * 1024;  // of a CTA that computes the low-rank products of few rows
+constexpr int kLowBeside = 16;          // rows whose low-rank products are computed beside the layer's weights
+constexpr int kLowSmemFew = 76 * 1024;  // of a CTA that computes them
 template <bool PAIR>
 struct Few {
     static constexpr int kRows = PAIR ? 256 : 128;   // rows of x per tile at most
@@ -52,12 +53,14 @@ struct Few {
     static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
     // A pair takes all of tensor memory, so that its CTAs hold the same columns.
     static constexpr int columns(int rows) { return PAIR ? kTmemColumns : tmem_columns(rows); }
-    // beside the stages: landing areas of `parts` parts
-    static constexpr int rest(int rows, int splits, int parts) { return parts * kW * pitch(own(rows, splits)) * 4 + 1024; }
-    static constexpr int rest(int rows, int splits) { return rest(rows, splits, splits); }
-    static constexpr int smem(int rows, int splits, int stages) { return smem(rows, splits, stages, splits); }
-    static constexpr int smem(int rows, int splits, int stages, int parts) {
-        const int need = stages * stage(rows) + rest(rows, splits, parts);
+    // beside the stages: landing areas of `parts` parts; with adapters 8 bytes for each of a CTA's columns, in eights
+    static constexpr int rest(int rows, int splits, int parts, bool adapters) {
+        return parts * kW * pitch(own(rows, splits)) * 4 + 1024 + (adapters ? (own(rows, splits) + 7) / 8 * 64 : 0);
+    }
+    static constexpr int rest(int rows, int splits) { return rest(rows, splits, splits, false); }
+    static constexpr int smem(int rows, int splits, int stages) { return smem(rows, splits, stages, splits, false); }
+    static constexpr int smem(int rows, int splits, int stages, int parts, bool adapters) {
+        const int need = stages * stage(rows) + rest(rows, splits, parts, adapters);
         const int least = smem_for_columns(columns(rows));
         return need > least ? need : least;
     }
@@ -100,19 +103,20 @@ void plan_few_tiles(int T, int N, int nk, bool gated, int sms, bool adapters, in
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
     const int64_t tiles = (int64_t)((T + rows - 1) / rows) * ((N + per_tile - 1) / per_tile) * F::kCtas;
     const float stage_kb = (float)F::stage(rows) / 1024.f;
-    // With adapters a CTA leaves room for one of the launch that computes their products, so that both run at once
-    const int smem_max = adapters ? kSmSmem - kLowSmemFew - 2 * (kSmemReserved + 256) : kCtaSmemMax;
+    // With adapters of a few rows a CTA leaves room for one of the launch that computes their products, so that both run at
+    // once.  With more rows that launch occupies the SMs and is done sooner alone (64 rows with an adapter each: 31 us, 35).
+    const int smem_max = adapters && T <= kLowBeside ? kSmSmem - kLowSmemFew - 2 * (kSmemReserved + 256) : kCtaSmemMax;
     for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
         const int kbs = (nk + splits - 1) / splits;
         // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
         // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
         const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
         const int parts = few_parts(splits, gated, adapters);
-        int stages = alone ? (smem_max - F::rest(rows, splits, parts)) / F::stage(rows) : 4;
+        int stages = alone ? (smem_max - F::rest(rows, splits, parts, adapters)) / F::stage(rows) : 4;
         const int most = PAIR ? kFewStages : alone ? 6 : 4;
         stages = stages < most ? stages : most;
         stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
-        const int smem = F::smem(rows, splits, stages, parts);
+        const int smem = F::smem(rows, splits, stages, parts, adapters);
         if (stages < 2 || smem > (F::columns(rows) == kTmemColumns ? kCtaSmemMax : smem_max)) continue;
         const int fit = kSmSmem / (smem + kSmemReserved + 256);  // CTAs an SM holds
         const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
@@ -209,8 +213,7 @@ inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices, int sms) 
     p.own_log2 = 2;
     while ((p.splits << p.own_log2) < p.rows) ++p.own_log2;
     const int landing = (p.splits << p.own_log2) * p.width * 4 + kLowRows * 4, share = (steps + p.splits - 1) / p.splits;
-    // beside the layer's launch where that is of few rows and does not take all of an SM
-    const int room = p.groups > 1 ? kCtaSmemMax : kLowSmemFew;
+    const int room = T > kLowBeside ? kCtaSmemMax : kLowSmemFew;
     p.stages = (room - 1024 - landing) / p.stage;
     p.stages = p.stages < 2 ? 2 : p.stages;
     p.stages = p.stages < kLowStages ? p.stages : kLowStages;

@@ -280,8 +280,8 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 
-// The addends v b[j]^T of `rows` weight rows (a multiple of 16; from feature n0 on, those from `half` on of the second
-// matrix) and `own` columns (a multiple of 4; rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
+// The addends v b[j]^T of ROWS weight rows (from feature n0 on, those from `half` on of the second matrix) and `own`
+// columns (a multiple of 4; rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
 //
 // By mma.sync, a column's adapter at a time: A is 16 rows of its b, B the low-rank products of the eight columns of the
 // group, and of D only that column is kept, so that a column sees no other one's adapter.  That leaves seven eighths of
@@ -289,92 +289,117 @@ constexpr int kFewThreads = 256;
 // it meets for the first time.  K may be in any order, so that one 16-byte load a lane serves two MMAs (ranks 8 c to
 // 8 c + 7 for lane c of four, the first four of each in the first MMA).
 //
-// While the launch before computes v, the first items are done without it, which brings these instructions to the SM and
-// their rows of b; those of the others are brought to L2.
-__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, float* dst, int pitch, int rows, int half, int own, int n0, int64_t t,
-                                                int cols) {
-    constexpr int kWarps = 6;
+// Steps of 16 rows, 4 columns and 32 ranks; the next step's loads are under way while one is computed, the first one's while
+// the launch before computes v.  What all others read of b is brought to L2 by then.
+struct AddendLoads {
+    uint4 p[4], q[4];  // of b: rows g and g + 8
+    uint4 hi, lo;      // of v
+};
+template <int ROWS>
+__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_s, float* dst, int pitch, int half, int own, int n0,
+                                                int64_t t, int cols) {
+    constexpr int kWarps = 6, kBlocks = ROWS / 16;
     const int warp = (int)(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
-    const int blocks = rows / 16, items = (own + 7) / 8 * blocks;
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {
-        if (round == 1) pdl_wait();  // v
-#pragma unroll 1
-        for (int item = warp; item < items; item += kWarps) {
-            const int r0 = item % blocks * 16, c0 = item / blocks * 8, m = r0 >= half;
-            const int n = n0 + r0 - (m ? half : 0) + g;  // this lane's features: n and n + 8
-            const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb + 8 * c4;
-            const int id = a.b[m] && lane < 8 && c0 + lane < cols ? adapter_of(a, t + c0 + lane) : -1;  // column `lane`
-            if (round == 0 && item >= kWarps) {
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const int j = __shfl_sync(0xffffffffu, id, c);
-                    if (j >= 0 && n < a.N)  // a line of 64 ranks a lane
-                        for (int r = 64 * c4; r < a.R; r += 256) {
-                            prefetch_l2(b - 8 * c4 + j * a.sb + r);
-                            if (n + 8 < a.N) prefetch_l2(b - 8 * c4 + 8 * a.ldb + j * a.sb + r);
-                        }
-                }
-                continue;
-            }
-            const bool mine = __shfl_sync(0xffffffffu, id, g) >= 0 && round == 1;
-            const uint16_t* const v = a.v + a.planes[m] * a.plane + (t + c0 + g) * a.R + 8 * c4;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int r = 0; r < a.R; r += 32) {
-                const bool ranks = r + 8 * c4 < a.R;
-                uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                if (mine && ranks) {
-                    hi = __ldcg(reinterpret_cast<const uint4*>(v + r));
-                    lo = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + r));
-                }
-#pragma unroll 1
-                for (int first = 0; first < 8; first += 4) {  // four columns' loads in flight
-                    if (c0 + first >= cols) break;
-                    uint4 p[4], q[4];
-                    int j[4];
+    const int items = (own + 7) / 8 * kBlocks;
+    // where each column's adapter begins, -1 for none
+    for (int c = threadIdx.x - 64; c < (own + 7) / 8 * 8; c += 32 * kWarps) {
+        const int j = c < cols ? adapter_of(a, t + c) : -1;
+        at_s[c] = j < 0 ? -1 : j * a.sb;
+    }
+    asm volatile("bar.sync 1, 192;" ::: "memory");  // the six warps
+    const auto matrix = [&](int item) { return (int)(item % kBlocks * 16 >= half); };
+    const auto feature = [&](int item) { return n0 + item % kBlocks * 16 - (matrix(item) ? half : 0); };
+    const int64_t eight = 8 * a.ldb;
+    const auto load_b = [&](int item, int r, int first, AddendLoads& to) {
+        const int m = matrix(item), n = feature(item) + g;  // this lane's features: n and n + 8
+        const bool in = item < items && a.b[m] && r + 8 * c4 < a.R, p_in = in && n < a.N, q_in = in && n + 8 < a.N;
+        const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb + 8 * c4 + r;
+        const int64_t* const at = at_s + item / kBlocks * 8 + first;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        j[c] = __shfl_sync(0xffffffffu, id, first + c);
-                        p[c] = q[c] = make_uint4(0u, 0u, 0u, 0u);
-                        if (j[c] >= 0 && ranks) {
-                            const uint16_t* const from = b + j[c] * a.sb + r;
-                            if (n < a.N) p[c] = __ldg(reinterpret_cast<const uint4*>(from));
-                            if (n + 8 < a.N) q[c] = __ldg(reinterpret_cast<const uint4*>(from + 8 * a.ldb));
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (j[c] < 0) continue;
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (a.f16) {
-                            mma_f16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, hi.x, hi.y);
-                            mma_f16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, hi.z, hi.w);
-                            mma_f16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, lo.x, lo.y);
-                            mma_f16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, lo.z, lo.w);
-                        } else {
-                            mma_bf16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, hi.x, hi.y);
-                            mma_bf16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, hi.z, hi.w);
-                            mma_bf16_16816(d, p[c].x, q[c].x, p[c].y, q[c].y, lo.x, lo.y);
-                            mma_bf16_16816(d, p[c].z, q[c].z, p[c].w, q[c].w, lo.z, lo.w);
-                        }
-                        if (c4 == (first + c) / 2) {  // columns 2 c4 and 2 c4 + 1 are this lane's
-                            sum[c & 1] += d[c & 1];
-                            sum[2 + (c & 1)] += d[2 + (c & 1)];
-                        }
-                    }
-                }
-            }
-            if (c0 + 2 * c4 < own) {
-                *reinterpret_cast<float2*>(dst + (r0 + g) * pitch + c0 + 2 * c4) = make_float2(sum[0], sum[1]);
-                *reinterpret_cast<float2*>(dst + (r0 + g + 8) * pitch + c0 + 2 * c4) = make_float2(sum[2], sum[3]);
+        for (int c = 0; c < 4; ++c) {
+            to.p[c] = to.q[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (!in) continue;
+            const int64_t from = at[c];
+            if (from >= 0 && p_in) to.p[c] = __ldg(reinterpret_cast<const uint4*>(b + from));
+            if (from >= 0 && q_in) to.q[c] = __ldg(reinterpret_cast<const uint4*>(b + from + eight));
+        }
+    };
+    const auto load_v = [&](int item, int r, AddendLoads& to) {
+        const int c = item / kBlocks * 8 + g, m = matrix(item);
+        to.hi = to.lo = make_uint4(0u, 0u, 0u, 0u);
+        if (item < items && a.b[m] && r + 8 * c4 < a.R && at_s[c] >= 0) {
+            const uint16_t* const v = a.v + a.planes[m] * a.plane + (t + c) * a.R + 8 * c4 + r;
+            to.hi = __ldcg(reinterpret_cast<const uint4*>(v));
+            to.lo = __ldcg(reinterpret_cast<const uint4*>(v + a.plane));
+        }
+    };
+    int item = warp, r = 0, first = 0;
+    AddendLoads now;
+    load_b(item, r, first, now);
+#pragma unroll 1
+    for (int i = warp; i < items; i += kWarps) {
+        const int c0 = i / kBlocks * 8, m = matrix(i), n = feature(i) + (lane & 15);
+        if (!a.b[m] || n >= a.N) continue;
+        const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
+#pragma unroll 1
+        for (int c = lane >> 4; c < min(8, cols - c0); c += 2)  // a lane's row of one column, every 64 ranks
+            if (at_s[c0 + c] >= 0)
+                for (int k = 0; k < a.R; k += 64) prefetch_l2(b + at_s[c0 + c] + k);
+    }
+    __syncwarp();
+    pdl_wait();  // v
+    load_v(item, r, now);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    while (item < items) {
+        const int c0 = item / kBlocks * 8, this_item = item, this_first = first;
+        first = first == 0 && cols > c0 + 4 ? 4 : 0;
+        if (first == 0) {
+            r += 32;
+            if (r >= a.R) {
+                r = 0;
+                item += kWarps;
             }
         }
+        AddendLoads next;
+        load_b(item, r, first, next);
+        load_v(item, r, next);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (at_s[c0 + this_first + c] < 0) continue;
+            const uint4 p = now.p[c], q = now.q[c];
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            if (a.f16) {
+                mma_f16_16816(d, p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
+                mma_f16_16816(d, p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
+                mma_f16_16816(d, p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
+                mma_f16_16816(d, p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
+            } else {
+                mma_bf16_16816(d, p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
+                mma_bf16_16816(d, p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
+                mma_bf16_16816(d, p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
+                mma_bf16_16816(d, p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
+            }
+            if (c4 == (this_first + c) / 2) {  // columns 2 c4 and 2 c4 + 1 are this lane's
+                sum[c & 1] += d[c & 1];
+                sum[2 + (c & 1)] += d[2 + (c & 1)];
+            }
+        }
+        if (item != this_item) {
+            if (c0 + 2 * c4 < own) {
+                float* const to = dst + (this_item % kBlocks * 16 + g) * pitch + c0 + 2 * c4;
+                *reinterpret_cast<float2*>(to) = make_float2(sum[0], sum[1]);
+                *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(sum[2], sum[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = 0.f;
+        }
+        now = next;
     }
 }
 
 template <bool PAIR, bool ADAPT>
-__global__ void __launch_bounds__(kFewThreads, ADAPT ? 3 : 4)
+__global__ void __launch_bounds__(kFewThreads, ADAPT ? 2 : 4)
 linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_constant__ ArgsOf<ADAPT> a) {
     using F = Few<PAIR>;
     extern __shared__ uint8_t lin_smem[];
@@ -425,7 +450,7 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
-    // with adapters: the addends of this CTA's columns
+    // with adapters: the addends of this CTA's columns, and behind them where their adapters begin
     [[maybe_unused]] float* const addends = landing + (direct ? 0 : (int)splits * F::kW * pitch);
     const int steps = k_end - k_begin;
     // The elected lane's role is all that its warp does until the lane is done: the rest of the warp waits at the end of
@@ -501,7 +526,7 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
         if constexpr (ADAPT) {
-            adapter_addends(a, addends, pitch, F::kW, per_cta, own, n0, (int64_t)t0 + my_c0, my_cols);
+            adapter_addends<F::kW>(a, reinterpret_cast<int64_t*>(addends + F::kW * pitch), addends, pitch, per_cta, own, n0, (int64_t)t0 + my_c0, my_cols);
         }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
@@ -1147,7 +1172,7 @@ cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int split
     const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
     static std::atomic<uint64_t> allowed{0};
     return launch_clusters(linear_few_kernel<PAIR, ADAPT>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
-                           F::smem(a.rows_t, splits, a.stages, few_parts(splits, a.gated, ADAPT)), m, a, st);
+                           F::smem(a.rows_t, splits, a.stages, few_parts(splits, a.gated, ADAPT), ADAPT), m, a, st);
 }
 
 template <bool ADAPT>

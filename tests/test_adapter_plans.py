@@ -21,8 +21,8 @@ static void few(int T, int N, int K, const LinPlan& p, bool gated) {
     using F = Few<PAIR>;
     ++cases;
     const int own = F::own(p.rows_t, p.splits), parts = few_parts(p.splits, gated, true);
-    const int smem = F::smem(p.rows_t, p.splits, p.stages, parts);
-    const int inner = 1024 + p.stages * F::stage(p.rows_t) + parts * F::kW * F::pitch(own) * 4;
+    const int smem = F::smem(p.rows_t, p.splits, p.stages, parts, true);
+    const int inner = 1024 + p.stages * F::stage(p.rows_t) + parts * F::kW * F::pitch(own) * 4 + (own + 7) / 8 * 64;
     if (parts < 1 || inner > smem || smem > kCtaSmemMax || !columns_covered(smem, F::columns(p.rows_t)) || p.rows_t > F::kRows ||
         p.rows_t % F::kStep || p.stages < 2 || p.stages > kFewStages || p.splits * F::kCtas > kFewSplits) {
         ++wrong;
