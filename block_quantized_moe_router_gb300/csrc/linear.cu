@@ -280,54 +280,55 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 
-// The addends v b[j]^T of ROWS weight rows (from feature n0 on, those from `half` on of the second matrix) and `own`
-// columns (a multiple of 4; rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
+// The addends v b[j]^T of ROWS weight rows (from feature n0 on, those from `half` on of the second matrix) and `cols`
+// columns (rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
 //
-// By mma.sync, a column's adapter at a time: A is 16 rows of its b, B the low-rank products of the eight columns of the
-// group, and of D only that column is kept, so that a column sees no other one's adapter.  That leaves seven eighths of
+// By mma.sync, a column's adapter at a time: A is 16 rows of its b, B the low-rank products of the four columns of the
+// item, and of D only that column is kept, so that a column sees no other one's adapter.  That leaves seven eighths of
 // an MMA unused and still takes half the instructions of plain FMAs, which count: few warps run here, each through code that
 // it meets for the first time.  K may be in any order, so that one 16-byte load a lane serves two MMAs (ranks 8 c to
 // 8 c + 7 for lane c of four, the first four of each in the first MMA).
 //
-// Steps of 16 rows, 4 columns and 32 ranks; the next step's loads are under way while one is computed, the first one's while
+// Items of 32 rows and 4 columns, steps of 2 columns and 32 ranks; the next step's loads are under way while one is computed, the first one's while
 // the launch before computes v.  What all others read of b is brought to L2 by then.
 struct AddendLoads {
-    uint4 p[4], q[4];  // of b: rows g and g + 8
-    uint4 hi, lo;      // of v
+    uint4 p[2][4];  // of b: rows g, g + 8, g + 16 and g + 24
+    uint4 hi, lo;   // of v
 };
 template <int ROWS>
-__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_s, float* dst, int pitch, int half, int own, int n0,
-                                                int64_t t, int cols) {
-    constexpr int kWarps = 6, kBlocks = ROWS / 16;
+__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_s, float* dst, int pitch, int half, int n0, int64_t t,
+                                                int cols) {
+    constexpr int kWarps = 6, kBlocks = ROWS / 32;
     const int warp = (int)(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
-    const int items = (own + 7) / 8 * kBlocks;
+    const int items = cols > 0 ? (cols + 3) / 4 * kBlocks : 0;
     // where each column's adapter begins, -1 for none
-    for (int c = threadIdx.x - 64; c < (own + 7) / 8 * 8; c += 32 * kWarps) {
+    for (int c = threadIdx.x - 64; c < (cols + 3) / 4 * 4; c += 32 * kWarps) {
         const int j = c < cols ? adapter_of(a, t + c) : -1;
         at_s[c] = j < 0 ? -1 : j * a.sb;
     }
     asm volatile("bar.sync 1, 192;" ::: "memory");  // the six warps
-    const auto matrix = [&](int item) { return (int)(item % kBlocks * 16 >= half); };
-    const auto feature = [&](int item) { return n0 + item % kBlocks * 16 - (matrix(item) ? half : 0); };
+    const auto matrix = [&](int item) { return (int)(item % kBlocks * 32 >= half); };
+    const auto feature = [&](int item) { return n0 + item % kBlocks * 32 - (matrix(item) ? half : 0); };
     const int64_t eight = 8 * a.ldb;
     const auto load_b = [&](int item, int r, int first, AddendLoads& to) {
-        const int m = matrix(item), n = feature(item) + g;  // this lane's features: n and n + 8
-        const bool in = item < items && a.b[m] && r + 8 * c4 < a.R, p_in = in && n < a.N, q_in = in && n + 8 < a.N;
+        const int m = matrix(item), n = feature(item) + g;  // this lane's first feature
+        const bool in = item < items && a.b[m] && r + 8 * c4 < a.R;
         const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb + 8 * c4 + r;
-        const int64_t* const at = at_s + item / kBlocks * 8 + first;
+        const int64_t* const at = at_s + item / kBlocks * 4 + first;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            to.p[c] = to.q[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (!in) continue;
-            const int64_t from = at[c];
-            if (from >= 0 && p_in) to.p[c] = __ldg(reinterpret_cast<const uint4*>(b + from));
-            if (from >= 0 && q_in) to.q[c] = __ldg(reinterpret_cast<const uint4*>(b + from + eight));
+        for (int c = 0; c < 2; ++c) {
+            const int64_t from = in ? at[c] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to.p[c][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (from >= 0 && n + 8 * i < a.N) to.p[c][i] = __ldg(reinterpret_cast<const uint4*>(b + from + i * eight));
+            }
         }
     };
     const auto load_v = [&](int item, int r, AddendLoads& to) {
-        const int c = item / kBlocks * 8 + g, m = matrix(item);
+        const int c = item / kBlocks * 4 + g, m = matrix(item);
         to.hi = to.lo = make_uint4(0u, 0u, 0u, 0u);
-        if (item < items && a.b[m] && r + 8 * c4 < a.R && at_s[c] >= 0) {
+        if (item < items && g < 4 && a.b[m] && r + 8 * c4 < a.R && at_s[c] >= 0) {
             const uint16_t* const v = a.v + a.planes[m] * a.plane + (t + c) * a.R + 8 * c4 + r;
             to.hi = __ldcg(reinterpret_cast<const uint4*>(v));
             to.lo = __ldcg(reinterpret_cast<const uint4*>(v + a.plane));
@@ -338,22 +339,22 @@ __device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_
     load_b(item, r, first, now);
 #pragma unroll 1
     for (int i = warp; i < items; i += kWarps) {
-        const int c0 = i / kBlocks * 8, m = matrix(i), n = feature(i) + (lane & 15);
+        const int c0 = i / kBlocks * 4, m = matrix(i), n = feature(i) + lane;
         if (!a.b[m] || n >= a.N) continue;
         const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
 #pragma unroll 1
-        for (int c = lane >> 4; c < min(8, cols - c0); c += 2)  // a lane's row of one column, every 64 ranks
-            if (at_s[c0 + c] >= 0)
-                for (int k = 0; k < a.R; k += 64) prefetch_l2(b + at_s[c0 + c] + k);
+        for (int c = c0; c < c0 + 4; ++c)  // a lane's row of one column, every 64 ranks
+            if (at_s[c] >= 0)
+                for (int k = 0; k < a.R; k += 64) prefetch_l2(b + at_s[c] + k);
     }
     __syncwarp();
     pdl_wait();  // v
     load_v(item, r, now);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum[2][4] = {};
 #pragma unroll 1
     while (item < items) {
-        const int c0 = item / kBlocks * 8, this_item = item, this_first = first;
-        first = first == 0 && cols > c0 + 4 ? 4 : 0;
+        const int c0 = item / kBlocks * 4, this_item = item, this_first = first;
+        first = first == 0 && cols > c0 + 2 ? 2 : 0;
         if (first == 0) {
             r += 32;
             if (r >= a.R) {
@@ -365,34 +366,40 @@ __device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_
         load_b(item, r, first, next);
         load_v(item, r, next);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
             if (at_s[c0 + this_first + c] < 0) continue;
-            const uint4 p = now.p[c], q = now.q[c];
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            if (a.f16) {
-                mma_f16_16816(d, p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
-                mma_f16_16816(d, p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
-                mma_f16_16816(d, p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
-                mma_f16_16816(d, p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
-            } else {
-                mma_bf16_16816(d, p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
-                mma_bf16_16816(d, p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
-                mma_bf16_16816(d, p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
-                mma_bf16_16816(d, p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
+            float d[2][4] = {};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 p = now.p[c][2 * i], q = now.p[c][2 * i + 1];
+                if (a.f16) {
+                    mma_f16_16816(d[i], p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
+                    mma_f16_16816(d[i], p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
+                    mma_f16_16816(d[i], p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
+                    mma_f16_16816(d[i], p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
+                } else {
+                    mma_bf16_16816(d[i], p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
+                    mma_bf16_16816(d[i], p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
+                    mma_bf16_16816(d[i], p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
+                    mma_bf16_16816(d[i], p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
+                }
             }
-            if (c4 == (this_first + c) / 2) {  // columns 2 c4 and 2 c4 + 1 are this lane's
-                sum[c & 1] += d[c & 1];
-                sum[2 + (c & 1)] += d[2 + (c & 1)];
+            if (2 * c4 == this_first) {  // columns 2 c4 and 2 c4 + 1 are this lane's
+                sum[0][c] += d[0][c];
+                sum[0][2 + c] += d[0][2 + c];
+                sum[1][c] += d[1][c];
+                sum[1][2 + c] += d[1][2 + c];
             }
         }
         if (item != this_item) {
-            if (c0 + 2 * c4 < own) {
-                float* const to = dst + (this_item % kBlocks * 16 + g) * pitch + c0 + 2 * c4;
-                *reinterpret_cast<float2*>(to) = make_float2(sum[0], sum[1]);
-                *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(sum[2], sum[3]);
+            if (c4 < 2) {
+                float* const to = dst + (this_item % kBlocks * 32 + g) * pitch + c0 + 2 * c4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float2*>(to + 8 * i * pitch) = make_float2(sum[i >> 1][2 * (i & 1)], sum[i >> 1][2 * (i & 1) + 1]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = 0.f;
+            for (int i = 0; i < 4; ++i) sum[0][i] = sum[1][i] = 0.f;
         }
         now = next;
     }
@@ -526,7 +533,7 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
         if constexpr (ADAPT) {
-            adapter_addends<F::kW>(a, reinterpret_cast<int64_t*>(addends + F::kW * pitch), addends, pitch, per_cta, own, n0, (int64_t)t0 + my_c0, my_cols);
+            adapter_addends<F::kW>(a, reinterpret_cast<int64_t*>(addends + F::kW * pitch), addends, pitch, per_cta, n0, (int64_t)t0 + my_c0, my_cols);
         }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
