@@ -134,13 +134,10 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
     }
     if (leads) {
         id_s[number] = id;
-        scale_s[number] = scale;
         place[tid] = (int8_t)number;
     }
     __syncthreads();
     if (tid < kLowRows && !leads) place[tid] = id >= 0 ? place[first] : (int8_t)-1;
-    __syncthreads();
-    cluster_wait();
     const int per_adapter = 1 << g.per_adapter_log2, units = adapters << g.per_adapter_log2, per_matrix = per_adapter / g.matrices;
     const int my_c0 = cta * own, my_cols = min(own, ncols - my_c0);  // this CTA's rows of x
     int done = 0;  // tiles
@@ -217,9 +214,13 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
             }
             __syncwarp();
         }
+        if (done == 0) {
+            if (leads) scale_s[number] = scale;  // not before: nobody waits for its load until now
+            cluster_wait();
+        }
         __syncthreads();  // all wait here for that
-        {  // A lane is a rank; the two warps of a lane quarter take alternate 32 columns, of those the ones with an adapter of this
-           // tile: two or three of 64 tokens with one each, all of a prompt.
+        {  // A lane is a rank; the two warps of a lane quarter take alternate 32 columns, of those, by fours, the ones with an adapter
+           // of this tile: two or three of 64 tokens with one each, all of a prompt.
             tc_fence_after();
             const int q = warp & 3, u = u0 + ((32 * q + lane) >> g.unit_log2), of = u >> g.per_adapter_log2;  // adapter of the lane
             const int rank = 32 * q + lane - ((max(of << g.per_adapter_log2, u0) - u0) << g.unit_log2);       // of those of that adapter here
@@ -228,13 +229,19 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
             const uint32_t to = smem_u32(landing + (cta << g.own_log2) * g.width + rank);
             for (int c0 = 32 * (warp >> 2); 32 * q < here * unit && c0 < ncols; c0 += 64) {
                 const int at = place[c0 + lane];
+                const unsigned has = __ballot_sync(0xffffffffu, at >= low && at <= high);
 #pragma unroll 1
-                for (unsigned left = __ballot_sync(0xffffffffu, at >= low && at <= high); left; left &= left - 1) {
-                    const int c = c0 + __ffs(left) - 1;
-                    const uint32_t v = tmem_ld_1(tmem + ((uint32_t)(32 * q) << 16) + c);
-                    const uint32_t there = map_rank(to + (c & (own - 1)) * g.width * 4, c >> g.own_log2);
+                for (int i = 0; i < 32; i += 4) {  // four columns at a time, where one of them has
+                    if (!(has >> i & 15u)) continue;
+                    const int c = c0 + i;
+                    uint32_t v[4];
+                    tmem_ld_4(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+                    const uint32_t there = map_rank(to + (c & (own - 1)) * g.width * 4, c >> g.own_log2);  // own is a multiple of four
+                    const uint32_t places = *reinterpret_cast<const uint32_t*>(place + c);
                     tmem_ld_wait();
-                    if (place[c] == mine) st_cluster(there, v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if ((int)(places >> (8 * k) & 0xFFu) == mine) st_cluster(there + k * g.width * 4, v[k]);
                     __syncwarp();
                 }
             }
@@ -279,6 +286,7 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
         }
         if ((tile + g.slots) * g.tile < units) cluster_sync();  // the landing areas and tensor memory are free
     }
+    if (done == 0) cluster_wait();
     if (done == 0 && warp == 0) {  // nothing used the x that came ahead
         if (elect_one())
             for (int i = 0; i < ahead; ++i) {

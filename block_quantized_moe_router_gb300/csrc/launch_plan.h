@@ -188,12 +188,13 @@ inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices, int sms) 
     const int per_adapter = (R + unit - 1) / unit * matrices;  // 1, 2 or 4
     p.per_adapter_log2 = per_adapter >> 1;
     const int steps = (K + kLowK - 1) / kLowK, here = T < p.rows ? T : p.rows;
-    // Long inputs are prompts, whose groups have an adapter or two: a tile for each, and many stages.  Short ones
-    // may have one to each row: eight units to a tile.
+    // Long inputs are prompts, whose groups have an adapter or two: a tile for both, and many stages (4096 gated rows of 7168: a
+    // group with two took 32 us with a tile each, others 21).  Short ones may have one to each row: 128 ranks to a tile.
     const bool prompt = T > 1024;
-    const int64_t units = prompt ? per_adapter : (int64_t)(L < here ? L : here) * per_adapter;
-    p.tile = kLowTile / unit < units ? kLowTile / unit : (int)units;
-    const int tiles = (int)((units + p.tile - 1) / p.tile);  // of a group, as far as that goes
+    const int64_t units = (int64_t)(L < here ? L : here) * per_adapter;
+    const int64_t wanted = prompt && 2 * per_adapter < units ? 2 * per_adapter : units;
+    p.tile = kLowTile / unit < wanted ? kLowTile / unit : (int)wanted;
+    const int tiles = prompt ? 1 : (int)((units + p.tile - 1) / p.tile);  // of a group, as far as that goes
     p.width = (per_adapter < p.tile ? per_adapter : p.tile) * unit;
     p.stage = (p.tile * unit + p.rows) * 128;
     // A round of tiles takes 4 us besides its stages, and those what an SM's share of the L2 rate allows (106 GB/s).
