@@ -1,305 +1,222 @@
 // adapters.cu -- the low-rank products of moe_linear_adapters: v[t] = scale[j] x[t] a[j]^T, j = ids[t].
 //
-// Rows are taken in groups of 128.  A group's adapters, in the order in which they first occur, have their ranks (both
-// matrices' in the gated form) stacked in units of 16 to 128, and a tile is up to 128 of these ranks, the rows of a
-// tcgen05.mma.kind::f16 whose columns are the group's rows of x: D = A x^T.  What a row needs of it are the units of its own
-// adapter; the rest is left out (a product costs its operands' way to the SM, and each of them comes once: an adapter's bytes
-// for a token, the rows of x for a prompt).  Both come by TMA, a unit as one box, through warps of their own (one thread
-// took 350 ns for a stage of two boxes); x starts while the adapters are found.  K is split over the CTAs of a cluster, which exchange the products that count through distributed
-// shared memory and add them in rank order.
+// Rows are taken in groups of 256.  In a group the rows of one adapter form batches of up to 32 in their order,
+// and an item is a batch and 32 of the stacked ranks (both matrices' in the gated form): D = A x^T by mma.sync,
+// ranks on the M side, rows of x on the N side (8 where the batch has no more, or 32).  Each byte of a that a batch needs
+// is read once for all of its rows, in 16-byte loads straight into the fragments: the sum may take K in any
+// order, so a lane's four 16-bit pairs of one 16-byte load serve as the operands of two MMAs, the same way on both sides.
+// K is split over the warps of a CTA and the CTAs of a cluster; the parts meet in shared memory and are added in
+// order.  A batch of one token costs its adapter's bytes, a prompt's its rows of x, read here before the layer
+// reads them again from L2: neither has work for tcgen05 (16 to 64 ranks of 128 lanes).
 //
-// Which adapters occur is known on the device alone.  Every CTA finds its group's by itself: a row leads if no row
-// before it has its adapter, and the leaders before it number it.
+// Which adapters occur is known on the device alone: every CTA of a group finds the batches by itself (a comparison
+// with the ids before it per row), so that no launch has to sort them.
 #include "cluster.cuh"
-#include "common.cuh"
 #include "kernels.h"
 #include "launch_plan.h"
 #include "tc_ptx.cuh"
+#include "rows.cuh"
 
 namespace moe {
 
 namespace {
 
-using namespace tc;
+constexpr int kGroup = kLowGroup, kBatch = kLowBatch, kRanks = kLowRanks;
 
-struct LowMaps {
-    CUtensorMap x, a[2];
-};
-struct LowArgs {
-    int T, R, L, matrices, steps, f16;  // steps of K in all
-    int rows, own_log2, unit_log2, per_adapter_log2, tile, width, slots, stages, stage, loaders;
-    int64_t plane;  // elements of 16 bits
+struct LowRankArgs {
+    int T, K, R, L, f16, matrices, slots, landing_rows;  // landing_rows: of a batch at most
+    int64_t ldx, lda, sa, plane;  // plane: elements of a plane of v
+    const uint16_t *x, *a[2];
     const float* scale;
     const int32_t* ids;
     uint16_t* v;
     int32_t* status;
 };
-constexpr int kLowThreads = 256;
-static_assert(kLowThreads / 32 - 2 == kLowLoaders);
 
-// kind::f16: fp32 D of 128 rows, A and B both bf16 (format 1) or both f16 (format 0), K-major.
-__device__ __forceinline__ uint32_t low_idesc(uint32_t N, bool f16) {
-    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((N >> 3) << 17) | (8u << 24);
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (F16) mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
+    else mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
-// grid (CTAs of a cluster, groups, slots): slot s takes the group's tiles s, s + slots, ...
-__global__ void __launch_bounds__(kLowThreads, 1)
-low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ LowArgs g) {
-    extern __shared__ uint8_t low_smem[];
-    __shared__ uint64_t full[kLowStages], empty[kLowStages], acc_full;
-    __shared__ __align__(16) int id_s[kLowRows];  // of the rows, then of the adapters in their order
-    __shared__ __align__(16) int8_t place[kLowRows];  // of a row's adapter in that order
-    __shared__ int leaders[kLowRows / 32];
-    __shared__ uint32_t tmem_slot;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(low_smem) + 1023) & ~uintptr_t(1023));
-    float* landing = reinterpret_cast<float*>(smem + g.stages * g.stage);  // [CTA][own row][rank of its adapter in the tile]
-    float* scale_s = landing + ((int)cluster_size() << g.own_log2) * g.width;           // of the adapters in their order
-    const int warp = warp_index(), lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int ctas = (int)cluster_size(), cta = (int)cluster_rank();
-    const int64_t t0 = (int64_t)blockIdx.y * g.rows;
-    const int ncols = (int)min((int64_t)g.rows, g.T - t0);
-    const int k_begin = (int)((int64_t)g.steps * cta / ctas), steps = (int)((int64_t)g.steps * (cta + 1) / ctas) - k_begin;
-    const int unit = 1 << g.unit_log2, own = 1 << g.own_log2;
-    const int x_at = g.tile * unit * 128;  // of a stage
-    uint32_t tm_cols = kTmemLeast;
-    while ((int)tm_cols < g.rows) tm_cols *= 2;
-    if (tid == 0) {
-        for (int s = 0; s < g.stages; ++s) {
-            mbar_init(&full[s], 1 + g.tile);  // x, and every unit
-            mbar_init(&empty[s], 1);
+// This warp's part of an item's sums, over the steps of 32 elements of K from `step` on, `stride` apart: NB blocks of 8
+// rows.  rows: where this lane's ranks of a begin (nullptr: none), their ranks being g, g + 8, g + 16 and g + 24.
+template <bool F16, int NB, int UNROLL>
+__device__ __forceinline__ void low_rank_sums(float (&d)[2][4][4], const uint16_t* const (&rank)[4],
+                                              const uint16_t* const (&row)[4], int step, int stride, int end, int K) {
+    const int c8 = 8 * (threadIdx.x & 3);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (; step < end; step += UNROLL * stride) {
+        uint4 w[UNROLL][4], x[UNROLL][NB];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = 32 * (step + u * stride) + c8;
+            const bool in = step + u * stride < end && k < K;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[u][i] = in && rank[i] ? ldg_stream128(rank[i] + k) : zero;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) x[u][i] = in && row[i] ? ldg_cached128(row[i] + k) : zero;
         }
-        mbar_init(&acc_full, 1);
-        fence_mbar_init();
-        prefetch_tmap(&maps.x);
-        prefetch_tmap(&maps.a[0]);
-        if (g.matrices == 2) prefetch_tmap(&maps.a[1]);
+        __syncwarp();  // the MMAs want the whole warp, and the loads above may part it
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const uint4 p = w[u][2 * m], q = w[u][2 * m + 1];
+                    mma16<F16>(d[m][i], p.x, q.x, p.y, q.y, x[u][i].x, x[u][i].y);
+                    mma16<F16>(d[m][i], p.z, q.z, p.w, q.w, x[u][i].z, x[u][i].w);
+                }
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, tm_cols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+}
+
+// grid (slots * CTAs of a cluster, groups): slot s takes the group's items s, s + slots, ...
+template <bool F16>
+__global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
+    __shared__ __align__(16) int id_s[kGroup];
+    __shared__ int batch_row[kBatch], leaders[kGroup / 32], item_id, item_first;
+    __shared__ __align__(16) float part[4][kBatch][kRanks + 4];     // sums of a warp: [row][rank]
+    extern __shared__ __align__(16) float landing[];                // [CTA][row][rank]
     pdl_wait();
-    // The layer's launch may start: whatever came before this one is done.  (Once the first loads are here, so that they are
-    // not behind the layer's: 8 rows 16.6 us for 12.4.)
-    pdl_trigger();
-    auto give_up = [&]() { status_or(g.status, MOE_DEV_TIMEOUT); };
-    const auto load_x = [&](int s, int i) {
-        mbar_arrive_expect_tx(&full[s], g.rows * 128);
-        tma_load_2d(smem + s * g.stage + x_at, &maps.x, (k_begin + i) * kLowK, (int)t0, &full[s]);
-    };
-    // roles of elected lanes as in linear.cu: the rest of their warps waits at the end of the role
-    const int ahead = min(steps, g.stages);  // stages whose x comes before the adapters are known
-    if (warp >= kLowRows / 32) {  // the others find the adapters meanwhile
-        if (elect_one())
-            for (int i = warp - kLowRows / 32; i < ahead; i += kLowThreads / 32 - kLowRows / 32) load_x(i, i);
-        __syncwarp();
+    pdl_trigger();  // the layer's launch may start: whatever came before this one is done
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = (int)cluster_size(), cta = (int)cluster_rank(), slot = (int)blockIdx.x / ctas;
+    if (ctas > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+    const int64_t t0 = (int64_t)blockIdx.y * kGroup;
+    int id = t0 + tid < g.T ? __ldg(g.ids + t0 + tid) : -1;
+    if (id < -1 || id >= g.L) {
+        if (blockIdx.x == 0) status_or(g.status, MOE_DEV_BAD_ADAPTER_ID);
+        id = -1;
     }
-    // the group's adapters
-    int id = -1;
-    float scale = 1.f;
-    if (tid < kLowRows) {
-        if (tid < ncols) id = __ldg(g.ids + t0 + tid);
-        if (id < -1 || id >= g.L) {
-            if (blockIdx.x == 0 && blockIdx.z == 0) status_or(g.status, MOE_DEV_BAD_ADAPTER_ID);
-            id = -1;
-        }
-        id_s[tid] = id;
-        if (g.scale && id >= 0) scale = __ldg(g.scale + id);
-    }
+    id_s[tid] = id;
     __syncthreads();
-    // the first row that has this row's adapter: of its warp's, or of those before
-    int first = (tid & ~31) + __ffs(__match_any_sync(0xffffffffu, id)) - 1;
-    if (tid < kLowRows) {
-        bool found = id < 0;
-        for (int i = 0; i < (tid & ~31) && !__all_sync(0xffffffffu, found); i += 4) {
+    int before = 0;  // rows of this adapter before this one
+    if (id >= 0) {
+        for (int i = 0; i < (tid & ~3); i += 4) {
             const int4 p = *reinterpret_cast<const int4*>(id_s + i);
-            const int at = p.x == id ? 0 : p.y == id ? 1 : p.z == id ? 2 : 3;
-            if (!found && (at < 3 || p.w == id)) {
-                first = i + at;
-                found = true;
-            }
+            before += (p.x == id) + (p.y == id) + (p.z == id) + (p.w == id);
         }
+        for (int i = tid & ~3; i < tid; ++i) before += id_s[i] == id;
     }
-    const bool leads = id >= 0 && first == tid;
+    const bool leads = id >= 0 && before % kBatch == 0;
     const unsigned lead_mask = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0 && warp < kLowRows / 32) leaders[warp] = __popc(lead_mask);
+    if (lane == 0) leaders[warp] = __popc(lead_mask);
     __syncthreads();
-    int adapters = 0, number = __popc(lead_mask & ((1u << lane) - 1u));
+    int batches = 0, batch = __popc(lead_mask & ((1u << lane) - 1u));  // of the group; the one this row leads
 #pragma unroll
-    for (int w = 0; w < kLowRows / 32; ++w) {
-        if (w < warp) number += leaders[w];
-        adapters += leaders[w];
+    for (int w = 0; w < kGroup / 32; ++w) {
+        if (w < warp) batch += leaders[w];
+        batches += leaders[w];
     }
-    if (leads) {
-        id_s[number] = id;
-        place[tid] = (int8_t)number;
-    }
-    __syncthreads();
-    if (tid < kLowRows && !leads) place[tid] = id >= 0 ? place[first] : (int8_t)-1;
-    const int per_adapter = 1 << g.per_adapter_log2, units = adapters << g.per_adapter_log2, per_matrix = per_adapter / g.matrices;
-    const int my_c0 = cta * own, my_cols = min(own, ncols - my_c0);  // this CTA's rows of x
-    int done = 0;  // tiles
-    for (int tile = blockIdx.z; tile * g.tile < units; tile += g.slots, ++done) {
-        const int u0 = tile * g.tile, here = min(g.tile, units - u0);
-        RingPos ring;  // `done` tiles of `steps` stages on
-        ring.slot = (done * steps) % g.stages;
-        ring.parity = (uint32_t)((done * steps) / g.stages) & 1u;
-        if (warp == 0) {
-            if (elect_one()) {
-                int i = 0;
-                RingPos at = ring;
-                for (; i < steps; ++i, at.next(g.stages)) {
-                    if (done == 0 && i < ahead) continue;
-                    if (!mbar_wait_suspended(&empty[at.slot], at.parity ^ 1)) {
-                        give_up();
-                        break;
-                    }
-                    load_x(at.slot, i);
-                }
-                // whoever gives up, no copy is in flight when the CTA ends
-                for (int left = i < g.stages ? i : g.stages; left > 0; --left) {
-                    at.back(g.stages);
-                    mbar_wait_suspended(&full[at.slot], at.parity);
-                }
-            }
-            __syncwarp();
-        } else if (warp >= 2) {
-            // Units of stages in turn, so that all loaders have some however few units there are; a unit that a short tile
-            // lacks arrives without bytes.  A loader goes on by a lap of the ring at most: a barrier's parity tells the
-            // lap before from this one, not from the one before that.
-            if (warp - 2 < g.loaders && elect_one()) {
-                RingPos at = ring;
-                int i = 0;  // stage
-                for (int k = warp - 2;; k += g.loaders) {
-                    for (; k >= g.tile; k -= g.tile) {
-                        ++i;
-                        at.next(g.stages);
-                    }
-                    if (i >= steps) break;
-                    if (!mbar_wait_suspended(&empty[at.slot], at.parity ^ 1)) {
-                        give_up();
-                        break;
-                    }
-                    uint64_t* const bar = &full[at.slot];
-                    mbar_arrive_expect_tx(bar, k < here ? unit * 128 : 0);
-                    if (k >= here) continue;
-                    const int of = (u0 + k) >> g.per_adapter_log2, u = (u0 + k) & (per_adapter - 1), second = u >= per_matrix;
-                    tma_load_3d(smem + at.slot * g.stage + k * unit * 128, &maps.a[second], (k_begin + i) * kLowK,
-                                (u - (second ? per_matrix : 0)) << g.unit_log2, id_s[of], bar);
-                }
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            if (elect_one()) {
-                const uint32_t idesc = low_idesc((uint32_t)g.rows, g.f16);
-                RingPos at = ring;
-                for (int i = 0; i < steps; ++i, at.next(g.stages)) {
-                    const int s = at.slot;
-                    if (!mbar_wait_suspended(&full[s], at.parity)) {
-                        give_up();
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = smem_desc(smem_u32(smem + s * g.stage), 16, 1024, kLayoutSw128);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)  // K 16 per MMA: 32 bytes (two units) along the swizzled row
-                        tc_mma_bf16(tmem, ad + 2 * j, ad + (x_at >> 4) + 2 * j, idesc, (i | j) != 0);
-                    tc_commit(&empty[s]);
-                }
-                tc_commit(&acc_full);  // arrives when every MMA has completed
-                if (!mbar_wait_suspended(&acc_full, (uint32_t)done & 1u)) give_up();
-                tc_fence_before();
-            }
-            __syncwarp();
+    const int per_matrix = (g.R + 15) / 16, passes = (per_matrix * g.matrices + 1) / 2;  // blocks of 16 ranks, items of a batch
+    const int steps = (g.K + 31) / 32;
+    const int begin = (int)((int64_t)steps * cta / ctas), end = (int)((int64_t)steps * (cta + 1) / ctas);
+    if (ctas > 1) cluster_wait();
+    for (int item = slot; item < batches * passes; item += g.slots) {
+        const int pass = item % passes;
+        if (leads && batch == item / passes) {
+            item_id = id;
+            item_first = before;
         }
-        if (done == 0) {
-            if (leads) scale_s[number] = scale;  // not before: nobody waits for its load until now
-            cluster_wait();
-        }
-        __syncthreads();  // all wait here for that
-        {  // A lane is a rank; the two warps of a lane quarter take alternate 32 columns, of those, by fours, the ones with an adapter
-           // of this tile: two or three of 64 tokens with one each, all of a prompt.
-            tc_fence_after();
-            const int q = warp & 3, u = u0 + ((32 * q + lane) >> g.unit_log2), of = u >> g.per_adapter_log2;  // adapter of the lane
-            const int rank = 32 * q + lane - ((max(of << g.per_adapter_log2, u0) - u0) << g.unit_log2);       // of those of that adapter here
-            const int mine = u < u0 + here ? of : kLowRows;
-            const int low = u0 >> g.per_adapter_log2, high = (u0 + here - 1) >> g.per_adapter_log2;  // adapters of the tile
-            const uint32_t to = smem_u32(landing + (cta << g.own_log2) * g.width + rank);
-            for (int c0 = 32 * (warp >> 2); 32 * q < here * unit && c0 < ncols; c0 += 64) {
-                const int at = place[c0 + lane];
-                const unsigned has = __ballot_sync(0xffffffffu, at >= low && at <= high);
-#pragma unroll 1
-                for (int i = 0; i < 32; i += 4) {  // four columns at a time, where one of them has
-                    if (!(has >> i & 15u)) continue;
-                    const int c = c0 + i;
-                    uint32_t v[4];
-                    tmem_ld_4(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-                    const uint32_t there = map_rank(to + (c & (own - 1)) * g.width * 4, c >> g.own_log2);  // own is a multiple of four
-                    const uint32_t places = *reinterpret_cast<const uint32_t*>(place + c);
-                    tmem_ld_wait();
+        __syncthreads();
+        const int j = item_id, first = item_first;
+        const bool here = id == j && before >= first && before < first + kBatch;
+        if (here) batch_row[before - first] = tid;
+        const int rows = __syncthreads_count(here);
+        const uint16_t *rank[4], *row[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if ((int)(places >> (8 * k) & 0xFFu) == mine) st_cluster(there + k * g.width * 4, v[k]);
-                    __syncwarp();
-                }
+        for (int i = 0; i < 4; ++i) {
+            const int block = 2 * pass + (i >> 1), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + 8 * (i & 1) + (lane >> 2);
+            rank[i] = block < per_matrix * g.matrices && r < g.R ? g.a[m] + j * g.sa + r * g.lda : nullptr;
+            row[i] = 8 * i + (lane >> 2) < rows ? g.x + (t0 + batch_row[8 * i + (lane >> 2)]) * g.ldx : nullptr;
+        }
+        float d[2][4][4] = {};
+        if (rows <= 8) low_rank_sums<F16, 1, 4>(d, rank, row, begin + warp, kGroup / 32, end, g.K);
+        else low_rank_sums<F16, 4, 2>(d, rank, row, begin + warp, kGroup / 32, end, g.K);
+        const int blocks = rows <= 8 ? 1 : 4;
+        // warps 4 to 7 hand theirs to warps 0 to 3, these add them to their own, and those four are added
+        const auto place = [&](int m, int b, int e) -> float& {
+            return part[warp & 3][8 * b + 2 * (lane & 3) + (e & 1)][16 * m + (lane >> 2) + 8 * (e >> 1)];
+        };
+        const auto each = [&](auto&& f) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (b < blocks) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f(d[m][b][e], place(m, b, e));
+                    }
+        };
+        if (warp >= 4) each([](float v, float& at) { at = v; });
+        __syncthreads();
+        if (warp < 4) each([](float v, float& at) { at = v + at; });
+        __syncthreads();
+        // a thread: one row of the batch (of 32), four ranks
+        const int at_row = tid >> 3, at_rank = 4 * (tid & 7);
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at_row < rows)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 p = *reinterpret_cast<const float4*>(&part[w][at_row][at_rank]);
+                z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
             }
-            tc_fence_before();
-        }
-        cluster_sync();  // every part has landed
-        const int fours_log2 = 29 - __clz(g.width);  // width is a power of two
-        for (int i = tid; i < my_cols << fours_log2; i += kLowThreads) {  // a row's four ranks
-            const int c = i >> fours_log2, n = 4 * (i & ((1 << fours_log2) - 1)), of = place[my_c0 + c];
-            const int from = max(of << g.per_adapter_log2, u0), end = min((of + 1) << g.per_adapter_log2, u0 + g.tile);  // its units here
-            if (of < 0 || n >= (end - from) << g.unit_log2) continue;
-            const int u = from - (of << g.per_adapter_log2) + (n >> g.unit_log2), m = u >= per_matrix;  // of the adapter
-            const int r = ((u - (m ? per_matrix : 0)) << g.unit_log2) + (n & (unit - 1));
-            if (r >= g.R) continue;  // R is a multiple of 8: all four or none
-            const float* src = landing + c * g.width + n;
-            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int s = 0; s < kLowSplits; ++s)
-                if (s < ctas) {
-                    const float4 p = *reinterpret_cast<const float4*>(src + (s << g.own_log2) * g.width);
+        if (ctas > 1) {
+            const uint32_t there = tc::smem_u32(landing + (cta * g.landing_rows + at_row) * kRanks + at_rank);
+            if (at_row < rows)
+                st_cluster_v4(map_rank(there, 0), __float_as_uint(z.x), __float_as_uint(z.y), __float_as_uint(z.z), __float_as_uint(z.w));
+            cluster_sync();
+            if (cta == 0 && at_row < rows) {
+                z = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = 0; c < ctas; ++c) {
+                    const float4 p = *reinterpret_cast<const float4*>(landing + (c * g.landing_rows + at_row) * kRanks + at_rank);
                     z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
                 }
-            const float times = scale_s[of];
-            const float v[4] = {z.x * times, z.y * times, z.z * times, z.w * times};
-            uint16_t* const to_v = g.v + 2 * m * g.plane;
-            const int64_t at = (t0 + my_c0 + c) * g.R + r;
-            uint32_t hi[4], lo[4];
+            }
+        }
+        const int block = 2 * pass + (at_rank >> 4), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + (at_rank & 15);
+        if (cta == 0 && at_row < rows && block < per_matrix * g.matrices && r < g.R) {  // R is a multiple of 8: all four or none
+            const float s = g.scale ? __ldg(g.scale + j) : 1.f;
+            const float v[4] = {z.x * s, z.y * s, z.z * s, z.w * s};
+            uint16_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // an infinite hi has no rest
-                if (g.f16) {
-                    const __half h = __float2half_rn(v[k]);
-                    hi[k] = __half_as_ushort(h);
-                    lo[k] = (hi[k] & 0x7C00u) == 0x7C00u ? 0 : __half_as_ushort(__float2half_rn(v[k] - __half2float(h)));
+            for (int i = 0; i < 4; ++i) {  // an infinite hi has no rest
+                if constexpr (F16) {
+                    const __half h = __float2half_rn(v[i]);
+                    hi[i] = __half_as_ushort(h);
+                    lo[i] = (hi[i] & 0x7C00u) == 0x7C00u ? 0 : __half_as_ushort(__float2half_rn(v[i] - __half2float(h)));
                 } else {
-                    const __nv_bfloat16 h = __float2bfloat16_rn(v[k]);
-                    hi[k] = __bfloat16_as_ushort(h);
-                    lo[k] = (hi[k] & 0x7F80u) == 0x7F80u ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(v[k] - __bfloat162float(h)));
+                    const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+                    hi[i] = __bfloat16_as_ushort(h);
+                    lo[i] = (hi[i] & 0x7F80u) == 0x7F80u ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(v[i] - __bfloat162float(h)));
                 }
             }
-            *reinterpret_cast<uint2*>(to_v + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(to_v + g.plane + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            uint16_t* to = g.v + 2 * m * g.plane + (t0 + batch_row[at_row]) * g.R + r;
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+            *reinterpret_cast<uint2*>(to + g.plane) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
         }
-        if ((tile + g.slots) * g.tile < units) cluster_sync();  // the landing areas and tensor memory are free
+        if (ctas > 1) cluster_sync();  // the landing area is free
+        __syncthreads();               // and the batch's rows
     }
-    if (done == 0) cluster_wait();
-    if (done == 0 && warp == 0) {  // nothing used the x that came ahead
-        if (elect_one())
-            for (int i = 0; i < ahead; ++i) {
-                for (int k = 0; k < g.tile; ++k) mbar_arrive(&full[i]);
-                mbar_wait_suspended(&full[i], 0);
-            }
-        __syncwarp();
-    }
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, tm_cols);
-    }
+}
+
+template <bool F16>
+cudaError_t launch_low_rank(const LowRankArgs& g, int groups, int splits, int smem, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.slots * splits), (unsigned)groups);
+    cfg.blockDim = dim3(kGroup);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, low_rank_kernel<F16>, g);
 }
 
 }  // namespace
@@ -307,49 +224,29 @@ low_rank_kernel(const __grid_constant__ LowMaps maps, const __grid_constant__ Lo
 cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                    const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                    void* out, void* workspace, int32_t* status, cudaStream_t st) {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    static std::atomic<uint64_t> allowed{0};
-    if (err == cudaSuccess) err = allow_large_launch(low_rank_kernel, kCtaSmemMax, allowed);
-    if (err != cudaSuccess) return err;
-    const AdapterProducts products = AdapterProducts::plan(d.T, ad.R, ad.a && ad.a_mul ? 2 : 1);
-    const LowPlan p = plan_low_rank(d.T, d.K, ad.L, ad.R, products.matrices, sms);
-    const void* of[2] = {ad.a ? ad.a : ad.a_mul, products.matrices == 2 ? ad.a_mul : nullptr};
-    LowMaps m{};
-    if (!encode_rows16(&m.x, x, d.K, d.T, d.ldx, p.rows, kLowK)) return cudaErrorInvalidValue;
-    for (int i = 0; i < products.matrices; ++i)
-        if (!encode_stack16(&m.a[i], of[i], d.K, ad.R, ad.L, ad.lda, ad.L > 1 ? ad.sa : ad.R * ad.lda, 1 << p.unit_log2, kLowK)) return cudaErrorInvalidValue;
-    LowArgs g{};
-    g.T = d.T; g.R = ad.R; g.L = ad.L; g.matrices = products.matrices; g.steps = (d.K + kLowK - 1) / kLowK; g.f16 = d.dtype == MOE_DT_F16;
-    g.rows = p.rows; g.own_log2 = p.own_log2; g.unit_log2 = p.unit_log2; g.tile = p.tile; g.width = p.width; g.per_adapter_log2 = p.per_adapter_log2; g.slots = p.slots; g.stages = p.stages; g.stage = p.stage; g.loaders = p.loaders;
-    g.plane = (int64_t)(products.plane / 2);
-    g.scale = ad.scale; g.ids = ad.ids; g.v = static_cast<uint16_t*>(workspace); g.status = status;
+    const AdapterProducts p = AdapterProducts::plan(d.T, ad.R, ad.a && ad.a_mul ? 2 : 1);
+    LowRankArgs g{};
+    g.T = d.T; g.K = d.K; g.R = ad.R; g.L = ad.L; g.f16 = d.dtype == MOE_DT_F16; g.matrices = p.matrices;
+    g.ldx = d.ldx; g.lda = ad.lda; g.sa = ad.sa; g.plane = (int64_t)(p.plane / 2);
+    g.x = static_cast<const uint16_t*>(x);
+    g.a[0] = static_cast<const uint16_t*>(ad.a ? ad.a : ad.a_mul);
+    g.a[1] = static_cast<const uint16_t*>(ad.a_mul);
+    g.scale = ad.scale; g.ids = ad.ids;
+    g.v = static_cast<uint16_t*>(workspace);
+    g.status = status;
+    const LowPlan plan = plan_low_rank(d.T, d.K, ad.L, ad.R, p.matrices);
+    g.slots = plan.slots;
+    g.landing_rows = plan.landing_rows;
     // groups are the grid's second dimension: at most 65535 a launch
-    for (int first = 0; first < p.groups; first += 65535) {
-        const int n = p.groups - first < 65535 ? p.groups - first : 65535;
-        const int64_t t = (int64_t)first * p.rows;
-        LowArgs h = g;
-        if (first) {
-            if (!encode_rows16(&m.x, static_cast<const uint16_t*>(x) + t * d.ldx, d.K, d.T - t, d.ldx, p.rows, kLowK)) return cudaErrorInvalidValue;
-            h.T = (int)(d.T - t);
-            h.ids += t;
-            h.v += t * g.R;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)p.splits, (unsigned)n, (unsigned)p.slots);
-        cfg.blockDim = dim3(kLowThreads);
-        cfg.dynamicSmemBytes = p.smem;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)p.splits;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        err = cudaLaunchKernelEx(&cfg, low_rank_kernel, m, h);
+    for (int first = 0; first < plan.groups; first += 65535) {
+        const int n = plan.groups - first < 65535 ? plan.groups - first : 65535;
+        LowRankArgs h = g;
+        const int64_t t = (int64_t)first * kGroup;
+        h.x += t * g.ldx;
+        h.ids += t;
+        h.v += t * g.R;
+        h.T = (int)(g.T - t);
+        const cudaError_t err = g.f16 ? launch_low_rank<true>(h, n, plan.splits, plan.smem, st) : launch_low_rank<false>(h, n, plan.splits, plan.smem, st);
         if (err != cudaSuccess) return err;
     }
     return launch_adapted_linear(d, ad, x, w, w_mul, bias, bias_mul, residual, out, workspace, status, st);

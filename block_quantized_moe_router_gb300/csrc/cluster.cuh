@@ -68,9 +68,6 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t mapped, uint32_t a, uint3
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mapped), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t mapped, uint32_t a) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapped), "r"(a) : "memory");
-}
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
@@ -155,15 +152,6 @@ inline bool encode_boxes16(CUtensorMap* m, const void* base, int rank, const int
 inline bool encode_rows16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
                           int box_cols) {
     return encode_boxes16(m, base, 2, {cols, rows, 1}, ld, 0, box_rows, box_cols);
-}
-// TMA load of a box of one matrix of a stack.
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z),
-        "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar)))
-        : "memory");
 }
 // [count][rows][cols], rows ld and matrices step apart.
 inline bool encode_stack16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,

@@ -39,8 +39,6 @@ constexpr bool columns_covered(int smem, int columns) {
 constexpr int kLinK = 64;        // K elements per stage (128 bytes per row)
 constexpr int kFewSplits = 8;    // parts of K at most; CTAs of a cluster too (the portable cluster size)
 constexpr int kFewStages = 8;
-constexpr int kLowBeside = 16;          // rows whose low-rank products are computed beside the layer's weights
-constexpr int kLowSmemFew = 76 * 1024;  // of a CTA that computes them
 template <bool PAIR>
 struct Few {
     static constexpr int kRows = PAIR ? 256 : 128;   // rows of x per tile at most
@@ -53,22 +51,15 @@ struct Few {
     static constexpr int stage(int rows) { return kA + rows / kCtas * 128; }
     // A pair takes all of tensor memory, so that its CTAs hold the same columns.
     static constexpr int columns(int rows) { return PAIR ? kTmemColumns : tmem_columns(rows); }
-    // beside the stages: landing areas of `parts` parts; with adapters 8 bytes for each of a CTA's columns, in eights
-    static constexpr int rest(int rows, int splits, int parts, bool adapters) {
-        return parts * kW * pitch(own(rows, splits)) * 4 + 1024 + (adapters ? (own(rows, splits) + 7) / 8 * 64 : 0);
+    static constexpr int rest(int rows, int splits) {  // beside the stages
+        return splits * kW * pitch(own(rows, splits)) * 4 + 1024;
     }
-    static constexpr int rest(int rows, int splits) { return rest(rows, splits, splits, false); }
-    static constexpr int smem(int rows, int splits, int stages) { return smem(rows, splits, stages, splits, false); }
-    static constexpr int smem(int rows, int splits, int stages, int parts, bool adapters) {
-        const int need = stages * stage(rows) + rest(rows, splits, parts, adapters);
+    static constexpr int smem(int rows, int splits, int stages) {
+        const int need = stages * stage(rows) + rest(rows, splits);
         const int least = smem_for_columns(columns(rows));
         return need > least ? need : least;
     }
 };
-
-// Landing areas of a CTA: one for each part of K, and one for the adapters' addends; a single ungated part is not
-// exchanged, and the addends take its place.
-constexpr int few_parts(int splits, bool gated, bool adapters) { return splits + (adapters && (splits > 1 || gated)); }
 
 // Tiles of the many-row kernel: 256 rows by `features`.
 constexpr int64_t many_tiles(int T, int N, int features) {
@@ -97,27 +88,23 @@ constexpr int few_usable(int cluster, int fit) { return cluster < 4 ? 152 : clus
 
 // The few-row choices with the rows of x in `tiles_t` tiles.
 template <bool PAIR>
-void plan_few_tiles(int T, int N, int nk, bool gated, int sms, bool adapters, int tiles_t, float& best_us, LinPlan& best) {
+void plan_few_tiles(int T, int N, int nk, bool gated, int sms, int tiles_t, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int rows = ((T + tiles_t - 1) / tiles_t + F::kStep - 1) / F::kStep * F::kStep;
     const int per_tile = F::kW * F::kCtas / (gated ? 2 : 1);
     const int64_t tiles = (int64_t)((T + rows - 1) / rows) * ((N + per_tile - 1) / per_tile) * F::kCtas;
     const float stage_kb = (float)F::stage(rows) / 1024.f;
-    // With adapters of a few rows a CTA leaves room for one of the launch that computes their products, so that both run at
-    // once.  With more rows that launch occupies the SMs and is done sooner alone (64 rows with an adapter each: 31 us, 35).
-    const int smem_max = adapters && T <= kLowBeside ? kSmSmem - kLowSmemFew - 2 * (kSmemReserved + 256) : kCtaSmemMax;
     for (int splits = 1; splits * F::kCtas <= kFewSplits && splits <= nk; splits *= 2) {
         const int kbs = (nk + splits - 1) / splits;
         // Pairs and CTAs alone on their SMs take more stages, so that latency from HBM does not hold the loads
         // back (64 rows of 7168 x 2048: 12.1 us with 4, 11.4 with 6; with 8 what follows starts later).
         const bool alone = PAIR || tiles * splits <= (int64_t)sms * few_usable(splits, 1) / 152;
-        const int parts = few_parts(splits, gated, adapters);
-        int stages = alone ? (smem_max - F::rest(rows, splits, parts, adapters)) / F::stage(rows) : 4;
+        int stages = alone ? (kCtaSmemMax - F::rest(rows, splits)) / F::stage(rows) : 4;
         const int most = PAIR ? kFewStages : alone ? 6 : 4;
         stages = stages < most ? stages : most;
         stages = kbs < stages ? (kbs < 2 ? 2 : kbs) : stages;
-        const int smem = F::smem(rows, splits, stages, parts, adapters);
-        if (stages < 2 || smem > (F::columns(rows) == kTmemColumns ? kCtaSmemMax : smem_max)) continue;
+        const int smem = F::smem(rows, splits, stages);
+        if (stages < 2 || smem > kCtaSmemMax) continue;
         const int fit = kSmSmem / (smem + kSmemReserved + 256);  // CTAs an SM holds
         const int64_t places = (int64_t)sms * fit * few_usable(splits * F::kCtas, fit) / 152;
         const int64_t ctas = tiles * splits, waves = (ctas + places - 1) / places;
@@ -135,14 +122,14 @@ void plan_few_tiles(int T, int N, int nk, bool gated, int sms, bool adapters, in
 // As few tiles of x as its rows need, or up to eight times as many where a narrow matrix leaves SMs idle
 // (256 x 2048 x 2048: 12.9 us with one, 10.0 with two; 128 x 256 x 7168: 9.5 with one, 5.9 with four).
 template <bool PAIR>
-void plan_few(int T, int N, int nk, bool gated, int sms, bool adapters, float& best_us, LinPlan& best) {
+void plan_few(int T, int N, int nk, bool gated, int sms, float& best_us, LinPlan& best) {
     using F = Few<PAIR>;
     const int least = (T + F::kRows - 1) / F::kRows;
     for (int m = 1; m <= 8 && (m == 1 || least * m * F::kStep < T + F::kStep) && least * m <= 65535; m *= 2)
-        plan_few_tiles<PAIR>(T, N, nk, gated, sms, adapters, least * m, best_us, best);
+        plan_few_tiles<PAIR>(T, N, nk, gated, sms, least * m, best_us, best);
 }
 
-inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, bool adapters = false) {
+inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms) {
     LinPlan best{};
     float best_us = 1e30f;
     const float per_k[3] = {0.38f, 0.31f, 0.25f};
@@ -156,75 +143,38 @@ inline LinPlan plan_linear(int T, int N, int nk, bool gated, int sms, bool adapt
             best = LinPlan{false, false, width, 0, 0, 0};
         }
     }
-    plan_few<false>(T, N, nk, gated, sms, adapters, best_us, best);
-    plan_few<true>(T, N, nk, gated, sms, adapters, best_us, best);
+    plan_few<false>(T, N, nk, gated, sms, best_us, best);
+    plan_few<true>(T, N, nk, gated, sms, best_us, best);
     return best;
 }
 
 // ---- the low-rank products of moe_linear_adapters -------------------------------------------------
-constexpr int kLowK = 64;         // elements of K per stage
-constexpr int kLowTile = 128;     // ranks of a tile at most, the MMA's rows
-constexpr int kLowRows = 128;     // rows of x of a group at most, the MMA's columns
-constexpr int kLowStages = 16;
-constexpr int kLowSplits = 8;
-constexpr int kLowLoaders = 6;    // warps that load adapters
+constexpr int kLowGroup = 256;    // rows of a group, and threads
+constexpr int kLowBatch = 32;     // rows of a batch: of one adapter
+constexpr int kLowRanks = 32;     // ranks of an item
+constexpr int kLowSplits = 8;     // CTAs of a cluster at most
+constexpr int kLowLandingMax = 24 * 1024;  // bytes: with the static shared memory below the 48 KB that need no permission
 
 struct LowPlan {
-    int rows, groups, own_log2;  // rows of x per group (a multiple of 16); rows of a CTA of the cluster
-    int unit_log2;               // ranks that are loaded as one
-    int per_adapter_log2;        // units of one adapter, both matrices'
-    int tile, width;             // units of a tile; ranks of a row's landing place
-    int splits, slots;           // CTAs of a cluster, each with a part of K; clusters of a group, which share its tiles
-    int loaders;                 // warps that share the units of the stages: not more than the ring has
-    int stages, stage, smem;     // smem: the ring, the landing places and the adapters' scales
+    int groups, slots, splits;    // slots: clusters of a group, which share its items; splits: CTAs of a cluster, parts of K
+    int landing_rows, smem;       // rows of a batch at most; bytes of the landing area
 };
-// T rows, L adapters of rank R on `matrices` matrices, K in stages of 64.
-inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices, int sms) {
+// Slots for all the items that a group can have, as far as 1024 clusters allow (32 at least), and a cluster of CTAs for each as
+// long as the SMs have room for them and every warp a step of K.
+inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices) {
     LowPlan p{};
-    p.rows = T >= kLowRows ? kLowRows : (T + 15) / 16 * 16;
-    p.groups = (int)(((int64_t)T + p.rows - 1) / p.rows);
-    p.unit_log2 = R <= 16 ? 4 : R <= 32 ? 5 : R <= 64 ? 6 : 7;
-    const int unit = 1 << p.unit_log2;
-    const int per_adapter = (R + unit - 1) / unit * matrices;  // 1, 2 or 4
-    p.per_adapter_log2 = per_adapter >> 1;
-    const int steps = (K + kLowK - 1) / kLowK, here = T < p.rows ? T : p.rows;
-    // Long inputs are prompts, whose groups have an adapter or two: a tile for both, and many stages (4096 gated rows of 7168: a
-    // group with two took 32 us with a tile each, others 21).  Short ones may have one to each row: 128 ranks to a tile.
-    const bool prompt = T > 1024;
-    const int64_t units = (int64_t)(L < here ? L : here) * per_adapter;
-    const int64_t wanted = prompt && 2 * per_adapter < units ? 2 * per_adapter : units;
-    p.tile = kLowTile / unit < wanted ? kLowTile / unit : (int)wanted;
-    const int tiles = prompt ? 1 : (int)((units + p.tile - 1) / p.tile);  // of a group, as far as that goes
-    p.width = (per_adapter < p.tile ? per_adapter : p.tile) * unit;
-    p.stage = (p.tile * unit + p.rows) * 128;
-    // A round of tiles takes 4 us besides its stages, and those what an SM's share of the L2 rate allows (106 GB/s).
-    float best = 1e30f;
-    for (int splits = 1; splits <= kLowSplits && (splits == 1 || 2 * splits <= steps); splits *= 2) {
-        const int64_t places = (int64_t)sms * (splits == 8 ? 120 : splits == 4 ? 144 : 152) / 152 / splits;  // clusters
-        const int64_t fit = places / p.groups;
-        const int slots = fit < 1 ? 1 : fit < tiles ? (int)fit : tiles;
-        const int64_t rounds = (tiles + slots - 1) / slots * (((int64_t)p.groups * slots + places - 1) / places);
-        const float us = (float)rounds * (4.f + (float)((steps + splits - 1) / splits) * (0.05f + (float)p.stage / 106e3f));
-        if (us < best) {
-            best = us;
-            p.splits = splits;
-            p.slots = slots;
-        }
-    }
-    p.own_log2 = 2;
-    while ((p.splits << p.own_log2) < p.rows) ++p.own_log2;
-    const int landing = (p.splits << p.own_log2) * p.width * 4 + kLowRows * 4, share = (steps + p.splits - 1) / p.splits;
-    const int room = T > kLowBeside ? kCtaSmemMax : kLowSmemFew;
-    p.stages = (room - 1024 - landing) / p.stage;
-    p.stages = p.stages < 2 ? 2 : p.stages;
-    p.stages = p.stages < kLowStages ? p.stages : kLowStages;
-    p.stages = p.stages < share ? p.stages : share;
-    p.loaders = p.stages * p.tile < kLowLoaders ? p.stages * p.tile : kLowLoaders;
-    p.smem = p.stages * p.stage + landing + 1024;
-    // the MMA reads 128 rows of a stage, however few of them are ranks
-    const int reach = (p.stages - 1) * p.stage + kLowTile * 128 + 1024, least = smem_for_columns(tmem_columns(p.rows));
-    if (p.smem < reach) p.smem = reach;
-    if (p.smem < least) p.smem = least;
+    const int rows = T < kLowGroup ? T : kLowGroup, steps = (int)(((int64_t)K + 31) / 32);
+    const int batches = (L < rows ? L : rows) + rows / kLowBatch, passes = ((R + 15) / 16 * matrices + 1) / 2;
+    p.groups = (int)(((int64_t)T + kLowGroup - 1) / kLowGroup);
+    p.slots = (batches < rows ? batches : rows) * passes;
+    if (p.slots > 32 && (int64_t)p.slots * p.groups > 1024) p.slots = 1024 / p.groups > 32 ? 1024 / p.groups : 32;
+    p.landing_rows = T < kLowBatch ? T : kLowBatch;
+    const int part = p.landing_rows * kLowRanks * (int)sizeof(float);
+    p.splits = 1;
+    while (p.splits < kLowSplits && 2 * p.splits * part <= kLowLandingMax && 2 * p.splits * (kLowGroup / 32) <= steps &&
+           (int64_t)p.slots * p.groups * p.splits * 2 <= 512)
+        p.splits *= 2;
+    p.smem = p.splits > 1 ? p.splits * part : 0;
     return p;
 }
 

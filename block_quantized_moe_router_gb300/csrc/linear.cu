@@ -21,8 +21,7 @@
 // from the launch before (adapters.cu), which lets this one start before it ends: x and the weights are not
 // its results, so only what reads v waits for it, and v takes no time where the weights take longer.  v is held as
 // two numbers of the layer's type, hi + lo: one rounding to bf16 would cost as much as the result's own.
-//   few rows   the warps that neither load nor issue MMAs compute the addends of this CTA's results meanwhile, by
-//              mma.sync over 8 rows and one adapter at a time, straight from global memory.
+//   few rows   a thread adds its results' low-rank products by FMA, straight from global memory, after the parts of K.
 //   many rows  a tile's accumulator takes further stages of K, hi and lo against b[j], for each adapter j that
 //              occurs in it; the MMAs leave out the lanes of the other rows (disable-output-lane).
 // Neither multiplies a row by another row's adapter, so that what is not finite in one stays in its rows.
@@ -41,6 +40,7 @@ namespace {
 using namespace tc;
 
 constexpr int kLinA = 128 * 128;                // bytes of a 128-row operand stage
+constexpr uint32_t kLayoutSw64 = 4, kLayoutSw32 = 6;  // of matrix descriptors: rows of 64 and 32 bytes
 
 struct LinMaps {
     CUtensorMap x, w, v, res, out;
@@ -280,128 +280,29 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 // ------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 
-// The addends v b[j]^T of ROWS weight rows (from feature n0 on, those from `half` on of the second matrix) and `cols`
-// columns (rows t .. t + cols - 1 of x) to dst [row][pitch].  Called by warps 2 to 7.
-//
-// By mma.sync, a column's adapter at a time: A is 16 rows of its b, B the low-rank products of the four columns of the
-// item, and of D only that column is kept, so that a column sees no other one's adapter.  That leaves seven eighths of
-// an MMA unused and still takes half the instructions of plain FMAs, which count: few warps run here, each through code that
-// it meets for the first time.  K may be in any order, so that one 16-byte load a lane serves two MMAs (ranks 8 c to
-// 8 c + 7 for lane c of four, the first four of each in the first MMA).
-//
-// Items of 32 rows and 4 columns, steps of 2 columns and 32 ranks; the next step's loads are under way while one is computed, the first one's while
-// the launch before computes v.  What all others read of b is brought to L2 by then.
-struct AddendLoads {
-    uint4 p[2][4];  // of b: rows g, g + 8, g + 16 and g + 24
-    uint4 hi, lo;   // of v
-};
-template <int ROWS>
-__device__ __forceinline__ void adapter_addends(const AdaptArgs& a, int64_t* at_s, float* dst, int pitch, int half, int n0, int64_t t,
-                                                int cols) {
-    constexpr int kWarps = 6, kBlocks = ROWS / 32;
-    const int warp = (int)(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
-    const int items = cols > 0 ? (cols + 3) / 4 * kBlocks : 0;
-    // where each column's adapter begins, -1 for none
-    for (int c = threadIdx.x - 64; c < (cols + 3) / 4 * 4; c += 32 * kWarps) {
-        const int j = c < cols ? adapter_of(a, t + c) : -1;
-        at_s[c] = j < 0 ? -1 : j * a.sb;
-    }
-    asm volatile("bar.sync 1, 192;" ::: "memory");  // the six warps
-    const auto matrix = [&](int item) { return (int)(item % kBlocks * 32 >= half); };
-    const auto feature = [&](int item) { return n0 + item % kBlocks * 32 - (matrix(item) ? half : 0); };
-    const int64_t eight = 8 * a.ldb;
-    const auto load_b = [&](int item, int r, int first, AddendLoads& to) {
-        const int m = matrix(item), n = feature(item) + g;  // this lane's first feature
-        const bool in = item < items && a.b[m] && r + 8 * c4 < a.R;
-        const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb + 8 * c4 + r;
-        const int64_t* const at = at_s + item / kBlocks * 4 + first;
+// z += v b[j]^T of feature n and up to C consecutive rows from t on, j each row's own adapter (one for the whole warp, whose lanes
+// hold consecutive features), for the first or the second matrix.  v is hi + lo, exact in fp32.
+template <int C>
+__device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int64_t t, int rows, int n, float (&z)[C]) {
+    if (!a.b[m]) return;
+    const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
+    const uint16_t* const v = a.v + a.planes[m] * a.plane + t * a.R;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int64_t from = in ? at[c] : -1;
+    for (int i = 0; i < C; ++i) {
+        const int j = i < rows ? adapter_of(a, t + i) : -1;
+        if (j < 0) continue;
+#pragma unroll 2
+        for (int r = 0; r < a.R; r += 8) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + j * a.sb + r));
+            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(v + (int64_t)i * a.R + r));
+            const uint4 l = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + (int64_t)i * a.R + r));
+            float f[8] = {}, g[8] = {};
+            add_packed(f, {h.x, h.y, h.z, h.w}, a.f16);
+            add_packed(f, {l.x, l.y, l.z, l.w}, a.f16);
+            add_packed(g, {w.x, w.y, w.z, w.w}, a.f16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                to.p[c][i] = make_uint4(0u, 0u, 0u, 0u);
-                if (from >= 0 && n + 8 * i < a.N) to.p[c][i] = __ldg(reinterpret_cast<const uint4*>(b + from + i * eight));
-            }
+            for (int k = 0; k < 8; ++k) z[i] += f[k] * g[k];
         }
-    };
-    const auto load_v = [&](int item, int r, AddendLoads& to) {
-        const int c = item / kBlocks * 4 + g, m = matrix(item);
-        to.hi = to.lo = make_uint4(0u, 0u, 0u, 0u);
-        if (item < items && g < 4 && a.b[m] && r + 8 * c4 < a.R && at_s[c] >= 0) {
-            const uint16_t* const v = a.v + a.planes[m] * a.plane + (t + c) * a.R + 8 * c4 + r;
-            to.hi = __ldcg(reinterpret_cast<const uint4*>(v));
-            to.lo = __ldcg(reinterpret_cast<const uint4*>(v + a.plane));
-        }
-    };
-    int item = warp, r = 0, first = 0;
-    AddendLoads now;
-    load_b(item, r, first, now);
-#pragma unroll 1
-    for (int i = warp; i < items; i += kWarps) {
-        const int c0 = i / kBlocks * 4, m = matrix(i), n = feature(i) + lane;
-        if (!a.b[m] || n >= a.N) continue;
-        const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
-#pragma unroll 1
-        for (int c = c0; c < c0 + 4; ++c)  // a lane's row of one column, every 64 ranks
-            if (at_s[c] >= 0)
-                for (int k = 0; k < a.R; k += 64) prefetch_l2(b + at_s[c] + k);
-    }
-    __syncwarp();
-    pdl_wait();  // v
-    load_v(item, r, now);
-    float sum[2][4] = {};
-#pragma unroll 1
-    while (item < items) {
-        const int c0 = item / kBlocks * 4, this_item = item, this_first = first;
-        first = first == 0 && cols > c0 + 2 ? 2 : 0;
-        if (first == 0) {
-            r += 32;
-            if (r >= a.R) {
-                r = 0;
-                item += kWarps;
-            }
-        }
-        AddendLoads next;
-        load_b(item, r, first, next);
-        load_v(item, r, next);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (at_s[c0 + this_first + c] < 0) continue;
-            float d[2][4] = {};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 p = now.p[c][2 * i], q = now.p[c][2 * i + 1];
-                if (a.f16) {
-                    mma_f16_16816(d[i], p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
-                    mma_f16_16816(d[i], p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
-                    mma_f16_16816(d[i], p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
-                    mma_f16_16816(d[i], p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
-                } else {
-                    mma_bf16_16816(d[i], p.x, q.x, p.y, q.y, now.hi.x, now.hi.y);
-                    mma_bf16_16816(d[i], p.z, q.z, p.w, q.w, now.hi.z, now.hi.w);
-                    mma_bf16_16816(d[i], p.x, q.x, p.y, q.y, now.lo.x, now.lo.y);
-                    mma_bf16_16816(d[i], p.z, q.z, p.w, q.w, now.lo.z, now.lo.w);
-                }
-            }
-            if (2 * c4 == this_first) {  // columns 2 c4 and 2 c4 + 1 are this lane's
-                sum[0][c] += d[0][c];
-                sum[0][2 + c] += d[0][2 + c];
-                sum[1][c] += d[1][c];
-                sum[1][2 + c] += d[1][2 + c];
-            }
-        }
-        if (item != this_item) {
-            if (c4 < 2) {
-                float* const to = dst + (this_item % kBlocks * 32 + g) * pitch + c0 + 2 * c4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float2*>(to + 8 * i * pitch) = make_float2(sum[i >> 1][2 * (i & 1)], sum[i >> 1][2 * (i & 1) + 1]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[0][i] = sum[1][i] = 0.f;
-        }
-        now = next;
     }
 }
 
@@ -457,8 +358,6 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
     auto give_up = [&]() { status_or(a.status, MOE_DEV_TIMEOUT); };
     const int my_c0 = (int)rank * own, my_cols = min(own, ncols - my_c0);  // this CTA's columns
     const bool direct = splits == 1 && !a.gated;  // a lane has all of its feature: nothing to exchange
-    // with adapters: the addends of this CTA's columns, and behind them where their adapters begin
-    [[maybe_unused]] float* const addends = landing + (direct ? 0 : (int)splits * F::kW * pitch);
     const int steps = k_end - k_begin;
     // The elected lane's role is all that its warp does until the lane is done: the rest of the warp waits at the end of
     // the role, so that nothing it might run shares the warp's uniform registers with the lane's copies and MMAs
@@ -524,22 +423,21 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
             tc_fence_before();
         }
         __syncwarp();
-    } else if (warp >= (ADAPT ? 2 : 6)) {
+    } else if (warp >= 6) {
         // what the end of the kernel reads comes to L2 while the weights stream: 128-byte lines
         if (a.res)
-            for (int i = threadIdx.x - (ADAPT ? 64 : 192); i < my_cols * 2; i += (ADAPT ? 192 : 64)) {
+            for (int i = threadIdx.x - 192; i < my_cols * 2; i += 64) {
                 const int n = n0 + 64 * (i & 1);
                 if (n < a.N && (i & 1) * 64 < per_cta)
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
-        if constexpr (ADAPT) {
-            adapter_addends<F::kW>(a, reinterpret_cast<int64_t*>(addends + F::kW * pitch), addends, pitch, per_cta, n0, (int64_t)t0 + my_c0, my_cols);
-        }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
+    if constexpr (ADAPT) pdl_wait();  // v
     if constexpr (!PAIR) cluster_wait();
     {  // the two warps of a lane quarter take alternate 16 columns
         tc_fence_after();
+        __syncwarp();  // the reads of tensor memory want the whole warp
         const int q = warp & 3;
         const int row = 32 * (PAIR ? q & 1 : q) + lane, c0 = PAIR && q >= 2 ? x_rows : 0;  // of tensor memory column 0
         const uint32_t mine = smem_u32(landing + ((int)rank * F::kW + row) * pitch);
@@ -552,13 +450,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                 float z[16];
                 tmem_ld_16(tmem + ((uint32_t)(32 * q) << 16) + c - c0, reinterpret_cast<uint32_t(&)[16]>(z));
                 tmem_ld_wait();
-                if constexpr (ADAPT) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 p = *reinterpret_cast<const float4*>(addends + row * pitch + c + i);
-                        z[i] += p.x; z[i + 1] += p.y; z[i + 2] += p.z; z[i + 3] += p.w;
-                    }
-                }
+                if constexpr (ADAPT)
+                    if (n < a.N) add_adapters(a, 0, (int64_t)t0 + c, rows, n, z);
                 if (n < a.N) finish_feature(a, (int64_t)t0 + c, rows, n, z, z, rw);
                 __syncwarp();
                 continue;
@@ -598,8 +491,8 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
         ahead(item + kFewThreads / 32);
         float z[4] = {}, u[4] = {};
 #pragma unroll
-        for (int s = 0; s < kFewSplits / F::kCtas + ADAPT; ++s)
-            if (s < (int)splits + ADAPT) {
+        for (int s = 0; s < kFewSplits / F::kCtas; ++s)
+            if (s < (int)splits) {
                 const float4 p = *reinterpret_cast<const float4*>(src + s * F::kW * pitch);
                 z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
                 if (a.gated) {
@@ -608,6 +501,11 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                 }
             }
         const int n = n0 + r;
+        if constexpr (ADAPT)
+            if (n < a.N) {
+                add_adapters(a, 0, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z);
+                if (a.gated) add_adapters(a, 1, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, u);
+            }
         if (n < a.N) finish_feature(a, (int64_t)t0 + my_c0 + c, min(4, my_cols - c), n, z, u, now);
     }
     __syncwarp();
@@ -1179,7 +1077,7 @@ cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int split
     const dim3 grid((N + per_tile - 1) / per_tile * cluster, (a.T + a.rows_t - 1) / a.rows_t);
     static std::atomic<uint64_t> allowed{0};
     return launch_clusters(linear_few_kernel<PAIR, ADAPT>, kCtaSmemMax, allowed, grid, cluster, kFewThreads,
-                           F::smem(a.rows_t, splits, a.stages, few_parts(splits, a.gated, ADAPT), ADAPT), m, a, st);
+                           F::smem(a.rows_t, splits, a.stages), m, a, st);
 }
 
 template <bool ADAPT>
@@ -1195,7 +1093,7 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
     a.func = d.func; a.gated = w_mul != nullptr; a.f16 = d.dtype == MOE_DT_F16;
     a.ldr = d.ldr; a.ldo = d.ldo;
     a.bias = bias; a.bias_mul = bias_mul; a.res = residual; a.out = out; a.status = status;
-    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms, ADAPT);
+    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms);
     MapsOf<ADAPT> m{};
     // rows of W per box, and rows of x
     const int box_w = plan.few ? (plan.pair ? 64 : 128) / (a.gated ? 2 : 1) : plan.width / 2;
