@@ -159,20 +159,21 @@ struct LowPlan {
     int groups, slots, splits;    // slots: clusters of a group, which share its items; splits: CTAs of a cluster, parts of K
     int landing_rows, smem;       // rows of a batch at most; bytes of the landing area
 };
-// Slots for all the items that a group can have, as far as 1024 clusters allow (32 at least), and a cluster of CTAs for each as
-// long as the SMs have room for them and every warp a step of K.
+// Slots for all the items that a group can have, as far as 1024 clusters allow (32 at least); long inputs are prompts, whose
+// groups have an adapter or two, and then for its full batches.  A cluster of CTAs for each as long as all of them are
+// resident, two to an SM, and every warp has a step of K.
 inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices) {
     LowPlan p{};
     const int rows = T < kLowGroup ? T : kLowGroup, steps = (int)(((int64_t)K + 31) / 32);
     const int batches = (L < rows ? L : rows) + rows / kLowBatch, passes = ((R + 15) / 16 * matrices + 1) / 2;
     p.groups = (int)(((int64_t)T + kLowGroup - 1) / kLowGroup);
-    p.slots = (batches < rows ? batches : rows) * passes;
+    p.slots = (T > 1024 ? rows / kLowBatch : batches < rows ? batches : rows) * passes;
     if (p.slots > 32 && (int64_t)p.slots * p.groups > 1024) p.slots = 1024 / p.groups > 32 ? 1024 / p.groups : 32;
     p.landing_rows = T < kLowBatch ? T : kLowBatch;
     const int part = p.landing_rows * kLowRanks * (int)sizeof(float);
     p.splits = 1;
     while (p.splits < kLowSplits && 2 * p.splits * part <= kLowLandingMax && 2 * p.splits * (kLowGroup / 32) <= steps &&
-           (int64_t)p.slots * p.groups * p.splits * 2 <= 512)
+           (int64_t)p.slots * p.groups * p.splits * 2 <= 304)
         p.splits *= 2;
     p.smem = p.splits > 1 ? p.splits * part : 0;
     return p;

@@ -281,27 +281,39 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 constexpr int kFewThreads = 256;
 
 // z += v b[j]^T of feature n and up to C consecutive rows from t on, j each row's own adapter (one for the whole warp, whose lanes
-// hold consecutive features), for the first or the second matrix.  v is hi + lo, exact in fp32.
+// hold consecutive features), for the first or the second matrix.  v is hi + lo, exact in fp32.  Two rows' loads of 8 ranks
+// are under way at once: a row after the other waits for each, four take more registers than there are.
 template <int C>
 __device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int64_t t, int rows, int n, float (&z)[C]) {
     if (!a.b[m]) return;
     const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
     const uint16_t* const v = a.v + a.planes[m] * a.plane + t * a.R;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int j = i < rows ? adapter_of(a, t + i) : -1;
-        if (j < 0) continue;
-#pragma unroll 2
-        for (int r = 0; r < a.R; r += 8) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + j * a.sb + r));
-            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(v + (int64_t)i * a.R + r));
-            const uint4 l = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + (int64_t)i * a.R + r));
-            float f[8] = {}, g[8] = {};
-            add_packed(f, {h.x, h.y, h.z, h.w}, a.f16);
-            add_packed(f, {l.x, l.y, l.z, l.w}, a.f16);
-            add_packed(g, {w.x, w.y, w.z, w.w}, a.f16);
+    for (int c = 0; c < C; c += 2) {
+        int j[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[i] += f[k] * g[k];
+        for (int i = 0; i < 2; ++i) j[i] = c + i < rows ? adapter_of(a, t + c + i) : -1;
+        if (max(j[0], j[1]) < 0) continue;
+#pragma unroll 1
+        for (int r = 0; r < a.R; r += 8) {
+            uint4 w[2], h[2], l[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (j[i] >= 0) {
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(b + j[i] * a.sb + r));
+                    h[i] = __ldcg(reinterpret_cast<const uint4*>(v + (int64_t)(c + i) * a.R + r));
+                    l[i] = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + (int64_t)(c + i) * a.R + r));
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (j[i] >= 0) {
+                    float f[8] = {}, g[8] = {};
+                    add_packed(f, {h[i].x, h[i].y, h[i].z, h[i].w}, a.f16);
+                    add_packed(f, {l[i].x, l[i].y, l[i].z, l[i].w}, a.f16);
+                    add_packed(g, {w[i].x, w[i].y, w[i].z, w[i].w}, a.f16);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) z[c + i] += f[k] * g[k];
+                }
         }
     }
 }
@@ -431,6 +443,16 @@ linear_few_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_const
                 if (n < a.N && (i & 1) * 64 < per_cta)
                     prefetch_l2(static_cast<const uint16_t*>(a.res) + ((int64_t)t0 + my_c0 + (i >> 1)) * a.ldr + n);
             }
+        if constexpr (ADAPT) {
+            // and of b: a lane's row of one column's adapter
+            const int blocks = F::kW / 32;
+            for (int i = warp - 6; i < my_cols * blocks; i += 2) {
+                const int row = i % blocks * 32, m = row >= per_cta, n = n0 + row - (m ? per_cta : 0) + lane;
+                const int j = adapter_of(a, (int64_t)t0 + my_c0 + i / blocks);
+                if (j >= 0 && a.b[m] && n < a.N)
+                    for (int r = 0; r < a.R; r += 64) prefetch_l2(static_cast<const uint16_t*>(a.b[m]) + j * a.sb + n * a.ldb + r);
+            }
+        }
     }
     __syncthreads();  // all wait here for that: a barrier, not polls, beside the threads that feed the MMAs
     if constexpr (ADAPT) pdl_wait();  // v
