@@ -7,10 +7,14 @@
 // order, so a lane's four 16-bit pairs of one 16-byte load serve as the operands of two MMAs, the same way on both sides.
 // K is split over the warps of a CTA and the CTAs of a cluster; the parts meet in shared memory and are added in
 // order.  A batch of one token costs its adapter's bytes, a prompt's its rows of x, read here before the layer
-// reads them again from L2: neither has work for tcgen05 (16 to 64 ranks of 128 lanes).
+// reads them again from L2.  tcgen05 would take 128 lanes for 16 to 64 ranks.
 //
 // Which adapters occur is known on the device alone: every CTA of a group finds the batches by itself (a comparison
 // with the ids before it per row), so that no launch has to sort them.
+//
+// Alone and cold, 1 gated row of 7168, rank 16: 8 to 11 us, latency; 512 rows of 2048 with 32 adapters: 13 us; 16384 rows of 2048,
+// rank 64: 65 us, the loads of x for every 32 ranks and of a for every 32 rows from L2.  A whole call with the layer: 16.9 us for
+// that one row, 36 for 64 gated rows of 4096 with an adapter each, 182 for 4096 gated rows of 7168, 363 for those 16384.
 #include "cluster.cuh"
 #include "kernels.h"
 #include "launch_plan.h"

@@ -46,3 +46,26 @@ def test_drawn(cuda_lib, seed):
     for c, (wide, out) in zip(cases, outs):
         _check(out.clone(), *_reference(c))
         assert torch.isnan(wide[:, out.shape[1]:].float()).all()
+
+
+@pytest.mark.parametrize("T,N,K,R,L,gated", [(2107, 51, 2632, 48, 96, True), (1100, 40, 264, 256, 300, True), (1025, 9, 8, 8, 1000, False)])
+def test_long_inputs_of_many_adapters(cuda_lib, T, N, K, R, L, gated):
+    """Prompts are expected to have an adapter or two to a group of rows; many are as right."""
+    c = _make(T, N, K, R, L, DT["f16"], "holes", gated, bias=True, residual=True, func=capi.MOE_FUNC_RELU, seed=T)
+    out = torch.full((T, N), float("nan"), dtype=torch.float16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda o, ws: capi.moe_linear_adapters(c["x"], c["w"], o, c["ids"], a=c["a"], b=c["b"], a_mul=c["a_mul"], b_mul=c["b_mul"],
+                                                  scale=c["scale"], w_mul=c["w_mul"], bias=c["bias"], bias_mul=c["bias_mul"],
+                                                  residual=c["residual"], func=c["func"], workspace=ws, dev_status=status)
+    call(out, _workspace(c))
+    torch.cuda.synchronize()
+    _check(out, *_reference(c))
+    # two streams at once, a workspace each
+    others, spaces, streams = [torch.empty_like(out) for _ in range(2)], [_workspace(c) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o, ws, s in zip(others, spaces, streams):
+            with torch.cuda.stream(s):
+                call(o, ws)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and all(torch.equal(o, out) for o in others)
