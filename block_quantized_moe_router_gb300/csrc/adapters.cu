@@ -57,9 +57,9 @@ __device__ __forceinline__ void low_rank_sums(float (&d)[2][4][4], const uint16_
             const int k = 32 * (step + u * stride) + c8;
             const bool in = step + u * stride < end && k < K;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[u][i] = in && rank[i] ? ldg_stream128(rank[i] + k) : zero;
+            for (int i = 0; i < 4; ++i) w[u][i] = in && rank[i] ? __ldcg(reinterpret_cast<const uint4*>(rank[i] + k)) : zero;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) x[u][i] = in && row[i] ? ldg_cached128(row[i] + k) : zero;
+            for (int i = 0; i < NB; ++i) x[u][i] = in && row[i] ? __ldcg(reinterpret_cast<const uint4*>(row[i] + k)) : zero;
         }
         __syncwarp();  // the MMAs want the whole warp, and the loads above may part it
 #pragma unroll
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
     const int ctas = (int)cluster_size(), cta = (int)cluster_rank(), slot = (int)blockIdx.x / ctas;
     if (ctas > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     const int64_t t0 = (int64_t)blockIdx.y * kGroup;
-    int id = t0 + tid < g.T ? __ldg(g.ids + t0 + tid) : -1;
+    int id = t0 + tid < g.T ? __ldcg(g.ids + t0 + tid) : -1;
     if (id < -1 || id >= g.L) {
         if (blockIdx.x == 0) status_or(g.status, MOE_DEV_BAD_ADAPTER_ID);
         id = -1;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
         }
         const int block = 2 * pass + (at_rank >> 4), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + (at_rank & 15);
         if (cta == 0 && at_row < rows && block < per_matrix * g.matrices && r < g.R) {  // R is a multiple of 8: all four or none
-            const float s = g.scale ? __ldg(g.scale + j) : 1.f;
+            const float s = g.scale ? __ldcg(g.scale + j) : 1.f;
             const float v[4] = {z.x * s, z.y * s, z.z * s, z.w * s};
             uint16_t hi[4], lo[4];
 #pragma unroll

@@ -73,7 +73,7 @@ sandwich_norm_kernel(BlockNormArgs a) {
             if (r) rv[i] = load_vec<S, MODE, VEC>(r, c0, a.H);
         }
     }
-    float g = a.row_gate ? __ldg(a.row_gate + t) : 1.f;
+    float g = a.row_gate ? __ldcg(a.row_gate + t) : 1.f;
     if (a.sigmoid) g = 1.f / (1.f + __expf(-g));
     if (a.post) {
         float sq = 0.f;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 256, V == 2 ? 3 : 4) sandwich_r
             if (r) rv[i] = load_raw(r + c0);
         }
     }
-    float g = a.row_gate ? __ldg(a.row_gate + t) : 1.f;
+    float g = a.row_gate ? __ldcg(a.row_gate + t) : 1.f;
     if (a.sigmoid) g = 1.f / (1.f + __expf(-g));
     if (a.post) {
         float sq = 0.f;

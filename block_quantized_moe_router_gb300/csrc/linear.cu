@@ -81,7 +81,7 @@ using ArgsOf = std::conditional_t<ADAPT, AdaptArgs, LinArgs>;
 
 // The adapter of row t; -1 for none (an id out of its range was reported by the launch before).
 __device__ __forceinline__ int adapter_of(const AdaptArgs& a, int64_t t) {
-    const int j = t < a.T ? __ldg(a.ids + t) : -1;
+    const int j = t < a.T ? __ldcg(a.ids + t) : -1;
     return j >= 0 && j < a.L ? j : -1;
 }
 
@@ -213,7 +213,7 @@ __device__ __forceinline__ void load_residual(const LinArgs& a, int64_t t, int r
 template <int C>
 __device__ __forceinline__ void finish_feature(const LinArgs& a, int64_t t, int rows, int n, float (&z)[C],
                                                const float (&u)[C], const uint32_t (&rw)[C]) {
-    const float b = a.bias ? __ldg(a.bias + n) : 0.f, c = a.bias_mul ? __ldg(a.bias_mul + n) : 0.f;
+    const float b = a.bias ? a.bias[n] : 0.f, c = a.bias_mul ? a.bias_mul[n] : 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) z[i] += b;
     apply_func(a.func, z);
@@ -300,7 +300,7 @@ __device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int64_t 
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (j[i] >= 0) {
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(b + j[i] * a.sb + r));
+                    w[i] = *reinterpret_cast<const uint4*>(b + j[i] * a.sb + r);
                     h[i] = __ldcg(reinterpret_cast<const uint4*>(v + (int64_t)(c + i) * a.R + r));
                     l[i] = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + (int64_t)(c + i) * a.R + r));
                 }
@@ -956,7 +956,7 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                 for (int j = 0; j < 4; ++j) {
                     const float* src = j < 2 ? a.bias : a.bias_mul;
                     const int f = fp + lane + 32 * (j & 1);
-                    bias_s[buf][lane + 32 * j] = src && f < a.N ? __ldg(src + f) : 0.f;
+                    bias_s[buf][lane + 32 * j] = src && f < a.N ? src[f] : 0.f;
                 }
             }
             if (a.res && !by_tma) {

@@ -505,10 +505,10 @@ topk_grouped_kernel(const float* __restrict__ logits, const float* __restrict__ 
     const float* row = logits + t * P.E;
     float raw[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) raw[j] = lane + 32 * j < P.E ? __ldg(row + lane + 32 * j) : 0.f;
+    for (int j = 0; j < EPL; ++j) raw[j] = lane + 32 * j < P.E ? __ldcg(row + lane + 32 * j) : 0.f;
     float bv[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) bv[j] = bias && lane + 32 * j < P.E ? __ldg(bias + lane + 32 * j) : 0.f;
+    for (int j = 0; j < EPL; ++j) bv[j] = bias && lane + 32 * j < P.E ? bias[lane + 32 * j] : 0.f;
     route_token<EPL>(P, raw, bv, row, bias, &scratch[warp], lane, ids + t * P.k, wout + t * P.k, status);
 }
 
@@ -660,7 +660,7 @@ route_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant
     }
     float bv[EPL];  // on its way while the parts land
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) bv[j] = a.bias && lane + 32 * j < experts ? __ldg(a.bias + lane + 32 * j) : 0.f;
+    for (int j = 0; j < EPL; ++j) bv[j] = a.bias && lane + 32 * j < experts ? a.bias[lane + 32 * j] : 0.f;
     __syncthreads();
     cluster_sync();  // every part has landed
     if (warp == 1) {
