@@ -159,20 +159,27 @@ class MoeLayer:
         except Exception:
             pass
 
-    def workspace(self, T: int) -> torch.Tensor:
-        self._ws = self._grown(self._ws, capi.moe_workspace_size(self.desc, T, self.act))
+    def workspace(self, T: int, stream=None) -> torch.Tensor:
+        """Scratch memory for T tokens, for work on `stream` (the current one by default).  One call of a layer uses it at a
+        time: calls on several streams have to wait for one another."""
+        self._ws = self._grown(self._ws, capi.moe_workspace_size(self.desc, T, self.act), stream)
         return self._ws
 
-    def _grown(self, ws, need):
+    def _grown(self, ws, need, stream=None):
         """`ws`, or a larger one in its place.  The one that was outgrown stays with the layer: a captured graph keeps
-        its address, another stream may still be using it.  Steps of half of it at least bound the sum of them all."""
+        its address, another stream may still be using it.  Steps of half of it at least bound the sum of them all.
+        The new one comes from the pool of the stream that uses it: memory that another stream's pool hands out may
+        still be in use by work queued there."""
         if ws is not None and ws.numel() >= need:
             return ws
         size = max(need, 256)
         if ws is not None:
             self._outgrown.append(ws)
             size = max(size, ws.numel() + ws.numel() // 2)
-        return torch.empty(size, dtype=torch.uint8, device="cuda")
+        if stream is None:
+            return torch.empty(size, dtype=torch.uint8, device="cuda")
+        with torch.cuda.stream(stream):
+            return torch.empty(size, dtype=torch.uint8, device="cuda")
 
     def route(self, x=None, *, token_ids=None, logits_in=None, topk_ids=None, topk_w=None,
               logits_out=None, stream=None):
@@ -210,7 +217,7 @@ class MoeLayer:
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
         capi.moe_ffn_forward(self.handle, T, self.act, self.g_act1, self.g_act2, x, topk_ids,
-                             topk_w, out, self.workspace(T), dev_status=self.status, stream=stream)
+                             topk_w, out, self.workspace(T, stream), dev_status=self.status, stream=stream)
         self._add_shared(x, out, stream, adapter_ids)
         return out
 
@@ -246,7 +253,8 @@ class MoeLayer:
         if not given:
             return capi.moe_linear(x, w, out, dev_status=self.status, **kw)
         self._ws_adapters = self._grown(self._ws_adapters,
-                                        capi.moe_adapter_workspace_size(x.shape[0], given[0].shape[1], len(given)))
+                                        capi.moe_adapter_workspace_size(x.shape[0], given[0].shape[1], len(given)),
+                                        kw.get("stream"))
         capi.moe_linear_adapters(x, w, out, ids, scale=ad.get("scale"), workspace=self._ws_adapters,
                                  dev_status=self.status, **pairs, **kw)
 
@@ -312,7 +320,7 @@ class MoeLayer:
                             vocab=0 if self.tid2eid is None else self.tid2eid.shape[0],
                             token_ids=token_ids, zero_experts=self.zero_experts)
         capi.moe_forward(self.handle, d, self.act, self.g_act1, self.g_act2, x, topk_ids, topk_w,
-                         out, self.workspace(T), logits_in=logits_in, logits_out=logits_out,
+                         out, self.workspace(T, stream), logits_in=logits_in, logits_out=logits_out,
                          dev_status=self.status, stream=stream)
         self._add_shared(x, out, stream, adapter_ids)
         return out, topk_ids, topk_w, logits_out
@@ -335,7 +343,7 @@ class MoeLayer:
                                 zero_experts=self.zero_experts)
             cached = self._host_route[T] = (d, capi.moe_workspace_size_host(self.desc, T, self.act))
         d, need = cached
-        self._ws_host = self._grown(self._ws_host, need)
+        self._ws_host = self._grown(self._ws_host, need, stream)
         capi.moe_forward_host(self.handle, d, self.act, self.g_act1, self.g_act2, x_host, out_host,
                               self._ws_host, token_ids_host=token_ids_host,
                               topk_ids_host=topk_ids_host, topk_w_host=topk_w_host,
