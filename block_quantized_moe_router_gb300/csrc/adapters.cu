@@ -29,11 +29,14 @@ constexpr int kGroup = kLowGroup, kBatch = kLowBatch, kRanks = kLowRanks;
 
 struct LowRankArgs {
     int T, K, R, L, f16, matrices, slots, landing_rows;  // landing_rows: of a batch at most
-    int64_t ldx, lda, sa, plane;  // plane: elements of a plane of v
+    int64_t ldx, lda, sa, plane, far_plane, marks_plane;  // elements of a plane of v, of far and of marks
     const uint16_t *x, *a[2];
     const float* scale;
     const int32_t* ids;
+    float* whole;  // v as it is; or nullptr, and v in two numbers
     uint16_t* v;
+    float* far;
+    uint8_t* marks;
     int32_t* status;
 };
 
@@ -180,25 +183,46 @@ __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
             }
         }
         const int block = 2 * pass + (at_rank >> 4), m = block >= per_matrix, r = 16 * (block - m * per_matrix) + (at_rank & 15);
-        if (cta == 0 && at_row < rows && block < per_matrix * g.matrices && r < g.R) {  // R is a multiple of 8: all four or none
-            const float s = g.scale ? __ldcg(g.scale + j) : 1.f;
-            const float v[4] = {z.x * s, z.y * s, z.z * s, z.w * s};
-            uint16_t hi[4], lo[4];
+        // R is a multiple of 8: all four ranks or none
+        const bool mine = cta == 0 && at_row < rows && block < per_matrix * g.matrices && r < g.R;
+        const float s = g.scale ? __ldcg(g.scale + j) : 1.f;
+        const float v[4] = {z.x * s, z.y * s, z.z * s, z.w * s};
+        const int64_t t = mine ? t0 + batch_row[at_row] : 0;
+        if (g.whole) {
+            if (mine) *reinterpret_cast<float4*>(g.whole + m * g.plane + t * g.R + r) = make_float4(v[0], v[1], v[2], v[3]);
+            if (ctas > 1) cluster_sync();  // the landing area is free
+            __syncthreads();               // and the batch's rows
+            continue;
+        }
+        float far[4] = {};
+        uint16_t hi[4], lo[4];
+        bool beyond = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // an infinite hi has no rest
-                if constexpr (F16) {
-                    const __half h = __float2half_rn(v[i]);
-                    hi[i] = __half_as_ushort(h);
-                    lo[i] = (hi[i] & 0x7C00u) == 0x7C00u ? 0 : __half_as_ushort(__float2half_rn(v[i] - __half2float(h)));
-                } else {
-                    const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
-                    hi[i] = __bfloat16_as_ushort(h);
-                    lo[i] = (hi[i] & 0x7F80u) == 0x7F80u ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(v[i] - __bfloat162float(h)));
-                }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F16) {
+                const __half h = __float2half_rn(v[i]);
+                hi[i] = __half_as_ushort(h);
+                lo[i] = __half_as_ushort(__float2half_rn(v[i] - __half2float(h)));
+            } else {
+                const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+                hi[i] = __bfloat16_as_ushort(h);
+                lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i] - __bfloat162float(h)));
             }
-            uint16_t* to = g.v + 2 * m * g.plane + (t0 + batch_row[at_row]) * g.R + r;
+            constexpr uint16_t kInf = F16 ? 0x7C00u : 0x7F80u;
+            if ((hi[i] & kInf) == kInf) {  // the type does not hold it
+                beyond = mine;
+                far[i] = v[i];
+                hi[i] = lo[i] = 0;
+            }
+        }
+        // the four lanes of a block of 16 ranks stand side by side
+        const bool marked = (__ballot_sync(0xffffffffu, beyond) >> (lane & 28)) & 15u;
+        if (mine) {
+            uint16_t* to = g.v + 2 * m * g.plane + t * g.R + r;
             *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
             *reinterpret_cast<uint2*>(to + g.plane) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+            if (marked) *reinterpret_cast<float4*>(g.far + m * g.far_plane + t * g.R + r) = make_float4(far[0], far[1], far[2], far[3]);
+            if (r % kFarRanks == 0) g.marks[m * g.marks_plane + t * kFarMarks + r / kFarRanks] = marked;
         }
         if (ctas > 1) cluster_sync();  // the landing area is free
         __syncthreads();               // and the batch's rows
@@ -228,15 +252,22 @@ cudaError_t launch_low_rank(const LowRankArgs& g, int groups, int splits, int sm
 cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                    const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                    void* out, void* workspace, int32_t* status, cudaStream_t st) {
+    LinPlan layer;
+    const cudaError_t planned = plan_layer(d, w_mul != nullptr, layer);
+    if (planned != cudaSuccess) return planned;
     const AdapterProducts p = AdapterProducts::plan(d.T, ad.R, ad.a && ad.a_mul ? 2 : 1);
     LowRankArgs g{};
     g.T = d.T; g.K = d.K; g.R = ad.R; g.L = ad.L; g.f16 = d.dtype == MOE_DT_F16; g.matrices = p.matrices;
-    g.ldx = d.ldx; g.lda = ad.lda; g.sa = ad.sa; g.plane = (int64_t)(p.plane / 2);
+    g.ldx = d.ldx; g.lda = ad.lda; g.sa = ad.sa;
+    g.plane = (int64_t)(p.plane / sizeof(uint16_t)); g.far_plane = (int64_t)(p.far_plane / sizeof(float)); g.marks_plane = (int64_t)p.marks_plane;
     g.x = static_cast<const uint16_t*>(x);
     g.a[0] = static_cast<const uint16_t*>(ad.a ? ad.a : ad.a_mul);
     g.a[1] = static_cast<const uint16_t*>(ad.a_mul);
     g.scale = ad.scale; g.ids = ad.ids;
+    g.whole = layer.few ? static_cast<float*>(workspace) : nullptr;
     g.v = static_cast<uint16_t*>(workspace);
+    g.far = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.far);
+    g.marks = static_cast<uint8_t*>(workspace) + p.marks;
     g.status = status;
     const LowPlan plan = plan_low_rank(d.T, d.K, ad.L, ad.R, p.matrices);
     g.slots = plan.slots;
@@ -248,12 +279,15 @@ cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_d
         const int64_t t = (int64_t)first * kGroup;
         h.x += t * g.ldx;
         h.ids += t;
+        if (h.whole) h.whole += t * g.R;
         h.v += t * g.R;
+        h.far += t * g.R;
+        h.marks += t * kFarMarks;
         h.T = (int)(g.T - t);
         const cudaError_t err = g.f16 ? launch_low_rank<true>(h, n, plan.splits, plan.smem, st) : launch_low_rank<false>(h, n, plan.splits, plan.smem, st);
         if (err != cudaSuccess) return err;
     }
-    return launch_adapted_linear(d, ad, x, w, w_mul, bias, bias_mul, residual, out, workspace, status, st);
+    return launch_adapted_linear(layer, d, ad, x, w, w_mul, bias, bias_mul, residual, out, workspace, status, st);
 }
 
 }  // namespace moe

@@ -52,22 +52,35 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc& d, const void* x, const voi
 // ---- low-rank adapters (adapters.cu), norms around a block (block_norm.cu) -------------------
 constexpr int kMaxRank = 256;
 constexpr int kMaxAdapters = 1 << 20;
-// The low-rank products v = scale x a^T of every row, in the workspace: for each matrix two planes [T][R] of the
-// layer's type, whose sum is v.
+// The low-rank products v = scale x a^T of every row, in the workspace.  Where the layer takes few rows they are floats [T][R] for
+// each matrix, over both of its first planes.  Where it takes many they are two planes [T][R] of the
+// layer's type, hi and lo, whose sum is v where that type holds v.  Where it does not (beyond f16's 65504, infinite, NaN)
+// hi and lo are 0 and v stands in a plane `far` [T][R] of floats; of far, blocks of kFarRanks ranks with such a v are written,
+// with 0 for the others, and a byte of `marks` [T][kFarMarks] tells whether the row's block is one.
+constexpr int kFarRanks = 16, kFarMarks = kMaxRank / kFarRanks;
 struct AdapterProducts {
     int matrices;
-    size_t plane, total;  // bytes of a plane, and of all
+    size_t plane, far_plane, marks_plane;  // bytes of a plane of each
+    size_t far, marks, total;              // where they begin, behind all planes of hi and lo; bytes of all
     static AdapterProducts plan(int64_t T, int R, int matrices) {
+        const auto whole = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
         AdapterProducts p;
         p.matrices = matrices;
-        p.plane = ((size_t)T * R * 2 + 255) / 256 * 256;
-        p.total = p.plane * 2 * matrices;
+        p.plane = whole((size_t)T * R * 2);
+        p.far_plane = whole((size_t)T * R * 4);
+        p.marks_plane = whole((size_t)T * kFarMarks);
+        p.far = p.plane * 2 * matrices;
+        p.marks = p.far + p.far_plane * matrices;
+        p.total = p.marks + p.marks_plane * matrices;
         return p;
     }
 };
-// The layer, given v (linear.cu).  It starts before the launch that computes v ends, which has to wait for all before
+struct LinPlan;
+// How the layer is launched on the current device.
+cudaError_t plan_layer(const moe_linear_desc& d, bool gated, LinPlan& plan);
+// The layer so launched, given v (linear.cu).  It starts before the launch that computes v ends, which has to wait for all before
 // it before it triggers.
-cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
+cudaError_t launch_adapted_linear(const LinPlan& plan, const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                   const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                   void* out, const void* v, int32_t* status, cudaStream_t st);
 cudaError_t launch_linear_adapters(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,

@@ -19,11 +19,15 @@
 //
 // With low-rank adapters (ADAPT) each row's product gains v b[j]^T, v = scale x a[j]^T, before the function.  v comes
 // from the launch before (adapters.cu), which lets this one start before it ends: x and the weights are not
-// its results, so only what reads v waits for it, and v takes no time where the weights take longer.  v is held as
-// two numbers of the layer's type, hi + lo: one rounding to bf16 would cost as much as the result's own.
+// its results, so only what reads v waits for it, and v takes no time where the weights take longer.
 //   few rows   a thread adds its results' low-rank products by FMA, straight from global memory, after the parts of K.
-//   many rows  a tile's accumulator takes further stages of K, hi and lo against b[j], for each adapter j that
-//              occurs in it; the MMAs leave out the lanes of the other rows (disable-output-lane).
+//              v is fp32.
+//   many rows  a tile's accumulator takes further stages of K, v against b[j], for each adapter j that
+//              occurs in it; the MMAs leave out the lanes of the other rows (disable-output-lane).  v is held as two numbers
+//              of the layer's type, hi + lo, which is what the MMAs take: one rounding to bf16 would cost as much as the
+//              result's own, two leave 2^-16 of v (f16: 2^-22, and 2^-25 besides).  What that type does not hold (f16 beyond 65504, infinities) never
+//              meets the MMAs, where it would reach the other matrix's columns as 0 times infinity: it is added in
+//              fp32 behind them, to the rows that have it.
 // Neither multiplies a row by another row's adapter, so that what is not finite in one stays in its rows.
 #include "cluster.cuh"
 #include "common.cuh"
@@ -71,6 +75,9 @@ struct AdaptArgs : LinArgs {
     int64_t plane, ldb, sb;  // elements of a plane of v; between rows of b and between its adapters
     const void* b[2];        // nullptr for a matrix without adapters
     const uint16_t* v;
+    const float* far;        // what v does not hold (AdapterProducts)
+    const uint8_t* marks;
+    int64_t far_plane, marks_plane;
     const int32_t* ids;
 };
 
@@ -281,13 +288,13 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
 constexpr int kFewThreads = 256;
 
 // z += v b[j]^T of feature n and up to C consecutive rows from t on, j each row's own adapter (one for the whole warp, whose lanes
-// hold consecutive features), for the first or the second matrix.  v is hi + lo, exact in fp32.  Two rows' loads of 8 ranks
+// hold consecutive features), for the first or the second matrix.  Two rows' loads of 8 ranks
 // are under way at once: a row after the other waits for each, four take more registers than there are.
 template <int C>
 __device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int64_t t, int rows, int n, float (&z)[C]) {
     if (!a.b[m]) return;
     const uint16_t* const b = static_cast<const uint16_t*>(a.b[m]) + n * a.ldb;
-    const uint16_t* const v = a.v + a.planes[m] * a.plane + t * a.R;
+    const float* const v = reinterpret_cast<const float*>(a.v + a.planes[m] * a.plane) + t * a.R;
 #pragma unroll
     for (int c = 0; c < C; c += 2) {
         int j[2];
@@ -296,20 +303,20 @@ __device__ __forceinline__ void add_adapters(const AdaptArgs& a, int m, int64_t 
         if (max(j[0], j[1]) < 0) continue;
 #pragma unroll 1
         for (int r = 0; r < a.R; r += 8) {
-            uint4 w[2], h[2], l[2];
+            uint4 w[2];
+            float4 lo[2], hi[2];  // of the eight
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (j[i] >= 0) {
                     w[i] = *reinterpret_cast<const uint4*>(b + j[i] * a.sb + r);
-                    h[i] = __ldcg(reinterpret_cast<const uint4*>(v + (int64_t)(c + i) * a.R + r));
-                    l[i] = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + (int64_t)(c + i) * a.R + r));
+                    lo[i] = __ldcg(reinterpret_cast<const float4*>(v + (int64_t)(c + i) * a.R + r));
+                    hi[i] = __ldcg(reinterpret_cast<const float4*>(v + (int64_t)(c + i) * a.R + r + 4));
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (j[i] >= 0) {
-                    float f[8] = {}, g[8] = {};
-                    add_packed(f, {h[i].x, h[i].y, h[i].z, h[i].w}, a.f16);
-                    add_packed(f, {l[i].x, l[i].y, l[i].z, l[i].w}, a.f16);
+                    const float f[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+                    float g[8] = {};
                     add_packed(g, {w[i].x, w[i].y, w[i].z, w[i].w}, a.f16);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) z[c + i] += f[k] * g[k];
@@ -605,6 +612,43 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
                      reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
+// The blocks of kFarRanks ranks of row t that hold values beyond the layer's type, a bit each, for one of the matrices.
+__device__ __forceinline__ uint32_t far_blocks(const AdaptArgs& a, int m, int64_t t) {
+    if (a.planes[m] < 0) return 0;
+    const uint4 w = __ldcg(reinterpret_cast<const uint4*>(a.marks + (a.planes[m] >> 1) * a.marks_plane + t * kFarMarks));
+    const uint32_t bytes[4] = {w.x, w.y, w.z, w.w};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits |= ((bytes[i] & 0x01010101u) * 0x01020408u >> 24) << 4 * i;  // byte k's lowest bit to bit k
+    return bits & ((1u << ((a.R + kFarRanks - 1) / kFarRanks)) - 1u);  // none is written behind the ranks
+}
+// z += such values times adapter j's b, in fp32: features n to n + C - 1 of row t.  Rare, and written to be small: every value takes
+// its turn, and its place among the registers is found by comparison.
+template <int C>
+__device__ __forceinline__ void add_far(const AdaptArgs& a, int m, int64_t t, int j, int n, uint32_t blocks, float (&z)[C]) {
+    const uint16_t* b = static_cast<const uint16_t*>(a.b[m]) + j * a.sb + n * a.ldb;
+    const float* const far = a.far + (a.planes[m] >> 1) * a.far_plane + t * a.R;
+#pragma unroll 1
+    for (int i = 0; i < C && n + i < a.N; ++i, b += a.ldb) {
+        float add = 0.f;
+#pragma unroll 1
+        for (uint32_t left = blocks; left; left &= left - 1) {
+            const int r0 = kFarRanks * (__ffs(left) - 1);
+#pragma unroll 1
+            for (int r = r0; r < min(r0 + kFarRanks, a.R); r += 8) {
+                const uint4 w = *reinterpret_cast<const uint4*>(b + r);
+                const float4 lo = __ldcg(reinterpret_cast<const float4*>(far + r)), hi = __ldcg(reinterpret_cast<const float4*>(far + r + 4));
+                float g[8] = {};
+                add_packed(g, {w.x, w.y, w.z, w.w}, a.f16);
+                add += lo.x * g[0] + lo.y * g[1] + lo.z * g[2] + lo.w * g[3] + hi.x * g[4] + hi.y * g[5] + hi.z * g[6] + hi.w * g[7];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            if (k == i) z[k] += add;
+    }
+}
+
 // An adapter of a tile, and the tile's rows that have another one or none; id -1 behind the last.
 struct TileAdapter {
     uint2 off[4];
@@ -837,8 +881,23 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
         const int row = 32 * q + lane, sw = (row >> 1) & 3;
         int n = 0;
         uint32_t pass = 0;
-        for (int64_t i = pair; i < sched.total && !abort_flag; i += pairs, ++n) {
+        for (auto i = sched.begin(pair); i.tile < sched.total && !abort_flag; sched.next(i, pairs), ++n) {
             const int b = n & 1;
+            [[maybe_unused]] int64_t t = 0;  // with adapters: this lane's row, the first feature, the row's adapter and far values
+            [[maybe_unused]] int f0 = 0, j = -1;
+            [[maybe_unused]] uint32_t far[2] = {0, 0};
+            if constexpr (ADAPT) {
+                int r0;
+                first(i, r0, f0);
+                t = (int64_t)r0 + row;
+                j = adapter_of(a, t);
+                pdl_wait();  // marks
+                if (j >= 0) {
+                    far[0] = far_blocks(a, 0, t);
+                    far[1] = far_blocks(a, 1, t);
+                }
+                __syncwarp();
+            }
             if (!__all_sync(0xffffffffu, mbar_wait_suspended(&acc_full[b], (n >> 1) & 1))) {
                 give_up();
                 break;
@@ -854,6 +913,10 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                     tmem_ld_16(trow + 16 * c, reinterpret_cast<uint32_t(&)[16]>(z));
                     if (a.gated) tmem_ld_16(trow + half + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
                     tmem_ld_wait();
+                    if constexpr (ADAPT) {
+                        if (far[0]) add_far(a, 0, t, j, f0 + 16 * c, far[0], z);
+                        if (far[1]) add_far(a, 1, t, j, f0 + 16 * c, far[1], u);
+                    }
                     uint8_t* line = rows_s + buf * 2 * kManySub + ((c >> 1) & 1) * kManySub + row * 64;
                     uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 1)) ^ sw) << 4));
                     uint4* p1 = reinterpret_cast<uint4*>(line + (((2 * (c & 1) + 1) ^ sw) << 4));
@@ -1102,20 +1165,24 @@ cudaError_t launch_few(const MapsOf<ADAPT>& m, const ArgsOf<ADAPT>& a, int split
                            F::smem(a.rows_t, splits, a.stages), m, a, st);
 }
 
+cudaError_t sm_count(int& sms) {
+    int dev = 0;
+    const cudaError_t err = cudaGetDevice(&dev);
+    return err == cudaSuccess ? cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) : err;
+}
+
 template <bool ADAPT>
-cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
+cudaError_t launch_layer(const LinPlan& plan, const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
                          const float* bias, const float* bias_mul, const void* residual, void* out,
                          const moe_adapter_desc* ad, const void* v, int32_t* status, cudaStream_t st) {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t err = sm_count(sms);
     if (err != cudaSuccess) return err;
     ArgsOf<ADAPT> a{};
     a.T = d.T; a.N = d.N; a.nk = (d.K + kLinK - 1) / kLinK;
     a.func = d.func; a.gated = w_mul != nullptr; a.f16 = d.dtype == MOE_DT_F16;
     a.ldr = d.ldr; a.ldo = d.ldo;
     a.bias = bias; a.bias_mul = bias_mul; a.res = residual; a.out = out; a.status = status;
-    const LinPlan plan = plan_linear(d.T, d.N, a.nk, a.gated, sms);
     MapsOf<ADAPT> m{};
     // rows of W per box, and rows of x
     const int box_w = plan.few ? (plan.pair ? 64 : 128) / (a.gated ? 2 : 1) : plan.width / 2;
@@ -1131,6 +1198,10 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
         a.planes[1] = ad->a_mul ? (ad->a ? 2 : 0) : -1;
         a.plane = (int64_t)(p.plane / sizeof(uint16_t));
         a.v = static_cast<const uint16_t*>(v);
+        a.far = reinterpret_cast<const float*>(static_cast<const char*>(v) + p.far);
+        a.marks = static_cast<const uint8_t*>(v) + p.marks;
+        a.far_plane = (int64_t)(p.far_plane / sizeof(float));
+        a.marks_plane = (int64_t)p.marks_plane;
         a.ids = ad->ids;
         if (!plan.few) {
             // Rows of 16, 32 or 64 ranks, swizzled over as many bytes: a stage has room for hi and lo of the rows and 14, 6
@@ -1164,15 +1235,24 @@ cudaError_t launch_layer(const moe_linear_desc& d, const void* x, const void* w,
 
 }  // namespace
 
+cudaError_t plan_layer(const moe_linear_desc& d, bool gated, LinPlan& plan) {
+    int sms = 0;
+    const cudaError_t err = sm_count(sms);
+    if (err == cudaSuccess) plan = plan_linear(d.T, d.N, (d.K + kLinK - 1) / kLinK, gated, sms);
+    return err;
+}
 cudaError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w, const void* w_mul,
                           const float* bias, const float* bias_mul, const void* residual, void* out,
                           int32_t* status, cudaStream_t st) {
-    return launch_layer<false>(d, x, w, w_mul, bias, bias_mul, residual, out, nullptr, nullptr, status, st);
+    LinPlan plan;
+    const cudaError_t err = plan_layer(d, w_mul != nullptr, plan);
+    if (err != cudaSuccess) return err;
+    return launch_layer<false>(plan, d, x, w, w_mul, bias, bias_mul, residual, out, nullptr, nullptr, status, st);
 }
-cudaError_t launch_adapted_linear(const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
+cudaError_t launch_adapted_linear(const LinPlan& plan, const moe_linear_desc& d, const moe_adapter_desc& ad, const void* x, const void* w,
                                   const void* w_mul, const float* bias, const float* bias_mul, const void* residual,
                                   void* out, const void* v, int32_t* status, cudaStream_t st) {
-    return launch_layer<true>(d, x, w, w_mul, bias, bias_mul, residual, out, &ad, v, status, st);
+    return launch_layer<true>(plan, d, x, w, w_mul, bias, bias_mul, residual, out, &ad, v, status, st);
 }
 
 }  // namespace moe

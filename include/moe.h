@@ -269,9 +269,10 @@ moe_status_t moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const vo
  * `lora_gateup` fields, which the pages' layer applies to one request's prompt at a time):
  *   z[t] = x[t] w^T + bias + scale[j] (x[t] a[j]^T) b[j]^T,  j = ids[t], nothing added for j = -1;
  *   u[t] the same of w_mul, bias_mul, a_mul and b_mul;  out = f(z) [* u] [+ residual].
- * x a^T is summed in fp32 and multiplied by the scale; it enters the second product as two numbers of the
- * layer's type whose sum holds 16 bits of it (bf16; f16: 22, as long as it stays within f16's range, where a
- * magnitude beyond 65504 is infinite).  All else as in moe_linear.  A row depends on its own adapter alone:
+ * v = scale[j] x a[j]^T is summed and scaled in fp32.  Where there are many rows it enters the second product as two
+ * numbers of the layer's type, whose sum is off by up to 2^-16 |v| (bf16; f16: 2^-22 |v| + 2^-25, so that 22 bits of
+ * it are held from 2^-3 on and fewer below); elsewhere as fp32, and so does at any number of rows what the type does not
+ * hold.  All else as in moe_linear.  A row depends on its own adapter alone, and each of its factors on that factor's:
  * a NaN or an infinity in one adapter stays in the rows that have it.  Rows of one adapter need not be
  * neighbours; what is read of the adapters are those that occur in ids.  An id outside [-1, L) sets
  * MOE_DEV_BAD_ADAPTER_ID, and its row has no adapter.
