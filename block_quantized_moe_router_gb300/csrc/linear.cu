@@ -27,7 +27,7 @@
 //              of the layer's type, hi + lo, which is what the MMAs take: one rounding to bf16 would cost as much as the
 //              result's own, two leave 2^-16 of v (f16: 2^-22, and 2^-25 besides).  What that type does not hold (f16 beyond 65504, infinities) never
 //              meets the MMAs, where it would reach the other matrix's columns as 0 times infinity: it is added in
-//              fp32 behind them, to the rows that have it.
+//              fp32 behind them, to the rows that have it.  Infinities in b are seen in the results.
 // Neither multiplies a row by another row's adapter, so that what is not finite in one stays in its rows.
 #include "cluster.cuh"
 #include "common.cuh"
@@ -622,31 +622,56 @@ __device__ __forceinline__ uint32_t far_blocks(const AdaptArgs& a, int m, int64_
     for (int i = 0; i < 4; ++i) bits |= ((bytes[i] & 0x01010101u) * 0x01020408u >> 24) << 4 * i;  // byte k's lowest bit to bit k
     return bits & ((1u << ((a.R + kFarRanks - 1) / kFarRanks)) - 1u);  // none is written behind the ranks
 }
-// z += such values times adapter j's b, in fp32: features n to n + C - 1 of row t.  Rare, and written to be small: every value takes
-// its turn, and its place among the registers is found by comparison.
+// z += such values times adapter j's b, in fp32: features n to n + C - 1 of row t.  `deep`: some of z is not finite.  Then a feature
+// whose b holds an infinity or a NaN gets the whole product in fp32 in place of what the MMAs made of hi and lo apart, of
+// which one may be 0 or of the other sign: infinity times v is not the sum of its products with both.  What the layer itself
+// adds is left out there, a number beside something infinite (were it infinite too, the sum might be NaN, and here is not).
+// Rare, and written to be small: every feature takes its turn, and its place among the registers is found by comparison.
 template <int C>
-__device__ __forceinline__ void add_far(const AdaptArgs& a, int m, int64_t t, int j, int n, uint32_t blocks, float (&z)[C]) {
+__device__ __forceinline__ void add_far(const AdaptArgs& a, int m, int64_t t, int j, int n, uint32_t blocks, bool deep, float (&z)[C]) {
     const uint16_t* b = static_cast<const uint16_t*>(a.b[m]) + j * a.sb + n * a.ldb;
+    const uint16_t* const v = a.v + a.planes[m] * a.plane + t * a.R;
     const float* const far = a.far + (a.planes[m] >> 1) * a.far_plane + t * a.R;
 #pragma unroll 1
     for (int i = 0; i < C && n + i < a.N; ++i, b += a.ldb) {
-        float add = 0.f;
+        float add = 0.f, all = 0.f;
+        bool ill = false;
 #pragma unroll 1
-        for (uint32_t left = blocks; left; left &= left - 1) {
-            const int r0 = kFarRanks * (__ffs(left) - 1);
-#pragma unroll 1
-            for (int r = r0; r < min(r0 + kFarRanks, a.R); r += 8) {
-                const uint4 w = *reinterpret_cast<const uint4*>(b + r);
-                const float4 lo = __ldcg(reinterpret_cast<const float4*>(far + r)), hi = __ldcg(reinterpret_cast<const float4*>(far + r + 4));
-                float g[8] = {};
-                add_packed(g, {w.x, w.y, w.z, w.w}, a.f16);
-                add += lo.x * g[0] + lo.y * g[1] + lo.z * g[2] + lo.w * g[3] + hi.x * g[4] + hi.y * g[5] + hi.z * g[6] + hi.w * g[7];
+        for (int r = 0; r < a.R; r += 8) {
+            const bool block = blocks >> (r / kFarRanks) & 1u;
+            if (!block && !deep) continue;
+            const uint4 w = *reinterpret_cast<const uint4*>(b + r);
+            float f[8] = {}, g[8] = {};
+            add_packed(g, {w.x, w.y, w.z, w.w}, a.f16);
+            if (block) {
+                const float4 p = __ldcg(reinterpret_cast<const float4*>(far + r)), q = __ldcg(reinterpret_cast<const float4*>(far + r + 4));
+                f[0] = p.x; f[1] = p.y; f[2] = p.z; f[3] = p.w; f[4] = q.x; f[5] = q.y; f[6] = q.z; f[7] = q.w;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) add += f[k] * g[k];
+            }
+            if (deep) {
+                const uint4 h = __ldcg(reinterpret_cast<const uint4*>(v + r)), l = __ldcg(reinterpret_cast<const uint4*>(v + a.plane + r));
+                add_packed(f, {h.x, h.y, h.z, h.w}, a.f16);
+                add_packed(f, {l.x, l.y, l.z, l.w}, a.f16);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    all += f[k] * g[k];
+                    ill = ill || !isfinite(g[k]);
+                }
             }
         }
 #pragma unroll
         for (int k = 0; k < C; ++k)
-            if (k == i) z[k] += add;
+            if (k == i) z[k] = ill ? all : z[k] + add;
     }
+}
+// Whether some of z is an infinity or a NaN: times 0 those are NaN.
+template <int C>
+__device__ __forceinline__ bool any_infinite(const float (&z)[C]) {
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) q = fmaf(z[i], 0.f, q);
+    return q != 0.f;
 }
 
 // An adapter of a tile, and the tile's rows that have another one or none; id -1 behind the last.
@@ -914,8 +939,11 @@ linear_many_kernel(const __grid_constant__ MapsOf<ADAPT> maps, const __grid_cons
                     if (a.gated) tmem_ld_16(trow + half + 16 * c, reinterpret_cast<uint32_t(&)[16]>(u));
                     tmem_ld_wait();
                     if constexpr (ADAPT) {
-                        if (far[0]) add_far(a, 0, t, j, f0 + 16 * c, far[0], z);
-                        if (far[1]) add_far(a, 1, t, j, f0 + 16 * c, far[1], u);
+                        if (j >= 0) {
+                            const bool deep = any_infinite(z), deep_mul = a.gated && any_infinite(u);
+                            if (a.b[0] && (far[0] || deep)) add_far(a, 0, t, j, f0 + 16 * c, far[0], deep, z);
+                            if (a.b[1] && (far[1] || deep_mul)) add_far(a, 1, t, j, f0 + 16 * c, far[1], deep_mul, u);
+                        }
                     }
                     uint8_t* line = rows_s + buf * 2 * kManySub + ((c >> 1) & 1) * kManySub + row * 64;
                     uint4* p0 = reinterpret_cast<uint4*>(line + (((2 * (c & 1)) ^ sw) << 4));

@@ -89,3 +89,64 @@ def test_small_products_of_few_rows(cuda_lib, T, N, K, R):
     ev = 2.0 ** -20 * K * 2.0 ** -23 * (x.abs() @ a.abs().t()) + 2.0 ** -22 * v.abs()
     bound = ev @ b.abs().t() + (R + 1) * 2.0 ** -23 * (v.abs() @ b.abs().t())
     assert float(((out - ref).abs() - bound - 2.0 ** -11 * ref.abs() - 2.0 ** -25).max()) <= 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,N,K,R", SIZES)
+@pytest.mark.parametrize("form", ["plain", "first", "second"])
+def test_infinite_b(cuda_lib, dt, T, N, K, R, form):
+    """Infinities in an adapter's b make its rows' results infinite at their features, by the signs of the products, also where a
+    product is held exactly in one number of the type; the other features stay what they are."""
+    gated = form != "plain"
+    c = _make(T, N, K, R, 4, DT[dt], "random", gated=gated, residual=True, seed=T + 1)
+    key = "b_mul" if form == "second" else "b"
+    ill = int(c["ids"][0])
+    c["scale"].fill_(1.0)
+    for name in ("a", "a_mul"):  # small whole numbers: products are held in one number, and none is 0
+        if c[name] is not None:
+            c[name].zero_()
+            c[name][:, :, 0] = 1.0
+    c["x"][:, 0] = (torch.arange(T, device="cuda") % 5 + 1) * torch.where(torch.arange(T, device="cuda") % 2 > 0, -1.0, 1.0)
+    b = c[key]
+    clean, b_clean = _run(c).double(), b.clone()
+    b[ill, 5, 2], b[ill, 9, R - 1], b[ill, N - 1, 0] = float("inf"), float("-inf"), float("inf")
+    b[ill, 20, 1], b[ill, 20, 3] = float("inf"), float("-inf")   # infinity minus infinity
+    b[ill, 30, 1], b[ill, 30, 3] = float("inf"), float("inf")
+    z = _product(c["x"], c["w"], c["a"], c["b"], c["scale"], c["ids"], 4)
+    y = z
+    if gated:
+        y = z * _product(c["x"], c["w_mul"], c["a_mul"], c["b_mul"], c["scale"], c["ids"], 4)
+    y = y + c["residual"].double()
+    out = _run(c).double()
+    touched = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    touched[:, [5, 9, 20, 30, N - 1]] = (c["ids"] == ill)[:, None]
+    assert torch.equal(torch.isnan(out), torch.isnan(y)) and bool(torch.isnan(y[touched]).any())
+    assert torch.equal(out[touched & ~torch.isnan(y)], y[touched & ~torch.isnan(y)]) and not torch.isfinite(y[touched]).any()
+    assert torch.equal(out[~touched], clean[~touched])
+    c[key] = b_clean
+    _check(_run(c), *_reference(c))
+
+
+@pytest.mark.parametrize("T,N,K,R", SIZES)
+def test_infinite_product_and_b(cuda_lib, T, N, K, R):
+    """An infinite product (a row of x) against finite b, infinite b and zeros in b: infinite by signs, infinite, NaN."""
+    c = _make(T, N, K, R, 3, DT["bf16"], "one", residual=True, seed=T + 2)
+    c["w"].zero_()
+    c["a"].zero_()
+    c["a"][1, 0, 0], c["a"][1, 1, 1] = 1.0, 1.0  # product 0 is x[0], product 1 is x[1], the others 0
+    c["x"][:, :2] = c["x"][:, :2].abs() + 0.5
+    t = T - 1
+    c["a"][1, 0, 0], c["scale"][1] = 2.0 ** 100, 2.0 ** 100  # times x: beyond fp32
+    c["x"][:, 0] = 0
+    c["x"][t, 0] = 1.0
+    c["b"][1, 0, 0], c["b"][1, 1, 0], c["b"][1, 2, 0], c["b"][1, 3, 0] = 3.0, -2.0, float("inf"), 0.0
+    c["b"][1, 0:4, 1:] = 0.0
+    c["b"][1, 4:, 0] = 1.0
+    out = _run(c).double()
+    inf = float("inf")
+    assert out[t, :3].tolist() == [inf, -inf, inf] and torch.isnan(out[t, 3]) and bool((out[t, 4:] == inf).all())
+    rest = out[:t]
+    assert torch.isnan(rest[:, 2]).all()  # 0 x infinity
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[2] = False
+    assert torch.isfinite(rest[:, keep]).all()
