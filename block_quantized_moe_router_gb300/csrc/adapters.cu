@@ -78,7 +78,8 @@ __device__ __forceinline__ void low_rank_sums(float (&d)[2][4][4], const uint16_
     }
 }
 
-// grid (slots * CTAs of a cluster, groups): slot s takes the group's items s, s + slots, ...
+// grid (slots * CTAs of a cluster, groups): slot s takes the group's items s, s + slots, ... in parts of K by its CTAs; where
+// a group has more items than slots, each CTA takes whole items of its own.
 template <bool F16>
 __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
     __shared__ __align__(16) int id_s[kGroup];
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
     pdl_wait();
     pdl_trigger();  // the layer's launch may start: whatever came before this one is done
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ctas = (int)cluster_size(), cta = (int)cluster_rank(), slot = (int)blockIdx.x / ctas;
-    if (ctas > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from the others
+    const int cluster = (int)cluster_size();
+    if (cluster > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from the others
     const int64_t t0 = (int64_t)blockIdx.y * kGroup;
     int id = t0 + tid < g.T ? __ldcg(g.ids + t0 + tid) : -1;
     if (id < -1 || id >= g.L) {
@@ -118,9 +119,10 @@ __global__ void __launch_bounds__(kGroup, 2) low_rank_kernel(LowRankArgs g) {
     }
     const int per_matrix = (g.R + 15) / 16, passes = (per_matrix * g.matrices + 1) / 2;  // blocks of 16 ranks, items of a batch
     const int steps = (g.K + 31) / 32;
+    const int ctas = batches * passes > g.slots ? 1 : cluster, cta = ctas > 1 ? (int)cluster_rank() : 0;  // of an item
     const int begin = (int)((int64_t)steps * cta / ctas), end = (int)((int64_t)steps * (cta + 1) / ctas);
-    if (ctas > 1) cluster_wait();
-    for (int item = slot; item < batches * passes; item += g.slots) {
+    if (cluster > 1) cluster_wait();
+    for (int item = (int)blockIdx.x / ctas; item < batches * passes; item += (int)gridDim.x / ctas) {
         const int pass = item % passes;
         if (leads && batch == item / passes) {
             item_id = id;

@@ -155,26 +155,35 @@ constexpr int kLowRanks = 32;     // ranks of an item
 constexpr int kLowSplits = 8;     // CTAs of a cluster at most
 constexpr int kLowLandingMax = 24 * 1024;  // bytes: with the static shared memory below the 48 KB that need no permission
 
+constexpr int kLowResident = 304;          // CTAs: two to an SM
+
 struct LowPlan {
     int groups, slots, splits;    // slots: clusters of a group, which share its items; splits: CTAs of a cluster, parts of K
     int landing_rows, smem;       // rows of a batch at most; bytes of the landing area
 };
-// Slots for all the items that a group can have, as far as 1024 clusters allow (32 at least); long inputs are prompts, whose
-// groups have an adapter or two, and then for its full batches.  A cluster of CTAs for each as long as all of them are
-// resident, two to an SM, and every warp has a step of K.
+// How many items a group has is known on the device alone: from its full batches, where it is part of a prompt, to a batch for each
+// row or adapter.  Where all that there can be are resident, each has a slot of its own, and a cluster of CTAs as
+// far as those are resident and every warp has a step of K.  Where not, the resident CTAs are dealt out in clusters as
+// large as slots for the full batches allow; groups with more items than slots deal their items out to single CTAs (adapters.cu), so
+// that both kinds use all of them.  (us, whole calls at rank 16 with slots for full batches alone / so; rows of 64 adapters
+// mixed: 1025 x 7168 x 2048 111 / 82, where 1024 rows take 81; 2048 rows 146 / 120; 1025 x 2 x 2048 x 7168 180 / 148, 4096 rows 354 /
+// 323, of 512 adapters 910 / 809; prompts of 1025 to 4096 rows the same within 2 %.)
 inline LowPlan plan_low_rank(int T, int K, int L, int R, int matrices) {
     LowPlan p{};
     const int rows = T < kLowGroup ? T : kLowGroup, steps = (int)(((int64_t)K + 31) / 32);
-    const int batches = (L < rows ? L : rows) + rows / kLowBatch, passes = ((R + 15) / 16 * matrices + 1) / 2;
+    const int passes = ((R + 15) / 16 * matrices + 1) / 2;  // items of a batch
+    const int batches = (L < rows ? L : rows) + rows / kLowBatch, full = (rows + kLowBatch - 1) / kLowBatch * passes;
     p.groups = (int)(((int64_t)T + kLowGroup - 1) / kLowGroup);
-    p.slots = (T > 1024 ? rows / kLowBatch : batches < rows ? batches : rows) * passes;
-    if (p.slots > 32 && (int64_t)p.slots * p.groups > 1024) p.slots = 1024 / p.groups > 32 ? 1024 / p.groups : 32;
     p.landing_rows = T < kLowBatch ? T : kLowBatch;
-    const int part = p.landing_rows * kLowRanks * (int)sizeof(float);
+    const int part = p.landing_rows * kLowRanks * (int)sizeof(float), all = (batches < rows ? batches : rows) * passes;
+    const bool resident = (int64_t)all * p.groups <= kLowResident;
+    const int least = resident ? all : full;  // slots that a larger cluster has to leave
     p.splits = 1;
     while (p.splits < kLowSplits && 2 * p.splits * part <= kLowLandingMax && 2 * p.splits * (kLowGroup / 32) <= steps &&
-           (int64_t)p.slots * p.groups * p.splits * 2 <= 304)
+           (int64_t)least * p.groups * p.splits * 2 <= kLowResident)
         p.splits *= 2;
+    const int share = kLowResident / p.splits / (p.groups < kLowResident ? p.groups : kLowResident);  // slots of a group, all resident
+    p.slots = resident || share < full ? least : share;
     p.smem = p.splits > 1 ? p.splits * part : 0;
     return p;
 }
