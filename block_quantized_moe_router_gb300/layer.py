@@ -76,11 +76,13 @@ def _check_adapters(ad, s, H):
             continue
         if sizes is None:
             sizes = tuple(a.shape[:2])
-            if len(sizes) < 2 or sizes[0] < 1 or sizes[1] % 8 or not 8 <= sizes[1] <= 256:
-                raise ValueError(f"adapters need ranks that are multiples of 8 up to 256, got {key}_a {tuple(a.shape)}")
+            if len(sizes) < 2 or not 1 <= sizes[0] <= 1 << 20 or sizes[1] % 8 or not 8 <= sizes[1] <= 256:
+                raise ValueError(f"adapters need ranks that are multiples of 8 up to 256, at most 2^20 of them, got {key}_a {tuple(a.shape)}")
         for name, t, shape in ((key + "_a", a, sizes + (cols,)), (key + "_b", b, (sizes[0], rows, sizes[1]))):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor {shape}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+            if t.data_ptr() % 16:
+                raise ValueError(f"{name} of the adapters must start at a multiple of 16 bytes")
     if sizes is None:
         raise ValueError("adapters hold none of gate, up and down")
     scale = ad.get("scale")
@@ -212,18 +214,17 @@ class MoeLayer:
         return topk_ids, topk_w, logits_out
 
     def ffn(self, x, topk_ids, topk_w, out=None, stream=None, adapter_ids=None):
-        self._adapters(adapter_ids)
+        ad = self._adapters(adapter_ids, x)
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
         capi.moe_ffn_forward(self.handle, T, self.act, self.g_act1, self.g_act2, x, topk_ids,
                              topk_w, out, self.workspace(T, stream), dev_status=self.status, stream=stream)
-        self._add_shared(x, out, stream, adapter_ids)
+        self._add_shared(x, out, stream, ad, adapter_ids)
         return out
 
-    def _add_shared(self, x, out, stream, adapter_ids=None):
+    def _add_shared(self, x, out, stream, ad=None, adapter_ids=None):
         """out += down(SiLU(gate x) * up x) of the bf16 shared expert, if the layer has one."""
-        ad = self._adapters(adapter_ids)
         if self.shared is None:
             return
         s = self.shared
@@ -235,13 +236,18 @@ class MoeLayer:
         self._linear(ad, "down", None, adapter_ids, h, s["down"], out, bias=s.get("down_bias"), residual=out,
                      stream=stream)
 
-    def _adapters(self, adapter_ids):
-        """The shared expert's adapters for a call that names them, None for one that does not."""
+    def _adapters(self, adapter_ids, x):
+        """The shared expert's adapters for a call that names them for the rows of x, None for one that does not.  What is wrong
+        with the ids is said here, before a kernel has written anything."""
         if adapter_ids is None:
             return None
         ad = None if self.shared is None else self.shared.get("adapters")
         if ad is None:
             raise ValueError("the layer was built without adapters")
+        if (adapter_ids.dtype != torch.int32 or adapter_ids.shape != x.shape[:1] or not adapter_ids.is_cuda
+                or not adapter_ids.is_contiguous() or adapter_ids.get_device() != x.get_device()):
+            raise ValueError(f"adapter_ids must be a contiguous int32 tensor {tuple(x.shape[:1])} on the device of x, "
+                             f"got {adapter_ids.dtype} {tuple(adapter_ids.shape)} on {adapter_ids.device}")
         return ad
 
     def _linear(self, ad, key, mul, ids, x, w, out, **kw):
@@ -268,6 +274,7 @@ class MoeLayer:
         if stream is not None:  # what is freed on return goes back to the stream that still uses it
             with torch.cuda.stream(stream):
                 return self.block(delta, residual, token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)
+        self._adapters(adapter_ids, delta)
         n = torch.empty_like(delta)
         r = torch.empty_like(delta)
         capi.moe_add_rms_norm(delta, self.norm_weight, n, residual=residual, sum_out=r,
@@ -297,7 +304,7 @@ class MoeLayer:
         """Route + FFN through moe_forward (one launch for a few tokens; with expert groups the
         routing runs first on its own).  adapter_ids: int32, each row's adapter of the shared expert, -1
         for none.  Returns (out, topk_ids, topk_w, logits_out)."""
-        self._adapters(adapter_ids)
+        ad = self._adapters(adapter_ids, x)
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device="cuda")
@@ -322,7 +329,7 @@ class MoeLayer:
         capi.moe_forward(self.handle, d, self.act, self.g_act1, self.g_act2, x, topk_ids, topk_w,
                          out, self.workspace(T, stream), logits_in=logits_in, logits_out=logits_out,
                          dev_status=self.status, stream=stream)
-        self._add_shared(x, out, stream, adapter_ids)
+        self._add_shared(x, out, stream, ad, adapter_ids)
         return out, topk_ids, topk_w, logits_out
 
     def forward_host(self, x_host, out_host, *, token_ids_host=None, topk_ids_host=None,
