@@ -271,6 +271,8 @@ class MoeLayer:
         by default)."""
         if self.norm_weight is None:
             raise ValueError("the layer was built without norm_weight")
+        if self.post_norm_weight is not None or self.block_gate is not None or self.residual_scale != 1:
+            raise ValueError("block() has no norm behind the layer, no gate and no residual scale; joined_block() has")
         if stream is not None:  # what is freed on return goes back to the stream that still uses it
             with torch.cuda.stream(stream):
                 return self.block(delta, residual, token_ids=token_ids, logits_in=logits_in, adapter_ids=adapter_ids)
