@@ -354,7 +354,8 @@ def _stack(t, dtype, L, rows, cols, dev, name):
     step, ld, one = t.stride()
     if one != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (ld if rows > 1 else cols), step
+    ld = ld if rows > 1 else cols
+    return t.data_ptr(), ld, (step if L > 1 else rows * ld)  # a lone adapter has no distance
 
 
 def _pair(a, b, dtype, L, R, N, K, dev, name):
