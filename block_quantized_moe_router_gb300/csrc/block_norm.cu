@@ -196,7 +196,7 @@ __device__ __forceinline__ void store_rounded(S* at, const float (&v)[8]) {
     }
 }
 
-// Many long rows, all on their boundaries: a CTA per row, V vectors to a thread.  What bounds it are the instructions beside
+// Many long rows of up to 8192 elements, all on their boundaries: a CTA per row, V vectors to a thread.  What bounds it are the instructions beside
 // the loads, of which each warp's sums are a large part: fewer warps to a row, as many rows to an SM as their registers allow
 // (us, 32768 rows of 7168 / 4096 of 4096 with an fp32 stream: V 1 by two rows to an SM 382 / 32.4, V 2 by three 293 / 32.4, V 4 by
 // four 269 / 36.4, by five 297 / 41; rows in pairs by CTAs that stay, the next ones brought ahead, 383 / 50).
@@ -312,7 +312,19 @@ cudaError_t launch_mode(const BlockNormArgs& a, cudaStream_t st) {
         const auto row = [&](auto kernel, int v) {
             return launch_pdl(kernel, dim3(a.T), dim3(((nvec + v - 1) / v + 31) / 32 * 32), st, a);
         };
-        if (a.T >= 512 && nvec <= 1024)
+        // sandwich_row_kernel from where its rows to an SM tell.  us, this kernel / V 2 / V 4, rows of
+        //   16 bits    512 rows        1024 rows           4096 rows           16384 rows
+        //     2048   3.9/4.3/5.4    5.8/6.0/6.3     15.2/13.8/15.6      50.3/43.5/44.7
+        //     4096   6.0/6.2/6.5    9.8/9.6/8.7     28.7/25.3/25.5      99.0/82.1/82.6
+        //     5120   8.0/6.3/7.3  12.1/10.9/12.8    36.9/32.4/32.0     128.9/107.2/102.1
+        //     8192  10.7/10.2/8.7 17.7/15.2/16.1    58.5/47.2/46.2     212.4/164.8/158.4
+        //   fp32 stream
+        //     2048   4.6/5.3/6.5    6.5/7.5/7.9     18.6/19.8/22.0      61.1/62.0/68.3
+        //     4096   7.2/7.7/8.7  12.0/13.0/12.0    34.9/34.6/39.9     122.0/118.4/127.4
+        //     8192  13.2/13.5/12.2 21.9/21.3/23.1   71.8/64.2/69.3     264.6/230.3/244.1
+        // (33 to 256 rows: this kernel by 5 to 25 %, 384 rows: within 20 % either way.)
+        const bool rows = sizeof(S) == 2 ? a.T >= 1024 || (a.T >= 512 && nvec > 512) : a.T >= 1024 && nvec >= 512;
+        if (rows && nvec <= 1024)
             return nvec > 512 && sizeof(S) == 2 ? row(sandwich_row_kernel<E, S, 4>, 4) : row(sandwich_row_kernel<E, S, 2>, 2);
     }
     if (nvec <= 1024) return launch_row_per_cta<E, S, MODE, 1>(a, nvec, st);
