@@ -12,9 +12,12 @@
 // Which adapters occur is known on the device alone: every CTA of a group finds the batches by itself (a comparison
 // with the ids before it per row), so that no launch has to sort them.
 //
-// Alone and cold, 1 gated row of 7168, rank 16: 8 to 11 us, latency; 512 rows of 2048 with 32 adapters: 13 us; 16384 rows of 2048,
-// rank 64: 65 us, the loads of x for every 32 ranks and of a for every 32 rows from L2.  A whole call with the layer: 16.9 us for
-// that one row, 36 for 64 gated rows of 4096 with an adapter each, 182 for 4096 gated rows of 7168, 363 for those 16384.
+// How v is held, and what becomes of a v that the layer's type does not hold: kernels.h.
+//
+// Alone and cold, 1 gated row of 7168, rank 16: 7 to 9 us, latency; 512 rows of 2048 with 32 adapters: 11 us; 4096 gated rows of 7168:
+// 22 us; 16384 rows of 2048, rank 64: 55 us, the loads of x for every 32 ranks and of a for every 32 rows from L2.  A whole call
+// with the layer: 17.0 us for that one row, 37.8 for 64 gated rows of 4096 with an adapter each, 179 for those 4096, 351 for the
+// 16384.  The 128 registers that two CTAs to an SM leave do not hold all: 56 bytes of spills beside the sums.
 #include "cluster.cuh"
 #include "kernels.h"
 #include "launch_plan.h"
@@ -47,7 +50,8 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 }
 
 // This warp's part of an item's sums, over the steps of 32 elements of K from `step` on, `stride` apart: NB blocks of 8
-// rows.  rows: where this lane's ranks of a begin (nullptr: none), their ranks being g, g + 8, g + 16 and g + 24.
+// rows.  With g = lane / 4, rank: where the item's ranks g, g + 8, g + 16 and g + 24 of a begin, row: where the batch's rows g, g + 8,
+// ... of x do (nullptr: none).
 template <bool F16, int NB, int UNROLL>
 __device__ __forceinline__ void low_rank_sums(float (&d)[2][4][4], const uint16_t* const (&rank)[4],
                                               const uint16_t* const (&row)[4], int step, int stride, int end, int K) {

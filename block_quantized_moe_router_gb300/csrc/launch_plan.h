@@ -76,6 +76,8 @@ constexpr int64_t many_tiles(int T, int N, int features) {
 //     allows; every row of x costs its exchange and sums, least where a part of K has a tile alone; 1.6 us
 //     a wave and 0.6 us once besides.  128 rows of the gated 2 x 2048 x 7168: 16.2 us in two parts by pairs,
 //     19.3 in four by single CTAs, 31.2 in the other kernel; 256 rows of 7168 x 2048: 15.4, 17.4 and 14.7.
+// moe_linear_adapters takes the same choices.  They count neither its addends nor that its few-row CTAs are two to an SM by
+// their registers, nor that beside the low-rank products no CTA is alone; never fitted for it.
 struct LinPlan {
     bool few, pair;
     int width;                   // many: columns per tile

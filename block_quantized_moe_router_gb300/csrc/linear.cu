@@ -19,7 +19,9 @@
 //
 // With low-rank adapters (ADAPT) each row's product gains v b[j]^T, v = scale x a[j]^T, before the function.  v comes
 // from the launch before (adapters.cu), which lets this one start before it ends: x and the weights are not
-// its results, so only what reads v waits for it, and v takes no time where the weights take longer.
+// its results, so only what reads v waits for it.  That hides v behind the weights where a CTA of this launch finds room beside
+// those of the other: two of theirs on an SM take all of its registers, so up to 152 of them (1 row of 7168 or 8 of 2048), and
+// the many-row kernel, which takes a whole SM, starts on those that the other has left.
 //   few rows   a thread adds its results' low-rank products by FMA, straight from global memory, after the parts of K.
 //              v is fp32.
 //   many rows  a tile's accumulator takes further stages of K, v against b[j], for each adapter j that

@@ -273,7 +273,9 @@ moe_status_t moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const vo
  * numbers of the layer's type, whose sum is off by up to 2^-16 |v| (bf16; f16: 2^-22 |v| + 2^-25, so that 22 bits of
  * it are held from 2^-3 on and fewer below); elsewhere as fp32, and so does at any number of rows what the type does not
  * hold.  All else as in moe_linear.  A row depends on its own adapter alone, and each of its factors on that factor's:
- * a NaN or an infinity in one adapter stays in the rows that have it.  Rows of one adapter need not be
+ * a NaN or an infinity in one adapter stays in the rows that have it (where an infinity in b meets one of the layer's
+ * own of the other sign, many rows may have the infinity of b for a NaN).  The order of the fp32 sums may depend on the ids of
+ * other rows; equal calls give equal bits.  Rows of one adapter need not be
  * neighbours; what is read of the adapters are those that occur in ids.  An id outside [-1, L) sets
  * MOE_DEV_BAD_ADAPTER_ID, and its row has no adapter.
  * workspace [device] 16-byte aligned, ws_bytes >= moe_adapter_workspace_size(T, R, matrices), matrices 2
